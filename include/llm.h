@@ -332,11 +332,158 @@ void llm_destroy(llm_handle *h);
 
 const char *llm_status_string(int status);
 /* The one-line reason of the handle's last failed call.  With h == NULL: the
- * reason of the calling thread's last failed llm_create, "" after one that
+ * reason of the calling thread's last failed llm_create or call without a
+ * handle (the operators of batched decoding), "" after an llm_create that
  * succeeded (llm_create_from_gguf reports through its `err` buffer).  The
  * string stays valid until the next call on the handle (with NULL: until this
- * thread's next llm_create). */
+ * thread's next such call). */
 const char *llm_last_error(const llm_handle *h);
+
+/* ------------------------------------------------- batched decoding --
+ * Operators for decoding several continuations of one prompt together
+ * ("What a Llama model computes, and why" §2 for the arithmetic of one row):
+ * the new tokens' rows are rotated and appended to a paged cache, attend over
+ * a prefix that all sequences share (the prompt's rows, read once for all of
+ * them) and over their own sequence's pages, and the resulting logits become
+ * log probabilities.  llm_decode_batch runs a handle's whole step on them.
+ *
+ * These calls take a stream and no handle (llm_decode_batch takes a handle and
+ * uses its stream): they only enqueue, allocate nothing, keep no state between
+ * calls and may be captured into a CUDA graph.  The device pointers must be
+ * valid on the current device, which the stream belongs to.  A failed call has
+ * enqueued nothing; llm_last_error(NULL) gives the calling thread's reason.
+ *
+ * Rows.  A call handles n_seqs sequences of n_new new tokens each; new token i
+ * of sequence s is row s*n_new + i of q, k, v and the outputs.  lens[s] counts
+ * the rows of s behind the prefix, the new ones among them: new token i is
+ * row e = lens[s] - n_new + i of its sequence's pages, at position prefix_len
+ * + e.  Rows with e < 0 are padding: they are neither read into any result nor
+ * written (a sequence with lens[s] = 0 takes no part).  So a batch whose
+ * sequences bring different numbers of new tokens pads each in front.
+ *
+ * Pages.  Row e of sequence s is row e % page_size of page
+ * page_table[s*max_pages + e / page_size]; a page is [page_size][n_kv_heads]
+ * [head_dim] FP16, once in k_pages and once in v_pages.  Table entries behind
+ * a sequence's last row are never read.  Sequences may share full pages as long
+ * as no row is appended to a shared one; the rows of one append call must lie
+ * at different places.
+ *
+ * Errors seen on the device (`err` may be NULL) are OR-ed into *err, and the
+ * accesses they concern are skipped: LLM_PAGES_BAD_PAGE, a page number outside
+ * [0, n_pages) (an append skips the row's K and V, attention the page's
+ * rows); LLM_PAGES_BAD_LEN, a row at or behind max_pages*page_size (skipped
+ * likewise) or, in llm_kv_append, behind the angle table (the whole row is
+ * skipped); LLM_PAGES_TIMEOUT, a bounded wait inside a kernel gave up (the
+ * outputs are invalid).  A row of attention left without any key is zero. */
+typedef struct {
+    int32_t n_seqs, n_new;               /* >= 0, >= 1 */
+    int32_t prefix_len;                  /* >= 0: rows all sequences share, before their pages */
+    int32_t page_size;                   /* a power of two */
+    int32_t n_pages, max_pages;          /* pages of the pool (>= 0), entries of a sequence's table row (>= 0) */
+    int32_t n_kv_heads, head_dim;        /* head_dim: a multiple of 8, at most 128 */
+    uint16_t *k_pages, *v_pages;         /* DEVICE, 16-byte aligned */
+    const int32_t *page_table;           /* DEVICE [n_seqs][max_pages] */
+    const int32_t *lens;                 /* DEVICE [n_seqs] */
+    int32_t *err;                        /* DEVICE, or NULL */
+} llm_pages;
+enum { LLM_PAGES_BAD_PAGE = 1, LLM_PAGES_BAD_LEN = 2, LLM_PAGES_TIMEOUT = 4 };
+
+/* cos and sin of the rotation angles of positions pos0 .. pos0+n_pos-1:
+ * cos_sin[(p * rope_dims/2 + j) * 2] = cos, + 1 = sin of pair j at position
+ * pos0 + p.  The angles are the decode step's ("The Forward Pass in Java",
+ * Example 6: a float that starts at the position and is multiplied by
+ * rope_base^(-2/rope_dims) once per pair; divided by rope_freqs[j] when not
+ * NULL), so a cache written with this table holds the same bits.  cos_sin
+ * (DEVICE, n_pos * rope_dims floats), rope_freqs (DEVICE).  Errors:
+ * INVALID_ARG, CUDA. */
+int llm_rope_table(float *cos_sin, int32_t pos0, int32_t n_pos, int32_t rope_dims, float rope_base,
+                   const float *rope_freqs, llm_stream_t stream);
+
+/* Rows of q, k and v (dtype LLM_F32 or LLM_F16): head h of row r at r*stride +
+ * h*head_dim, strides in elements.  Every pointer is DEVICE and 16-byte
+ * aligned and every stride a multiple of 16 bytes (so q, k and v may be parts
+ * of one fused projection's rows).  q_out (q_out_dtype) receives the rotated q
+ * and may be q itself (same type and stride); n_heads = 0: k and v only.
+ * cos_sin: the angle table of positions 0 .. table_rows-1 (llm_rope_table's
+ * layout, pos0 = 0). */
+typedef struct {
+    int32_t n_heads, rope_dims, rope_neox;   /* as in llm_config */
+    int32_t table_rows;
+    int32_t dtype, q_out_dtype;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    void *q_out;
+    int64_t q_out_stride;
+    const float *cos_sin;                    /* 8-byte aligned */
+} llm_append;
+
+/* Rotates the new rows' q and k (each product and sum rounded once in F32, as
+ * the decode step does) and writes k and v into their pages as FP16 (round to
+ * nearest even) and q into q_out.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int llm_kv_append(const llm_pages *pages, const llm_append *a, llm_stream_t stream);
+
+/* Attention of the new rows.  q [rows][n_heads][head_dim] (dtype q_dtype, row
+ * stride q_stride), out likewise; LLM_F32 or LLM_F16 each; 16-byte aligned,
+ * strides multiples of 16 bytes.  n_heads is a multiple of n_kv_heads; head h
+ * reads kv head h / (n_heads / n_kv_heads).  prefix_k, prefix_v: rows
+ * 0..prefix_len-1 of the shared prefix, FP16, kv head g of row t at t *
+ * prefix_stride + g * head_dim (16-byte aligned, the stride a multiple of 8 and
+ * at least n_kv_heads * head_dim; a handle's cache from llm_kv_view has the
+ * stride n_kv_heads * head_dim); unused when prefix_len is 0.  Row (s, i)
+ * attends to the whole prefix and to rows 0..e of its sequence's pages with
+ * softmax(scale * q.k); scale > 0, or 0 for 1/sqrt(head_dim).
+ * workspace: DEVICE, 256-byte aligned, at least llm_attend_batch_workspace()
+ * bytes.  Its contents do not matter before a call and mean nothing after it;
+ * two calls (or replays of graphs that captured them) that may run at the same
+ * time need a workspace each. */
+typedef struct {
+    int32_t n_heads, q_dtype, out_dtype;
+    float scale;
+    const void *q;
+    int64_t q_stride;
+    void *out;
+    int64_t out_stride;
+    const uint16_t *prefix_k, *prefix_v;
+    int64_t prefix_stride;
+    void *workspace;
+    int64_t workspace_bytes;
+} llm_attend;
+
+/* The arithmetic: F32 softmax statistics and sums.  F16 outputs round each
+ * probability to FP16 before it meets V, F32 outputs keep it as two FP16 parts
+ * (as the decode step's attention), an F32 q is split into two parts too, so
+ * every product with a cached value is exact.  Errors: INVALID_ARG,
+ * UNSUPPORTED, CUDA. */
+int llm_attend_batch(const llm_pages *pages, const llm_attend *a, llm_stream_t stream);
+
+/* Bytes of workspace that a call with these sizes needs (the pointers are not
+ * looked at), or a negative llm_status. */
+int64_t llm_attend_batch_workspace(const llm_pages *pages, const llm_attend *a);
+
+/* n_rows rows of vocab logits (LLM_F32 or LLM_F16; row r at r * stride
+ * elements, any alignment of the type).  For each row, with p = softmax(row):
+ *   logprob[r*n_targets + t]  ln p of token targets[r*n_targets + t]; 0 for
+ *                             target -1 (none), NaN for another token outside
+ *                             [0, vocab)
+ *   entropy[r]                -sum p ln p (NULL: not wanted)
+ *   top_id, top_logprob       [n_rows][top]: the top largest logits' tokens,
+ *                             equal ones by the lowest index, and their ln p
+ * top is at most 32 and vocab; 0: none.  A logit of -infinity is a token of
+ * probability 0 (logprob -infinity, no part in the entropy).  A row with no
+ * other logits gives logprob -infinity and entropy 0; a row with a NaN or
+ * +infinity gives NaN, its top_id by the logits that are numbers (-1 where
+ * there are fewer than top).  DEVICE pointers; n_rows >= 0, vocab >= 1.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+    int32_t n_rows, vocab, dtype, n_targets, top;
+    const void *logits;
+    int64_t stride;
+    const int32_t *targets;
+    float *logprob, *entropy;
+    int32_t *top_id;
+    float *top_logprob;
+} llm_logprobs_args;
+int llm_logprobs(const llm_logprobs_args *a, llm_stream_t stream);
 
 /* ------------------------------------------------------------ GGUF files --
  * A model file in the GGUF version 3 layout of "Loading GGUF with the FFM API"

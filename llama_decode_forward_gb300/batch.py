@@ -1,0 +1,179 @@
+"""Batched decoding over CUDA tensors: the operators llm_kv_append,
+llm_attend_batch and llm_logprobs of include/llm.h.
+
+Each class checks its tensors once, keeps them (and the C arguments made of
+them) and enqueues one call of its operator whenever it is called, on the
+current stream or the one given: a decoding loop writes each step's values into
+the same tensors, or captures the calls into a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding as _b
+
+_DTYPES = {torch.float32: _b.LLM_F32, torch.float16: _b.LLM_F16}
+
+
+def _stream(stream) -> int:
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream
+
+
+def _run(rc: int) -> None:
+    if rc != _b.LLM_OK:
+        raise _b.LlmError(rc, _b._lib.llm_last_error(None).decode())
+
+
+def _tensor(name, t, dtypes, shape, device, strided=False):
+    """Refuses a tensor of another type, shape, device or memory order: row
+    major without gaps, or with strided=True free in its first stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} is on {t.device}, not on {device or 'a CUDA device'}")
+    if len(t.shape) != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    inner = t[0] if strided and t.shape[0] else t
+    if not inner.is_contiguous():
+        raise ValueError(f"{name} is not contiguous{' within a row' if strided else ''}")
+    return t
+
+
+class PagedBatch:
+    """n_seqs sequences of n_new new tokens each behind a shared prefix of
+    prefix_len rows (llm_pages).  k_pages, v_pages: float16 [n_pages,
+    page_size, n_kv_heads, head_dim]; page_table int32 [n_seqs, max_pages];
+    lens int32 [n_seqs], the rows behind the prefix, the new ones among them.
+    ``err`` (int32, one value) collects the errors seen on the device
+    (LLM_PAGES_*); errors() reads it."""
+
+    def __init__(self, k_pages, v_pages, page_table, lens, n_new: int = 1, prefix_len: int = 0, err=None):
+        _tensor("k_pages", k_pages, (torch.float16,), (None,) * 4, None)
+        dev = k_pages.device
+        _tensor("v_pages", v_pages, (torch.float16,), tuple(k_pages.shape), dev)
+        _tensor("lens", lens, (torch.int32,), (None,), dev)
+        _tensor("page_table", page_table, (torch.int32,), (lens.shape[0], None), dev)
+        if err is None:
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+        _tensor("err", err, (torch.int32,), (1,), dev)
+        self.k_pages, self.v_pages, self.page_table, self.lens, self.err = k_pages, v_pages, page_table, lens, err
+        self.device = dev
+        n_pages, page_size, n_kv, hd = k_pages.shape
+        self.rows = lens.shape[0] * n_new
+        self.struct = _b.llm_pages(n_seqs=lens.shape[0], n_new=n_new, prefix_len=prefix_len, page_size=page_size,
+                                   n_pages=n_pages, max_pages=page_table.shape[1], n_kv_heads=n_kv, head_dim=hd,
+                                   k_pages=k_pages.data_ptr(), v_pages=v_pages.data_ptr(),
+                                   page_table=page_table.data_ptr(), lens=lens.data_ptr(), err=err.data_ptr())
+
+    def errors(self) -> int:
+        """The LLM_PAGES_* bits seen so far (waits for the device)."""
+        return int(self.err.item())
+
+
+class _Op:
+    """One operator with its arguments; calling it enqueues one run."""
+
+    def __call__(self, stream=None) -> None:
+        if torch.cuda.current_device() != self._index:
+            raise ValueError(f"the operator's tensors are on cuda:{self._index}, the current device is another")
+        rc = self._fn(*self._args, _stream(stream))
+        if rc:
+            _run(rc)
+
+
+class KvAppend(_Op):
+    """llm_kv_append: rotates q [rows, n_heads, head_dim] into q_out and k
+    [rows, n_kv_heads, head_dim] on its way into the pages, which take v too.
+    q, k, v: float32 or float16, free in the row stride (parts of one fused
+    projection); q None: no queries.  q_out: float32 or float16, q itself for a
+    rotation in place.  cos_sin: float32 [positions, rope_dims / 2, 2] from
+    rope_table() or the caller's own."""
+
+    def __init__(self, pages: PagedBatch, q, k, v, cos_sin, q_out=None, rope_neox: bool = False):
+        p, dev = pages.struct, pages.device
+        kv = (pages.rows, p.n_kv_heads, p.head_dim)
+        _tensor("k", k, _DTYPES, kv, dev, strided=True)
+        _tensor("v", v, (k.dtype,), kv, dev, strided=True)
+        _tensor("cos_sin", cos_sin, (torch.float32,), (None, None, 2), dev)
+        a = _b.llm_append(n_heads=0, rope_dims=2 * cos_sin.shape[1], rope_neox=int(rope_neox),
+                          table_rows=cos_sin.shape[0], dtype=_DTYPES[k.dtype], q_out_dtype=_b.LLM_F32,
+                          k=k.data_ptr(), v=v.data_ptr(), k_stride=k.stride(0), v_stride=v.stride(0),
+                          cos_sin=cos_sin.data_ptr())
+        if q is not None:
+            _tensor("q", q, (k.dtype,), (pages.rows, None, p.head_dim), dev, strided=True)
+            _tensor("q_out", q_out, _DTYPES, tuple(q.shape), dev, strided=True)
+            a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), q.stride(0)
+            a.q_out, a.q_out_stride, a.q_out_dtype = q_out.data_ptr(), q_out.stride(0), _DTYPES[q_out.dtype]
+        self._kept, self._fn, self._index = (pages, q, k, v, cos_sin, q_out), _b._lib.llm_kv_append, dev.index
+        self._args = ctypes.byref(p), ctypes.byref(a)
+
+
+class AttendBatch(_Op):
+    """llm_attend_batch: out = attention of q [rows, n_heads, head_dim] over
+    the shared prefix_k, prefix_v (float16 [at least prefix_len, n_kv_heads,
+    head_dim], free in the row stride) and the sequences' pages.  q, out:
+    float32 or float16, free in the row stride.  The operator owns its
+    workspace, so runs of one object must not overlap in time: give each stream
+    (and each captured graph that may run beside another) its own."""
+
+    def __init__(self, pages: PagedBatch, q, out, prefix_k=None, prefix_v=None, scale: float = 0.0):
+        p, dev = pages.struct, pages.device
+        _tensor("q", q, _DTYPES, (pages.rows, None, p.head_dim), dev, strided=True)
+        _tensor("out", out, _DTYPES, tuple(q.shape), dev, strided=True)
+        a = _b.llm_attend(n_heads=q.shape[1], q_dtype=_DTYPES[q.dtype], out_dtype=_DTYPES[out.dtype], scale=scale,
+                          q=q.data_ptr(), q_stride=q.stride(0), out=out.data_ptr(), out_stride=out.stride(0))
+        if p.prefix_len > 0:
+            for name, t in (("prefix_k", prefix_k), ("prefix_v", prefix_v)):
+                _tensor(name, t, (torch.float16,), (None, p.n_kv_heads, p.head_dim), dev, strided=True)
+                if t.shape[0] < p.prefix_len:
+                    raise ValueError(f"{name} holds {t.shape[0]} rows, the prefix has {p.prefix_len}")
+            if prefix_k.stride(0) != prefix_v.stride(0):
+                raise ValueError("prefix_k and prefix_v have different row strides")
+            a.prefix_k, a.prefix_v, a.prefix_stride = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.stride(0)
+        n = _b._lib.llm_attend_batch_workspace(ctypes.byref(p), ctypes.byref(a))
+        if n < 0:
+            _run(int(n))
+        self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = self.workspace.data_ptr(), int(n)
+        self._kept, self._fn, self._index = (pages, q, out, prefix_k, prefix_v), _b._lib.llm_attend_batch, dev.index
+        self._args = ctypes.byref(p), ctypes.byref(a)
+
+
+class LogProbs(_Op):
+    """llm_logprobs of logits [rows, vocab] (float32 or float16, free in the
+    row stride): the log probability of each token of targets (int32 [rows,
+    n_targets], -1: none; None: no targets), the entropy and the ``top`` most
+    likely tokens of each row, in the tensors logprob, entropy, top_id and
+    top_logprob."""
+
+    def __init__(self, logits, targets=None, top: int = 0):
+        _tensor("logits", logits, _DTYPES, (None, None), None, strided=True)
+        n, dev = logits.shape[0], logits.device
+        if targets is not None:
+            _tensor("targets", targets, (torch.int32,), (n, None), dev)
+        n_targets = 0 if targets is None else targets.shape[1]
+        self.logprob = torch.empty(n, n_targets, dtype=torch.float32, device=dev)
+        self.entropy = torch.empty(n, dtype=torch.float32, device=dev)
+        self.top_id = torch.empty(n, max(top, 0), dtype=torch.int32, device=dev)
+        self.top_logprob = torch.empty(n, max(top, 0), dtype=torch.float32, device=dev)
+        a = _b.llm_logprobs_args(n_rows=n, vocab=logits.shape[1], dtype=_DTYPES[logits.dtype], n_targets=n_targets,
+                                 top=top, logits=logits.data_ptr(), stride=logits.stride(0),
+                                 targets=targets.data_ptr() if n_targets else None, logprob=self.logprob.data_ptr(),
+                                 entropy=self.entropy.data_ptr(), top_id=self.top_id.data_ptr(),
+                                 top_logprob=self.top_logprob.data_ptr())
+        self._kept, self._fn, self._index = (logits, targets), _b._lib.llm_logprobs, dev.index
+        self._args = (ctypes.byref(a),)
+
+
+def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, pos0: int = 0, device="cuda",
+               stream=None) -> torch.Tensor:
+    """llm_rope_table: float32 [n_pos, rope_dims / 2, 2] of the decode step's
+    angles at positions pos0 .. pos0 + n_pos - 1."""
+    out = torch.empty(n_pos, rope_dims // 2, 2, dtype=torch.float32, device=device)
+    if rope_freqs is not None:
+        _tensor("rope_freqs", rope_freqs, (torch.float32,), (rope_dims // 2,), out.device)
+    _run(_b._lib.llm_rope_table(out.data_ptr(), pos0, n_pos, rope_dims, rope_base,
+                                rope_freqs.data_ptr() if rope_freqs is not None else None, _stream(stream)))
+    return out

@@ -20,6 +20,7 @@ LLM_ERR_INVALID_ARG, LLM_ERR_UNSUPPORTED, LLM_ERR_OUT_OF_RANGE = -1, -2, -3
 LLM_ERR_CUDA, LLM_ERR_NO_MEMORY, LLM_ERR_DEVICE_TIMEOUT, LLM_ERR_STATE, LLM_ERR_NONFINITE = -4, -5, -6, -7, -8
 LLM_ERR_CHECK = -9
 LLM_NUMERICS_EXACT, LLM_NUMERICS_LLAMACPP = 0, 1
+LLM_PAGES_BAD_PAGE, LLM_PAGES_BAD_LEN, LLM_PAGES_TIMEOUT = 1, 2, 4
 LLM_DEBUG_Q, LLM_DEBUG_K, LLM_DEBUG_V, LLM_DEBUG_ATTN_OUT, LLM_DEBUG_FFN_SWIGLU, LLM_DEBUG_FFN_OUT = range(6)
 
 
@@ -38,6 +39,35 @@ class llm_layer_weights(ctypes.Structure):
 class llm_weights(ctypes.Structure):
     _fields_ = [("tok_embd", ctypes.c_void_p), ("output_norm", ctypes.c_void_p), ("output", ctypes.c_void_p),
                 ("rope_freqs", ctypes.c_void_p), ("layers", ctypes.POINTER(llm_layer_weights))]
+
+
+class llm_pages(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_new", "prefix_len", "page_size", "n_pages", "max_pages",
+                                              "n_kv_heads", "head_dim")] + \
+               [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "page_table", "lens", "err")]
+
+
+class llm_append(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_heads", "rope_dims", "rope_neox", "table_rows", "dtype",
+                                              "q_out_dtype")] + \
+               [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_int64), ("cos_sin", ctypes.c_void_p)]
+
+
+class llm_attend(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("q_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("prefix_k", ctypes.c_void_p),
+                ("prefix_v", ctypes.c_void_p), ("prefix_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
+class llm_logprobs_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_rows", "vocab", "dtype", "n_targets", "top")] + \
+               [("logits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("targets", ctypes.c_void_p),
+                ("logprob", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("top_id", ctypes.c_void_p),
+                ("top_logprob", ctypes.c_void_p)]
 
 
 class llm_gguf_layout(ctypes.Structure):
@@ -95,6 +125,11 @@ _SIGS = {
     "llm_test_guards": ([_vp], ctypes.c_int64),
     "llm_test_poke_guard": ([_vp, _int], _int),
     "llm_prefill_f16_copy": ([_vp, _int], _int),
+    "llm_rope_table": ([_vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp], _int),
+    "llm_kv_append": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_append), _vp], _int),
+    "llm_attend_batch_workspace": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_attend)], ctypes.c_int64),
+    "llm_attend_batch": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_attend), _vp], _int),
+    "llm_logprobs": ([ctypes.POINTER(llm_logprobs_args), _vp], _int),
 }
 
 

@@ -343,9 +343,25 @@ int check_shape(const llm_config* c, std::string* why) {
 }
 }  // namespace llm
 
-// Reason of the calling thread's last failed llm_create: there is no handle
-// to hold it then, so llm_last_error(NULL) returns it.
+// Reason of the calling thread's last failed llm_create or call without a
+// handle: no handle holds it, so llm_last_error(NULL) returns it.
 static thread_local std::string t_create_error;
+
+namespace llm {
+int fail_op(int status, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    try {
+        t_create_error = buf;
+    } catch (...) {                        // no memory for the reason: no exception leaves a C entry
+        t_create_error.clear();
+    }
+    return status;
+}
+}  // namespace llm
 
 // A failed llm_create: keep the handle's reason for llm_last_error(NULL) and
 // release what was allocated so far.
@@ -528,7 +544,7 @@ extern "C" int llm_create(const llm_config* cfg, const llm_weights* w, llm_strea
     CKC(cudaMemsetAsync(h->trace, 0, (size_t)h->sms * kTraceSlots * 8, h->st));
 #endif
 
-    h->theta_scale = (float)pow((double)c.rope_base, -2.0 / (double)c.rope_dims);
+    h->theta_scale = rope_theta_scale(c.rope_base, c.rope_dims);
     h->attn_div = (float)sqrt((double)c.head_dim);
     h->kernel = step_kernel_ptr(c.wtype, c.numerics == LLM_NUMERICS_LLAMACPP);
     // row partials a CTA keeps for one GEMV phase (multi-warp teams): its rows

@@ -1,8 +1,11 @@
 // Internal device layouts and helpers of libllmdecode (not part of the ABI).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "../../include/llm.h"
@@ -204,6 +207,14 @@ size_t prefill_workspace_bytes(const PrefillCtx& c);
 // size, and its expansion (asynchronous on c.st; *launches counts kernels).
 size_t prefill_f16_copy_bytes(const PrefillCtx& c);
 cudaError_t prefill_make_f16_copy(const PrefillCtx& c, __half* dst, int* launches);
+// cos/sin of positions pos0 .. pos0+n-1 (prefill.cu), with theta_scale =
+// rope_theta_scale(base, rope_dims), the factor between two pairs' angles.
+inline float rope_theta_scale(float base, int rope_dims) { return (float)pow((double)base, -2.0 / (double)rope_dims); }
+cudaError_t rope_table(cudaStream_t st, float* tab, int n, int pos0, int rope_dims, float theta_scale,
+                       const float* freqs);
+// Records the calling thread's reason (llm_last_error(NULL)) of a failed call
+// without a handle; returns `status`.
+int fail_op(int status, const char* fmt, ...);
 cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_host, int n, int pos0, const char** msg);
 
 __host__ __device__ inline int dtype_bytes_x16(int wtype) {   // bytes per element, times 16
@@ -442,6 +453,72 @@ __device__ __forceinline__ unsigned long long argmax_key(float v, int idx) {
 
 __device__ __forceinline__ int argmax_key_index(unsigned long long k) {
     return k == 0ull ? 0 : (int)(0xFFFFFFFFu - (uint32_t)(k & 0xFFFFFFFFull));
+}
+
+// ------------------------------------------------------ launches, waits --
+// Programmatic dependent launch.  Every kernel of the batched prefill and
+// of the batched operators is launched with programmatic stream serialization (launch_dep) and lets the
+// next kernel be scheduled as soon as all its own CTAs are running
+// (griddep_launch); each waits for the whole previous kernel to complete, its
+// memory visible (griddep_wait), before it touches activations.  So a
+// kernel's launch and setup overlap the tail of the one before, and nothing
+// else changes.  (Without the launch attribute both are no-ops.)
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void griddep_entry() {
+    griddep_launch();
+    griddep_wait();
+}
+
+// A launch with programmatic stream serialization (see griddep_entry).
+template <class... KArgs, class... Args>
+cudaError_t launch_dep(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+constexpr long long kSpinLimit = 200000000ll;   // mbarrier polls before a wait gives up
+__device__ __forceinline__ bool wait_parity(uint64_t* bar, uint32_t par, int* err) {
+    for (long long i = 0; i < kSpinLimit; i++)
+        if (mbar_test_wait(bar, par)) return true;
+    atomicOr(err, kErrTimeout);
+    return false;
+}
+
+// (not volatile: a pure function of its operands, so the compiler may
+// interleave independent accumulation chains)
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t h2_bits(__half a, __half b) {
+    return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
+}
+
+inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    return fn;
 }
 
 }  // namespace llm

@@ -44,44 +44,6 @@ constexpr int kGABytes = kGBM * kGBK * 2;
 // down (2048: 128 tiles of 64), gate/up (16384: 256 tiles of 256; 296 tiles
 // of 224 were slower)
 constexpr int kBnQkv = 128, kBnNarrow = 64, kBnWide = 256;
-constexpr long long kSpinLimit = 200000000ll;   // mbarrier polls before a wait gives up
-
-// Programmatic dependent launch.  Every kernel of the batched prefill is
-// launched with programmatic stream serialization (launch_dep) and lets the
-// next kernel be scheduled as soon as all its own CTAs are running
-// (griddep_launch); each waits for the whole previous kernel to complete, its
-// memory visible (griddep_wait), before it touches activations.  So a
-// kernel's launch and setup overlap the tail of the one before, and nothing
-// else changes.  (Without the launch attribute both are no-ops.)
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void griddep_entry() {
-    griddep_launch();
-    griddep_wait();
-}
-
-// A launch with programmatic stream serialization (see griddep_entry).
-template <class... KArgs, class... Args>
-cudaError_t launch_dep(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
-}
-
-__device__ __forceinline__ bool wait_parity(uint64_t* bar, uint32_t par, int* err) {
-    for (long long i = 0; i < kSpinLimit; i++)
-        if (mbar_test_wait(bar, par)) return true;
-    atomicOr(err, kErrTimeout);
-    return false;
-}
 
 // The same wait with the threads suspended between probes (about 1 us at
 // most per probe): for warps that wait through a whole main loop, whose
@@ -788,19 +750,6 @@ __global__ void argmax_publish_kernel(unsigned long long* best, int* out) {
     *best = 0ull;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    return fn;
-}
-
 // 2-D map of a [rows][K] F16 matrix, box 64 x box_rows, 128-byte swizzle.
 // ------------------------------------------------ attention on tensor cores --
 // Causal attention of 16 prompt rows of one kv head over the cache ("The
@@ -820,20 +769,6 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // its own in the order sp = 1, 2, ... (the same bits in every run).  The
 // output row is divided by its sum and rounded to F16 (the O projection's
 // operand).
-// (not volatile: a pure function of its operands, so the compiler may
-// interleave independent accumulation chains)
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t h2_bits(__half a, __half b) {
-    return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
-}
-
 constexpr int kAttnKT = 128;                     // cache positions per K/V tile
 
 template <int HD>
@@ -1121,6 +1056,13 @@ cudaError_t gemm(cudaStream_t st, int sms, const CUtensorMap& ma, const CUtensor
 
 }  // namespace
 
+cudaError_t rope_table(cudaStream_t st, float* tab, int n, int pos0, int rope_dims, float theta_scale,
+                       const float* freqs) {
+    const int cells = n * (rope_dims / 2);
+    return launch_dep(rope_table_kernel, dim3((cells + 255) / 256), dim3(256), 0, st, tab, n, pos0, rope_dims / 2,
+                      theta_scale, freqs);
+}
+
 bool prefill_supported(const PrefillCtx& c) {
     return (c.wtype == LLM_F16 || c.wtype == LLM_Q8_0) && c.dim % kGBK == 0 && c.q_dim % kGBK == 0 && c.ffn % kGBK == 0 &&
            c.n_heads / c.n_kv * c.hd <= 8 * 128 && c.rope_dims / 2 <= 128;
@@ -1252,12 +1194,7 @@ cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_hos
         PF_CK(cudaMemcpyAsync(tok, tokens_host + b0, (size_t)nb * 4, cudaMemcpyHostToDevice, c.st), "token upload");
         PF_CK(launch_dep(embed_rows_kernel, dim3(nb), dim3(256), 0, c.st, tok, nb, c.embd, c.wtype, c.dim, X),
               "embedding");
-        {
-            const int cells = nb * (c.rope_dims / 2);
-            PF_CK(launch_dep(rope_table_kernel, dim3((cells + 255) / 256), dim3(256), 0, c.st, rtab, nb, p0,
-                             c.rope_dims / 2, c.theta_scale, c.rope_freqs),
-                  "RoPE table");
-        }
+        PF_CK(rope_table(c.st, rtab, nb, p0, c.rope_dims, c.theta_scale, c.rope_freqs), "RoPE table");
         // RMSNorm: one warp per row, two rows per block, so a batch's rows
         // spread over every SM (the row stream is bound by each SM's intake)
         constexpr int kNormRows = 2;
