@@ -1,47 +1,16 @@
 // Operators of batched decoding: the paged K/V append with RoPE on the way,
-// attention of a batch that shares a prefix, and log probabilities (declared
-// in include/llm.h, which defines what each computes).
+// and log probabilities (declared in include/llm.h, which defines what each
+// computes).
 #include <limits.h>
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
 #include <algorithm>
 
-#include "llm_internal.cuh"
+#include "batch_ops.cuh"
 
 namespace llm {
 
 namespace {
-
-// What the kernels need of an llm_pages.
-struct PagesDev {
-    int n_seqs, n_new, prefix_len, page_shift, n_pages, max_pages, n_kv, hd;
-    __half *k, *v;
-    const int* table;
-    const int* lens;
-    int* err;
-};
-
-__device__ __forceinline__ void flag(int* err, int bit) {
-    if (err) atomicOr(err, bit);
-}
-
-// First row (of the pool's n_pages * page_size rows) and validity of the page
-// that holds row e >= 0 of sequence s; a bad place is flagged and gives -1.
-__device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
-    const int i = e >> p.page_shift;
-    if (i >= p.max_pages) {
-        flag(p.err, LLM_PAGES_BAD_LEN);
-        return -1;
-    }
-    const int page = p.table[(long long)s * p.max_pages + i];
-    if (page < 0 || page >= p.n_pages) {
-        flag(p.err, LLM_PAGES_BAD_PAGE);
-        return -1;
-    }
-    return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
-}
 
 // ------------------------------------------------------------- append --
 struct AppendDev {
@@ -111,80 +80,6 @@ __global__ void append_kernel(const __grid_constant__ PagesDev p, const __grid_c
     }
 }
 
-// ---------------------------------------------------------- attention --
-struct AttendDev {
-    int n_heads;
-    float scale;
-    const void* q;
-    long long q_stride;
-    void* out;
-    long long out_stride;
-    const __half *pk, *pv;
-    long long p_stride;
-};
-
-constexpr int kAttendWarps = 4;
-
-// One block per (row, head): the warps take the keys in turn, each with its own
-// running maximum and sum, and join at the end.
-template <class T, class U>
-__global__ void __launch_bounds__(32 * kAttendWarps) attend_kernel(const __grid_constant__ PagesDev p,
-                                                                   const __grid_constant__ AttendDev a) {
-    griddep_entry();
-    const int row = blockIdx.x, h = blockIdx.y, s = row / p.n_new;
-    const int e = p.lens[s] - p.n_new + row % p.n_new;
-    if (e < 0) return;
-    const int g = h / (a.n_heads / p.n_kv), warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const T* q = static_cast<const T*>(a.q) + (long long)row * a.q_stride + (long long)h * p.hd;
-    float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) qv[i] = lane + 32 * i < p.hd ? to_f32(q[lane + 32 * i]) * a.scale : 0.f;
-    for (long long t = warp; t < (long long)p.prefix_len + e + 1; t += kAttendWarps) {
-        const __half *k, *v;
-        if (t < p.prefix_len) {
-            k = a.pk + t * a.p_stride + g * p.hd;
-            v = a.pv + t * a.p_stride + g * p.hd;
-        } else {
-            const long long slot = page_row(p, s, (int)(t - p.prefix_len));
-            if (slot < 0) continue;
-            k = p.k + (slot * p.n_kv + g) * p.hd;
-            v = p.v + (slot * p.n_kv + g) * p.hd;
-        }
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (lane + 32 * i < p.hd) x = fmaf(qv[i], __half2float(k[lane + 32 * i]), x);
-        x = warp_sum(x);
-        const float mn = fmaxf(m, x), c = m == mn ? 1.f : expf(m - mn), w = expf(x - mn);
-        m = mn;
-        l = l * c + w;
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            if (lane + 32 * i < p.hd) o[i] = fmaf(w, __half2float(v[lane + 32 * i]), o[i] * c);
-    }
-    __shared__ float part[kAttendWarps][128], ml[kAttendWarps][2];
-    if (lane == 0) {
-        ml[warp][0] = m;
-        ml[warp][1] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++) part[warp][lane + 32 * i] = o[i];
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kAttendWarps; w++) M = fmaxf(M, ml[w][0]);
-    const int d = threadIdx.x;
-    float acc = 0.f;
-    for (int w = 0; w < kAttendWarps; w++) {
-        const float c = ml[w][0] == -INFINITY ? 0.f : expf(ml[w][0] - M);
-        L += ml[w][1] * c;
-        acc += part[w][d] * c;
-    }
-    if (d < p.hd) {
-        U* out = static_cast<U*>(a.out) + (long long)row * a.out_stride + (long long)h * p.hd;
-        from_f32(out[d], L == 0.f ? 0.f : acc / L);
-    }
-}
-
 // --------------------------------------------------- log probabilities --
 // One block per row: the statistics, then one pass per alternative for the
 // largest key below the one found before.
@@ -251,67 +146,6 @@ __global__ void __launch_bounds__(512) logprobs_kernel(const __grid_constant__ l
     }
 }
 
-// ------------------------------------------------------------- checks --
-bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-int type_bytes(int t) { return t == LLM_F32 ? 4 : t == LLM_F16 ? 2 : 0; }
-
-// The sizes of a batch's pages; the pointers too when they are going to be used.
-int check_pages(const llm_pages* p, bool pointers) {
-    if (!p) return fail_op(LLM_ERR_INVALID_ARG, "pages is NULL");
-    if (p->n_seqs < 0 || p->n_new < 1 || p->prefix_len < 0 || p->n_pages < 0 || p->max_pages < 0 || p->n_kv_heads < 1 ||
-        p->head_dim < 1)
-        return fail_op(LLM_ERR_INVALID_ARG, "a size of the batch is out of range");
-    if (p->page_size < 1 || (p->page_size & (p->page_size - 1)))
-        return fail_op(LLM_ERR_INVALID_ARG, "page_size %d is not a power of two", p->page_size);
-    if (p->head_dim % 8 || p->head_dim > 128)
-        return fail_op(LLM_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 8 up to 128", p->head_dim);
-    if ((long long)p->n_seqs * p->n_new > INT_MAX || (long long)p->max_pages * p->page_size > INT_MAX ||
-        (long long)p->n_kv_heads * p->head_dim > INT_MAX)
-        return fail_op(LLM_ERR_UNSUPPORTED, "rows, a sequence's capacity or a cache row exceed 2^31 - 1");
-    if (!pointers || p->n_seqs == 0) return LLM_OK;
-    if (!p->lens || (p->max_pages > 0 && (!p->page_table || !p->k_pages || !p->v_pages)))
-        return fail_op(LLM_ERR_INVALID_ARG, "a pointer of the pages is NULL");
-    if (!aligned(p->k_pages, 16) || !aligned(p->v_pages, 16) || !aligned(p->page_table, 4) || !aligned(p->lens, 4) ||
-        !aligned(p->err, 4))
-        return fail_op(LLM_ERR_INVALID_ARG, "a pointer of the pages is not aligned");
-    return LLM_OK;
-}
-
-// One strided operand: type, alignment, stride of at least `width` elements.
-int check_rows(const char* name, const void* p, int dtype, int64_t stride, long long width, long long rows) {
-    const int b = type_bytes(dtype);
-    if (!b) return fail_op(LLM_ERR_UNSUPPORTED, "%s: type %d is neither LLM_F32 nor LLM_F16", name, dtype);
-    if (!p) return fail_op(LLM_ERR_INVALID_ARG, "%s is NULL", name);
-    if (!aligned(p, 16) || stride % (16 / b)) return fail_op(LLM_ERR_INVALID_ARG, "%s: pointer or stride not 16-byte aligned", name);
-    if (rows > 1 && stride < width) return fail_op(LLM_ERR_INVALID_ARG, "%s: stride %lld below a row's %lld", name, (long long)stride, width);
-    return LLM_OK;
-}
-
-PagesDev pages_dev(const llm_pages* p) {
-    int shift = 0;
-    while ((1 << shift) < p->page_size) shift++;
-    return {p->n_seqs, p->n_new, p->prefix_len, shift, p->n_pages, p->max_pages, p->n_kv_heads, p->head_dim,
-            reinterpret_cast<__half*>(p->k_pages), reinterpret_cast<__half*>(p->v_pages), p->page_table, p->lens, p->err};
-}
-
-int launched(cudaError_t e, const char* what) {
-    if (e == cudaSuccess) return LLM_OK;
-    cudaGetLastError();
-    return fail_op(LLM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-int check_attend(const llm_pages* p, const llm_attend* a) {
-    if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the attention arguments are NULL");
-    if (a->n_heads < 1 || a->n_heads % p->n_kv_heads)
-        return fail_op(LLM_ERR_INVALID_ARG, "n_heads %d is not a multiple of n_kv_heads %d", a->n_heads, p->n_kv_heads);
-    if ((long long)p->n_seqs * p->n_new * (a->n_heads / p->n_kv_heads) > INT_MAX / 2)
-        return fail_op(LLM_ERR_UNSUPPORTED, "too many rows");
-    if (!type_bytes(a->q_dtype) || !type_bytes(a->out_dtype))
-        return fail_op(LLM_ERR_UNSUPPORTED, "q or out is neither LLM_F32 nor LLM_F16");
-    if (!(a->scale >= 0.f) || !(a->scale < INFINITY)) return fail_op(LLM_ERR_INVALID_ARG, "scale is not a finite number >= 0");
-    return LLM_OK;
-}
-
 }  // namespace
 
 }  // namespace llm
@@ -358,37 +192,6 @@ extern "C" int llm_kv_append(const llm_pages* pages, const llm_append* a, llm_st
                       : (qh ? launch_dep(append_kernel<float, __half>, grid, block, 0, stream, pd, ad)
                             : launch_dep(append_kernel<float, float>, grid, block, 0, stream, pd, ad)),
                     "llm_kv_append");
-}
-
-extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_attend* a) {
-    int rc = check_pages(pages, false);
-    if (rc || (rc = check_attend(pages, a))) return rc;
-    return 0;
-}
-
-extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
-    int rc = check_pages(pages, true);
-    if (rc || (rc = check_attend(pages, a))) return rc;
-    if (pages->n_seqs == 0) return LLM_OK;
-    const long long rows = (long long)pages->n_seqs * pages->n_new, width = (long long)a->n_heads * pages->head_dim;
-    if ((rc = check_rows("q", a->q, a->q_dtype, a->q_stride, width, rows)) ||
-        (rc = check_rows("out", a->out, a->out_dtype, a->out_stride, width, rows)))
-        return rc;
-    if (pages->prefix_len > 0 &&
-        ((rc = check_rows("prefix_k", a->prefix_k, LLM_F16, a->prefix_stride, (long long)pages->n_kv_heads * pages->head_dim, 2)) ||
-         (rc = check_rows("prefix_v", a->prefix_v, LLM_F16, a->prefix_stride, (long long)pages->n_kv_heads * pages->head_dim, 2))))
-        return rc;
-    const PagesDev pd = pages_dev(pages);
-    const float scale = a->scale == 0.f ? (float)(1.0 / sqrt((double)pages->head_dim)) : a->scale;
-    const AttendDev ad{a->n_heads, scale, a->q, a->q_stride, a->out, a->out_stride, reinterpret_cast<const __half*>(a->prefix_k),
-                       reinterpret_cast<const __half*>(a->prefix_v), a->prefix_stride};
-    const dim3 grid((unsigned)rows, a->n_heads), block(32 * kAttendWarps);
-    const bool h = a->q_dtype == LLM_F16, oh = a->out_dtype == LLM_F16;
-    return launched(h ? (oh ? launch_dep(attend_kernel<__half, __half>, grid, block, 0, stream, pd, ad)
-                            : launch_dep(attend_kernel<__half, float>, grid, block, 0, stream, pd, ad))
-                      : (oh ? launch_dep(attend_kernel<float, __half>, grid, block, 0, stream, pd, ad)
-                            : launch_dep(attend_kernel<float, float>, grid, block, 0, stream, pd, ad)),
-                    "llm_attend_batch");
 }
 
 extern "C" int llm_logprobs(const llm_logprobs_args* a, llm_stream_t stream) {

@@ -92,6 +92,15 @@ def test_attend_refused(kw, status):
     refused(B._lib.llm_attend_batch(ref(pages()), ref(attend(**kw)), None), status)
 
 
+@pytest.mark.parametrize("kw", [dict(workspace=None), dict(workspace=P + 128), dict(workspace_bytes=0),
+                                dict(workspace_bytes=-1)])
+def test_attend_refuses_a_bad_workspace(kw):
+    refused(B._lib.llm_attend_batch(ref(pages(prefix_len=100)), ref(attend(**kw)), None), BAD)
+    need = B._lib.llm_attend_batch_workspace(ref(pages(prefix_len=100)), ref(attend()))
+    assert need > 0
+    refused(B._lib.llm_attend_batch(ref(pages(prefix_len=100)), ref(attend(workspace_bytes=need - 1)), None), BAD)
+
+
 @pytest.mark.parametrize("kw", [dict(prefix_k=None), dict(prefix_v=None), dict(prefix_k=P + 8), dict(prefix_v=P + 2),
                                 dict(prefix_stride=64), dict(prefix_stride=132)])
 def test_attend_refuses_bad_prefix(kw):

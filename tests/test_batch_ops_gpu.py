@@ -402,6 +402,32 @@ def test_attend_bad_pages(lib):
     check_attend(c, q[:1], out, None, None)
 
 
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("what", [math.inf, math.nan])
+def test_attend_wild_values_of_later_tokens(lib, types, what):
+    """K or V of a new token that is not finite reaches that token and the ones
+    behind it, none before it."""
+    b = Batch(lib, [37, 4], 4, 40, 16, 2, 64)
+    q, pk, pv = rand(1, 8, 4, 64, dtype=types[0]), rand(2, 40, 2, 64, dtype=F16), rand(3, 40, 2, 64, dtype=F16)
+    p, r = b.slot(0, 35)
+    b.v[p, r, 0, 5] = what
+    p, r = b.slot(1, 1)
+    b.k[p, r, 1, 9] = math.nan
+    b.v[p, r, 1, :] = what
+    out = torch.empty(8, 4, 64, dtype=types[1], device="cuda")
+    lib.AttendBatch(b.pages, q, out, pk, pv)()
+    assert out[:2].isfinite().all() and out[4].isfinite().all()
+    assert not out[2:4, :2, 5].isfinite().any() and out[2:4, 2:].isfinite().all()
+    assert not out[5:, 2:].isfinite().any() and out[5:, :2].isfinite().all()
+    wild = out.clone()
+    for s, e in ((0, 35), (1, 1)):
+        p, r = b.slot(s, e)
+        b.k[p, r] = b.v[p, r] = 0.5
+    lib.AttendBatch(b.pages, q, out, pk, pv)()
+    check_attend(b, q, out, pk, pv)
+    assert torch.equal(out[:2], wild[:2]) and torch.equal(out[4], wild[4])
+
+
 def test_attend_same_bits_every_run(lib):
     b, q, pk, pv, out = run_attend(lib, (8, 2, 64), [200, 1, 77, 500, 350], 2, 3000, 16, F32, F32)
     first = out.clone()
