@@ -718,15 +718,6 @@ struct Plan {
     size_t off_pml, off_so, off_sml, bytes;
 };
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    return n;
-}
-
 Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
     Plan pl{};
     const int gq = a->n_heads / p->n_kv_heads;

@@ -37,6 +37,9 @@ __device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
     return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
 }
 
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+
 // ------------------------------------------------------------- checks --
 inline bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline int type_bytes(int t) { return t == LLM_F32 ? 4 : t == LLM_F16 ? 2 : 0; }
@@ -84,6 +87,16 @@ inline int launched(cudaError_t e, const char* what) {
     if (e == cudaSuccess) return LLM_OK;
     cudaGetLastError();
     return fail_op(LLM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// SMs of the current device (152 where there is none to ask).
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    return n;
 }
 
 }  // namespace llm
