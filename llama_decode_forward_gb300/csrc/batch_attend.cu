@@ -91,16 +91,21 @@ __device__ __forceinline__ long long q_offset(const AttendDev& a, int hd, int g,
 // ------------------------------------------------------------- prefix --
 constexpr int kKT = 64;                      // keys per tile
 
+// Blocks of an SM: two of head sizes up to 64 overlap one's softmax with the
+// other's waits; the tiles of larger heads fill an SM's shared memory at one.
+constexpr int prefix_ctas(int hd) { return hd <= 64 ? 2 : 1; }
+
 template <int HDP, bool SPLITQ>
 struct PrefixPlan {
     static constexpr int kSlabs = HDP / 64;                        // 64-column (128-byte) slabs of a row
-    static constexpr int kQBytes = 128 * HDP * 2;                  // the query tile (twice with SPLITQ)
+    static constexpr bool kQInTmem = HDP == 64;
+    static constexpr int kQBytes = kQInTmem ? 0 : 128 * HDP * 2;   // the query tile (twice with SPLITQ)
     static constexpr int kTileBytes = kKT * HDP * 2;               // K or V
-    static constexpr int kCtas = HDP == 128 && SPLITQ ? 1 : 2;     // per SM
-    static constexpr int kStages = HDP == 64 ? 4 : SPLITQ ? 4 : 2;
+    static constexpr int kCtas = prefix_ctas(HDP);                 // per SM
+    static constexpr int kStages = HDP == 64 ? 6 : SPLITQ ? 4 : 5;
     static constexpr int kBarBytes = 256;
     static constexpr int kSmem = kQBytes * (SPLITQ ? 2 : 1) + kStages * 2 * kTileBytes + kBarBytes + 1024;
-    static constexpr int kTmemCols = 256;                          // S0 | S1 (64 each) | O (HDP)
+    static constexpr int kTmemCols = 256;                          // S0 | S1 (64 each) | O (HDP) | Q (32 a part)
 };
 
 constexpr int kPrefixThreads = 192;
@@ -115,6 +120,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t par, int* err) 
 // The same for a whole warp that goes on to warp-wide instructions.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, int* err) {
     return __all_sync(0xffffffffu, bar_wait(bar, par, err));
+}
+
+// One lane of the warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
 }
 
 // Descriptor of a 128-byte-swizzled tile: K-major rows of 64 F16 values, 8-row
@@ -161,6 +173,13 @@ __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* v) {
         "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -171,9 +190,15 @@ __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::
 //              row's 64 scores, writes its probabilities back over them as
 //              F16 (with SPLITP the rounded-off rest beside them), and rescales
 //              O when the row's maximum has moved by more than kLag;
-//   warp 4     TMA: 64-key tiles of K and V into a ring;
-//   warp 5     MMA: S = Q K^T (Q from shared memory) into one of two score
-//              buffers, one tile ahead of O += P V (P from tensor memory).
+//   warp 4     MMA: S = Q K^T into one of two score buffers, one tile ahead;
+//   warp 5     TMA: 64-key tiles of K and V into a ring; MMA: O += P V, P from
+//              tensor memory.
+// Two MMA warps, because each wait and each issue takes one of them 150 to 200
+// cycles; a seventh warp for the copies would leave two blocks of an SM 128
+// registers a thread, and the scores would spill.
+// Q is read from tensor memory too where it fits (head sizes up to 64): an MMA
+// whose 128-row operand comes from shared memory takes 48 cycles at this width,
+// for 32 of work.
 // SPLITQ: Q as two F16 parts; SPLITP: P as two F16 parts.
 template <int HDP, bool SPLITQ, bool SPLITP>
 __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas)
@@ -189,10 +214,11 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
     uint64_t* empty = full + NS;
     uint64_t* sfull = empty + NS;            // [2] scores of a tile are in buffer b
     uint64_t* pfull = sfull + 2;             // [2] probabilities of a tile are in buffer b
-    uint64_t* pvdone = pfull + 2;            // one phase per tile: its P V has been added
-    uint64_t* qfull = pvdone + 1;
-    uint64_t* fin = qfull + 1;               // every MMA issued has completed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
+    uint64_t* pvdone = pfull + 2;            // [2] the P V of a tile in buffer b has been added
+    uint64_t* qfull = pvdone + 2;
+    uint64_t* fin = qfull + 1;               // every P V has been added
+    uint64_t* qfin = fin + 1;                // every MMA of the scores has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qfin + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int mtiles = (a.rows + 127) / 128;
     const int m0 = (int)(blockIdx.x % mtiles) * 128, sp = (int)(blockIdx.x / mtiles), g = blockIdx.y;
@@ -206,13 +232,14 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
         for (int b = 0; b < 2; b++) {
             mbar_init(&sfull[b], 1);
             mbar_init(&pfull[b], 4);
+            mbar_init(&pvdone[b], 1);
         }
-        mbar_init(pvdone, 1);
         mbar_init(qfull, 4);
         mbar_init(fin, 1);
+        mbar_init(qfin, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 5) {
+    if (warp == 4) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(G::kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -227,70 +254,110 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
     griddep_launch();
 
     if (warp == 4) {
-        if (lane == 0) {
-            int it = 0;
-            for (; it < n; it++) {
-                const int s = it % NS;
-                if (!bar_wait(&empty[s], (uint32_t)(((it / NS) & 1) ^ 1), p.err)) break;
-                uint8_t* st = ring + s * 2 * G::kTileBytes;
-                mbar_arrive_expect_tx(&full[s], 2 * G::kTileBytes);
-#pragma unroll
-                for (int c = 0; c < G::kSlabs; c++) {
-                    tma_3d_g2s(st + c * kKT * 128, &mk, c * 64, g, (t0 + it) * kKT, &full[s]);
-                    tma_3d_g2s(st + G::kTileBytes + c * kKT * 128, &mv, c * 64, g, (t0 + it) * kKT, &full[s]);
-                }
-            }
-            // the last copies have landed before the CTA can exit
-            for (int k = it - 1; k >= 0 && k >= it - NS; k--) bar_wait(&full[k % NS], (uint32_t)((k / NS) & 1), p.err);
-        }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            // F16 operands, F32 accumulators, M 128; scores: N 64, both K-major;
-            // output: N HDP, V with the keys (K) as rows, so MN-major
-            constexpr uint32_t is = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
-            constexpr uint32_t io = (1u << 4) | (1u << 16) | ((uint32_t)(HDP >> 3) << 17) | (8u << 24);
-            const uint32_t qa = smem_addr(qs);
-            auto scores = [&](int it) {
-                const uint32_t kb = smem_addr(ring + (it % NS) * 2 * G::kTileBytes);
+        // The whole warp walks the loop and one elected lane issues: the tile
+        // counters and descriptors stay in uniform registers (a loop of one
+        // lane alone took 90 to 140 cycles per MMA to issue, and set the pace).
+        // F16 operands, F32 accumulators, M 128, N 64, both K-major.
+        constexpr uint32_t is = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
+        const uint64_t dq = desc_sw128(smem_addr(qs), 16), dk = desc_sw128(smem_addr(ring), 16);
+        bool ok = warp_wait(qfull, 0, p.err);
+        for (int it = 0; it < n && ok; it++) {
+            if (!(ok = warp_wait(&full[it % NS], (uint32_t)((it / NS) & 1), p.err))) break;
+            // these scores go where tile it - 2's probabilities were
+            if (it > 1 && !(ok = warp_wait(&pvdone[it & 1], (uint32_t)(((it >> 1) - 1) & 1), p.err))) break;
+            tm_fence_after();
+            const uint64_t k = dk + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
+            const uint32_t d = tmem + (uint32_t)((it & 1) * 64);
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (SPLITQ ? 2 : 1); part++)
 #pragma unroll
-                    for (int kk = 0; kk < HDP / 16; kk++)
-                        mma_ss(tmem + (uint32_t)((it & 1) * 64),
-                               desc_sw128(qa + part * G::kQBytes + (kk / 4) * 128 * 128 + (kk % 4) * 32, 16),
-                               desc_sw128(kb + (kk / 4) * kKT * 128 + (kk % 4) * 32, 16), is, part + kk > 0);
+                    for (int kk = 0; kk < HDP / 16; kk++) {
+                        const uint64_t kd = k + (((kk / 4) * kKT * 128 + (kk % 4) * 32) >> 4);
+                        if (G::kQInTmem)
+                            mma_ts(d, tmem + 192 + part * 32 + kk * 8, kd, is, part + kk > 0);
+                        else
+                            mma_ss(d, dq + ((part * G::kQBytes + (kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4), kd, is, part + kk > 0);
+                    }
                 mma_commit(&sfull[it & 1]);
-            };
-            bool ok = bar_wait(qfull, 0, p.err) && bar_wait(&full[0], 0, p.err);
+            }
+            __syncwarp();
+        }
+        // every MMA issued has completed before the tensor memory is freed
+        if (elect_one()) mma_commit(qfin);
+        __syncwarp();
+        warp_wait(qfin, 0, p.err);
+    } else if (warp == 5) {
+        // N HDP; V has the keys (the MMA's K) as rows, so it is MN-major
+        constexpr uint32_t io = (1u << 4) | (1u << 16) | ((uint32_t)(HDP >> 3) << 17) | (8u << 24);
+        const uint64_t dv = desc_sw128(smem_addr(ring) + G::kTileBytes, kKT * 128);
+        auto load = [&](int it) {            // tile it into its stage
+            uint8_t* st = ring + (it % NS) * 2 * G::kTileBytes;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[it % NS], 2 * G::kTileBytes);
+#pragma unroll
+                for (int c = 0; c < G::kSlabs; c++) tma_3d_g2s(st + c * kKT * 128, &mk, c * 64, g, (t0 + it) * kKT, &full[it % NS]);
+#pragma unroll
+                for (int c = 0; c < G::kSlabs; c++)
+                    tma_3d_g2s(st + G::kTileBytes + c * kKT * 128, &mv, c * 64, g, (t0 + it) * kKT, &full[it % NS]);
+            }
+            __syncwarp();
+        };
+        int loaded = 0;
+        for (; loaded < min(n, NS); loaded++) load(loaded);
+        for (int it = 0; it < n; it++) {
+            // tile it - 1's stage is free when its P V is done, while the softmax of tile it runs
+            if (it > 0 && loaded < n) {
+                if (!warp_wait(&empty[(it - 1) % NS], (uint32_t)(((it - 1) / NS) & 1), p.err)) break;
+                load(loaded++);
+            }
+            if (!warp_wait(&pfull[it & 1], (uint32_t)((it >> 1) & 1), p.err)) break;
             tm_fence_after();
-            if (ok) scores(0);
-            for (int it = 0; it < n && ok; it++) {
-                if (it + 1 < n) {
-                    // the next tile's scores go where tile it - 1's probabilities were
-                    if (it > 0 && !(ok = bar_wait(pvdone, (uint32_t)((it - 1) & 1), p.err))) break;
-                    if (!(ok = bar_wait(&full[(it + 1) % NS], (uint32_t)(((it + 1) / NS) & 1), p.err))) break;
-                    tm_fence_after();
-                    scores(it + 1);
-                }
-                if (!(ok = bar_wait(&pfull[it & 1], (uint32_t)((it >> 1) & 1), p.err))) break;
-                tm_fence_after();
-                const uint32_t vb = smem_addr(ring + (it % NS) * 2 * G::kTileBytes + G::kTileBytes);
-                const uint32_t pa = tmem + (uint32_t)((it & 1) * 64);
+            const uint64_t v = dv + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
+            const uint32_t pa = tmem + (uint32_t)((it & 1) * 64);
+            if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (SPLITP ? 2 : 1); part++)
 #pragma unroll
                     for (int kk = 0; kk < kKT / 16; kk++)
-                        mma_ts(to, pa + part * 32 + kk * 8, desc_sw128(vb + kk * 16 * 128, kKT * 128), io,
-                               it > 0 || part + kk > 0);
+                        mma_ts(to, pa + part * 32 + kk * 8, v + (kk * 16 * 128 >> 4), io, it > 0 || part + kk > 0);
+                mma_commit(&pvdone[it & 1]);
                 mma_commit(&empty[it % NS]);
-                mma_commit(pvdone);
             }
-            mma_commit(fin);                 // every MMA issued has completed before the memory is freed
-            bar_wait(fin, 0, p.err);
+            __syncwarp();
         }
+        if (elect_one()) mma_commit(fin);
+        __syncwarp();
+        warp_wait(fin, 0, p.err);
+        // every copy has landed before the block can end (at once, unless a wait gave up)
+        for (int k = loaded - 1; k >= 0 && k >= loaded - NS; k--) warp_wait(&full[k % NS], (uint32_t)((k / NS) & 1), p.err);
     } else {
-        // ---- Q into shared memory, swizzled as the descriptors say
-        for (int i = threadIdx.x; i < 128 * (HDP / 8); i += 128) {
+        // ---- Q into tensor memory, this thread's row, or into shared memory,
+        // swizzled as the descriptors say
+        if constexpr (G::kQInTmem) {
+            const int r = m0 + warp * 32 + lane;
+            const long long at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
+            const uint32_t tq = tmem + ((uint32_t)(warp * 32) << 16) + 192;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                uint32_t hi[16], lo[SPLITQ ? 16 : 1];
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (r < a.rows && h * 32 + c * 8 < p.hd) load_q8(a, at + h * 32 + c * 8, x);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        hi[4 * c + k] = pack_hi(x[2 * k], x[2 * k + 1]);
+                        if (SPLITQ) lo[SPLITQ ? 4 * c + k : 0] = pack_lo(x[2 * k], x[2 * k + 1], hi[4 * c + k]);
+                    }
+                }
+                tm_st16(tq + h * 16, hi);
+                if (SPLITQ) tm_st16(tq + 32 + h * 16, lo);
+            }
+            tm_wait_st();
+            tm_fence_before();
+        }
+        for (int i = threadIdx.x; !G::kQInTmem && i < 128 * (HDP / 8); i += 128) {
             const int r = i / (HDP / 8), c = i % (HDP / 8);
             float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             if (m0 + r < a.rows && c * 8 < p.hd) load_q8(a, q_offset(a, p.hd, g, m0 + r) + c * 8, x);
@@ -322,9 +389,10 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
                 for (int c = 0; c < 64; c++)
                     if (c >= valid) s[c] = 0xFF800000u;           // -infinity
             }
-            float mx = -INFINITY;
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // four chains side by side
 #pragma unroll
-            for (int c = 0; c < 64; c++) mx = fmaxf(mx, __uint_as_float(s[c]));
+            for (int c = 0; c < 64; c++) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             const float top = fmaxf(mx * a.sc, -1e30f) - kHead;
             if (it == 0) {
                 M = top;
@@ -335,7 +403,7 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
                     M = top;
                 }
                 l *= c;
-                if (!(ok = warp_wait(pvdone, (uint32_t)((it - 1) & 1), p.err))) break;
+                if (!(ok = warp_wait(&pvdone[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1), p.err))) break;
                 tm_fence_after();
 #pragma unroll
                 for (int h = 0; h < HDP; h += 32) {
@@ -348,25 +416,27 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
                 }
             }
             float l0 = 0.f, l1 = 0.f;
-            uint32_t hi[32], lo[SPLITP ? 32 : 1];
 #pragma unroll
-            for (int c = 0; c < 32; c++) {
-                const float x = exp2_fast(fmaf(__uint_as_float(s[2 * c]), a.sc, -M));
-                const float y = exp2_fast(fmaf(__uint_as_float(s[2 * c + 1]), a.sc, -M));
-                l0 += x;
-                l1 += y;
-                hi[c] = pack_hi(x, y);
-                if (SPLITP) lo[SPLITP ? c : 0] = pack_lo(x, y, hi[c]);
+            for (int h = 0; h < 32; h += 16) {
+                uint32_t hi[16], lo[SPLITP ? 16 : 1];
+#pragma unroll
+                for (int c = 0; c < 16; c++) {
+                    const float x = exp2_fast(fmaf(__uint_as_float(s[2 * (h + c)]), a.sc, -M));
+                    const float y = exp2_fast(fmaf(__uint_as_float(s[2 * (h + c) + 1]), a.sc, -M));
+                    l0 += x;
+                    l1 += y;
+                    hi[c] = pack_hi(x, y);
+                    if (SPLITP) lo[SPLITP ? c : 0] = pack_lo(x, y, hi[c]);
+                }
+                tm_st16(sb + h, hi);
+                if (SPLITP) tm_st16(sb + 32 + h, lo);
             }
             l += l0 + l1;
-            tm_st32(sb, hi);
-            if (SPLITP) tm_st32(sb + 32, lo);
             tm_wait_st();
             tm_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&pfull[it & 1]);
         }
-        // (not pvdone's phase n - 1: phase n - 2 of the other parity may not be over yet)
         if (ok) ok = warp_wait(fin, 0, p.err);
         tm_fence_after();
         if (ok) {
@@ -388,7 +458,7 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
     }
     tm_fence_before();
     __syncthreads();
-    if (warp == 5)
+    if (warp == 4)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols));
 }
 
@@ -723,7 +793,7 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
     const int gq = a->n_heads / p->n_kv_heads;
     const long long srows = (long long)p->n_new * gq, rows = srows * p->n_seqs;
     pl.mtiles = (int)((rows + 127) / 128);
-    const int slots = 2 * sms;
+    const int slots = prefix_ctas(p->head_dim) * sms;
     if (p->prefix_len > 0) {
         const long long ntiles = (p->prefix_len + kKT - 1) / kKT, base = (long long)pl.mtiles * p->n_kv_heads;
         const long long want = std::max<long long>(1, slots / base);
