@@ -422,7 +422,7 @@ typedef struct {
  * nearest even) and q into q_out.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int llm_kv_append(const llm_pages *pages, const llm_append *a, llm_stream_t stream);
 
-/* Attention of the new rows.  q [rows][n_heads][head_dim] (dtype q_dtype, row
+/* Attention of the new rows, of at most 4096 sequences.  q [rows][n_heads][head_dim] (dtype q_dtype, row
  * stride q_stride), out likewise; LLM_F32 or LLM_F16 each; 16-byte aligned,
  * strides multiples of 16 bytes.  n_heads is a multiple of n_kv_heads; head h
  * reads kv head h / (n_heads / n_kv_heads).  prefix_k, prefix_v: rows

@@ -36,9 +36,10 @@ struct AttendDev {
     int out_f16;
     float* prefix_o;                // [prefix splits][n_kv][rows][hd]
     float2* prefix_ml;              // [prefix splits][n_kv][rows]: M, l
-    float* suffix_o;                // [n_seqs][n_kv][suffix splits][n_new * gq][hd]
+    float* suffix_o;                // [units of all sequences + workers][up to 16 rows][hd]
     float2* suffix_ml;
-    int prefix_splits, suffix_splits;
+    int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
+    int prefix_splits, suffix_workers;
 };
 
 // Probabilities are kept as 2^(y - M) with M = (a recent maximum) - kHead, so
@@ -463,317 +464,425 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
 }
 
 // ------------------------------------------------------------- suffix --
-constexpr int kSuffixWarps = 4, kSuffixBufs = 3;
+// A unit of work is up to 8 NT query rows (row tile j % rt of kv head j / rt, j
+// < units of a sequence) of one sequence against its pages, cut into pieces of
+// 16 cached rows.  The pieces of all units, in order, are dealt out evenly:
+// worker w (one warp) takes pieces [w T / W, (w + 1) T / W) of the T, whatever
+// units they belong to, so ragged lengths leave no warp waiting.  A worker
+// leaves one part per unit that it touches, in slot unit + worker (each step of
+// the walk raises one or both, so no two parts share a slot).
+constexpr int kSuffixWarps = 4, kMaxSeqs = 4096;
+constexpr int kQuantum = 2;                  // pieces that are worth a worker of their own
 
-// Rows of a sequence's pages that its new tokens see, and how its splits share
-// them: `per` 64-row tiles each.
-struct SuffixCut {
-    int len, per, parts;
+// Query rows of a unit.
+__host__ __device__ constexpr int unit_rows(int srows) { return srows <= 8 ? 8 : 16; }
+
+// Blocks that an SM holds at once, by their registers: the pieces are dealt to
+// as many, so that all run together.
+__host__ __device__ constexpr int suffix_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? 4 : 3) : 2; }
+
+// Row counts of the sequences (clipped to their pages) and the sums of their
+// pieces before each: the suffix kernel's blocks compute them, block 0 leaves
+// them for the join.
+struct Deal {
+    long long total;                         // pieces of all units
+    int workers;
+    int units;                               // of a sequence
 };
-__device__ __forceinline__ SuffixCut suffix_cut(const PagesDev& p, int s, int splits) {
-    SuffixCut c;
-    const long long cap = (long long)p.max_pages << p.page_shift;
-    c.len = (int)max(0ll, min((long long)p.lens[s], cap));
-    const int tiles = (c.len + 63) / 64;
-    c.per = max(1, (tiles + splits - 1) / max(1, splits));
-    c.parts = (tiles + c.per - 1) / c.per;
-    return c;
+__device__ __forceinline__ Deal deal_of(int pieces, int units, int max_workers) {
+    Deal d;
+    d.units = units;
+    d.total = (long long)pieces * units;
+    d.workers = (int)min((long long)max_workers, (d.total + kQuantum - 1) / kQuantum);
+    return d;
+}
+__device__ __forceinline__ int clipped_len(const PagesDev& p, int s) {
+    return (int)max(0ll, min((long long)p.lens[s], (long long)p.max_pages << p.page_shift));
 }
 
-// 16 query rows of one kv head of one sequence against one split of its pages.
-// Each warp takes every fourth 16-row piece of the split with a running
-// softmax of its own; its rows arrive by cp.async, three pieces in flight, in
-// rows padded to HDP + 8 halves (ldmatrix without bank conflicts), so the warps
-// only meet at the end.  Scores and sums are mma.sync m16n8k16 products.
-template <int HDP, bool SPLITQ, bool SPLITP>
-__global__ void __launch_bounds__(32 * kSuffixWarps) suffix_kernel(const __grid_constant__ PagesDev p,
-                                                                   const __grid_constant__ AttendDev a, int first) {
-    constexpr int PITCH = HDP + 8;
-    extern __shared__ __align__(16) uint8_t smraw[];
+// D += A B for one m16n8k16 tile with the 16 rows of A from ldmatrix.
+__device__ __forceinline__ void mma_kn8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of F16 pairs, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// Each warp walks its pieces alone: the rows of the next piece are on their way
+// to registers (and the pages of the one behind it are being looked up) while
+// one is multiplied, across units.  The products are mma.sync m16n8k16 with the
+// cached rows as the 16 (scores S^T = K q^T, sums O^T = V^T P^T), so 8 query rows
+// waste none of them, and the operands need no shared memory:
+// - lane (r, t) = (lane / 4, lane % 4) loads 16-byte chunks t, t + 4, ... of cached
+//   rows r and r + 8, 64 contiguous bytes of a row per instruction.  The order of
+//   the dims in a dot product is free, so MMA k-step 2 i + h takes dims 8 (t + 4 i) +
+//   4 h + {0, 1 | 2, 3} of each lane, as they lie in its registers; q is loaded in
+//   the same order;
+// - V's registers become V^T's by 8 x 8 transposes across the warp (movmatrix):
+//   register w of chunk i of row r turns into dim 8 (r / 2) + 32 i + 2 w + r % 2, r
+//   now counting dims.
+// The stream of rows is the bound.  At 64 continuations of 2048 rows each (268 MB)
+// a ring of TMA boxes (16 rows x 128 bytes a request) brought 3.6 TB/s, plain
+// loads of the same rows 6.3 TB/s.
+template <int HDP, int NT, bool SPLITQ, bool SPLITP>
+__global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
+    suffix_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
+    constexpr int CH = HDP / 32, RU = 8 * NT;                // 16-byte chunks of a row in a lane
+    extern __shared__ int seqs[];
     if (first) griddep_wait();               // otherwise the prefix kernel has waited for the work before it
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int srows = p.n_new * a.gq, rt = (srows + 15) / 16;
-    const int sp = (int)(blockIdx.x % a.suffix_splits), tile = (int)(blockIdx.x / a.suffix_splits) % rt;
-    const int s = (int)(blockIdx.x / a.suffix_splits) / rt, g = blockIdx.y;
-    const SuffixCut cut = suffix_cut(p, s, a.suffix_splits);
-    const int k0 = sp * cut.per * 64, k1 = min(cut.len, k0 + cut.per * 64);
-    if (k0 < k1) {
-        __half* mine = reinterpret_cast<__half*>(smraw) + warp * kSuffixBufs * 2 * 16 * PITCH;
-        if (p.hd < HDP) {
-            // columns behind hd: zero once, never written again
-            const int w = (HDP - p.hd) / 8;
-            for (int i = lane; i < kSuffixBufs * 32 * w; i += 32)
-                *reinterpret_cast<uint4*>(mine + (i / w) * PITCH + p.hd + (i % w) * 8) = make_uint4(0, 0, 0, 0);
+    const int srows = p.n_new * a.gq, rt = (srows + RU - 1) / RU, units = p.n_kv * rt;
+    int* starts = seqs;                      // [n_seqs + 1]
+    int* lens = starts + p.n_seqs + 1;       // [n_seqs]
+    {
+        // prefix sums of the sequences' pieces
+        __shared__ int sums[kSuffixWarps];
+        const int each = (p.n_seqs + 32 * kSuffixWarps - 1) / (32 * kSuffixWarps), s0 = threadIdx.x * each;
+        int mine = 0;
+        for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
+            lens[s] = clipped_len(p, s);
+            mine += (lens[s] + 15) / 16;
         }
-        const int r = lane >> 2, t = lane & 3;
-        // this thread's two rows of the tile; rows behind the last repeat it (never stored)
-        const int ra = min(tile * 16 + r, srows - 1), rb = min(tile * 16 + r + 8, srows - 1);
-        // the last row each of them sees (a padding row: none)
-        const int ea = p.lens[s] - p.n_new + ra / a.gq, eb = p.lens[s] - p.n_new + rb / a.gq;
-        uint32_t qhi[HDP / 16][4], qlo[SPLITQ ? HDP / 16 : 1][4];
-        {
-            const long long oa = q_offset(a, p.hd, g, s * srows + ra), ob = q_offset(a, p.hd, g, s * srows + rb);
+        int sum = mine;
 #pragma unroll
-            for (int ks = 0; ks < HDP / 16; ks++)
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int col = ks * 16 + (j >> 1) * 8 + 2 * t;
-                    const long long at = ((j & 1) ? ob : oa) + col;
-                    float2 x = make_float2(0.f, 0.f);
-                    if (col < p.hd)
-                        x = a.q_f16 ? __half22float2(*reinterpret_cast<const __half2*>(static_cast<const __half*>(a.q) + at))
-                                    : *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at);
-                    qhi[ks][j] = pack_hi(x.x, x.y);
-                    if (SPLITQ) qlo[SPLITQ ? ks : 0][j] = pack_lo(x.x, x.y, qhi[ks][j]);
-                }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
         }
-        float o[HDP / 8][4];
-#pragma unroll
-        for (int i = 0; i < HDP / 8; i++) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float Ma = -INFINITY, Mb = -INFINITY, la = 0.f, lb = 0.f;
-        const int w8 = p.hd / 8;
-        // rows of this warp's pieces: k0 + 16 (warp + 4 i); a row on a bad page is
-        // marked and its bytes are zero
-        unsigned long long bad = 0;          // 16 bits per buffer
-        auto load = [&](int piece, int buf) {
-            const int e0 = k0 + piece * 16;
-            __half* kb = mine + buf * 2 * 16 * PITCH;
-            // lanes 0..15 look their row up, then all lanes copy
-            long long row = -1;
-            if (lane < 16 && e0 + lane < k1) row = page_row(p, s, e0 + lane);
-            const unsigned long long out = __ballot_sync(0xffffffffu, row < 0) & 0xFFFFu;
-            bad = (bad & ~(0xFFFFull << (16 * buf))) | out << (16 * buf);
-            for (int i0 = 0; i0 < 16 * w8; i0 += 32) {
-                const int i = i0 + lane, rr = i / w8, c = i % w8;
-                const long long at = __shfl_sync(0xffffffffu, row, rr & 15);
-                if (rr >= 16) continue;
-                __half *kd = kb + rr * PITCH + c * 8, *vd = kd + 16 * PITCH;
-                if (at >= 0) {
-                    const long long src = (at * p.n_kv + g) * p.hd + c * 8;
-                    cp_async16(kd, p.k + src);
-                    cp_async16(vd, p.v + src);
-                } else {
-                    *reinterpret_cast<uint4*>(kd) = make_uint4(0, 0, 0, 0);
-                    *reinterpret_cast<uint4*>(vd) = make_uint4(0, 0, 0, 0);
-                }
-            }
-            cp_async_commit();
-        };
-        const int pieces = (k1 - k0 + 15) / 16;
-        int next = warp;
-#pragma unroll
-        for (int b = 0; b < kSuffixBufs - 1; b++) {
-            if (next < pieces) load(next, b);
-            else cp_async_commit();
-            next += kSuffixWarps;
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int at = sum - mine;
+        for (int w = 0; w < warp; w++) at += sums[w];
+        for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
+            starts[s] = at;
+            at += (lens[s] + 15) / 16;
+            if (blockIdx.x == 0) a.starts[s + 1] = at;
         }
-        int buf = 0;
-        for (int piece = warp; piece < pieces; piece += kSuffixWarps) {
-            // the buffer read last turn takes the piece two turns ahead
-            int nb = buf + kSuffixBufs - 1;
-            if (nb >= kSuffixBufs) nb -= kSuffixBufs;
-            __syncwarp();
-            if (next < pieces) load(next, nb);
-            else cp_async_commit();
-            next += kSuffixWarps;
-            asm volatile("cp.async.wait_group %0;" ::"n"(kSuffixBufs - 1) : "memory");
-            __syncwarp();
-            const __half* kb = mine + buf * 2 * 16 * PITCH;
-            const uint32_t kbase = smem_addr(kb), vbase = smem_addr(kb + 16 * PITCH);
-            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-            const int mi = lane >> 3, ri = lane & 7;
-            {
-                const uint32_t krow = kbase + (uint32_t)((ri + (mi >= 2 ? 8 : 0)) * PITCH * 2);
-#pragma unroll
-                for (int ks = 0; ks < HDP / 16; ks++) {
-                    uint32_t b0, b1, b2, b3;
-                    ldsm_x4(krow + (uint32_t)((ks * 16 + (mi & 1) * 8) * 2), b0, b1, b2, b3);
-                    mma16816(sc[0], qhi[ks], b0, b1);
-                    mma16816(sc[1], qhi[ks], b2, b3);
-                    if (SPLITQ) {
-                        mma16816(sc[0], qlo[SPLITQ ? ks : 0], b0, b1);
-                        mma16816(sc[1], qlo[SPLITQ ? ks : 0], b2, b3);
-                    }
-                }
-            }
-            const int e0 = k0 + piece * 16;
-            const uint32_t gone = (uint32_t)(bad >> (16 * buf)) & 0xFFFFu;
-            float ma = -INFINITY, mb = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < 2; nt++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const int rr = nt * 8 + 2 * t + k;
-                    const bool there = !((gone >> rr) & 1u);
-                    sc[nt][k] = there && e0 + rr <= ea ? sc[nt][k] * a.sc : -INFINITY;
-                    sc[nt][2 + k] = there && e0 + rr <= eb ? sc[nt][2 + k] * a.sc : -INFINITY;
-                    ma = fmaxf(ma, sc[nt][k]);
-                    mb = fmaxf(mb, sc[nt][2 + k]);
-                }
-            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
-            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 2));
-            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-            // new references; -1e30 in place of -infinity (no key seen yet) keeps the differences numbers
-            const float na = fmaxf(Ma, fmaxf(ma, -1e30f) - kHead), nb2 = fmaxf(Mb, fmaxf(mb, -1e30f) - kHead);
-            const float ca = exp2_fast(Ma - na), cb = exp2_fast(Mb - nb2);
-            Ma = na;
-            Mb = nb2;
-            float sa = 0.f, sb = 0.f;
-#pragma unroll
-            for (int nt = 0; nt < 2; nt++)
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    sc[nt][k] = exp2_fast(sc[nt][k] - Ma);
-                    sc[nt][2 + k] = exp2_fast(sc[nt][2 + k] - Mb);
-                    sa += sc[nt][k];
-                    sb += sc[nt][2 + k];
-                }
-            la = la * ca + sa;               // this thread's columns; the quad's are added at the end
-            lb = lb * cb + sb;
-#pragma unroll
-            for (int i = 0; i < HDP / 8; i++) {
-                o[i][0] *= ca;
-                o[i][1] *= ca;
-                o[i][2] *= cb;
-                o[i][3] *= cb;
-            }
-            uint32_t ph[4], pl[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float x = sc[j >> 1][(j & 1) * 2], y = sc[j >> 1][(j & 1) * 2 + 1];
-                ph[j] = pack_hi(x, y);
-                if (SPLITP) pl[j] = pack_lo(x, y, ph[j]);
-            }
-            // a row that some new tokens see and others do not: where its V is not
-            // finite, 0 * V would reach those that do not, so it is added to the
-            // others alone and taken out of the product
-            if (p.n_new > 1 && e0 + 15 > p.lens[s] - p.n_new + tile * 16 / a.gq) {
-                uint32_t odd = 0;
-                for (int i = lane; i < 16 * w8; i += 32) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(kb + (16 + i / w8) * PITCH + (i % w8) * 8);
-                    auto wild = [](uint32_t x) { return (x & 0x7C00u) == 0x7C00u || (x & 0x7C000000u) == 0x7C000000u; };
-                    if (wild(v.x) || wild(v.y) || wild(v.z) || wild(v.w)) odd |= 1u << (i / w8);
-                }
-                odd = __reduce_or_sync(0xffffffffu, odd);
-                for (uint32_t left = odd; left; left &= left - 1) {
-                    const int kk = __ffs(left) - 1, from = (lane & ~3) | ((kk & 7) >> 1);
-                    const float xa = kk < 8 ? (kk & 1 ? sc[0][1] : sc[0][0]) : (kk & 1 ? sc[1][1] : sc[1][0]);
-                    const float xb = kk < 8 ? (kk & 1 ? sc[0][3] : sc[0][2]) : (kk & 1 ? sc[1][3] : sc[1][2]);
-                    const float pa = __shfl_sync(0xffffffffu, xa, from), pb = __shfl_sync(0xffffffffu, xb, from);
-#pragma unroll
-                    for (int i = 0; i < HDP / 8; i++) {
-                        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(kb + (16 + kk) * PITCH + i * 8 + 2 * t));
-                        if (pa != 0.f) { o[i][0] = fmaf(pa, v.x, o[i][0]); o[i][1] = fmaf(pa, v.y, o[i][1]); }
-                        if (pb != 0.f) { o[i][2] = fmaf(pb, v.x, o[i][2]); o[i][3] = fmaf(pb, v.y, o[i][3]); }
-                    }
-                }
-                __syncwarp();
-                for (int i = lane; odd && i < 16 * w8; i += 32)
-                    if ((odd >> (i / w8)) & 1u)
-                        *reinterpret_cast<uint4*>(const_cast<__half*>(kb) + (16 + i / w8) * PITCH + (i % w8) * 8) = make_uint4(0, 0, 0, 0);
-                __syncwarp();
-            }
-            const uint32_t vrow = vbase + (uint32_t)((ri + (mi & 1) * 8) * PITCH * 2);
-#pragma unroll
-            for (int i = 0; i < HDP / 8; i += 2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4_t(vrow + (uint32_t)(((i + (mi >> 1)) * 8) * 2), b0, b1, b2, b3);
-                mma16816(o[i], ph, b0, b1);
-                mma16816(o[i + 1], ph, b2, b3);
-                if (SPLITP) {
-                    mma16816(o[i], pl, b0, b1);
-                    mma16816(o[i + 1], pl, b2, b3);
-                }
-            }
-            buf = buf + 1 == kSuffixBufs ? 0 : buf + 1;
-        }
-        la += __shfl_xor_sync(0xffffffffu, la, 1);
-        la += __shfl_xor_sync(0xffffffffu, la, 2);
-        lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-        lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-        cp_async_wait_all();
-        __syncthreads();                     // every warp is done with its rows: their memory takes the parts
-        float* po = reinterpret_cast<float*>(smraw);                  // [warps][16][HDP]
-        float2* pm = reinterpret_cast<float2*>(po + kSuffixWarps * 16 * HDP);   // [warps][16]
-        if (t == 0) {
-            pm[warp * 16 + r] = make_float2(Ma, la);
-            pm[warp * 16 + r + 8] = make_float2(Mb, lb);
-        }
-#pragma unroll
-        for (int i = 0; i < HDP / 8; i++) {
-            *reinterpret_cast<float2*>(po + (warp * 16 + r) * HDP + i * 8 + 2 * t) = make_float2(o[i][0], o[i][1]);
-            *reinterpret_cast<float2*>(po + (warp * 16 + r + 8) * HDP + i * 8 + 2 * t) = make_float2(o[i][2], o[i][3]);
+        if (threadIdx.x == 0) {
+            int all = 0;
+            for (int w = 0; w < kSuffixWarps; w++) all += sums[w];
+            starts[p.n_seqs] = all;
+            if (blockIdx.x == 0) a.starts[0] = 0;
         }
         __syncthreads();
-        const long long part = (((long long)s * p.n_kv + g) * a.suffix_splits + sp) * srows + tile * 16;
-        for (int i = threadIdx.x; i < 16 * p.hd; i += 32 * kSuffixWarps) {
-            const int rr = i / p.hd, d = i % p.hd;
-            if (tile * 16 + rr >= srows) break;
-            float M = -INFINITY, L = 0.f, x = 0.f;
+    }
+    const Deal deal = deal_of(starts[p.n_seqs], units, (int)gridDim.x * kSuffixWarps);
+    const int me = blockIdx.x * kSuffixWarps + warp;
+    if (me < deal.workers) {
+        const long long x0 = deal.total * me / deal.workers, x1 = deal.total * (me + 1) / deal.workers;
+        // where the first piece lies: the last sequence that starts at or before it
+        int s = 0;
+        for (int lo = 0, hi = p.n_seqs; hi - lo > 1;) {
+            const int mid = (lo + hi) / 2;
+            ((long long)starts[mid] * units <= x0 ? lo : hi) = mid;
+            s = lo;
+        }
+        int np = starts[s + 1] - starts[s];
+        const long long in_seq = x0 - (long long)starts[s] * units;
+        int j = (int)(in_seq / np), pc = (int)(in_seq % np);
+        const int n = (int)(x1 - x0), r = lane >> 2, t = lane & 3;
+        const long long pitch = (long long)p.n_kv * p.hd;
+
+        // the pages of this lane's rows r and r + 8 of the piece that is loaded next
+        int ls = s, lj = j, lpc = pc, lnp = np, page[2] = {-1, -1};
+        auto look = [&]() {
 #pragma unroll
-            for (int w = 0; w < kSuffixWarps; w++) M = fmaxf(M, pm[w * 16 + rr].x);
-#pragma unroll
-            for (int w = 0; w < kSuffixWarps; w++) {
-                const float2 ml = pm[w * 16 + rr];
-                const float c = exp2_fast(ml.x - M);          // a warp without a piece: 2^-infinity = 0
-                L += c * ml.y;
-                x = fmaf(c, po[(w * 16 + rr) * HDP + d], x);
+            for (int k = 0; k < 2; k++) {
+                const int e = lpc * 16 + r + 8 * k;
+                page[k] = e < lens[ls] ? p.table[(long long)ls * p.max_pages + (e >> p.page_shift)] : INT_MIN;
             }
-            a.suffix_o[(part + rr) * p.hd + d] = x;
-            if (d == 0) a.suffix_ml[part + rr] = make_float2(M, L);
+        };
+        look();
+        uint4 kx[2][CH], vx[2][CH];          // rows r and r + 8 of the piece on its way
+        bool there_x[2];                     // neither behind the sequence's last row nor on a bad page
+        auto load = [&](bool more) {         // requests the piece, moves on and looks the next one up
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                there_x[k] = page[k] >= 0 && page[k] < p.n_pages;
+                if (!there_x[k] && page[k] != INT_MIN) flag(p.err, LLM_PAGES_BAD_PAGE);
+                const int e = lpc * 16 + r + 8 * k;
+                const long long at = (((long long)page[k] << p.page_shift) + (e & ((1 << p.page_shift) - 1))) * pitch +
+                                     (long long)(lj / rt) * p.hd + 8 * t;
+#pragma unroll
+                for (int i = 0; i < CH; i++) {
+                    kx[k][i] = vx[k][i] = make_uint4(0, 0, 0, 0);
+                    if (there_x[k] && 8 * (t + 4 * i) < p.hd) {
+                        kx[k][i] = __ldcs(reinterpret_cast<const uint4*>(p.k + at + 32 * i));
+                        vx[k][i] = __ldcs(reinterpret_cast<const uint4*>(p.v + at + 32 * i));
+                    }
+                }
+            }
+            if (more) {
+                if (++lpc == lnp) {
+                    lpc = 0;
+                    if (++lj == units) {
+                        lj = 0;
+                        do lnp = starts[ls + 2] - starts[ls + 1], ls++;
+                        while (lnp == 0);
+                    }
+                }
+                look();
+            }
+        };
+        load(n > 1);
+        for (int it = 0; it < n;) {
+            // ---- one unit: pieces pc .. of its np, as far as this worker goes
+            const int tile = j % rt, g = j / rt, count = min(n - it, np - pc);
+            const int last = p.lens[s] - p.n_new, e_min = last + tile * RU / a.gq;
+            // q as the second operand: query row r of each eight; rows behind the last repeat it (never stored)
+            uint32_t qhi[NT][2 * CH][2], qlo[NT][SPLITQ ? 2 * CH : 1][2];
+            int e[NT][2];                    // the last cached row that query rows 2t and 2t + 1 see
+#pragma unroll
+            for (int q = 0; q < NT; q++) {
+                const long long at = q_offset(a, p.hd, g, s * srows + min(tile * RU + q * 8 + r, srows - 1));
+#pragma unroll
+                for (int k = 0; k < 2; k++) e[q][k] = last + min(tile * RU + q * 8 + 2 * t + k, srows - 1) / a.gq;
+#pragma unroll
+                for (int i = 0; i < CH; i++) {
+                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (8 * (t + 4 * i) < p.hd) load_q8(a, at + 8 * (t + 4 * i), x);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint32_t hi = pack_hi(x[2 * k], x[2 * k + 1]);
+                        qhi[q][2 * i + k / 2][k % 2] = hi;
+                        if (SPLITQ) qlo[q][SPLITQ ? 2 * i + k / 2 : 0][k % 2] = pack_lo(x[2 * k], x[2 * k + 1], hi);
+                    }
+                }
+            }
+            float o[NT][2 * CH][4], M[NT][2], l[NT][2];
+#pragma unroll
+            for (int q = 0; q < NT; q++) {
+#pragma unroll
+                for (int d = 0; d < 2 * CH; d++) o[q][d][0] = o[q][d][1] = o[q][d][2] = o[q][d][3] = 0.f;
+                M[q][0] = M[q][1] = -1e30f;  // no key seen yet: low, but a number
+                l[q][0] = l[q][1] = 0.f;
+            }
+            for (int i0 = 0; i0 < count; i0++, it++) {
+                uint32_t k0[4 * CH], k1[4 * CH], v0[4 * CH], v1[4 * CH];     // rows r (0) and r + 8 (1)
+#pragma unroll
+                for (int i = 0; i < CH; i++) {
+                    k0[4 * i] = kx[0][i].x; k0[4 * i + 1] = kx[0][i].y; k0[4 * i + 2] = kx[0][i].z; k0[4 * i + 3] = kx[0][i].w;
+                    k1[4 * i] = kx[1][i].x; k1[4 * i + 1] = kx[1][i].y; k1[4 * i + 2] = kx[1][i].z; k1[4 * i + 3] = kx[1][i].w;
+                    v0[4 * i] = vx[0][i].x; v0[4 * i + 1] = vx[0][i].y; v0[4 * i + 2] = vx[0][i].z; v0[4 * i + 3] = vx[0][i].w;
+                    v1[4 * i] = vx[1][i].x; v1[4 * i + 1] = vx[1][i].y; v1[4 * i + 2] = vx[1][i].z; v1[4 * i + 3] = vx[1][i].w;
+                }
+                const bool there[2] = {there_x[0], there_x[1]};
+                if (it + 1 < n) load(it + 2 < n);
+                float sc[NT][4];
+#pragma unroll
+                for (int q = 0; q < NT; q++) {
+                    sc[q][0] = sc[q][1] = sc[q][2] = sc[q][3] = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < 2 * CH; ks++) {
+                        mma_kn8(sc[q], k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], qhi[q][ks][0], qhi[q][ks][1]);
+                        if (SPLITQ)
+                            mma_kn8(sc[q], k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], qlo[q][SPLITQ ? ks : 0][0],
+                                    qlo[q][SPLITQ ? ks : 0][1]);
+                    }
+                }
+                // rows that are not there, and those that some query rows do not see
+                const int e0 = (pc + i0) * 16;
+#pragma unroll
+                for (int q = 0; q < NT; q++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (!there[k >> 1] || e0 + r + (k >> 1) * 8 > e[q][k & 1]) sc[q][k] = -INFINITY;
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int q = 0; q < NT; q++) {
+                    float top[2];
+                    bool move = false;
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float m = fmaxf(sc[q][k], sc[q][2 + k]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        top[k] = fmaxf(m * a.sc, -1e30f) - kHead;
+                        move |= top[k] > M[q][k] + kLag;
+                    }
+                    if (__any_sync(0xffffffffu, move)) {
+                        float c[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float up = fmaxf(M[q][k], top[k]);
+                            c[k] = exp2_fast(M[q][k] - up);
+                            M[q][k] = up;
+                            l[q][k] *= c[k];
+                        }
+#pragma unroll
+                        for (int d = 0; d < 2 * CH; d++) {
+                            o[q][d][0] *= c[0];
+                            o[q][d][1] *= c[1];
+                            o[q][d][2] *= c[0];
+                            o[q][d][3] *= c[1];
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        sc[q][k] = exp2_fast(fmaf(sc[q][k], a.sc, -M[q][k & 1]));
+                        l[q][k & 1] += sc[q][k];          // this thread's cached rows; all are added at the end
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const uint32_t hi = pack_hi(sc[q][2 * k], sc[q][2 * k + 1]);
+                        ph[q][k] = transpose8(hi);
+                        if (SPLITP) pl[q][k] = transpose8(pack_lo(sc[q][2 * k], sc[q][2 * k + 1], hi));
+                    }
+                }
+                // a row that some new tokens see and others do not: where its V is not
+                // finite, 0 * V would reach those that do not, so it is added to the
+                // others alone and taken out of the product
+                if (p.n_new > 1 && e0 + 15 > e_min) {
+                    bool wild[2] = {false, false};
+#pragma unroll
+                    for (int i = 0; i < 4 * CH; i++) {
+                        wild[0] |= (v0[i] & 0x7C00u) == 0x7C00u || (v0[i] & 0x7C000000u) == 0x7C000000u;
+                        wild[1] |= (v1[i] & 0x7C00u) == 0x7C00u || (v1[i] & 0x7C000000u) == 0x7C000000u;
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const uint32_t who = __ballot_sync(0xffffffffu, wild[k]);
+                        for (int kr = 0; kr < 8 && who; kr++) {
+                            if (!((who >> (4 * kr)) & 15u)) continue;
+#pragma unroll
+                            for (int q = 0; q < NT; q++) {
+                                const float pa = __shfl_sync(0xffffffffu, sc[q][2 * k], 4 * kr + t), pb = __shfl_sync(0xffffffffu, sc[q][2 * k + 1], 4 * kr + t);
+#pragma unroll
+                                for (int i = 0; i < 4 * CH; i++) {
+                                    const uint32_t w = __shfl_sync(0xffffffffu, k ? v1[i] : v0[i], 4 * kr + (r >> 1));
+                                    const float v = __half2float(__ushort_as_half((unsigned short)(r & 1 ? w >> 16 : w & 0xFFFFu)));
+                                    if (pa != 0.f) o[q][i / 2][2 * (i & 1)] = fmaf(pa, v, o[q][i / 2][2 * (i & 1)]);
+                                    if (pb != 0.f) o[q][i / 2][2 * (i & 1) + 1] = fmaf(pb, v, o[q][i / 2][2 * (i & 1) + 1]);
+                                }
+                            }
+                            if (r == kr)
+#pragma unroll
+                                for (int i = 0; i < 4 * CH; i++) (k ? v1[i] : v0[i]) = 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < 2 * CH; d++) {
+                    const uint32_t a0 = transpose8(v0[2 * d]), a1 = transpose8(v0[2 * d + 1]), a2 = transpose8(v1[2 * d]), a3 = transpose8(v1[2 * d + 1]);
+#pragma unroll
+                    for (int q = 0; q < NT; q++) {
+                        mma_kn8(o[q][d], a0, a1, a2, a3, ph[q][0], ph[q][1]);
+                        if (SPLITP) mma_kn8(o[q][d], a0, a1, a2, a3, pl[q][0], pl[q][1]);
+                    }
+                }
+            }
+            // ---- this worker's part of the unit
+            const long long slot = ((long long)s * units + j + me) * min(srows, RU);
+#pragma unroll
+            for (int q = 0; q < NT; q++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[q][k] += __shfl_xor_sync(0xffffffffu, l[q][k], d);
+                    const int row = q * 8 + 2 * t + k;
+                    if (tile * RU + row >= srows) continue;
+                    float* dst = a.suffix_o + (slot + row) * p.hd;
+#pragma unroll
+                    for (int i = 0; i < 4 * CH; i++) {
+                        const int d = 8 * (r >> 1) + 32 * (i / 4) + 2 * (i % 4) + (r & 1);
+                        if (d < p.hd) dst[d] = o[q][i / 2][2 * (i & 1) + k];
+                    }
+                    if (r == 0) a.suffix_ml[slot + row] = make_float2(M[q][k], l[q][k]);
+                }
+            pc = 0;
+            if (it < n && ++j == units) {
+                j = 0;
+                do np = starts[s + 2] - starts[s + 1], s++;
+                while (np == 0);
+            }
         }
     }
     if (!first) griddep_wait();              // this grid's end is the prefix kernel's too, for the join
 }
 
 // --------------------------------------------------------------- join --
-// One warp per (row, head): the prefix's parts, then the sequence's.
+// One warp per (row, head): the prefix's parts, then the sequence's.  LP lanes
+// hold the hd values of a part, four each, and the warp's 32 / LP groups take
+// the parts in turn, eight of them in flight per group.
+template <int LP>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a) {
+    constexpr int GROUPS = 32 / LP, AHEAD = 8;
     griddep_entry();
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, grp = lane / LP, d = 4 * (lane % LP);
+    if (w >= (long long)p.n_seqs * p.n_new * a.n_heads) return;
     const int token = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-    if (token >= p.n_seqs * p.n_new) return;
     const int s = token / p.n_new, i = token % p.n_new, g = h / a.gq, hq = h % a.gq;
-    if (p.lens[s] - p.n_new + i < 0) return;                   // padding
-    const SuffixCut cut = suffix_cut(p, s, a.suffix_splits);
-    if (lane == 0 && p.lens[s] > cut.len) flag(p.err, LLM_PAGES_BAD_LEN);
-    const int np = a.prefix_splits, n = np + cut.parts, srows = p.n_new * a.gq;
+    const int len = p.lens[s];
+    if (len - p.n_new + i < 0) return;                         // padding
+    if (lane == 0 && len > clipped_len(p, s)) flag(p.err, LLM_PAGES_BAD_LEN);
+    const int np = a.prefix_splits, srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
+    int parts = 0;
+    long long suf = 0;                                         // row of the first part
+    const int step = min(srows, ru);
+    if (a.suffix_workers > 0) {
+        const int b = a.starts[s], pieces = a.starts[s + 1] - b;
+        const Deal deal = deal_of(a.starts[p.n_seqs], p.n_kv * rt, a.suffix_workers);
+        if (pieces > 0) {
+            // pieces x .. y of all belong to this unit; piece x is worker ((x + 1) W - 1) / T's
+            const int j = g * rt + row / ru;
+            const long long x = (long long)b * deal.units + (long long)j * pieces, y = x + pieces - 1;
+            const long long w0 = ((x + 1) * deal.workers - 1) / deal.total, w1 = ((y + 1) * deal.workers - 1) / deal.total;
+            parts = (int)(w1 - w0) + 1;
+            suf = ((long long)s * deal.units + j + w0) * step + row % ru;
+        }
+    }
+    const int n = np + parts;
     const long long pre = (long long)g * a.rows + (long long)token * a.gq + hq, pre_step = (long long)p.n_kv * a.rows;
-    const long long suf = ((long long)s * p.n_kv + g) * a.suffix_splits * srows + i * a.gq + hq;
-    auto ml_of = [&](int k) { return k < np ? a.prefix_ml[pre + k * pre_step] : a.suffix_ml[suf + (long long)(k - np) * srows]; };
     float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, ml_of(k).x);
+    for (int k = lane; k < n; k += 32) M = fmaxf(M, k < np ? a.prefix_ml[pre + k * pre_step].x : a.suffix_ml[suf + (long long)(k - np) * step].x);
     M = warp_max(M);
-    const int d = 4 * lane;
     float L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < n; k0 += 32) {
         float wk = 0.f;
         if (k0 + lane < n) {
-            const float2 ml = ml_of(k0 + lane);
+            const int k = k0 + lane;
+            const float2 ml = k < np ? a.prefix_ml[pre + k * pre_step] : a.suffix_ml[suf + (long long)(k - np) * step];
             wk = exp2_fast(ml.x - M);
             L += wk * ml.y;
         }
-#pragma unroll 4
-        for (int k = 0; k < min(32, n - k0); k++) {
-            const float c = __shfl_sync(0xffffffffu, wk, k);
-            if (d < p.hd) {
-                const int kk = k0 + k;
-                const float4 v = *reinterpret_cast<const float4*>((kk < np ? a.prefix_o + (pre + kk * pre_step) * p.hd
-                                                                           : a.suffix_o + (suf + (long long)(kk - np) * srows) * p.hd) + d);
-                x.x = fmaf(c, v.x, x.x);
-                x.y = fmaf(c, v.y, x.y);
-                x.z = fmaf(c, v.z, x.z);
-                x.w = fmaf(c, v.w, x.w);
+        for (int q0 = 0; q0 < min(32, n - k0); q0 += GROUPS * AHEAD) {
+            float4 v[AHEAD];
+#pragma unroll
+            for (int q = 0; q < AHEAD; q++) {
+                const int k = k0 + q0 + q * GROUPS + grp;
+                v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < n && d < p.hd)
+                    v[q] = *reinterpret_cast<const float4*>((k < np ? a.prefix_o + (pre + k * pre_step) * p.hd
+                                                                    : a.suffix_o + (suf + (long long)(k - np) * step) * p.hd) + d);
+            }
+#pragma unroll
+            for (int q = 0; q < AHEAD; q++) {
+                const float c = __shfl_sync(0xffffffffu, wk, (q0 + q * GROUPS + grp) & 31);
+                x.x = fmaf(c, v[q].x, x.x);
+                x.y = fmaf(c, v[q].y, x.y);
+                x.z = fmaf(c, v[q].z, x.z);
+                x.w = fmaf(c, v[q].w, x.w);
             }
         }
     }
     L = warp_sum(L);
+#pragma unroll
+    for (int o = LP; o < 32; o <<= 1) {
+        x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+        x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+        x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+        x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+    }
     const float inv = L == 0.f ? 0.f : 1.f / L;                // a row without any key is zero
-    if (d >= p.hd) return;
+    if (d >= p.hd || grp > 0) return;
     const long long at = (long long)token * a.out_stride + (long long)h * p.hd + d;
     if (a.out_f16)
         *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) = make_uint2(pack_hi(x.x * inv, x.y * inv), pack_hi(x.z * inv, x.w * inv));
@@ -783,9 +892,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
 
 // --------------------------------------------------------------- host --
 struct Plan {
-    int prefix_splits, suffix_splits, mtiles;
+    int prefix_splits, suffix_blocks, mtiles;
     long long prefix_rows, suffix_rows;      // parts of one row each
-    size_t off_pml, off_so, off_sml, bytes;
+    size_t off_pml, off_so, off_sml, off_starts, bytes;
 };
 
 Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
@@ -799,13 +908,18 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
         const long long want = std::max<long long>(1, slots / base);
         pl.prefix_splits = (int)std::max<long long>(1, std::min<long long>(want, ntiles / 2));
     }
-    if (p->max_pages > 0) {
-        const long long units = (long long)p->n_seqs * p->n_kv_heads * ((srows + 15) / 16);
-        const long long tiles = ((long long)p->max_pages * p->page_size + 63) / 64;
-        pl.suffix_splits = (int)std::max<long long>(1, std::min<long long>({32, 4 * sms / std::max(1ll, units), tiles}));
-    }
     pl.prefix_rows = (long long)pl.prefix_splits * p->n_kv_heads * rows;
-    pl.suffix_rows = (long long)p->n_seqs * p->n_kv_heads * pl.suffix_splits * srows;
+    if (p->max_pages > 0) {
+        // workers for as many blocks as an SM holds at once, but no more than the
+        // longest sequences could keep busy
+        const int ru = unit_rows((int)srows);
+        const long long units = (long long)p->n_kv_heads * ((srows + ru - 1) / ru),
+                        most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16),
+                        blocks = (most + kQuantum * kSuffixWarps - 1) / (kQuantum * kSuffixWarps);
+        const int ctas = suffix_ctas(p->head_dim <= 64 ? 64 : 128, ru / 8);
+        pl.suffix_blocks = (int)std::max<long long>(1, std::min<long long>(blocks, (long long)ctas * sms));
+        pl.suffix_rows = (units * p->n_seqs + pl.suffix_blocks * kSuffixWarps) * std::min<long long>(srows, ru);
+    }
     auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
     size_t at = up((size_t)pl.prefix_rows * p->head_dim * 4);
     pl.off_pml = at;
@@ -814,18 +928,20 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
     at += up((size_t)pl.suffix_rows * p->head_dim * 4);
     pl.off_sml = at;
     at += up((size_t)pl.suffix_rows * 8);
+    pl.off_starts = at;
+    if (pl.suffix_blocks > 0) at += up((size_t)(p->n_seqs + 1) * 4);
     pl.bytes = at;
     return pl;
 }
 
-// K or V rows of the prefix as {hd, n_kv, rows}: columns behind hd and rows
-// behind the prefix read as zero.
-bool prefix_map(CUtensorMap* m, const uint16_t* base, const llm_pages* p, int64_t stride) {
+// Cached rows as {hd, n_kv, rows}, `stride` elements apart, in boxes of
+// box_rows: columns behind hd and rows behind the last read as zero.
+bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long rows, int64_t stride, int box_rows) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
-    cuuint64_t dim[3] = {(cuuint64_t)p->head_dim, (cuuint64_t)p->n_kv_heads, (cuuint64_t)p->prefix_len};
-    cuuint64_t step[2] = {(cuuint64_t)p->head_dim * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[3] = {64, 1, kKT}, es[3] = {1, 1, 1};
+    cuuint64_t dim[3] = {(cuuint64_t)hd, (cuuint64_t)n_kv, (cuuint64_t)(rows > 0 ? rows : 1)};
+    cuuint64_t step[2] = {(cuuint64_t)hd * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(base), dim, step, box, es,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -841,21 +957,21 @@ cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensor
     return launch_dep(k, dim3((unsigned)mtiles * ad.prefix_splits, pd.n_kv), dim3(kPrefixThreads), (size_t)G::kSmem, st, mk, mv, pd, ad);
 }
 
-template <int HDP, bool SPLITQ, bool SPLITP>
-cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first) {
-    auto k = suffix_kernel<HDP, SPLITQ, SPLITP>;
-    constexpr int rows = kSuffixWarps * kSuffixBufs * 2 * 16 * (HDP + 8) * 2, parts = kSuffixWarps * 16 * (HDP + 2) * 4;
-    constexpr int smem = rows > parts ? rows : parts;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const long long rt = (pd.n_new * ad.gq + 15) / 16;
-    return launch_dep(k, dim3((unsigned)(ad.suffix_splits * rt * pd.n_seqs), pd.n_kv), dim3(32 * kSuffixWarps), (size_t)smem, st, pd, ad, first);
+template <int HDP, int NT, bool SPLITQ, bool SPLITP>
+cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
+    // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
+    static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
+    return launch_dep(suffix_kernel<HDP, NT, SPLITQ, SPLITP>, dim3((unsigned)blocks), dim3(32 * kSuffixWarps),
+                      (size_t)(2 * pd.n_seqs + 1) * 4, st, pd, ad, first);
 }
 
 int check_attend(const llm_pages* p, const llm_attend* a) {
     if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the attention arguments are NULL");
     if (a->n_heads < 1 || a->n_heads % p->n_kv_heads)
         return fail_op(LLM_ERR_INVALID_ARG, "n_heads %d is not a multiple of n_kv_heads %d", a->n_heads, p->n_kv_heads);
+    if (p->n_seqs > kMaxSeqs) return fail_op(LLM_ERR_UNSUPPORTED, "n_seqs %d exceeds %d", p->n_seqs, kMaxSeqs);
+    if ((long long)p->n_seqs * ((long long)p->max_pages * p->page_size / 16 + 1) > INT_MAX / 2)
+        return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold more than 2^34 rows together");
     if (p->n_kv_heads > 65535) return fail_op(LLM_ERR_UNSUPPORTED, "n_kv_heads %d exceeds 65535", p->n_kv_heads);
     if ((long long)p->n_seqs * p->n_new * a->n_heads > INT_MAX / 64)
         return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^25 rows of all heads");
@@ -909,13 +1025,15 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
     ad.suffix_o = reinterpret_cast<float*>(ws + pl.off_so);
     ad.suffix_ml = reinterpret_cast<float2*>(ws + pl.off_sml);
     ad.prefix_splits = pl.prefix_splits;
-    ad.suffix_splits = pl.suffix_splits;
+    ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
+    ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
     const bool sq = !ad.q_f16, so = !ad.out_f16;
     const int hd = pages->head_dim;
     cudaError_t e = cudaSuccess;
     if (prefix) {
         CUtensorMap mk, mv;
-        if (!prefix_map(&mk, a->prefix_k, pages, a->prefix_stride) || !prefix_map(&mv, a->prefix_v, pages, a->prefix_stride))
+        if (!rows_map(&mk, a->prefix_k, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT) ||
+            !rows_map(&mv, a->prefix_v, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT))
             return fail_op(LLM_ERR_CUDA, "a tensor map of the prefix");
 #define LLM_PREFIX(HDP)                                                                                          \
     (sq ? (so ? launch_prefix<HDP, true, true>(stream, mk, mv, pd, ad, pl.mtiles)                                 \
@@ -926,15 +1044,21 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
 #undef LLM_PREFIX
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (prefix)");
     }
-    if (pl.suffix_splits > 0) {
+    if (pl.suffix_blocks > 0) {
         const int first = prefix ? 0 : 1;
-#define LLM_SUFFIX(HDP)                                                                                          \
-    (sq ? (so ? launch_suffix<HDP, true, true>(stream, pd, ad, first) : launch_suffix<HDP, true, false>(stream, pd, ad, first)) \
-        : (so ? launch_suffix<HDP, false, true>(stream, pd, ad, first) : launch_suffix<HDP, false, false>(stream, pd, ad, first)))
-        e = hd <= 32 ? LLM_SUFFIX(32) : hd <= 64 ? LLM_SUFFIX(64) : LLM_SUFFIX(128);
+#define LLM_SUFFIX(HDP, NT)                                                                                      \
+    (sq ? (so ? launch_suffix<HDP, NT, true, true>(stream, pd, ad, first, pl.suffix_blocks)               \
+              : launch_suffix<HDP, NT, true, false>(stream, pd, ad, first, pl.suffix_blocks))             \
+        : (so ? launch_suffix<HDP, NT, false, true>(stream, pd, ad, first, pl.suffix_blocks)              \
+              : launch_suffix<HDP, NT, false, false>(stream, pd, ad, first, pl.suffix_blocks)))
+        const bool eight = unit_rows(pages->n_new * ad.gq) == 8;
+        e = hd <= 64 ? (eight ? LLM_SUFFIX(64, 1) : LLM_SUFFIX(64, 2)) : (eight ? LLM_SUFFIX(128, 1) : LLM_SUFFIX(128, 2));
 #undef LLM_SUFFIX
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (suffix)");
     }
-    const long long warps = rows * a->n_heads;
-    return launched(launch_dep(join_kernel, dim3((unsigned)((warps + 3) / 4)), dim3(128), 0, stream, pd, ad), "llm_attend_batch (join)");
+    const dim3 grid((unsigned)((rows * a->n_heads + 3) / 4));
+    return launched(hd <= 32   ? launch_dep(join_kernel<8>, grid, dim3(128), 0, stream, pd, ad)
+                    : hd <= 64 ? launch_dep(join_kernel<16>, grid, dim3(128), 0, stream, pd, ad)
+                               : launch_dep(join_kernel<32>, grid, dim3(128), 0, stream, pd, ad),
+                    "llm_attend_batch (join)");
 }

@@ -82,6 +82,13 @@ def test_append_refused(kw, status):
     refused(B._lib.llm_kv_append(ref(pages()), ref(append(**kw)), None), status)
 
 
+@pytest.mark.parametrize("kw", [dict(n_seqs=4097), dict(n_seqs=4096, max_pages=1 << 20)])
+def test_attend_refuses_what_append_takes(kw):
+    for rc in (B._lib.llm_attend_batch(ref(pages(**kw)), ref(attend()), None),
+               B._lib.llm_attend_batch_workspace(ref(pages(**kw)), ref(attend()))):
+        refused(rc, UNSUP)
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(n_heads=0), BAD), (dict(n_heads=3), BAD), (dict(q_dtype=L.LLM_Q8_0), UNSUP), (dict(out_dtype=7), UNSUP),
     (dict(scale=-1.0), BAD), (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(q=None), BAD),

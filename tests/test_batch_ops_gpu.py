@@ -314,7 +314,7 @@ def test_attend_prefix_lengths(lib, prefix, types):
 
 
 @pytest.mark.parametrize("types", [(F32, F32), (F16, F16)])
-@pytest.mark.parametrize("page", [1, 4, 32, 128, 512])
+@pytest.mark.parametrize("page", [1, 4, 8, 32, 128, 512])
 def test_attend_page_sizes(lib, page, types):
     run_attend(lib, (4, 2, 64), [1, 31, 32, 33, 127, 129, 700], 1, 50, page, *types)
 
