@@ -34,12 +34,12 @@ struct AttendDev {
     void* out;
     long long out_stride;
     int out_f16;
-    float* prefix_o;                // [prefix splits][n_kv][rows][hd]
-    float2* prefix_ml;              // [prefix splits][n_kv][rows]: M, l
+    float* prefix_o;                // [n_kv * row tiles + blocks][2 groups][128][hd]
+    float2* prefix_ml;              // [n_kv * row tiles + blocks][2][128]: M, l
     float* suffix_o;                // [units of all sequences + workers][up to 16 rows][hd]
     float2* suffix_ml;
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
-    int prefix_splits, suffix_workers;
+    int prefix_blocks, suffix_workers;
 };
 
 // Probabilities are kept as 2^(y - M) with M = (a recent maximum) - kHead, so
@@ -89,38 +89,49 @@ __device__ __forceinline__ long long q_offset(const AttendDev& a, int hd, int g,
     return (long long)(r / a.gq) * a.q_stride + (long long)(g * a.gq + r % a.gq) * hd;
 }
 
+// ------------------------------------------------------------- deals --
+// Work in units of equal or unequal size, laid out in a row, is cut into `total`
+// pieces and dealt to workers evenly: worker w takes pieces [w T / W, (w + 1) T /
+// W), whatever units they belong to.  A worker leaves one part per unit that it
+// touches, in slot unit + worker: each step of that walk raises one or both, so no
+// two parts share a slot.  Piece x is worker ((x + 1) W - 1) / T's.
+__device__ __forceinline__ long long owner_of(long long x, int workers, long long total) {
+    const long long y = (x + 1) * workers - 1;
+    return (unsigned long long)(total * workers) >> 32 ? y / total : (long long)((uint32_t)y / (uint32_t)total);
+}
+
 // ------------------------------------------------------------- prefix --
 constexpr int kKT = 64;                      // keys per tile
 
-// Blocks of an SM: two of head sizes up to 64 overlap one's softmax with the
-// other's waits; the tiles of larger heads fill an SM's shared memory at one.
-constexpr int prefix_ctas(int hd) { return hd <= 64 ? 2 : 1; }
-
-template <int HDP, bool SPLITQ>
+template <int HDP>
 struct PrefixPlan {
+    // score buffers of 64 columns, half of them each softmax group's; with the two
+    // groups' O (HDP columns each) and Q (HDP / 2 columns a part) they fill at most the
+    // 512 columns of tensor memory
+    static constexpr int kScores = HDP == 64 ? 4 : 2;
+    static constexpr int kO = kScores * 64, kQ = kO + 2 * HDP, kTmemCols = 512;
+
     static constexpr int kSlabs = HDP / 64;                        // 64-column (128-byte) slabs of a row
-    static constexpr bool kQInTmem = HDP == 64;
-    static constexpr int kQBytes = kQInTmem ? 0 : 128 * HDP * 2;   // the query tile (twice with SPLITQ)
     static constexpr int kTileBytes = kKT * HDP * 2;               // K or V
-    static constexpr int kCtas = prefix_ctas(HDP);                 // per SM
-    static constexpr int kStages = HDP == 64 ? 6 : SPLITQ ? 4 : 5;
-    static constexpr int kBarBytes = 256;
-    static constexpr int kSmem = kQBytes * (SPLITQ ? 2 : 1) + kStages * 2 * kTileBytes + kBarBytes + 1024;
-    static constexpr int kTmemCols = 256;                          // S0 | S1 (64 each) | O (HDP) | Q (32 a part)
+    // more than half of an SM's shared memory: a second block there would only wait
+    // for the first one's tensor memory
+    static constexpr int kStages = HDP == 64 ? 8 : 5;
+    static constexpr int kSmem = kStages * 2 * kTileBytes + 512 + 1024;
 };
 
-constexpr int kPrefixThreads = 192;
+constexpr int kSoftmaxWarps = 8, kPrefixThreads = 32 * (kSoftmaxWarps + 3);
+constexpr int kPrefixRegs = 88;              // with two blocks of the suffix kernel (128 x 128): 63,744 of 65,536
 
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t par, int* err) {
-    for (long long i = 0; i < kSpinLimit / 16; i++)
-        if (mbar_try_wait(bar, par)) return true;
+constexpr int kWaitLimit = 10000000;         // probes (each suspends the warp for a while) before a wait gives up
+// A whole warp's bounded wait for a phase.  The first probe stands outside the loop
+// and every branch is the warp's: a completed phase costs 75 cycles (a loop of each
+// lane's own took 250).
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, int* err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
+    for (int i = 0; i < kWaitLimit; i++)
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
     flag(err, LLM_PAGES_TIMEOUT);
     return false;
-}
-
-// The same for a whole warp that goes on to warp-wide instructions.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, int* err) {
-    return __all_sync(0xffffffffu, bar_wait(bar, par, err));
 }
 
 // One lane of the warp, the same one every time.
@@ -138,12 +149,6 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t slab) {
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -164,15 +169,12 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t* v) {
           "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
         : "r"(a));
 }
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* v) {
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t* v) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(a));
 }
 __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* v) {
     asm volatile(
@@ -186,61 +188,63 @@ __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sy
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 128 query rows of kv head g against one split of the prefix:
-//   warps 0-3  softmax, one query row per thread (its TMEM lane): reads the
-//              row's 64 scores, writes its probabilities back over them as
-//              F16 (with SPLITP the rounded-off rest beside them), and rescales
-//              O when the row's maximum has moved by more than kLag;
-//   warp 4     MMA: S = Q K^T into one of two score buffers, one tile ahead;
-//   warp 5     TMA: 64-key tiles of K and V into a ring; MMA: O += P V, P from
-//              tensor memory.
-// Two MMA warps, because each wait and each issue takes one of them 150 to 200
-// cycles; a seventh warp for the copies would leave two blocks of an SM 128
-// registers a thread, and the scores would spill.
-// Q is read from tensor memory too where it fits (head sizes up to 64): an MMA
-// whose 128-row operand comes from shared memory takes 48 cycles at this width,
-// for 32 of work.
-// SPLITQ: Q as two F16 parts; SPLITP: P as two F16 parts.
+// The prefix's tiles against tiles of 128 query rows.  Unit u is row tile u % mt of
+// kv head u / mt, a piece is one of its 64-key tiles, a worker is a block (one per
+// SM).  Of a block's warps
+//   0-3, 4-7  two groups do the softmax of the block's even and odd tiles, one query
+//        row per thread (its lane of tensor memory), each with a maximum, a sum and
+//        an O of its own: one group's exponentials run beside the other's waits and
+//        maxima.  A thread reads the row's 64 scores in halves, writes the
+//        probabilities over each half as F16 (with SPLITP the rounded-off rest beside
+//        them), and rescales O when the row's maximum has moved by more than kLag;
+//   8, 9 issue a group's products each, S = Q K^T (a tile ahead, where its score
+//        buffers allow) and O += P V;
+//   10   loads 64-key tiles of K and V into a ring (TMA).
+// Q and P are operands in tensor memory: an MMA whose 128-row operand comes from
+// shared memory takes 48 cycles at this width, for 32 of work.  The MMA warps walk
+// their loops whole and one elected lane issues: counters and descriptors stay in
+// uniform registers (a loop of one lane took 90 to 140 cycles an instruction); a
+// wait costs them 75 cycles and the MMAs of a product 200 to 400.  Halving the scores keeps a thread within 88 registers, so that the
+// suffix kernel's blocks fit beside a block of this one.  SPLITQ: Q as two F16
+// parts; SPLITP: P as two.
 template <int HDP, bool SPLITQ, bool SPLITP>
-__global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas)
+__global__ void __maxnreg__(kPrefixRegs)
     prefix_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a) {
-    using G = PrefixPlan<HDP, SPLITQ>;
-    constexpr int NS = G::kStages;
+    using G = PrefixPlan<HDP>;
+    constexpr int NS = G::kStages, kScores = G::kScores;
     extern __shared__ __align__(1024) uint8_t smraw[];
-    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
-    uint8_t* qs = sm;
-    uint8_t* ring = sm + G::kQBytes * (SPLITQ ? 2 : 1);
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smraw) + 1023) & ~(uintptr_t)1023);
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + NS * 2 * G::kTileBytes);
     uint64_t* empty = full + NS;
-    uint64_t* sfull = empty + NS;            // [2] scores of a tile are in buffer b
-    uint64_t* pfull = sfull + 2;             // [2] probabilities of a tile are in buffer b
-    uint64_t* pvdone = pfull + 2;            // [2] the P V of a tile in buffer b has been added
-    uint64_t* qfull = pvdone + 2;
-    uint64_t* fin = qfull + 1;               // every P V has been added
-    uint64_t* qfin = fin + 1;                // every MMA of the scores has completed
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qfin + 1);
+    uint64_t* sfull = empty + NS;            // [kScores] scores of a tile are in buffer b
+    uint64_t* pfull = sfull + kScores;       // [kScores] its probabilities are
+    uint64_t* pvdone = pfull + kScores;      // [kScores] its P V has been added
+    uint64_t* qfull = pvdone + kScores;      // a unit's Q is in tensor memory
+    uint64_t* fin = qfull + 1;               // [2] every MMA of a group has completed
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int mtiles = (a.rows + 127) / 128;
-    const int m0 = (int)(blockIdx.x % mtiles) * 128, sp = (int)(blockIdx.x / mtiles), g = blockIdx.y;
-    const int ntiles = (p.prefix_len + kKT - 1) / kKT;
-    const int t0 = (int)((long long)ntiles * sp / a.prefix_splits), n = (int)((long long)ntiles * (sp + 1) / a.prefix_splits) - t0;
+    const int mt = (a.rows + 127) / 128, ntiles = (p.prefix_len + kKT - 1) / kKT;
+    const long long total = (long long)mt * p.n_kv * ntiles;
+    const long long x0 = total * blockIdx.x / gridDim.x;
+    const int n = (int)(total * (blockIdx.x + 1) / gridDim.x - x0);          // this block's pieces
+    const int u0 = (int)(x0 / ntiles), t0 = (int)(x0 % ntiles);              // unit and tile of the first
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; s++) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; b++) {
+        for (int b = 0; b < kScores; b++) {
             mbar_init(&sfull[b], 1);
-            mbar_init(&pfull[b], 4);
+            mbar_init(&pfull[b], kSoftmaxWarps / 2);
             mbar_init(&pvdone[b], 1);
         }
-        mbar_init(qfull, 4);
-        mbar_init(fin, 1);
-        mbar_init(qfin, 1);
+        mbar_init(qfull, kSoftmaxWarps);
+        mbar_init(&fin[0], 1);
+        mbar_init(&fin[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 4) {
+    if (warp == kSoftmaxWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
                      "r"(G::kTmemCols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -248,229 +252,234 @@ __global__ void __launch_bounds__(kPrefixThreads, PrefixPlan<HDP, SPLITQ>::kCtas
     tm_fence_before();
     __syncthreads();
     tm_fence_after();
-    const uint32_t tmem = *tmem_slot, to = tmem + 128;
+    const uint32_t tmem = *tmem_slot;
     // the suffix kernel may start once every CTA here has seen the work before
     // this kernel complete: it needs that work, but nothing of this kernel's
     griddep_wait();
     griddep_launch();
 
-    if (warp == 4) {
-        // The whole warp walks the loop and one elected lane issues: the tile
-        // counters and descriptors stay in uniform registers (a loop of one
-        // lane alone took 90 to 140 cycles per MMA to issue, and set the pace).
-        // F16 operands, F32 accumulators, M 128, N 64, both K-major.
+    if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 1) {
+        // ---- the products of one group's tiles.  F16 operands, F32 accumulators, M 128.  Scores:
+        // N 64, K is K-major; sums: N HDP, V has the keys (the MMA's K) as rows, so it is MN-major
         constexpr uint32_t is = (1u << 4) | ((uint32_t)(kKT >> 3) << 17) | (8u << 24);
-        const uint64_t dq = desc_sw128(smem_addr(qs), 16), dk = desc_sw128(smem_addr(ring), 16);
-        bool ok = warp_wait(qfull, 0, p.err);
-        for (int it = 0; it < n && ok; it++) {
-            if (!(ok = warp_wait(&full[it % NS], (uint32_t)((it / NS) & 1), p.err))) break;
-            // these scores go where tile it - 2's probabilities were
-            if (it > 1 && !(ok = warp_wait(&pvdone[it & 1], (uint32_t)(((it >> 1) - 1) & 1), p.err))) break;
+        constexpr uint32_t io = (1u << 4) | (1u << 16) | ((uint32_t)(HDP >> 3) << 17) | (8u << 24);
+        constexpr int AHEAD = kScores / 2 - 1;                         // tiles that the scores run ahead of the sums
+        const int group = warp - kSoftmaxWarps;
+        const uint64_t dk = desc_sw128(smem_addr(ring), 16), dv = desc_sw128(smem_addr(ring) + G::kTileBytes, kKT * 128);
+        const uint32_t o = tmem + G::kO + group * HDP;
+        auto scores = [&](int it) {
+            // they go where tile it - kScores's probabilities were
+            if (!warp_wait(&full[it % NS], (uint32_t)((it / NS) & 1), p.err)) return false;
+            if (it >= kScores && !warp_wait(&pvdone[it % kScores], (uint32_t)((it / kScores - 1) & 1), p.err)) return false;
             tm_fence_after();
             const uint64_t k = dk + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
-            const uint32_t d = tmem + (uint32_t)((it & 1) * 64);
             if (elect_one()) {
 #pragma unroll
                 for (int part = 0; part < (SPLITQ ? 2 : 1); part++)
 #pragma unroll
-                    for (int kk = 0; kk < HDP / 16; kk++) {
-                        const uint64_t kd = k + (((kk / 4) * kKT * 128 + (kk % 4) * 32) >> 4);
-                        if (G::kQInTmem)
-                            mma_ts(d, tmem + 192 + part * 32 + kk * 8, kd, is, part + kk > 0);
-                        else
-                            mma_ss(d, dq + ((part * G::kQBytes + (kk / 4) * 128 * 128 + (kk % 4) * 32) >> 4), kd, is, part + kk > 0);
-                    }
-                mma_commit(&sfull[it & 1]);
+                    for (int kk = 0; kk < HDP / 16; kk++)
+                        mma_ts(tmem + (uint32_t)((it % kScores) * 64), tmem + G::kQ + part * (HDP / 2) + kk * 8,
+                               k + (((kk / 4) * kKT * 128 + (kk % 4) * 32) >> 4), is, part + kk > 0);
+                mma_commit(&sfull[it % kScores]);
             }
             __syncwarp();
+            return true;
+        };
+        bool ok = true;
+        for (int begin = 0, tile0 = t0, unit = 0; begin < n && ok; tile0 = 0, unit++) {
+            const int end = min(n, begin + ntiles - tile0), first = begin + ((begin ^ group) & 1);
+            ok = warp_wait(qfull, (uint32_t)(unit & 1), p.err);
+            if (ok && AHEAD > 0 && first < end) ok = scores(first);
+            for (int it = first; it < end && ok; it += 2) {
+                if (it + 2 * AHEAD < end && !(ok = scores(it + 2 * AHEAD))) break;
+                if (!(ok = warp_wait(&pfull[it % kScores], (uint32_t)((it / kScores) & 1), p.err))) break;
+                tm_fence_after();
+                const uint64_t v = dv + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
+                const uint32_t pa = tmem + (uint32_t)((it % kScores) * 64), more = it > first;
+                if (elect_one()) {
+#pragma unroll
+                    for (int part = 0; part < (SPLITP ? 2 : 1); part++)
+#pragma unroll
+                        for (int kk = 0; kk < kKT / 16; kk++)
+                            mma_ts(o, pa + (kk / 2) * 32 + part * 16 + (kk % 2) * 8, v + (kk * 16 * 128 >> 4), io, part + kk > 0 ? 1u : more);
+                    mma_commit(&pvdone[it % kScores]);
+                    mma_commit(&empty[it % NS]);
+                }
+                __syncwarp();
+            }
+            begin = end;
         }
         // every MMA issued has completed before the tensor memory is freed
-        if (elect_one()) mma_commit(qfin);
+        if (elect_one()) mma_commit(&fin[group]);
         __syncwarp();
-        warp_wait(qfin, 0, p.err);
-    } else if (warp == 5) {
-        // N HDP; V has the keys (the MMA's K) as rows, so it is MN-major
-        constexpr uint32_t io = (1u << 4) | (1u << 16) | ((uint32_t)(HDP >> 3) << 17) | (8u << 24);
-        const uint64_t dv = desc_sw128(smem_addr(ring) + G::kTileBytes, kKT * 128);
-        auto load = [&](int it) {            // tile it into its stage
+        warp_wait(&fin[group], 0, p.err);
+    } else if (warp == kSoftmaxWarps + 2) {
+        // ---- copies
+        int lt = t0, lu = u0, it = 0;
+        for (; it < n; it++) {
+            if (it >= NS && !warp_wait(&empty[it % NS], (uint32_t)((it / NS - 1) & 1), p.err)) break;
             uint8_t* st = ring + (it % NS) * 2 * G::kTileBytes;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[it % NS], 2 * G::kTileBytes);
 #pragma unroll
-                for (int c = 0; c < G::kSlabs; c++) tma_3d_g2s(st + c * kKT * 128, &mk, c * 64, g, (t0 + it) * kKT, &full[it % NS]);
+                for (int c = 0; c < G::kSlabs; c++) tma_3d_g2s(st + c * kKT * 128, &mk, c * 64, lu / mt, lt * kKT, &full[it % NS]);
 #pragma unroll
                 for (int c = 0; c < G::kSlabs; c++)
-                    tma_3d_g2s(st + G::kTileBytes + c * kKT * 128, &mv, c * 64, g, (t0 + it) * kKT, &full[it % NS]);
+                    tma_3d_g2s(st + G::kTileBytes + c * kKT * 128, &mv, c * 64, lu / mt, lt * kKT, &full[it % NS]);
             }
             __syncwarp();
-        };
-        int loaded = 0;
-        for (; loaded < min(n, NS); loaded++) load(loaded);
-        for (int it = 0; it < n; it++) {
-            // tile it - 1's stage is free when its P V is done, while the softmax of tile it runs
-            if (it > 0 && loaded < n) {
-                if (!warp_wait(&empty[(it - 1) % NS], (uint32_t)(((it - 1) / NS) & 1), p.err)) break;
-                load(loaded++);
-            }
-            if (!warp_wait(&pfull[it & 1], (uint32_t)((it >> 1) & 1), p.err)) break;
-            tm_fence_after();
-            const uint64_t v = dv + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
-            const uint32_t pa = tmem + (uint32_t)((it & 1) * 64);
-            if (elect_one()) {
-#pragma unroll
-                for (int part = 0; part < (SPLITP ? 2 : 1); part++)
-#pragma unroll
-                    for (int kk = 0; kk < kKT / 16; kk++)
-                        mma_ts(to, pa + part * 32 + kk * 8, v + (kk * 16 * 128 >> 4), io, it > 0 || part + kk > 0);
-                mma_commit(&pvdone[it & 1]);
-                mma_commit(&empty[it % NS]);
-            }
-            __syncwarp();
+            if (++lt == ntiles) lt = 0, lu++;
         }
-        if (elect_one()) mma_commit(fin);
-        __syncwarp();
-        warp_wait(fin, 0, p.err);
         // every copy has landed before the block can end (at once, unless a wait gave up)
-        for (int k = loaded - 1; k >= 0 && k >= loaded - NS; k--) warp_wait(&full[k % NS], (uint32_t)((k / NS) & 1), p.err);
+        for (int k = it - 1; k >= 0 && k >= it - NS; k--) warp_wait(&full[k % NS], (uint32_t)((k / NS) & 1), p.err);
     } else {
-        // ---- Q into tensor memory, this thread's row, or into shared memory,
-        // swizzled as the descriptors say
-        if constexpr (G::kQInTmem) {
-            const int r = m0 + warp * 32 + lane;
-            const long long at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
-            const uint32_t tq = tmem + ((uint32_t)(warp * 32) << 16) + 192;
+        // ---- softmax
+        const int group = warp >> 2, lrow = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, to = tmem + lanes + G::kO + group * HDP;
+        float M = 0.f, l = 0.f;              // M: the reference less kHead
+        // after a wait that gave up the warp goes on without waiting, to no result
+        bool ok = true;
+        for (int begin = 0, tile0 = t0, unit = u0; begin < n; tile0 = 0, unit++) {
+            // ---- a unit's tiles, `begin` to `end` of the block's: first this group's half of the
+            // row's Q into tensor memory, once the last scores of the unit before are there
+            const int end = min(n, begin + ntiles - tile0), r = unit % mt * 128 + lrow, g = unit / mt;
+            if (begin > 0) ok = ok && warp_wait(&sfull[(begin - 1) % kScores], (uint32_t)(((begin - 1) / kScores) & 1), p.err);
+            tm_fence_after();
+            const long long q_at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < HDP / 64; h++) {
+                const int c0 = group * (HDP / 2) + h * 32;             // 32 columns from here
                 uint32_t hi[16], lo[SPLITQ ? 16 : 1];
 #pragma unroll
                 for (int c = 0; c < 4; c++) {
                     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    if (r < a.rows && h * 32 + c * 8 < p.hd) load_q8(a, at + h * 32 + c * 8, x);
+                    if (r < a.rows && c0 + c * 8 < p.hd) load_q8(a, q_at + c0 + c * 8, x);
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
                         hi[4 * c + k] = pack_hi(x[2 * k], x[2 * k + 1]);
                         if (SPLITQ) lo[SPLITQ ? 4 * c + k : 0] = pack_lo(x[2 * k], x[2 * k + 1], hi[4 * c + k]);
                     }
                 }
-                tm_st16(tq + h * 16, hi);
-                if (SPLITQ) tm_st16(tq + 32 + h * 16, lo);
+                tm_st16(tmem + lanes + G::kQ + c0 / 2, hi);
+                if (SPLITQ) tm_st16(tmem + lanes + G::kQ + HDP / 2 + c0 / 2, lo);
             }
-            tm_wait_st();
-            tm_fence_before();
-        }
-        for (int i = threadIdx.x; !G::kQInTmem && i < 128 * (HDP / 8); i += 128) {
-            const int r = i / (HDP / 8), c = i % (HDP / 8);
-            float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            if (m0 + r < a.rows && c * 8 < p.hd) load_q8(a, q_offset(a, p.hd, g, m0 + r) + c * 8, x);
-            const uint4 hi = make_uint4(pack_hi(x[0], x[1]), pack_hi(x[2], x[3]), pack_hi(x[4], x[5]), pack_hi(x[6], x[7]));
-            uint8_t* at = qs + (c / 8) * 128 * 128 + r * 128 + (((c % 8) ^ (r & 7)) << 4);
-            *reinterpret_cast<uint4*>(at) = hi;
-            if (SPLITQ)
-                *reinterpret_cast<uint4*>(at + G::kQBytes) = make_uint4(pack_lo(x[0], x[1], hi.x), pack_lo(x[2], x[3], hi.y),
-                                                                         pack_lo(x[4], x[5], hi.z), pack_lo(x[6], x[7], hi.w));
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(qfull);
-        // ---- softmax of row m0 + 32 warp + lane
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        float M = 0.f, l = 0.f;              // M: the reference less kHead
-        bool ok = true;
-        for (int it = 0; it < n; it++) {
-            const uint32_t sb = tmem + lanes + (uint32_t)((it & 1) * 64);
-            if (!(ok = warp_wait(&sfull[it & 1], (uint32_t)((it >> 1) & 1), p.err))) break;
-            tm_fence_after();
-            uint32_t s[64];
-            tm_ld32(sb, s);
-            tm_ld32(sb + 32, s + 32);
-            tm_wait_ld();
-            const int valid = p.prefix_len - (t0 + it) * kKT;
-            if (valid < kKT) {
-#pragma unroll
-                for (int c = 0; c < 64; c++)
-                    if (c >= valid) s[c] = 0xFF800000u;           // -infinity
-            }
-            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};      // four chains side by side
-#pragma unroll
-            for (int c = 0; c < 64; c++) mx4[c & 3] = fmaxf(mx4[c & 3], __uint_as_float(s[c]));
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            const float top = fmaxf(mx * a.sc, -1e30f) - kHead;
-            if (it == 0) {
-                M = top;
-            } else if (__any_sync(0xffffffffu, top > M + kLag)) {
-                float c = 1.f;
-                if (top > M + kLag) {
-                    c = exp2_fast(M - top);
-                    M = top;
-                }
-                l *= c;
-                if (!(ok = warp_wait(&pvdone[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1), p.err))) break;
-                tm_fence_after();
-#pragma unroll
-                for (int h = 0; h < HDP; h += 32) {
-                    uint32_t o[32];
-                    tm_ld32(to + lanes + h, o);
-                    tm_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
-                    tm_st32(to + lanes + h, o);
-                }
-            }
-            float l0 = 0.f, l1 = 0.f;
-#pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-                uint32_t hi[16], lo[SPLITP ? 16 : 1];
-#pragma unroll
-                for (int c = 0; c < 16; c++) {
-                    const float x = exp2_fast(fmaf(__uint_as_float(s[2 * (h + c)]), a.sc, -M));
-                    const float y = exp2_fast(fmaf(__uint_as_float(s[2 * (h + c) + 1]), a.sc, -M));
-                    l0 += x;
-                    l1 += y;
-                    hi[c] = pack_hi(x, y);
-                    if (SPLITP) lo[SPLITP ? c : 0] = pack_lo(x, y, hi[c]);
-                }
-                tm_st16(sb + h, hi);
-                if (SPLITP) tm_st16(sb + 32 + h, lo);
-            }
-            l += l0 + l1;
             tm_wait_st();
             tm_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[it & 1]);
-        }
-        if (ok) ok = warp_wait(fin, 0, p.err);
-        tm_fence_after();
-        if (ok) {
-            const int r = m0 + warp * 32 + lane;
-            const long long at = ((long long)sp * p.n_kv + g) * a.rows + r;
+            if (lane == 0) mbar_arrive(qfull);
+            const int first = begin + ((begin ^ group) & 1);           // the group's first tile of the unit
+            for (int it = first; it < end; it += 2) {
+                const uint32_t sb = tmem + lanes + (uint32_t)((it % kScores) * 64);
+                const int left = p.prefix_len - (tile0 + it - begin) * kKT;      // keys from this tile on
+                ok = ok && warp_wait(&sfull[it % kScores], (uint32_t)((it / kScores) & 1), p.err);
+                tm_fence_after();
+                // 32 scores, keys behind the prefix at -infinity
+                auto scores = [&](int h, uint32_t (&s)[32]) {
+                    tm_ld32(sb + h * 32, s);
+                    tm_wait_ld();
+                    if (left < h * 32 + 32) {
 #pragma unroll
-            for (int h = 0; h < HDP; h += 32) {
-                uint32_t o[32];
-                tm_ld32(to + lanes + h, o);
+                        for (int c = 0; c < 32; c++)
+                            if (h * 32 + c >= left) s[c] = 0xFF800000u;
+                    }
+                };
+                auto largest = [&](const uint32_t (&s)[32]) {
+                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};       // four chains side by side
+#pragma unroll
+                    for (int c = 0; c < 32; c++) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(s[c]));
+                    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+                };
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                auto probabilities = [&](int h, const uint32_t (&s)[32]) {
+                    uint32_t hi[16], lo[SPLITP ? 16 : 1];
+                    const float2 sc2 = make_float2(a.sc, a.sc), m2 = make_float2(-M, -M);
+#pragma unroll
+                    for (int c = 0; c < 16; c++) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, m2);
+                        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                        l2[c & 1] = __fadd2_rn(l2[c & 1], e);
+                        hi[c] = pack_hi(e.x, e.y);
+                        if (SPLITP) lo[SPLITP ? c : 0] = pack_lo(e.x, e.y, hi[c]);
+                    }
+                    tm_st16(sb + h * 32, hi);
+                    if (SPLITP) tm_st16(sb + h * 32 + 16, lo);
+                };
+                uint32_t s[32];
+                scores(0, s);
+                float mx = largest(s);
+                scores(1, s);
+                mx = fmaxf(mx, largest(s));
+                const float top = fmaxf(mx * a.sc, -1e30f) - kHead;
+                if (it == first) {
+                    M = top;
+                    l = 0.f;
+                } else if (__any_sync(0xffffffffu, top > M + kLag)) {
+                    float c = 1.f;
+                    if (top > M + kLag) {
+                        c = exp2_fast(M - top);
+                        M = top;
+                    }
+                    l *= c;
+                    ok = ok && warp_wait(&pvdone[(it - 2) % kScores], (uint32_t)(((it - 2) / kScores) & 1), p.err);
+                    tm_fence_after();
+#pragma unroll 1
+                    for (int h = 0; h < HDP; h += 16) {
+                        uint32_t o[16];
+                        tm_ld16(to + h, o);
+                        tm_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 16; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * c);
+                        tm_st16(to + h, o);
+                    }
+                }
+                // the exponentials of the block's tiles take turns (a warp of each group shares a
+                // scheduler's one exponential unit): left alone both groups ran them at the same time
+                // and waited for the rest at the same time, 700 cycles a tile
+                if (it > 0) asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3) + 4 * group) : "memory");
+                probabilities(1, s);
+                scores(0, s);                // read a second time: 64 scores at once would not leave the registers
+                probabilities(0, s);
+                if (it + 1 < n) asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 3) + 4 * (group ^ 1)) : "memory");
+                l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+                tm_wait_st();
+                tm_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[it % kScores]);
+            }
+            // ---- this group's part of the unit; without a tile of its own an empty one
+            const int last = end - 1 - ((end - 1 - first) & 1);
+            const bool any = first < end;
+            if (any) ok = ok && warp_wait(&pvdone[last % kScores], (uint32_t)((last / kScores) & 1), p.err);
+            tm_fence_after();
+            const long long at = (((long long)unit + blockIdx.x) * 2 + group) * 128 + lrow;
+#pragma unroll 1
+            for (int h = 0; h < HDP; h += 16) {
+                uint32_t o[16];
+                tm_ld16(to + h, o);
                 tm_wait_ld();
                 if (r < a.rows)
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
+                    for (int k = 0; k < 16; k += 4)
                         if (h + k < p.hd)
-                            *reinterpret_cast<uint4*>(a.prefix_o + at * p.hd + h + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                            *reinterpret_cast<uint4*>(a.prefix_o + at * p.hd + h + k) =
+                                any ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
             }
-            if (r < a.rows) a.prefix_ml[at] = make_float2(M, l);
+            if (r < a.rows) a.prefix_ml[at] = any ? make_float2(M, l) : make_float2(-1e30f, 0.f);
+            // O has been read before the next unit's first P V, which waits for these warps' probabilities
+            tm_fence_before();
+            begin = end;
         }
     }
     tm_fence_before();
     __syncthreads();
-    if (warp == 4)
+    if (warp == kSoftmaxWarps)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(G::kTmemCols));
 }
 
 // ------------------------------------------------------------- suffix --
-// A unit of work is up to 8 NT query rows (row tile j % rt of kv head j / rt, j
-// < units of a sequence) of one sequence against its pages, cut into pieces of
-// 16 cached rows.  The pieces of all units, in order, are dealt out evenly:
-// worker w (one warp) takes pieces [w T / W, (w + 1) T / W) of the T, whatever
-// units they belong to, so ragged lengths leave no warp waiting.  A worker
-// leaves one part per unit that it touches, in slot unit + worker (each step of
-// the walk raises one or both, so no two parts share a slot).
+// A unit is up to 8 NT query rows (row tile j % rt of kv head j / rt, j < units of
+// a sequence) of one sequence against its pages, a piece 16 of its cached rows, a
+// worker one warp: ragged lengths leave no warp waiting.
 constexpr int kSuffixWarps = 4, kMaxSeqs = 4096;
 constexpr int kQuantum = 2;                  // pieces that are worth a worker of their own
 
@@ -822,55 +831,72 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
     const int len = p.lens[s];
     if (len - p.n_new + i < 0) return;                         // padding
     if (lane == 0 && len > clipped_len(p, s)) flag(p.err, LLM_PAGES_BAD_LEN);
-    const int np = a.prefix_splits, srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
-    int parts = 0;
-    long long suf = 0;                                         // row of the first part
+    const int srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
+    int np = 0, ns = 0;                      // the row's parts of the prefix and of its pages
+    long long pre = 0, suf = 0;              // the first ones' rows
+    if (a.prefix_blocks > 0) {
+        const int mt = (a.rows + 127) / 128, ntiles = (p.prefix_len + kKT - 1) / kKT, r = token * a.gq + hq, u = g * mt + r / 128;
+        const long long total = (long long)mt * p.n_kv * ntiles, x = (long long)u * ntiles;
+        const long long w0 = owner_of(x, a.prefix_blocks, total);
+        np = 2 * ((int)(owner_of(x + ntiles - 1, a.prefix_blocks, total) - w0) + 1);       // a part of each softmax group
+        pre = (u + w0) * 256 + r % 128;
+    }
     const int step = min(srows, ru);
     if (a.suffix_workers > 0) {
         const int b = a.starts[s], pieces = a.starts[s + 1] - b;
         const Deal deal = deal_of(a.starts[p.n_seqs], p.n_kv * rt, a.suffix_workers);
         if (pieces > 0) {
-            // pieces x .. y of all belong to this unit; piece x is worker ((x + 1) W - 1) / T's
             const int j = g * rt + row / ru;
-            const long long x = (long long)b * deal.units + (long long)j * pieces, y = x + pieces - 1;
-            const long long w0 = ((x + 1) * deal.workers - 1) / deal.total, w1 = ((y + 1) * deal.workers - 1) / deal.total;
-            parts = (int)(w1 - w0) + 1;
+            const long long x = (long long)b * deal.units + (long long)j * pieces;
+            const long long w0 = owner_of(x, deal.workers, deal.total);
+            ns = (int)(owner_of(x + pieces - 1, deal.workers, deal.total) - w0) + 1;
             suf = ((long long)s * deal.units + j + w0) * step + row % ru;
         }
     }
-    const int n = np + parts;
-    const long long pre = (long long)g * a.rows + (long long)token * a.gq + hq, pre_step = (long long)p.n_kv * a.rows;
-    float M = -INFINITY;
-    for (int k = lane; k < n; k += 32) M = fmaxf(M, k < np ? a.prefix_ml[pre + k * pre_step].x : a.suffix_ml[suf + (long long)(k - np) * step].x);
-    M = warp_max(M);
-    float L = 0.f;
+    const int n = np + ns;
+    auto part = [&](int k) { return k < np ? pre + (long long)k * 128 : suf + (long long)(k - np) * step; };
+    float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        float wk = 0.f;
-        if (k0 + lane < n) {
-            const int k = k0 + lane;
-            const float2 ml = k < np ? a.prefix_ml[pre + k * pre_step] : a.suffix_ml[suf + (long long)(k - np) * step];
-            wk = exp2_fast(ml.x - M);
-            L += wk * ml.y;
+    for (int k0 = 0; k0 < n; k0 += GROUPS * AHEAD) {
+        // the parts' statistics and values are requested together
+        float2 ml[(GROUPS * AHEAD + 31) / 32];
+        float4 v[AHEAD];
+#pragma unroll
+        for (int c = 0; c < (GROUPS * AHEAD + 31) / 32; c++) {
+            const int k = k0 + c * 32 + lane;
+            ml[c] = make_float2(-INFINITY, 0.f);
+            if (k < n && c * 32 + lane < GROUPS * AHEAD) ml[c] = (k < np ? a.prefix_ml : a.suffix_ml)[part(k)];
         }
-        for (int q0 = 0; q0 < min(32, n - k0); q0 += GROUPS * AHEAD) {
-            float4 v[AHEAD];
 #pragma unroll
-            for (int q = 0; q < AHEAD; q++) {
-                const int k = k0 + q0 + q * GROUPS + grp;
-                v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k < n && d < p.hd)
-                    v[q] = *reinterpret_cast<const float4*>((k < np ? a.prefix_o + (pre + k * pre_step) * p.hd
-                                                                    : a.suffix_o + (suf + (long long)(k - np) * step) * p.hd) + d);
-            }
+        for (int q = 0; q < AHEAD; q++) {
+            const int k = k0 + q * GROUPS + grp;
+            v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < n && d < p.hd) v[q] = *reinterpret_cast<const float4*>((k < np ? a.prefix_o : a.suffix_o) + part(k) * p.hd + d);
+        }
+        float top = M;
 #pragma unroll
-            for (int q = 0; q < AHEAD; q++) {
-                const float c = __shfl_sync(0xffffffffu, wk, (q0 + q * GROUPS + grp) & 31);
-                x.x = fmaf(c, v[q].x, x.x);
-                x.y = fmaf(c, v[q].y, x.y);
-                x.z = fmaf(c, v[q].z, x.z);
-                x.w = fmaf(c, v[q].w, x.w);
-            }
+        for (int c = 0; c < (GROUPS * AHEAD + 31) / 32; c++) top = fmaxf(top, ml[c].x);
+        top = warp_max(top);
+        const float c0 = M == -INFINITY ? 0.f : exp2_fast(M - top);
+        M = top;
+        L *= c0;
+        x.x *= c0;
+        x.y *= c0;
+        x.z *= c0;
+        x.w *= c0;
+        float wk[(GROUPS * AHEAD + 31) / 32];
+#pragma unroll
+        for (int c = 0; c < (GROUPS * AHEAD + 31) / 32; c++) {
+            wk[c] = exp2_fast(ml[c].x - M);
+            L += wk[c] * ml[c].y;
+        }
+#pragma unroll
+        for (int q = 0; q < AHEAD; q++) {
+            const float c = __shfl_sync(0xffffffffu, wk[q * GROUPS / 32], (q * GROUPS + grp) & 31);
+            x.x = fmaf(c, v[q].x, x.x);
+            x.y = fmaf(c, v[q].y, x.y);
+            x.z = fmaf(c, v[q].z, x.z);
+            x.w = fmaf(c, v[q].w, x.w);
         }
     }
     L = warp_sum(L);
@@ -892,7 +918,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
 
 // --------------------------------------------------------------- host --
 struct Plan {
-    int prefix_splits, suffix_blocks, mtiles;
+    int prefix_blocks, suffix_blocks;
     long long prefix_rows, suffix_rows;      // parts of one row each
     size_t off_pml, off_so, off_sml, off_starts, bytes;
 };
@@ -901,14 +927,12 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
     Plan pl{};
     const int gq = a->n_heads / p->n_kv_heads;
     const long long srows = (long long)p->n_new * gq, rows = srows * p->n_seqs;
-    pl.mtiles = (int)((rows + 127) / 128);
-    const int slots = prefix_ctas(p->head_dim) * sms;
     if (p->prefix_len > 0) {
-        const long long ntiles = (p->prefix_len + kKT - 1) / kKT, base = (long long)pl.mtiles * p->n_kv_heads;
-        const long long want = std::max<long long>(1, slots / base);
-        pl.prefix_splits = (int)std::max<long long>(1, std::min<long long>(want, ntiles / 2));
+        // a block per SM, but none with less than two tiles
+        const long long units = (rows + 127) / 128 * p->n_kv_heads, tiles = units * ((p->prefix_len + kKT - 1) / kKT);
+        pl.prefix_blocks = (int)std::max<long long>(1, std::min<long long>(sms, tiles / 2));
+        pl.prefix_rows = (units + pl.prefix_blocks) * 256;
     }
-    pl.prefix_rows = (long long)pl.prefix_splits * p->n_kv_heads * rows;
     if (p->max_pages > 0) {
         // workers for as many blocks as an SM holds at once, but no more than the
         // longest sequences could keep busy
@@ -948,13 +972,11 @@ bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long 
 }
 
 template <int HDP, bool SPLITQ, bool SPLITP>
-cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd,
-                          const AttendDev& ad, int mtiles) {
-    using G = PrefixPlan<HDP, SPLITQ>;
+cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad) {
     auto k = prefix_kernel<HDP, SPLITQ, SPLITP>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_dep(k, dim3((unsigned)mtiles * ad.prefix_splits, pd.n_kv), dim3(kPrefixThreads), (size_t)G::kSmem, st, mk, mv, pd, ad);
+    return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
 }
 
 template <int HDP, int NT, bool SPLITQ, bool SPLITP>
@@ -969,6 +991,8 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
     if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the attention arguments are NULL");
     if (a->n_heads < 1 || a->n_heads % p->n_kv_heads)
         return fail_op(LLM_ERR_INVALID_ARG, "n_heads %d is not a multiple of n_kv_heads %d", a->n_heads, p->n_kv_heads);
+    if (((long long)p->max_pages * p->page_size / 16 + 1) > (1ll << 50) / std::max(1ll, (long long)p->n_seqs * p->n_new * a->n_heads))
+        return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold too many rows for that many heads");
     if (p->n_seqs > kMaxSeqs) return fail_op(LLM_ERR_UNSUPPORTED, "n_seqs %d exceeds %d", p->n_seqs, kMaxSeqs);
     if ((long long)p->n_seqs * ((long long)p->max_pages * p->page_size / 16 + 1) > INT_MAX / 2)
         return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold more than 2^34 rows together");
@@ -1024,7 +1048,7 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
     ad.prefix_ml = reinterpret_cast<float2*>(ws + pl.off_pml);
     ad.suffix_o = reinterpret_cast<float*>(ws + pl.off_so);
     ad.suffix_ml = reinterpret_cast<float2*>(ws + pl.off_sml);
-    ad.prefix_splits = pl.prefix_splits;
+    ad.prefix_blocks = pl.prefix_blocks;
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
     const bool sq = !ad.q_f16, so = !ad.out_f16;
@@ -1036,10 +1060,10 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
             !rows_map(&mv, a->prefix_v, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT))
             return fail_op(LLM_ERR_CUDA, "a tensor map of the prefix");
 #define LLM_PREFIX(HDP)                                                                                          \
-    (sq ? (so ? launch_prefix<HDP, true, true>(stream, mk, mv, pd, ad, pl.mtiles)                                 \
-              : launch_prefix<HDP, true, false>(stream, mk, mv, pd, ad, pl.mtiles))                               \
-        : (so ? launch_prefix<HDP, false, true>(stream, mk, mv, pd, ad, pl.mtiles)                                \
-              : launch_prefix<HDP, false, false>(stream, mk, mv, pd, ad, pl.mtiles)))
+    (sq ? (so ? launch_prefix<HDP, true, true>(stream, mk, mv, pd, ad)                                 \
+              : launch_prefix<HDP, true, false>(stream, mk, mv, pd, ad))                               \
+        : (so ? launch_prefix<HDP, false, true>(stream, mk, mv, pd, ad)                                \
+              : launch_prefix<HDP, false, false>(stream, mk, mv, pd, ad)))
         e = hd <= 64 ? LLM_PREFIX(64) : LLM_PREFIX(128);
 #undef LLM_PREFIX
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (prefix)");
