@@ -54,6 +54,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
+// max(a, b, c) in one instruction; a NaN counts as no value.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // Two F32 values as a pair of F16 (low half first), and what is left of them.
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {
     uint32_t r;
@@ -386,7 +393,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                 auto largest = [&](const uint32_t (&s)[32]) {
                     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};       // four chains side by side
 #pragma unroll
-                    for (int c = 0; c < 32; c++) m[c & 3] = fmaxf(m[c & 3], __uint_as_float(s[c]));
+                    for (int c = 0; c < 32; c += 2) m[c / 2 & 3] = max3(m[c / 2 & 3], __uint_as_float(s[c]), __uint_as_float(s[c + 1]));
                     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 };
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -812,7 +819,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
             }
         }
     }
-    if (!first) griddep_wait();              // this grid's end is the prefix kernel's too, for the join
+    // this grid's end is the prefix kernel's too, for the join; only the last block waits for it, so
+    // that the others make room for the next while the prefix kernel runs
+    if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();
 }
 
 // --------------------------------------------------------------- join --
@@ -971,10 +980,17 @@ bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Percent of an SM's memory as shared memory for the prefix kernel and a suffix
+// kernel that runs beside it: an SM that holds a block of one takes none of the
+// other under another division.  (A suffix kernel alone wants the cache: 268 MB of
+// pages 56 us, 46 us with the default.)
+constexpr int kCarveout = 72;
+
 template <int HDP, bool SPLITQ, bool SPLITP>
 cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad) {
     auto k = prefix_kernel<HDP, SPLITQ, SPLITP>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
     if (e != cudaSuccess) return e;
     return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
 }
@@ -983,7 +999,11 @@ template <int HDP, int NT, bool SPLITQ, bool SPLITP>
 cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
     // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
     static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
-    return launch_dep(suffix_kernel<HDP, NT, SPLITQ, SPLITP>, dim3((unsigned)blocks), dim3(32 * kSuffixWarps),
+    auto k = suffix_kernel<HDP, NT, SPLITQ, SPLITP>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                               first ? (int)cudaSharedmemCarveoutDefault : kCarveout);
+    if (e != cudaSuccess) return e;
+    return launch_dep(k, dim3((unsigned)blocks), dim3(32 * kSuffixWarps),
                       (size_t)(2 * pd.n_seqs + 1) * 4, st, pd, ad, first);
 }
 
