@@ -414,7 +414,7 @@ typedef struct {
     int64_t q_stride, k_stride, v_stride;
     void *q_out;
     int64_t q_out_stride;
-    const float *cos_sin;                    /* 8-byte aligned */
+    const float *cos_sin;                    /* 16-byte aligned */
 } llm_append;
 
 /* Rotates the new rows' q and k (each product and sum rounded once in F32, as

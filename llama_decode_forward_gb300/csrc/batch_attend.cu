@@ -54,13 +54,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// max(a, b, c) in one instruction; a NaN counts as no value.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float y;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
-    return y;
-}
-
 // Two F32 values as a pair of F16 (low half first), and what is left of them.
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {
     uint32_t r;

@@ -13,9 +13,22 @@ namespace llm {
 namespace {
 
 // ------------------------------------------------------------- append --
+// Division of numbers below 2^31 by a fixed one: with 2^s >= d and m = floor(2^32
+// (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
+struct Div {
+    uint32_t d, m, s;
+    explicit Div(uint32_t by = 1) : d(by), s(0) {
+        while ((1ull << s) < by) s++;
+        m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s); }
+};
+
 struct AppendDev {
     int n_heads, half, neox, table_rows;
-    int row_blocks;                          // blocks of one row
+    int group;                               // elements of an item's two groups
+    int q_blocks, row_blocks;                // blocks of a row's q, and of all of it
+    Div by_row_blocks, by_head, by_new;      // divisions by row_blocks, a head's items and n_new
     const void *q, *k, *v;
     long long q_stride, k_stride, v_stride;
     void* q_out;
@@ -23,22 +36,39 @@ struct AppendDev {
     const float2* cs;
 };
 
-// Four consecutive elements, as F32.
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+// N (4 or 8) consecutive elements, as F32.
+template <int N>
+__device__ __forceinline__ void load_n(const float* p, float (&x)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(p + k);
+        x[k] = v.x; x[k + 1] = v.y; x[k + 2] = v.z; x[k + 3] = v.w;
+    }
 }
-__device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+template <int N>
+__device__ __forceinline__ void load_n(const __half* p, float (&x)[N]) {
+    uint32_t w[N / 2];
+    if (N == 8) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
+    else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+    for (int k = 0; k < N / 2; k++) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+    }
 }
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+template <int N>
+__device__ __forceinline__ void store_n(float* p, const float (&x)[N]) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) *reinterpret_cast<float4*>(p + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
 }
-__device__ __forceinline__ void store4(__half* p, const float (&x)[4]) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(h2_bits(__float2half_rn(x[0]), __float2half_rn(x[1])),
-                                              h2_bits(__float2half_rn(x[2]), __float2half_rn(x[3])));
+template <int N>
+__device__ __forceinline__ void store_n(__half* p, const float (&x)[N]) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; k++) w[k] = h2_bits(__float2half_rn(x[2 * k]), __float2half_rn(x[2 * k + 1]));
+    if (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
+    else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
 }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(__half* p, float x) { *p = __float2half_rn(x); }
@@ -51,44 +81,50 @@ __device__ __forceinline__ void turn(float& x0, float& x1, float2 r) {
     x1 = __fadd_rn(__fmul_rn(a, r.y), __fmul_rn(b, r.x));
 }
 
-// The two groups of four elements of a head that item i (of hd / 8) handles:
-// NEOX pairs join element j of the first half with element j of the second, so
-// an item takes four of each; otherwise, and behind the rotated elements, eight
-// in a row.
-struct Fours {
+// The two groups of N elements of a head that item i handles: NEOX pairs join
+// element j of the first half with element j of the second, so an item takes N of
+// each; otherwise, and behind the rotated elements, 2 N in a row.
+struct Groups {
     int a, b, j;                             // first elements; first pair, or -1: not rotated
 };
-__device__ __forceinline__ Fours fours(int i, int half, int neox) {
-    if (8 * i >= 2 * half) return {8 * i, 8 * i + 4, -1};
-    return neox ? Fours{4 * i, half + 4 * i, 4 * i} : Fours{8 * i, 8 * i + 4, 4 * i};
+template <int N>
+__device__ __forceinline__ Groups groups_of(int i, int half, int neox) {
+    if (2 * N * i >= 2 * half) return {2 * N * i, 2 * N * i + N, -1};
+    return neox ? Groups{N * i, half + N * i, N * i} : Groups{2 * N * i, 2 * N * i + N, N * i};
 }
 
-// One thread per eight elements of a head of q, k or v; a row's blocks are
-// whole, so its sequence, place and angles are the block's.  The elements are
-// loaded before the row's place is known: the chain length -> page -> store
-// runs beside that load.  VEC: rope_dims / 2 is a multiple of four, so items
-// are two groups of four; otherwise the pairs are taken one at a time.  Bound
-// by the stream of rows.
+// One thread per item of a head of q, k or v; a row has blocks of its own for q and
+// for k and v, so its sequence, place and angles are the block's.  The elements are
+// loaded before the row's place is known: the chain length -> page -> store runs
+// beside that load.  N: elements of an item's two groups, 8 where head_dim and
+// rope_dims are multiples of 16, else 4 where rope_dims is one of 8, else 0: eight
+// elements taken pair by pair.  Bound by the stream of rows, and close behind it by
+// instructions: 8000 rows of 4 KB (F16) took 27 us with groups of four and
+// divisions by sizes, 26 us without those.
 constexpr int kAppendThreads = 128;
-template <class T, class U, bool VEC>
+constexpr int append_item(int n) { return n ? 2 * n : 8; }
+template <class T, class U, int N>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ PagesDev p,
                                                                 const __grid_constant__ AppendDev a) {
     griddep_entry();
-    const int row = (int)(blockIdx.x / (unsigned)a.row_blocks), per_head = p.hd / 8;
-    const int item = (int)(blockIdx.x % (unsigned)a.row_blocks) * kAppendThreads + (int)threadIdx.x;
-    const int h = item / per_head, i = item % per_head;
-    if (h >= a.n_heads + 2 * p.n_kv) return;
-    const bool is_q = h < a.n_heads, is_v = h >= a.n_heads + p.n_kv;
-    const int g = is_q ? h : is_v ? h - a.n_heads - p.n_kv : h - a.n_heads, half = is_v ? 0 : a.half;
-    const T* x = static_cast<const T*>(is_q ? a.q : is_v ? a.v : a.k) +
-                 row * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + (long long)g * p.hd;
-    const Fours f = fours(i, half, a.neox);
-    float u[4], w[4];
-    if (VEC) {
-        load4(x + f.a, u);
-        load4(x + f.b, w);
+    const int row = a.by_row_blocks.of(blockIdx.x), block = blockIdx.x - row * a.row_blocks, per_head = p.hd / append_item(N);
+    const bool is_q = block < a.q_blocks;
+    const int item = (is_q ? block : block - a.q_blocks) * kAppendThreads + (int)threadIdx.x;
+    const int h = a.by_head.of(item), i = item - h * per_head;
+    if (h >= (is_q ? a.n_heads : 2 * p.n_kv)) return;
+    const bool is_v = !is_q && h >= p.n_kv;
+    const int g = is_v ? h - p.n_kv : h, half = is_v ? 0 : a.half;
+    const T* x = is_q ? static_cast<const T*>(a.q) + row * a.q_stride
+                      : is_v ? static_cast<const T*>(a.v) + row * a.v_stride : static_cast<const T*>(a.k) + row * a.k_stride;
+    x += g * p.hd;
+    constexpr int W = N ? N : 4;
+    const Groups f = groups_of<W>(i, half, a.neox);
+    float u[W], w[W];
+    if (N) {
+        load_n<W>(x + f.a, u);
+        load_n<W>(x + f.b, w);
     }
-    const int s = row / p.n_new, e = p.lens[s] - p.n_new + row % p.n_new;
+    const int s = a.by_new.of(row), e = p.lens[s] - p.n_new + (row - s * p.n_new);
     if (e < 0) return;                       // padding
     const long long pos = (long long)p.prefix_len + e;
     if (pos >= a.table_rows) {
@@ -105,27 +141,28 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         yk = (is_v ? p.v : p.k) + (slot * p.n_kv + g) * p.hd;
     }
     const float2* cs = a.cs + pos * a.half;
-    if (VEC) {
+    if (N) {
         if (f.j >= 0) {
-            float2 r[4];
+            float2 r[W];                     // W pairs: two to a 16-byte load (rows of the table are multiples of 32 bytes)
 #pragma unroll
-            for (int k = 0; k < 4; k++) r[k] = __ldg(cs + f.j + k);
-            if (a.neox) {
+            for (int k = 0; k < W; k += 2) {
+                const float4 v = __ldg(reinterpret_cast<const float4*>(cs + f.j + k));
+                r[k] = make_float2(v.x, v.y);
+                r[k + 1] = make_float2(v.z, v.w);
+            }
 #pragma unroll
-                for (int k = 0; k < 4; k++) turn(u[k], w[k], r[k]);
-            } else {
-                turn(u[0], u[1], r[0]);
-                turn(u[2], u[3], r[1]);
-                turn(w[0], w[1], r[2]);
-                turn(w[2], w[3], r[3]);
+            for (int k = 0; k < W; k++) {
+                if (a.neox) turn(u[k], w[k], r[k]);
+                else if (k < W / 2) turn(u[(2 * k) % W], u[(2 * k) % W + 1], r[k]);
+                else turn(w[(2 * k) % W], w[(2 * k) % W + 1], r[k]);
             }
         }
         if (is_q) {
-            store4(yq + f.a, u);
-            store4(yq + f.b, w);
+            store_n<W>(yq + f.a, u);
+            store_n<W>(yq + f.b, w);
         } else {
-            store4(yk + f.a, u);
-            store4(yk + f.b, w);
+            store_n<W>(yk + f.a, u);
+            store_n<W>(yk + f.b, w);
         }
     } else {
         for (int k = 0; k < 4; k++) {
@@ -146,24 +183,26 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
 
 template <class T, class U>
 cudaError_t launch_append(cudaStream_t st, const PagesDev& pd, const AppendDev& ad, long long rows) {
-    auto k = ad.half % 4 == 0 ? append_kernel<T, U, true> : append_kernel<T, U, false>;
+    auto k = ad.group == 8 ? append_kernel<T, U, 8> : ad.group == 4 ? append_kernel<T, U, 4> : append_kernel<T, U, 0>;
     return launch_dep(k, dim3((unsigned)(rows * ad.row_blocks)), dim3(kAppendThreads), 0, st, pd, ad);
 }
 
 // --------------------------------------------------- log probabilities --
 // One pass over a row: every thread keeps the running maximum m of its logits,
 // s = sum e^(x - m) and t = sum e^(x - m) (x - m) (from which the entropy is
-// ln s - t / s), every warp the `top` largest keys it has met (lane i the
-// i-th).  A row is shared by a cluster of 1 to 16 blocks, so that few rows
-// still occupy every SM; the blocks' results meet in the first one's shared
-// memory.  Bound by the stream of logits.
+// ln s - t / s), every warp the keys that may be among the row's `top` largest.
+// A row is shared by a cluster of 1 to 16 blocks, so that few rows still occupy
+// every SM; the blocks' results meet in the first one's shared memory.  Bound by
+// the stream of logits; for one row by the chain of its steps.
 //
-// A key (argmax_key) orders by value, then by the lower index.  A warp looks
-// at its logits one by one only when one of them reaches the floor: a key that
-// at least `top` keys of the row are known to reach (the warp's own last key,
-// or another warp's, through shared memory).  In its first block of logits, when
-// no list is filled yet, the floor is the top-th of the 32 lanes' best keys.
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32, kLpElems = 16;   // elements of a lane per block
+// A key (argmax_key) orders by value, then by the lower index.  A warp looks at
+// its logits one by one only when one of them reaches the floor: a key that at
+// least `top` keys of the row are known to reach.  For a warp's first logits that
+// is the top-th largest of its lanes' largest; later its own top-th key, or another
+// warp's, through shared memory.  Keys that reach it wait in shared memory; 32 of
+// them are sorted into the warp's list (lane i the i-th) at a time.  At the end the
+// few keys of a block that reach its floor are ranked by counting the larger ones.
+constexpr int kLpElems = 16;                 // logits of a lane per step
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct LpStat {
@@ -180,35 +219,49 @@ __device__ __forceinline__ LpStat lp_join(LpStat a, LpStat b) {
     r.t = (ca == 0.f ? 0.f : ca * (a.t + a.s * da)) + (cb == 0.f ? 0.f : cb * (b.t + b.s * db));
     return r;
 }
+template <int FROM>
+__device__ __forceinline__ LpStat lp_join_warp(LpStat st) {
+#pragma unroll
+    for (int o = FROM; o > 0; o >>= 1)
+        st = lp_join(st, LpStat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
+                                __shfl_xor_sync(0xffffffffu, st.t, o)});
+    return st;
+}
 
 typedef unsigned long long u64;
 
-// Lane i's key of two descending lists' merge, the 32 largest.
-__device__ __forceinline__ u64 merge32(u64 a, u64 b, int lane) {
-    u64 k = max(a, __shfl_xor_sync(0xffffffffu, b, 31));       // b reversed: a bitonic sequence of the 32 largest
+// Lane i's value of two descending lists' merge, the 32 largest.
+template <class K>
+__device__ __forceinline__ K merge32(K a, K b, int lane) {
+    K k = max(a, __shfl_xor_sync(0xffffffffu, b, 31));         // b reversed: a bitonic sequence of the 32 largest
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const u64 o = __shfl_xor_sync(0xffffffffu, k, d);
+        const K o = __shfl_xor_sync(0xffffffffu, k, d);
         k = (lane & d) ? min(k, o) : max(k, o);
     }
     return k;
 }
-__device__ __forceinline__ u64 sort32(u64 k, int lane) {
+// The lanes' values in descending order.
+template <class K>
+__device__ __forceinline__ K sort32(K k, int lane) {
 #pragma unroll
     for (int n = 2; n <= 32; n <<= 1)
 #pragma unroll
         for (int d = n >> 1; d > 0; d >>= 1) {
-            const u64 o = __shfl_xor_sync(0xffffffffu, k, d);
+            const K o = __shfl_xor_sync(0xffffffffu, k, d);
             const bool up = (lane & n) != 0;                   // ascending halves build the bitonic sequences
             k = (((lane & d) != 0) == up) ? max(k, o) : min(k, o);
         }
     return k;
 }
 
-// The value a key stands for (0: below everything).
-__device__ __forceinline__ float key_value(u64 k) {
-    const uint32_t o = (uint32_t)(k >> 32);
-    return k == 0 ? -INFINITY : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+// The upper half of a value's key, and the value of an upper half (0: below everything).
+__device__ __forceinline__ uint32_t order_of(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return v != v ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return o == 0 ? -INFINITY : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -241,36 +294,75 @@ __device__ __forceinline__ u64 peer_u64(uint32_t a) {
     return v;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_constant__ llm_logprobs_args a) {
-    constexpr int VE = 16 / sizeof(T), NV = kLpElems / VE;     // elements of a 16-byte load, loads of a lane per block
-    const uint32_t rank = cluster_rank(), blocks = cluster_size();
-    const long long r = blockIdx.x / blocks;
+// How many of the first n keys of `list` are larger than key.
+__device__ __forceinline__ int rank_of(u64 key, const u64* list, int n) {
+    int c = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; i++) c += list[i] > key;
+    return c;
+}
+
+// NT threads a block: 512 for few rows (the shortest chain), 128 for many (a warp
+// then sees more of its row, and finds the floor sooner; 512 rows of 151,936: 114 us
+// with 512 threads a block).
+template <class T, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_constant__ llm_logprobs_args a) {
+    constexpr int VE = 16 / sizeof(T), NV = kLpElems / VE;     // elements of a 16-byte load, loads of a lane per step
+    constexpr int NW = NT / 32;
+    const int rank = (int)cluster_rank(), blocks = (int)cluster_size();
+    const long long r = blockIdx.x / (unsigned)blocks;
     const T* x = static_cast<const T*>(a.logits) + r * a.stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, top = a.top;
-    __shared__ LpStat stat[kLpWarps];
-    __shared__ u64 list[kLpWarps][32];
+    __shared__ LpStat stat[NW];
+    __shared__ u64 wait[NW][64];             // keys that reached the floor and are not in the warp's list yet
+    __shared__ u64 list[NW * 96], best[32];  // the block's keys that reach its floor; its largest in order
     __shared__ u64 floor_all;
-    if (threadIdx.x == 0) floor_all = 0;
+    __shared__ int count;
+    if (threadIdx.x == 0) {
+        floor_all = 0;
+        count = 0;
+    }
+    if (threadIdx.x < 32) best[threadIdx.x] = 0;
     __syncthreads();
     griddep_entry();
     // 16-byte words of the row, from the aligned one that holds its first element
     const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
     const uint4* words = reinterpret_cast<const uint4*>(x - lead);
-    const long long n_words = ((long long)lead + a.vocab + VE - 1) / VE;
-    const long long w0 = n_words * rank / blocks, w1 = n_words * (rank + 1) / blocks;
+    const int n_words = (lead + a.vocab + VE - 1) / VE;
+    constexpr int STEP = 32 * NV;            // words of a warp's step; a block's words are whole steps
+    const int steps = (n_words + STEP - 1) / STEP;
+    const int w0 = (int)((long long)steps * rank / blocks) * STEP, w1 = min(n_words, (int)((long long)steps * (rank + 1) / blocks) * STEP);
+    uint4 raw[NV];
+    // a step that lies within the row and this block's words is plain loads; in the others, at the
+    // ends, each word and its elements are looked at
+    auto whole = [&](int b) { return b * VE >= lead && (b + STEP) * VE - lead <= a.vocab && b + STEP <= w1; };
+    auto fetch = [&](int b) {
+#pragma unroll
+        for (int k = 0; k < NV; k++) raw[k] = __ldcs(words + b + k * 32 + lane);
+    };
     LpStat st{-INFINITY, 0.f, 0.f};
     u64 keys = 0, floor = 0;
-    bool first = true;
-    for (long long b = w0 + (long long)warp * 32 * NV; b < w1; b += (long long)kLpWarps * 32 * NV) {
+    int waiting = 0;
+    float floor_v = -INFINITY;
+    auto raise = [&](u64 f) {
+        floor = max(floor, f);
+        floor_v = value_of((uint32_t)(floor >> 32));
+    };
+    auto sort_in = [&](u64 k) {              // 32 keys into the warp's list
+        keys = merge32(keys, sort32(k, lane), lane);
+        const u64 last = __shfl_sync(0xffffffffu, keys, top - 1);
+        if (last > floor && lane == 0) atomicMax(&floor_all, last);
+        raise(last);
+    };
+    const int first = w0 + warp * STEP;
+    if (first < w1 && whole(first)) fetch(first);
+    for (int b = first; b < w1; b += NW * STEP) {
         float v[kLpElems];
-        bool inside = true;                                    // every element of this lane is one of the row's
+        const bool inside = whole(b);
+        if (inside) {
 #pragma unroll
-        for (int k = 0; k < NV; k++) {
-            const long long w = b + k * 32 + lane, e = w * VE - lead;
-            if (w < w1 && e >= 0 && e + VE <= a.vocab) {
-                const uint4 u = __ldcs(words + w);
-                const uint32_t us[4] = {u.x, u.y, u.z, u.w};
+            for (int k = 0; k < NV; k++) {
+                const uint32_t us[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     if (sizeof(T) == 4) {
@@ -281,16 +373,20 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
                         v[k * VE + (VE == 8 ? 2 * i + 1 : 0)] = f.y;
                     }
                 }
-            } else {
-                inside = false;
-#pragma unroll
-                for (int i = 0; i < VE; i++)
-                    v[k * VE + i] = w < w1 && e + i >= 0 && e + i < a.vocab ? to_f32(x[e + i]) : -INFINITY;
             }
-        }
-        float bm = v[0];
+        } else {
 #pragma unroll
-        for (int i = 1; i < kLpElems; i++) bm = fmaxf(bm, v[i]);
+            for (int k = 0; k < NV; k++)
+#pragma unroll
+                for (int i = 0; i < VE; i++) {
+                    const int w = b + k * 32 + lane, e = w * VE - lead + i;
+                    v[k * VE + i] = w < w1 && e >= 0 && e < a.vocab ? to_f32(x[e]) : -INFINITY;
+                }
+        }
+        if (b + NW * STEP < w1 && whole(b + NW * STEP)) fetch(b + NW * STEP);
+        float bm = fmaxf(v[0], v[1]);
+#pragma unroll
+        for (int i = 2; i < kLpElems; i += 2) bm = max3(bm, v[i], v[i + 1]);
         if (bm > st.m) {
             const float d = st.m - bm, c = exp2f(d * kLog2e);
             st.t = st.s == 0.f ? 0.f : c * (st.t + st.s * d);
@@ -298,133 +394,174 @@ __global__ void __launch_bounds__(kLpThreads, 2) logprobs_kernel(const __grid_co
             st.m = bm;
         }
         if (st.m > -INFINITY) {
-            // four sums side by side; -infinity - m gives e = 0, whose (x - m) is cut off at a number
-            float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+            // two pairs of sums side by side; -infinity - m gives e = 0, whose (x - m) is cut off at a number
+            float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 m2 = make_float2(-st.m, -st.m), log2e = make_float2(kLog2e, kLog2e);
 #pragma unroll
-            for (int i = 0; i < kLpElems; i++) {
-                const float d = v[i] - st.m;
-                float e;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(d * kLog2e));
-                s[i & 3] += e;
-                t[i & 3] = fmaf(e, fmaxf(d, -1e4f), t[i & 3]);
+            for (int i = 0; i < kLpElems; i += 2) {
+                const float2 d = __fadd2_rn(make_float2(v[i], v[i + 1]), m2), y = __fmul2_rn(d, log2e);
+                float2 e;
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+                s[(i >> 1) & 1] = __fadd2_rn(s[(i >> 1) & 1], e);
+                t[(i >> 1) & 1] = __ffma2_rn(e, make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f)), t[(i >> 1) & 1]);
             }
-            st.s += (s[0] + s[1]) + (s[2] + s[3]);
-            st.t += (t[0] + t[1]) + (t[2] + t[3]);
+            st.s += (s[0].x + s[0].y) + (s[1].x + s[1].y);
+            st.t += (t[0].x + t[0].y) + (t[1].x + t[1].y);
         } else {
 #pragma unroll
             for (int i = 0; i < kLpElems; i++)
                 if (v[i] != v[i]) st.s = NAN;
         }
         if (top == 0) continue;
-        auto key_of = [&](int i) {
-            const long long e = (b + (i / VE) * 32 + lane) * VE - lead + i % VE;
-            const bool there = inside || (b + (i / VE) * 32 + lane < w1 && e >= 0 && e < a.vocab);
-            return there ? argmax_key(v[i] + 0.f, (int)e) : 0ull;          // -0 + 0 = +0: equal values, equal order
-        };
-        if (first) {
-            first = false;
-            u64 best = 0;
+        if (b == first) {
+            // (+ 0: a largest of -0 stands for equal +0s too.)  Many alternatives: of the lanes' two
+            // largest each, or the last lanes' poor ones would let half of the logits through
+            // (a lane without an element of the row has -infinity and counts as none)
+            uint32_t near = sort32(inside || bm > -INFINITY ? order_of(bm + 0.f) : 0u, lane);
+            if (top > 16) {
+                float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kLpElems; i++) best = max(best, key_of(i));
-            const u64 bound = __shfl_sync(0xffffffffu, sort32(best, lane), top - 1);
-            if (bound) floor = max(floor, bound - 1);
+                for (int i = 0; i < kLpElems; i++) {
+                    m2 = fmaxf(m2, fminf(m1, v[i]));
+                    m1 = fmaxf(m1, v[i]);
+                }
+                near = merge32(near, sort32(inside || m2 > -INFINITY ? order_of(m2 + 0.f) : 0u, lane), lane);
+            }
+            const uint32_t bound = __shfl_sync(0xffffffffu, near, top - 1);
+            raise((u64)bound << 32);
+            if (bound && lane == 0) atomicMax(&floor_all, floor);
         }
-        floor = max(floor, *static_cast<volatile u64*>(&floor_all));
-        if (!__any_sync(0xffffffffu, bm >= key_value(floor))) continue;
-        const u64 before = floor;
+        if (!__any_sync(0xffffffffu, bm >= floor_v)) continue;
+        raise(*static_cast<volatile u64*>(&floor_all));       // (only here: the other warps' floor seldom matters sooner)
+        if (!__any_sync(0xffffffffu, bm >= floor_v)) continue;
+        uint32_t mask = 0;
 #pragma unroll
-        for (int i = 0; i < kLpElems; i++) {
-            const u64 key = key_of(i);
-            for (uint32_t who = __ballot_sync(0xffffffffu, key > floor); who; who &= who - 1) {
-                const u64 c = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
-                if (c <= floor) continue;
-                const u64 up = __shfl_up_sync(0xffffffffu, keys, 1);
-                const bool above = keys > c, shift = lane > 0 && !(up > c);
-                keys = above ? keys : shift ? up : c;
-                floor = max(floor, __shfl_sync(0xffffffffu, keys, top - 1));
+        for (int i = 0; i < kLpElems; i++) mask |= v[i] >= floor_v ? 1u << i : 0u;
+        while (__any_sync(0xffffffffu, mask)) {
+            const int i = __ffs(mask) - 1;
+            u64 key = 0;
+            if (mask) {
+                float z = v[0];
+#pragma unroll
+                for (int k = 1; k < kLpElems; k++) z = k == i ? v[k] : z;
+                const int e = (b + (i / VE) * 32 + lane) * VE - lead + i % VE;
+                if (inside || (b + (i / VE) * 32 + lane < w1 && e >= 0 && e < a.vocab))
+                    key = argmax_key(z + 0.f, e);              // -0 + 0 = +0: equal values, equal order
+                mask &= mask - 1;
+            }
+            const bool in = key != 0 && key >= floor;
+            const uint32_t who = __ballot_sync(0xffffffffu, in);
+            if (in) wait[warp][waiting + __popc(who & ((1u << lane) - 1))] = key;
+            waiting += __popc(who);
+            __syncwarp();
+            if (waiting >= 32) {
+                sort_in(wait[warp][lane]);
+                const u64 rest = wait[warp][32 + lane];
+                __syncwarp();
+                wait[warp][lane] = rest;
+                waiting -= 32;
+                __syncwarp();
             }
         }
-        if (floor > before && lane == 0) atomicMax(&floor_all, floor);
     }
-    // the warps' results, then the cluster's
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        st = lp_join(st, LpStat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                                __shfl_xor_sync(0xffffffffu, st.t, o)});
-    if (lane >= top) keys = 0;
+    // many alternatives: the last ones sorted in too, so that the block's floor leaves fewer to rank
+    if (top > 8 && waiting > 0) {
+        sort_in(lane < waiting ? wait[warp][lane] : 0ull);
+        waiting = 0;
+    }
+    st = lp_join_warp<16>(st);
     if (lane == 0) stat[warp] = st;
-    list[warp][lane] = keys;
-    __syncthreads();
-    for (int n = kLpWarps / 2; n > 0 && top > 0; n >>= 1) {
-        if (warp < n) list[warp][lane] = merge32(list[warp][lane], list[warp + n][lane], lane);
+    __syncthreads();                         // the floor is the block's now
+    if (top > 0) {
+        // the keys that reach it, from the lists and the waiting ones
+        const u64 f = floor_all;
+        auto take = [&](u64 key) {
+            const uint32_t who = __ballot_sync(0xffffffffu, key != 0 && key >= f);
+            int at = 0;
+            if (lane == 0 && who) at = atomicAdd(&count, __popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+            if ((who >> lane) & 1u) list[at] = key;
+        };
+        take(keys);
+        take(lane < waiting ? wait[warp][lane] : 0ull);
         __syncthreads();
+        const int n = count;
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const int k = rank_of(list[i], list, n);
+            if (k < top) best[k] = list[i];
+        }
     }
     if (warp == 0) {
-        st = lane < kLpWarps ? stat[lane] : LpStat{-INFINITY, 0.f, 0.f};
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1)
-            st = lp_join(st, LpStat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                                    __shfl_xor_sync(0xffffffffu, st.t, o)});
+        st = lp_join_warp<16>(lane < NW ? stat[lane] : LpStat{-INFINITY, 0.f, 0.f});
         if (lane == 0) stat[0] = st;
     }
+    __syncthreads();
     if (blocks > 1) {
-        __syncwarp();
         cluster_barrier();
         if (rank == 0) {
-            // warp w takes block w's list, lane w of warp 0 its sums
-            u64 k = 0;
-            if (warp < blocks) k = peer_u64(peer(&list[0][lane], warp));
+            // the blocks' sums, and of their largest keys those that reach the largest top-th one
             if (warp == 0) {
                 st = LpStat{-INFINITY, 0.f, 0.f};
+                u64 f = 0;
                 if (lane < blocks) {
                     const uint32_t at = peer(&stat[0], lane);
                     st = LpStat{peer_f32(at), peer_f32(at + 4), peer_f32(at + 8)};
+                    if (top > 0) f = peer_u64(peer(&best[top - 1], lane));
                 }
+                st = lp_join_warp<8>(st);
 #pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    st = lp_join(st, LpStat{__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.s, o),
-                                            __shfl_xor_sync(0xffffffffu, st.t, o)});
+                for (int o = 8; o > 0; o >>= 1) f = max(f, __shfl_xor_sync(0xffffffffu, f, o));
+                if (lane == 0) {
+                    floor_all = f;
+                    count = 0;
+                }
+            }
+            u64 mine[16 * 32 / NT];          // key i of block i / 32
+#pragma unroll
+            for (int c = 0; c < 16 * 32 / NT; c++) {
+                const int i = c * NT + threadIdx.x;
+                mine[c] = i / 32 < blocks && i % 32 < top ? peer_u64(peer(&best[i % 32], i / 32)) : 0ull;
             }
             __syncthreads();
-            list[warp][lane] = k;
+            const u64 f = floor_all;
+#pragma unroll
+            for (int c = 0; c < 16 * 32 / NT; c++)
+                if (mine[c] != 0 && mine[c] >= f) list[atomicAdd(&count, 1)] = mine[c];
             if (threadIdx.x == 0) stat[0] = st;
             __syncthreads();
-            for (int n = kLpWarps / 2; n > 0 && top > 0; n >>= 1) {
-                if (warp < n && n <= (int)blocks) list[warp][lane] = merge32(list[warp][lane], list[warp + n][lane], lane);
-                __syncthreads();
+            const int n = count;
+            for (int i = threadIdx.x; i < n; i += NT) {
+                const int k = rank_of(list[i], list, n);
+                if (k < top) best[k] = list[i];
             }
+            __syncthreads();
         }
         cluster_barrier();                                     // a block's shared memory stays until it has been read
         if (rank != 0) return;
     }
-    __syncthreads();
     st = stat[0];
     const float ls = logf(st.s);
     auto logp = [&](float z) { return st.s == 0.f || (z == -INFINITY && st.s == st.s) ? -INFINITY : (z - st.m) - ls; };
     if (threadIdx.x == 0 && a.entropy) a.entropy[r] = st.s == 0.f ? 0.f : ls - st.t / st.s;
-    for (int k = threadIdx.x; k < a.n_targets; k += kLpThreads) {
+    for (int k = threadIdx.x; k < a.n_targets; k += NT) {
         const int id = a.targets[r * a.n_targets + k];
         a.logprob[r * a.n_targets + k] = id == -1 ? 0.f : id < 0 || id >= a.vocab ? NAN : logp(to_f32(x[id]));
     }
     if (threadIdx.x < top) {
-        const u64 key = list[0][threadIdx.x];
+        const u64 key = best[threadIdx.x];
         a.top_id[r * top + threadIdx.x] = key ? argmax_key_index(key) : -1;
-        a.top_logprob[r * top + threadIdx.x] = key ? logp(key_value(key)) : NAN;
+        a.top_logprob[r * top + threadIdx.x] = key ? logp(value_of((uint32_t)(key >> 32))) : NAN;
     }
 }
 
-template <class T>
-cudaError_t launch_logprobs(const llm_logprobs_args& a, cudaStream_t st) {
-    // blocks of a row: enough to give every SM two, none with less than one
-    // block of its lanes' elements, at most 16 (beyond 8 by opt-in)
-    const int sms = sm_count();
-    int blocks = 1;
-    while (blocks < 16 && (long long)a.n_rows * blocks < 2 * sms && a.vocab > blocks * kLpThreads * kLpElems) blocks *= 2;
-    const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+template <class T, int NT>
+cudaError_t launch_logprobs(const llm_logprobs_args& a, int blocks, cudaStream_t st) {
+    const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.n_rows * blocks);
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(NT);
     cfg.stream = st;
     cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -434,7 +571,22 @@ cudaError_t launch_logprobs(const llm_logprobs_args& a, cudaStream_t st) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a);
+    return cudaLaunchKernelEx(&cfg, logprobs_kernel<T, NT>, a);
+}
+
+// Few rows (not one for each SM): blocks of 512 threads, enough of them to give
+// every SM two, none with less than one step's logits, at most 16 a row (beyond 8
+// by opt-in).  More rows: blocks of 128, six or more for each SM.
+template <class T>
+cudaError_t launch_logprobs(const llm_logprobs_args& a, cudaStream_t st) {
+    const int sms = sm_count();
+    int blocks = 1;
+    if (a.n_rows < sms) {
+        while (blocks < 16 && (long long)a.n_rows * blocks < 2 * sms && a.vocab > blocks * 512 * kLpElems) blocks *= 2;
+        return launch_logprobs<T, 512>(a, blocks, st);
+    }
+    while (blocks < 16 && (long long)a.n_rows * blocks < 6 * sms && a.vocab > blocks * 128 * kLpElems) blocks *= 2;
+    return launch_logprobs<T, 128>(a, blocks, st);
 }
 
 }  // namespace
@@ -468,15 +620,18 @@ extern "C" int llm_kv_append(const llm_pages* pages, const llm_append* a, llm_st
     if (a->n_heads > 0 && ((rc = check_rows("q", a->q, a->dtype, a->q_stride, qw, rows)) ||
                            (rc = check_rows("q_out", a->q_out, a->q_out_dtype, a->q_out_stride, qw, rows))))
         return rc;
-    if (a->rope_dims > 0 && (!a->cos_sin || !aligned(a->cos_sin, 8)))
-        return fail_op(LLM_ERR_INVALID_ARG, "cos_sin is NULL or not 8-byte aligned");
+    if (a->rope_dims > 0 && (!a->cos_sin || !aligned(a->cos_sin, 16)))
+        return fail_op(LLM_ERR_INVALID_ARG, "cos_sin is NULL or not 16-byte aligned");
     if (a->n_heads > 0 && a->q == a->q_out && (a->dtype != a->q_out_dtype || a->q_stride != a->q_out_stride))
         return fail_op(LLM_ERR_INVALID_ARG, "q_out is q with another type or stride");
     const PagesDev pd = pages_dev(pages);
-    const long long items = (a->n_heads + 2LL * pages->n_kv_heads) * (pages->head_dim / 8), row_blocks = (items + kAppendThreads - 1) / kAppendThreads;
-    if (items > INT_MAX / 2 || rows * row_blocks > INT_MAX)
+    const int half = a->rope_dims / 2, group = pages->head_dim % 16 == 0 && half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : 0;
+    const long long per_head = pages->head_dim / append_item(group), q_blocks = (a->n_heads * per_head + kAppendThreads - 1) / kAppendThreads,
+                    row_blocks = q_blocks + (2 * pages->n_kv_heads * per_head + kAppendThreads - 1) / kAppendThreads;
+    if (qw > INT_MAX || rows * row_blocks > INT_MAX)
         return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^31 blocks of %d threads", kAppendThreads);
-    const AppendDev ad{a->n_heads, a->rope_dims / 2, a->rope_neox, a->table_rows, (int)row_blocks, a->q, a->k, a->v, a->q_stride,
+    const AppendDev ad{a->n_heads, half, a->rope_neox, a->table_rows, group, (int)q_blocks, (int)row_blocks,
+                       Div((uint32_t)row_blocks), Div((uint32_t)per_head), Div((uint32_t)pages->n_new), a->q, a->k, a->v, a->q_stride,
                        a->k_stride, a->v_stride, a->q_out, a->q_out_stride, reinterpret_cast<const float2*>(a->cos_sin)};
     const bool h = a->dtype == LLM_F16, qh = a->n_heads > 0 && a->q_out_dtype == LLM_F16;
     return launched(h ? (qh ? launch_append<__half, __half>(stream, pd, ad, rows) : launch_append<__half, float>(stream, pd, ad, rows))
@@ -488,6 +643,7 @@ extern "C" int llm_logprobs(const llm_logprobs_args* a, llm_stream_t stream) {
     if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the arguments are NULL");
     if (a->n_rows < 0 || a->vocab < 1 || a->n_targets < 0 || a->top < 0 || a->top > a->vocab)
         return fail_op(LLM_ERR_INVALID_ARG, "n_rows, vocab, n_targets or top is out of range");
+    if (a->vocab > 1 << 30) return fail_op(LLM_ERR_UNSUPPORTED, "vocab %d exceeds 2^30", a->vocab);
     if (a->top > 32) return fail_op(LLM_ERR_UNSUPPORTED, "top %d exceeds 32", a->top);
     const int b = type_bytes(a->dtype);
     if (!b) return fail_op(LLM_ERR_UNSUPPORTED, "logits of type %d", a->dtype);

@@ -37,6 +37,13 @@ __device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
     return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
 }
 
+// max(a, b, c) in one instruction; a NaN counts as no value.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
 

@@ -72,7 +72,7 @@ def test_workspace_query_refuses_bad_sizes(kw, status):
     (dict(n_heads=-1), BAD), (dict(table_rows=-1), BAD), (dict(rope_dims=63), BAD), (dict(rope_dims=66), BAD),
     (dict(rope_dims=-2), BAD), (dict(dtype=L.LLM_Q8_0), UNSUP), (dict(dtype=2), UNSUP),
     (dict(q_out_dtype=L.LLM_Q8_0), UNSUP), (dict(q=None), BAD), (dict(k=None), BAD), (dict(v=None), BAD),
-    (dict(q_out=None), BAD), (dict(cos_sin=None), BAD), (dict(cos_sin=P + 4), BAD), (dict(q=P + 4), BAD),
+    (dict(q_out=None), BAD), (dict(cos_sin=None), BAD), (dict(cos_sin=P + 8), BAD), (dict(q=P + 4), BAD),
     (dict(k=P + 8), BAD), (dict(v=P + 8), BAD), (dict(q_out=P + 8), BAD), (dict(q_stride=252), BAD),
     (dict(k_stride=130), BAD), (dict(k_stride=64), BAD), (dict(v_stride=-128), BAD), (dict(q_out_stride=248), BAD),
     (dict(q_out=P), BAD),                                                      # q itself, but of another type
