@@ -21,6 +21,15 @@ def _stream(stream) -> int:
     return torch.cuda.current_stream().cuda_stream if stream is None else stream
 
 
+# The current device and its current stream without a Stream object (they are asked
+# at every call); None where PyTorch has no such functions.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _current_device is None or _current_stream is None:
+    _current_device = torch.cuda.current_device
+    _current_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+
+
 def _run(rc: int) -> None:
     if rc != _b.LLM_OK:
         raise _b.LlmError(rc, _b._lib.llm_last_error(None).decode())
@@ -76,9 +85,10 @@ class _Op:
     """One operator with its arguments; calling it enqueues one run."""
 
     def __call__(self, stream=None) -> None:
-        if torch.cuda.current_device() != self._index:
-            raise ValueError(f"the operator's tensors are on cuda:{self._index}, the current device is another")
-        rc = self._fn(*self._args, _stream(stream))
+        index = self._index
+        if _current_device() != index:
+            raise ValueError(f"the operator's tensors are on cuda:{index}, the current device is another")
+        rc = self._fn(*self._args, _current_stream(index) if stream is None else stream)
         if rc:
             _run(rc)
 
@@ -106,8 +116,8 @@ class KvAppend(_Op):
             _tensor("q_out", q_out, _DTYPES, tuple(q.shape), dev, strided=True)
             a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), q.stride(0)
             a.q_out, a.q_out_stride, a.q_out_dtype = q_out.data_ptr(), q_out.stride(0), _DTYPES[q_out.dtype]
-        self._kept, self._fn, self._index = (pages, q, k, v, cos_sin, q_out), _b._lib.llm_kv_append, dev.index
-        self._args = ctypes.byref(p), ctypes.byref(a)
+        self._kept, self._fn, self._index = (pages, a, q, k, v, cos_sin, q_out), _b._lib.llm_kv_append, dev.index
+        self._args = ctypes.addressof(p), ctypes.addressof(a)
 
 
 class AttendBatch(_Op):
@@ -137,8 +147,8 @@ class AttendBatch(_Op):
             _run(int(n))
         self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
         a.workspace, a.workspace_bytes = self.workspace.data_ptr(), int(n)
-        self._kept, self._fn, self._index = (pages, q, out, prefix_k, prefix_v), _b._lib.llm_attend_batch, dev.index
-        self._args = ctypes.byref(p), ctypes.byref(a)
+        self._kept, self._fn, self._index = (pages, a, q, out, prefix_k, prefix_v), _b._lib.llm_attend_batch, dev.index
+        self._args = ctypes.addressof(p), ctypes.addressof(a)
 
 
 class LogProbs(_Op):
@@ -163,8 +173,8 @@ class LogProbs(_Op):
                                  targets=targets.data_ptr() if n_targets else None, logprob=self.logprob.data_ptr(),
                                  entropy=self.entropy.data_ptr(), top_id=self.top_id.data_ptr(),
                                  top_logprob=self.top_logprob.data_ptr())
-        self._kept, self._fn, self._index = (logits, targets), _b._lib.llm_logprobs, dev.index
-        self._args = (ctypes.byref(a),)
+        self._kept, self._fn, self._index = (a, logits, targets), _b._lib.llm_logprobs, dev.index
+        self._args = (ctypes.addressof(a),)
 
 
 def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, pos0: int = 0, device="cuda",

@@ -126,10 +126,10 @@ _SIGS = {
     "llm_test_poke_guard": ([_vp, _int], _int),
     "llm_prefill_f16_copy": ([_vp, _int], _int),
     "llm_rope_table": ([_vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp], _int),
-    "llm_kv_append": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_append), _vp], _int),
-    "llm_attend_batch_workspace": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_attend)], ctypes.c_int64),
-    "llm_attend_batch": ([ctypes.POINTER(llm_pages), ctypes.POINTER(llm_attend), _vp], _int),
-    "llm_logprobs": ([ctypes.POINTER(llm_logprobs_args), _vp], _int),
+    "llm_kv_append": ([_vp, _vp, _vp], _int),
+    "llm_attend_batch_workspace": ([_vp, _vp], ctypes.c_int64),
+    "llm_attend_batch": ([_vp, _vp, _vp], _int),
+    "llm_logprobs": ([_vp, _vp], _int),
 }
 
 

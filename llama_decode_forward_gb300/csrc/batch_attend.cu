@@ -824,14 +824,20 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 template <int LP>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a) {
     constexpr int GROUPS = 32 / LP, AHEAD = 8;
-    griddep_entry();
+    griddep_launch();
     const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31, grp = lane / LP, d = 4 * (lane % LP);
-    if (w >= (long long)p.n_seqs * p.n_new * a.n_heads) return;
+    if (w >= (long long)p.n_seqs * p.n_new * a.n_heads) {
+        griddep_wait();                      // (every path: this grid must not end before those it follows)
+        return;
+    }
     const int token = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
     const int s = token / p.n_new, i = token % p.n_new, g = h / a.gq, hq = h % a.gq;
     const int len = p.lens[s];
-    if (len - p.n_new + i < 0) return;                         // padding
+    if (len - p.n_new + i < 0) {             // padding
+        griddep_wait();
+        return;
+    }
     if (lane == 0 && len > clipped_len(p, s)) flag(p.err, LLM_PAGES_BAD_LEN);
     const int srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
     int np = 0, ns = 0;                      // the row's parts of the prefix and of its pages
@@ -843,6 +849,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         np = 2 * ((int)(owner_of(x + ntiles - 1, a.prefix_blocks, total) - w0) + 1);       // a part of each softmax group
         pre = (u + w0) * 256 + r % 128;
     }
+    // the lengths (written before this kernel's predecessors began) and the prefix's parts are known
+    // by now; the rest comes from those
+    griddep_wait();
     const int step = min(srows, ru);
     if (a.suffix_workers > 0) {
         const int b = a.starts[s], pieces = a.starts[s + 1] - b;
@@ -982,8 +991,11 @@ constexpr int kCarveout = 72;
 template <int HDP, bool SPLITQ, bool SPLITP>
 cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad) {
     auto k = prefix_kernel<HDP, SPLITQ, SPLITP>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
+    static OncePerDevice once;
+    const cudaError_t e = once([&] {
+        const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
+    });
     if (e != cudaSuccess) return e;
     return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
 }
@@ -993,11 +1005,19 @@ cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& 
     // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
     static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
     auto k = suffix_kernel<HDP, NT, SPLITQ, SPLITP>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                               first ? (int)cudaSharedmemCarveoutDefault : kCarveout);
-    if (e != cudaSuccess) return e;
-    return launch_dep(k, dim3((unsigned)blocks), dim3(32 * kSuffixWarps),
-                      (size_t)(2 * pd.n_seqs + 1) * 4, st, pd, ad, first);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(32 * kSuffixWarps);
+    cfg.dynamicSmemBytes = (size_t)(2 * pd.n_seqs + 1) * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    at[1].val.sharedMemCarveout = kCarveout;
+    cfg.attrs = at;
+    cfg.numAttrs = first ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, k, pd, ad, first);
 }
 
 int check_attend(const llm_pages* p, const llm_attend* a) {

@@ -294,12 +294,32 @@ __device__ __forceinline__ u64 peer_u64(uint32_t a) {
     return v;
 }
 
-// How many of the first n keys of `list` are larger than key.
+// How many of the n keys of `list` are larger than key: eight at a time, the list
+// (16-byte aligned) with zeros behind its n keys up to a multiple of eight.
 __device__ __forceinline__ int rank_of(u64 key, const u64* list, int n) {
+    const uint32_t at = smem_addr(list);
     int c = 0;
-#pragma unroll 4
-    for (int i = 0; i < n; i++) c += list[i] > key;
+    for (int i = 0; i < n; i += 8) {
+        u64 k[8];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(k[j]), "=l"(k[j + 1]) : "r"(at + (uint32_t)((i + j) * 8)));
+#pragma unroll
+        for (int j = 0; j < 8; j++) c += k[j] > key;
+    }
     return c;
+}
+
+// The `top` largest of list's n keys into best[], in order.  All threads, with the
+// list complete but for the zeros behind it.
+template <int NT>
+__device__ __forceinline__ void put_in_order(u64* list, int n, int top, u64* best) {
+    if (threadIdx.x < 8) list[n + threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += NT) {
+        const int k = rank_of(list[i], list, n);
+        if (k < top) best[k] = list[i];
+    }
 }
 
 // NT threads a block: 512 for few rows (the shortest chain), 128 for many (a warp
@@ -314,8 +334,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
     const T* x = static_cast<const T*>(a.logits) + r * a.stride;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, top = a.top;
     __shared__ LpStat stat[NW];
-    __shared__ u64 wait[NW][64];             // keys that reached the floor and are not in the warp's list yet
-    __shared__ u64 list[NW * 96], best[32];  // the block's keys that reach its floor; its largest in order
+    __shared__ __align__(16) u64 wait[NW][64 + 8];   // keys that reached the floor and are not in the warp's list yet
+    __shared__ __align__(16) u64 list[(NW * 64 > 512 ? NW * 64 : 512) + 8], best[32];   // the block's keys that reach its floor; its largest in order
     __shared__ u64 floor_all;
     __shared__ int count;
     if (threadIdx.x == 0) {
@@ -341,6 +361,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
         for (int k = 0; k < NV; k++) raw[k] = __ldcs(words + b + k * 32 + lane);
     };
     LpStat st{-INFINITY, 0.f, 0.f};
+    // the targets' logits are wanted at the end: the first block asks for them now
+    float of_target = 0.f;
+    if (rank == 0 && (int)threadIdx.x < a.n_targets) {
+        const int id = a.targets[r * a.n_targets + threadIdx.x];
+        if (id >= 0 && id < a.vocab) of_target = to_f32(x[id]);
+    }
     u64 keys = 0, floor = 0;
     int waiting = 0;
     float floor_v = -INFINITY;
@@ -419,7 +445,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
             // largest each, or the last lanes' poor ones would let half of the logits through
             // (a lane without an element of the row has -infinity and counts as none)
             uint32_t near = sort32(inside || bm > -INFINITY ? order_of(bm + 0.f) : 0u, lane);
-            if (top > 16) {
+            if (top > 24) {
                 float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < kLpElems; i++) {
@@ -465,16 +491,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
             }
         }
     }
-    // many alternatives: the last ones sorted in too, so that the block's floor leaves fewer to rank
+    // many alternatives: the warp's own top-th key as a floor leaves the block fewer to rank
     if (top > 8 && waiting > 0) {
-        sort_in(lane < waiting ? wait[warp][lane] : 0ull);
-        waiting = 0;
+        const u64 listed = __shfl_sync(0xffffffffu, keys, 0);
+        if (listed) {
+            sort_in(lane < waiting ? wait[warp][lane] : 0ull);
+            waiting = 0;
+        } else {
+            if (lane < 8) wait[warp][waiting + lane] = 0;
+            __syncwarp();
+            for (int i = lane; i < waiting; i += 32)
+                if (rank_of(wait[warp][i], wait[warp], waiting) == top - 1) atomicMax(&floor_all, wait[warp][i]);
+        }
     }
     st = lp_join_warp<16>(st);
     if (lane == 0) stat[warp] = st;
     __syncthreads();                         // the floor is the block's now
     if (top > 0) {
-        // the keys that reach it, from the lists and the waiting ones
+        // the keys that reach it, from the lists and the waiting ones; of these the largest in order
         const u64 f = floor_all;
         auto take = [&](u64 key) {
             const uint32_t who = __ballot_sync(0xffffffffu, key != 0 && key >= f);
@@ -486,11 +520,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
         take(keys);
         take(lane < waiting ? wait[warp][lane] : 0ull);
         __syncthreads();
-        const int n = count;
-        for (int i = threadIdx.x; i < n; i += NT) {
-            const int k = rank_of(list[i], list, n);
-            if (k < top) best[k] = list[i];
-        }
+        put_in_order<NT>(list, count, top, best);
     }
     if (warp == 0) {
         st = lp_join_warp<16>(lane < NW ? stat[lane] : LpStat{-INFINITY, 0.f, 0.f});
@@ -517,23 +547,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
                     count = 0;
                 }
             }
-            u64 mine[16 * 32 / NT];          // key i of block i / 32
+            constexpr int C = 16 * 32 / NT;
+            u64 mine[C];                     // key i % 32 of block i / 32
 #pragma unroll
-            for (int c = 0; c < 16 * 32 / NT; c++) {
+            for (int c = 0; c < C; c++) {
                 const int i = c * NT + threadIdx.x;
                 mine[c] = i / 32 < blocks && i % 32 < top ? peer_u64(peer(&best[i % 32], i / 32)) : 0ull;
             }
             __syncthreads();
-            const u64 f = floor_all;
-#pragma unroll
-            for (int c = 0; c < 16 * 32 / NT; c++)
-                if (mine[c] != 0 && mine[c] >= f) list[atomicAdd(&count, 1)] = mine[c];
             if (threadIdx.x == 0) stat[0] = st;
-            __syncthreads();
-            const int n = count;
-            for (int i = threadIdx.x; i < n; i += NT) {
-                const int k = rank_of(list[i], list, n);
-                if (k < top) best[k] = list[i];
+            if (top > 0) {
+                const u64 f = floor_all;
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    if (mine[c] != 0 && mine[c] >= f) list[atomicAdd(&count, 1)] = mine[c];
+                __syncthreads();
+                put_in_order<NT>(list, count, top, best);
             }
             __syncthreads();
         }
@@ -546,7 +575,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
     if (threadIdx.x == 0 && a.entropy) a.entropy[r] = st.s == 0.f ? 0.f : ls - st.t / st.s;
     for (int k = threadIdx.x; k < a.n_targets; k += NT) {
         const int id = a.targets[r * a.n_targets + k];
-        a.logprob[r * a.n_targets + k] = id == -1 ? 0.f : id < 0 || id >= a.vocab ? NAN : logp(to_f32(x[id]));
+        a.logprob[r * a.n_targets + k] = id == -1 ? 0.f : id < 0 || id >= a.vocab ? NAN : logp(k < NT ? of_target : to_f32(x[id]));
     }
     if (threadIdx.x < top) {
         const u64 key = best[threadIdx.x];
@@ -557,7 +586,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
 
 template <class T, int NT>
 cudaError_t launch_logprobs(const llm_logprobs_args& a, int blocks, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    static OncePerDevice once;
+    const cudaError_t e = once([] { return cudaFuncSetAttribute(logprobs_kernel<T, NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1); });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)a.n_rows * blocks);

@@ -4,6 +4,8 @@
 
 #include <limits.h>
 
+#include <atomic>
+
 #include "llm_internal.cuh"
 
 namespace llm {
@@ -96,14 +98,43 @@ inline int launched(cudaError_t e, const char* what) {
     return fail_op(LLM_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// The current device, 0 where there is none to ask.
+inline int device_now() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return dev;
+}
+constexpr int kDevicesKept = 64;             // devices whose answers are kept; others are asked every time
+
 // SMs of the current device (152 where there is none to ask).
 inline int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    static std::atomic<int> known[kDevicesKept];
+    const int dev = device_now();
+    int n = dev < kDevicesKept ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
         return 152;
     }
+    if (dev < kDevicesKept) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
+
+// Runs `set` (the attributes of one kernel) the first time on each device; one
+// static array of flags per kernel.
+struct OncePerDevice {
+    std::atomic<bool> done[kDevicesKept];
+    template <class Set>
+    cudaError_t operator()(Set set) {
+        const int dev = device_now();
+        if (dev < kDevicesKept && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+        const cudaError_t e = set();
+        if (e == cudaSuccess && dev < kDevicesKept) done[dev].store(true, std::memory_order_release);
+        return e;
+    }
+};
 
 }  // namespace llm
