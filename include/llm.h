@@ -485,6 +485,38 @@ typedef struct {
 } llm_logprobs_args;
 int llm_logprobs(const llm_logprobs_args *a, llm_stream_t stream);
 
+/* One step of a batch on a handle's model ("What a Llama model computes, and
+ * why" §2 and §4): the new rows' embedding, every layer (with llm_kv_append into
+ * the batch's pages and llm_attend_batch over the handle's own cache rows 0 ..
+ * prefix_len-1, the shared prompt that llm_prefill or decode steps wrote, and
+ * those pages), the final RMSNorm and the logits product.  Projections and
+ * logits are the batched prefill's tensor-core products on F16 operands, so F16
+ * and Q8_0 models whose llm_prefill runs batched are supported, with head_dim up
+ * to 128 and at most 512 rows (n_seqs * n_new).
+ * Sizes, page_table, lens and err are as in llm_pages, with lens counting the
+ * new rows; prefix_len <= max_seq.  pages: DEVICE, 16-byte aligned,
+ * llm_batch_pages_bytes() bytes, [n_layers][K, V][n_pages][page_size]
+ * [n_kv_heads][head_dim] FP16.  tokens: DEVICE [n_seqs * n_new]; those of
+ * padding rows are not looked at, another one outside [0, vocab) counts as 0 and
+ * sets the handle's device error (llm_sync: OUT_OF_RANGE).  logits: DEVICE
+ * [n_seqs * n_new][vocab] F32, 16-byte aligned; a padding row's are unspecified.
+ * Enqueued on the handle's stream without waiting.  The handle keeps the step's
+ * working memory and an angle table; a call that needs more of either than any
+ * before it waits for the stream and allocates, so let one call go before a
+ * capture into a CUDA graph.  llm_logits_device and the handle's cache are left
+ * as they are.  Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_RANGE, STATE,
+ * NO_MEMORY, CUDA (some of the step's kernels may then have been enqueued). */
+typedef struct {
+    int32_t n_seqs, n_new, prefix_len;
+    int32_t page_size, n_pages, max_pages;
+    void *pages;
+    const int32_t *page_table, *lens, *tokens;
+    float *logits;
+    int32_t *err;
+} llm_batch;
+int64_t llm_batch_pages_bytes(const llm_handle *h, int32_t n_pages, int32_t page_size);
+int llm_decode_batch(llm_handle *h, const llm_batch *b);
+
 /* ------------------------------------------------------------ GGUF files --
  * A model file in the GGUF version 3 layout of "Loading GGUF with the FFM API"
  * (codeloopback.dev, llm-gguf-loader-ffm): a 24-byte header (magic "GGUF",

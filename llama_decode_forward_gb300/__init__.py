@@ -7,7 +7,7 @@ builds the library if needed and fails if it cannot be built or loaded.
 from .binding import *  # noqa: F401,F403
 from .binding import Decoder, DeviceWeights, LlmError, LIBRARY_PATH, declared_symbols  # noqa: F401
 
-_BATCH = ("AttendBatch", "KvAppend", "LogProbs", "PagedBatch", "rope_table")
+_BATCH = ("AttendBatch", "BatchDecoder", "KvAppend", "LogProbs", "PagedBatch", "rope_table")
 
 
 def __getattr__(name):

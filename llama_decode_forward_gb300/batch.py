@@ -177,6 +177,41 @@ class LogProbs(_Op):
         self._args = (ctypes.addressof(a),)
 
 
+class BatchDecoder:
+    """Steps of n_seqs continuations of the prompt in rows 0 .. prefix_len - 1 of a
+    decoder's cache (llm_decode_batch).  tokens int32 [n_seqs, n_new], lens int32
+    [n_seqs] (the rows behind the prompt, this step's among them) and page_table
+    int32 [n_seqs, max_pages] are this object's tensors, to be written before each
+    step; logits float32 [n_seqs, n_new, vocab] is the step's result.  ``pages``
+    holds every layer's K and V pages; page_table starts with each sequence's own
+    pages in a row.  step() enqueues on the decoder's stream."""
+
+    def __init__(self, decoder, n_seqs: int, max_len: int, prefix_len: int, n_new: int = 1, page_size: int = 16):
+        c = _b.llm_get_config(decoder.h)
+        dev = torch.device("cuda", torch.cuda.current_device())
+        max_pages = -(-max_len // page_size)
+        n_pages = n_seqs * max_pages
+        self.decoder = decoder
+        self.pages = torch.zeros(max(1, _b.llm_batch_pages_bytes(decoder.h, n_pages, page_size)) // 2, dtype=torch.float16,
+                                 device=dev)
+        self.page_table = torch.arange(n_pages, dtype=torch.int32, device=dev).view(n_seqs, max_pages)
+        self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.tokens = torch.zeros(n_seqs, n_new, dtype=torch.int32, device=dev)
+        self.logits = torch.empty(n_seqs, n_new, c.vocab, dtype=torch.float32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.struct = _b.llm_batch(n_seqs=n_seqs, n_new=n_new, prefix_len=prefix_len, page_size=page_size,
+                                   n_pages=n_pages, max_pages=max_pages, pages=self.pages.data_ptr(),
+                                   page_table=self.page_table.data_ptr(), lens=self.lens.data_ptr(),
+                                   tokens=self.tokens.data_ptr(), logits=self.logits.data_ptr(), err=self.err.data_ptr())
+
+    def step(self) -> None:
+        _b.llm_decode_batch(self.decoder.h, self.struct)
+
+    def errors(self) -> int:
+        """The LLM_PAGES_* bits seen so far (waits for the device)."""
+        return int(self.err.item())
+
+
 def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, pos0: int = 0, device="cuda",
                stream=None) -> torch.Tensor:
     """llm_rope_table: float32 [n_pos, rope_dims / 2, 2] of the decode step's

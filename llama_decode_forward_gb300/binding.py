@@ -70,6 +70,11 @@ class llm_logprobs_args(ctypes.Structure):
                 ("top_logprob", ctypes.c_void_p)]
 
 
+class llm_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_new", "prefix_len", "page_size", "n_pages", "max_pages")] + \
+               [(n, ctypes.c_void_p) for n in ("pages", "page_table", "lens", "tokens", "logits", "err")]
+
+
 class llm_gguf_layout(ctypes.Structure):
     _fields_ = [("version", ctypes.c_uint32), ("n_tensors", ctypes.c_int64), ("n_kv", ctypes.c_int64),
                 ("alignment", ctypes.c_uint64), ("infos_end", ctypes.c_uint64), ("data_start", ctypes.c_uint64),
@@ -130,6 +135,8 @@ _SIGS = {
     "llm_attend_batch_workspace": ([_vp, _vp], ctypes.c_int64),
     "llm_attend_batch": ([_vp, _vp, _vp], _int),
     "llm_logprobs": ([_vp, _vp], _int),
+    "llm_batch_pages_bytes": ([_vp, _i32, _i32], ctypes.c_int64),
+    "llm_decode_batch": ([_vp, _vp], _int),
 }
 
 
@@ -243,6 +250,18 @@ def llm_prefill_f16_copy(h, enable: bool = True) -> None:
     """Keep (or free) the F16 copy of a Q8_0 handle's layer matrices that the
     batched prefill's GEMMs then read."""
     _check(_lib.llm_prefill_f16_copy(h, 1 if enable else 0), h)
+
+
+def llm_batch_pages_bytes(h, n_pages: int, page_size: int) -> int:
+    n = int(_lib.llm_batch_pages_bytes(h, int(n_pages), int(page_size)))
+    if n < 0:
+        raise LlmError(n, "n_pages or page_size")
+    return n
+
+
+def llm_decode_batch(h, batch: llm_batch) -> None:
+    """One step of a batch of sequences, enqueued on the handle's stream."""
+    _check(_lib.llm_decode_batch(h, ctypes.addressof(batch)), h)
 
 
 def llm_sync(h):

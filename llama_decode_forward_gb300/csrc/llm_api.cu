@@ -1,5 +1,6 @@
 // C ABI of libllmdecode (declared in include/llm.h): handle lifetime, weight
 // repacking, argument validation and step launches.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -147,6 +148,10 @@ struct llm_handle {
     size_t prefill_ws_bytes = 0;
     __half* f16_copy = nullptr;      // llm_prefill_f16_copy: F16 copy of the Q8_0 layer matrices
     size_t f16_copy_bytes = 0;
+    float* batch_tab = nullptr;      // llm_decode_batch: angles of positions 0 .. batch_tab_rows-1
+    int batch_tab_rows = 0;
+    void* batch_ws = nullptr;        // and the attention's workspace
+    size_t batch_ws_bytes = 0;
     int test_logits_limit = 0;       // llm_test_logits_limit: > 0 narrows the checked logits bound
 };
 
@@ -305,6 +310,8 @@ static void free_handle(llm_handle* h) {
     cudaFree(h->kv_maps);
     guarded_free(h->ws_mem);
     cudaFree(h->f16_copy);
+    cudaFree(h->batch_tab);
+    cudaFree(h->batch_ws);
     cudaFree(h->trace);
     if (h->pinned) cudaFreeHost(h->pinned);
     cudaGetLastError();
@@ -833,6 +840,83 @@ extern "C" int llm_prefill_f16_copy(llm_handle* h, int enable) {
     return fail(h, LLM_ERR_CUDA, "F16 prefill copy: %s", cudaGetErrorString(e));
 }
 
+// The batched prefill's workspace, allocated on first use.
+static int need_prefill_ws(llm_handle* h, const PrefillCtx& pc) {
+    const size_t need = prefill_workspace_bytes(pc);
+    if (h->prefill_ws_bytes >= need) return LLM_OK;
+    CK(h, cudaStreamSynchronize(h->st));
+    guarded_free(h->ws_mem);
+    h->prefill_ws = nullptr;
+    h->prefill_ws_bytes = 0;
+    CK(h, guarded_alloc(h->ws_mem, need, h->st));
+    h->prefill_ws = h->ws_mem.ptr();
+    h->prefill_ws_bytes = need;
+    return LLM_OK;
+}
+
+extern "C" int64_t llm_batch_pages_bytes(const llm_handle* h, int32_t n_pages, int32_t page_size) {
+    if (!alive(h) || n_pages < 0 || page_size < 1 || (page_size & (page_size - 1))) return LLM_ERR_INVALID_ARG;
+    const long long row = 2LL * h->cfg.n_layers * h->kv_dim * 2, rows = (long long)n_pages * page_size;
+    return rows > LLONG_MAX / row ? LLM_ERR_INVALID_ARG : rows * row;
+}
+
+extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
+    LIVE_OR_RETURN(h);
+    if (!b) return fail(h, LLM_ERR_INVALID_ARG, "the batch is NULL");
+    if (h->broken) return fail(h, LLM_ERR_STATE, "handle has a device error; call llm_reset");
+    const PrefillCtx pc = prefill_ctx(h);
+    if (!prefill_supported(pc)) return fail(h, LLM_ERR_UNSUPPORTED, "this model's prefill runs the decode step token by token");
+    if (b->n_seqs < 0 || b->n_new < 1 || (long long)b->n_seqs * b->n_new > kPrefillRows)
+        return fail(h, LLM_ERR_OUT_OF_RANGE, "%d sequences of %d new tokens: not 0 to %d rows", b->n_seqs, b->n_new, kPrefillRows);
+    if (b->prefix_len < 0 || b->prefix_len > h->cfg.max_seq)
+        return fail(h, LLM_ERR_OUT_OF_RANGE, "prefix_len %d not in [0, %d]", b->prefix_len, h->cfg.max_seq);
+    const long long positions = (long long)b->prefix_len + (long long)b->max_pages * b->page_size;
+    if (b->max_pages < 0 || b->page_size < 1 || positions > (1 << 24))
+        return fail(h, LLM_ERR_OUT_OF_RANGE, "max_pages or page_size is out of range, or positions exceed 2^24");
+    if (!b->page_table || !b->lens || !b->tokens || !b->logits || !b->pages) return fail(h, LLM_ERR_INVALID_ARG, "NULL argument");
+    if ((reinterpret_cast<uintptr_t>(b->logits) & 15) || (reinterpret_cast<uintptr_t>(b->pages) & 15) ||
+        ((reinterpret_cast<uintptr_t>(b->tokens) | reinterpret_cast<uintptr_t>(b->lens) | reinterpret_cast<uintptr_t>(b->page_table) |
+          reinterpret_cast<uintptr_t>(b->err)) & 3))
+        return fail(h, LLM_ERR_INVALID_ARG, "a pointer of the batch is not aligned");
+    if (llm_batch_pages_bytes(h, b->n_pages, b->page_size) < 0)
+        return fail(h, LLM_ERR_INVALID_ARG, "n_pages %d of %d rows: negative, not a power of two, or too large", b->n_pages, b->page_size);
+    // what the operators refuse, before anything is enqueued
+    const llm_pages pages{b->n_seqs, b->n_new, b->prefix_len, b->page_size, b->n_pages, b->max_pages, h->cfg.n_kv_heads, h->cfg.head_dim,
+                          static_cast<uint16_t*>(b->pages), static_cast<uint16_t*>(b->pages), b->page_table, b->lens, b->err};
+    llm_attend at{};
+    at.n_heads = h->cfg.n_heads;
+    at.q_dtype = LLM_F32;
+    at.out_dtype = LLM_F16;
+    const int64_t need = llm_attend_batch_workspace(&pages, &at);
+    if (need < 0) return fail(h, (int)need, "%s", llm_last_error(nullptr));
+    if (b->n_seqs == 0) return LLM_OK;
+    int rc;
+    if ((rc = need_prefill_ws(h, pc))) return rc;
+    if (h->batch_ws_bytes < (size_t)need) {
+        CK(h, cudaStreamSynchronize(h->st));
+        cudaFree(h->batch_ws);
+        h->batch_ws = nullptr;
+        h->batch_ws_bytes = 0;
+        CK(h, dev_alloc(&h->batch_ws, (size_t)need));
+        h->batch_ws_bytes = (size_t)need;
+    }
+    if (h->batch_tab_rows < positions) {
+        CK(h, cudaStreamSynchronize(h->st));
+        cudaFree(h->batch_tab);
+        h->batch_tab = nullptr;
+        h->batch_tab_rows = 0;
+        CK(h, dev_alloc((void**)&h->batch_tab, (size_t)positions * h->cfg.rope_dims * 4));
+        CK(h, rope_table(h->st, h->batch_tab, (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs));
+        h->launches++;
+        h->batch_tab_rows = (int)positions;
+    }
+    const char* why = nullptr;
+    int launches = 0;
+    rc = decode_batch_rows(pc, *b, h->prefill_ws, h->batch_tab, h->batch_tab_rows, h->batch_ws, (int64_t)h->batch_ws_bytes, &why, &launches);
+    h->launches += launches;
+    return rc ? fail(h, rc, "batch step: %s", why ? why : llm_last_error(nullptr)) : LLM_OK;
+}
+
 extern "C" int llm_prefill(llm_handle* h, const int32_t* tokens_host, int32_t n, int32_t pos0, float* logits_host,
                            int32_t* argmax_host) {
     LIVE_OR_RETURN(h);
@@ -847,16 +931,7 @@ extern "C" int llm_prefill(llm_handle* h, const int32_t* tokens_host, int32_t n,
     const PrefillCtx pc = prefill_ctx(h);
     if (prefill_supported(pc)) {
         // F16 weights: tensor-core batches of up to kPrefillRows tokens
-        const size_t need = prefill_workspace_bytes(pc);
-        if (h->prefill_ws_bytes < need) {
-            CK(h, cudaStreamSynchronize(h->st));
-            guarded_free(h->ws_mem);
-            h->prefill_ws = nullptr;
-            h->prefill_ws_bytes = 0;
-            CK(h, guarded_alloc(h->ws_mem, need, h->st));
-            h->prefill_ws = h->ws_mem.ptr();
-            h->prefill_ws_bytes = need;
-        }
+        if ((rc = need_prefill_ws(h, pc))) return rc;
         const char* what = "";
         const cudaError_t e = prefill_f16(pc, h->prefill_ws, tokens_host, n, pos0, &what);
         if (e != cudaSuccess) {

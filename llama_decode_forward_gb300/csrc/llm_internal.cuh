@@ -215,6 +215,12 @@ cudaError_t rope_table(cudaStream_t st, float* tab, int n, int pos0, int rope_di
 // Records the calling thread's reason (llm_last_error(NULL)) of a failed call
 // without a handle; returns `status`.
 int fail_op(int status, const char* fmt, ...);
+// A step of a batch (llm_decode_batch): `ws` holds prefill_workspace_bytes(c), tab the
+// angles of positions 0 .. tab_rows-1, attend_ws the attention's workspace.  Returns a
+// status; a CUDA error's text and the failing step are in *why (otherwise the reason is
+// llm_last_error(NULL)'s).  *launches counts kernels.
+int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* tab, int tab_rows, void* attend_ws,
+                      int64_t attend_ws_bytes, const char** why, int* launches);
 cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_host, int n, int pos0, const char** msg);
 
 __host__ __device__ inline int dtype_bytes_x16(int wtype) {   // bytes per element, times 16

@@ -465,7 +465,29 @@ __global__ void embed_rows_kernel(const int* tok, int n, DMat embd, int wtype, i
     }
 }
 
-// A Q8_0 matrix (library layout) expanded to F16 for the tensor-core GEMMs:
+// The same for a batch's rows, whose tokens are on the device: padding rows (before a
+// sequence's first) take token 0, and so does a token outside the vocabulary, which is
+// reported.
+__global__ void embed_batch_kernel(const int* tok, const int* lens, int n_new, int vocab, DMat embd, int wtype, int dim, float* X,
+                                   int* err) {
+    griddep_entry();
+    const int i = blockIdx.x;
+    int t = lens[i / n_new] < n_new - i % n_new ? 0 : tok[i];
+    if (t < 0 || t >= vocab) {
+        if (threadIdx.x == 0) atomicOr(err, kErrToken);
+        t = 0;
+    }
+    const size_t r = (size_t)t;
+    for (int d = threadIdx.x; d < dim; d += blockDim.x) {
+        float v;
+        if (wtype == LLM_Q8_0)
+            v = __fmul_rn(__half2float(embd.d[r * embd.dstride + d / 32]), (float)(int)(int8_t)embd.q[r * embd.cols + d]);
+        else
+            v = __half2float(reinterpret_cast<const __half*>(embd.q)[r * embd.cols + d]);
+        X[(size_t)i * dim + d] = v;
+    }
+}
+
 // RMSNorm of every row ("The Forward Pass in Java", Example 4: y = (x*scale)*g,
 // scale = 1/sqrt(mean(x^2) + eps)); the GEMM operand is y rounded to F16.
 // One warp per row, 8 values per 16-byte step (dim % 8 == 0).
@@ -1121,39 +1143,42 @@ size_t prefill_workspace_bytes(const PrefillCtx& c) {
            al(M * c.q_dim * 2) + al(M * c.ffn * 2) + al((size_t)c.dim * 4) + al(M * (c.rope_dims / 2) * 8);
 }
 
-// Runs the batch; `ws` holds prefill_workspace_bytes(c).  Returns a CUDA error
-// or cudaSuccess; *msg names the failing step.
-cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_host, int n, int pos0, const char** msg) {
-    auto al = [](size_t b) { return (b + 255) & ~(size_t)255; };
+namespace {
+
+// The workspace's parts, and the tensor maps of the GEMMs' operands.
+struct BatchBuffers {
+    int* tok;
+    float* X;
+    __half* Xh;
+    float* QKV;
+    __half *Ah, *Hh;
+    float *ylast, *rtab;
+    CUtensorMap mXh, mAh, mHh;
+    std::vector<CUtensorMap> mw;             // [n_layers][QKV, O, gate/up, down]
+    bool q8;                                 // the layers' weights are expanded from the quants in the GEMMs
+};
+
+// The weight operands are the F16 matrices, the F16 copy of the Q8_0 ones, or the
+// int8 quants of the Q8_0 ones (expanded to F16 tile by tile inside the GEMM), per
+// layer: QKV, O, gate/up (single rows), down; box heights = the GEMMs' tile widths.
+bool batch_buffers(const PrefillCtx& c, void* ws, BatchBuffers& b, const char** msg) {
+    auto al = [](size_t n) { return (n + 255) & ~(size_t)255; };
     const size_t M = kPrefillRows;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    int* tok = reinterpret_cast<int*>(w); w += al(M * 4);
-    float* X = reinterpret_cast<float*>(w); w += al(M * c.dim * 4);
-    __half* Xh = reinterpret_cast<__half*>(w); w += al(M * c.dim * 2);
-    float* QKV = reinterpret_cast<float*>(w); w += al(M * (c.q_dim + 2 * c.kv_dim) * 4);
-    __half* Ah = reinterpret_cast<__half*>(w); w += al(M * c.q_dim * 2);
-    __half* Hh = reinterpret_cast<__half*>(w); w += al(M * c.ffn * 2);
-    float* ylast = reinterpret_cast<float*>(w); w += al((size_t)c.dim * 4);
-    float* rtab = reinterpret_cast<float*>(w); w += al(M * (c.rope_dims / 2) * 8);   // the batch's cos/sin table
-    cudaError_t e;
-#define PF_CK(call, what)                 \
-    do {                                  \
-        if ((e = (call)) != cudaSuccess) { \
-            *msg = what;                  \
-            return e;                     \
-        }                                 \
-    } while (0)
-    CUtensorMap mXh, mAh, mHh;
-    if (!gemm_map(&mXh, Xh, c.dim, (int)M) || !gemm_map(&mAh, Ah, c.q_dim, (int)M) || !gemm_map(&mHh, Hh, c.ffn, (int)M)) {
+    b.tok = reinterpret_cast<int*>(w); w += al(M * 4);
+    b.X = reinterpret_cast<float*>(w); w += al(M * c.dim * 4);
+    b.Xh = reinterpret_cast<__half*>(w); w += al(M * c.dim * 2);
+    b.QKV = reinterpret_cast<float*>(w); w += al(M * (c.q_dim + 2 * c.kv_dim) * 4);
+    b.Ah = reinterpret_cast<__half*>(w); w += al(M * c.q_dim * 2);
+    b.Hh = reinterpret_cast<__half*>(w); w += al(M * c.ffn * 2);
+    b.ylast = reinterpret_cast<float*>(w); w += al((size_t)c.dim * 4);
+    b.rtab = reinterpret_cast<float*>(w); w += al(M * (c.rope_dims / 2) * 8);   // the batch's cos/sin table
+    if (!gemm_map(&b.mXh, b.Xh, c.dim, (int)M) || !gemm_map(&b.mAh, b.Ah, c.q_dim, (int)M) || !gemm_map(&b.mHh, b.Hh, c.ffn, (int)M)) {
         *msg = "tensor map of an activation operand";
-        return cudaErrorInvalidValue;
+        return false;
     }
-    // weight operands: the F16 matrices, the F16 copy of the Q8_0 ones, or
-    // the int8 quants of the Q8_0 ones (expanded to F16 tile by tile inside
-    // the GEMM), per layer: QKV, O, gate/up (single rows), down; box heights =
-    // the GEMMs' tile widths
-    const bool q8 = c.wtype == LLM_Q8_0 && !c.f16_copy;
-    std::vector<CUtensorMap> mw((size_t)4 * c.n_layers);
+    b.q8 = c.wtype == LLM_Q8_0 && !c.f16_copy;
+    b.mw.resize((size_t)4 * c.n_layers);
     static constexpr int kBox[4] = {kBnQkv, kBnNarrow, kBnWide, kBnNarrow};
     for (int l = 0; l < c.n_layers; l++) {
         const LayerDev& L = c.layers[l];
@@ -1162,13 +1187,37 @@ cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_hos
             int rows, cols;
             copy_shape(c, l, k, &rows, &cols);
             const void* base = c.f16_copy ? static_cast<const void*>(c.f16_copy + copy_offset(c, l, k)) : dm[k]->q;
-            if (!(q8 ? q8_map(&mw[4 * l + k], base, cols, rows, kBox[k])
-                     : gemm_map(&mw[4 * l + k], base, cols, rows, kBox[k]))) {
+            if (!(b.q8 ? q8_map(&b.mw[4 * l + k], base, cols, rows, kBox[k])
+                       : gemm_map(&b.mw[4 * l + k], base, cols, rows, kBox[k]))) {
                 *msg = "tensor map of a weight matrix";
-                return cudaErrorInvalidValue;
+                return false;
             }
         }
     }
+    return true;
+}
+
+}  // namespace
+
+// Runs the batch; `ws` holds prefill_workspace_bytes(c).  Returns a CUDA error
+// or cudaSuccess; *msg names the failing step.
+cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_host, int n, int pos0, const char** msg) {
+    BatchBuffers bb;
+    if (!batch_buffers(c, ws, bb, msg)) return cudaErrorInvalidValue;
+    int* tok = bb.tok;
+    float *X = bb.X, *QKV = bb.QKV, *ylast = bb.ylast, *rtab = bb.rtab;
+    __half *Xh = bb.Xh, *Ah = bb.Ah, *Hh = bb.Hh;
+    const CUtensorMap &mXh = bb.mXh, &mAh = bb.mAh, &mHh = bb.mHh;
+    const std::vector<CUtensorMap>& mw = bb.mw;
+    const bool q8 = bb.q8;
+    cudaError_t e;
+#define PF_CK(call, what)                 \
+    do {                                  \
+        if ((e = (call)) != cudaSuccess) { \
+            *msg = what;                  \
+            return e;                     \
+        }                                 \
+    } while (0)
     auto run = [&](auto bn, auto epi, const CUtensorMap& ma, const CUtensorMap& mb, const DMat& wm, const GemmOut& o,
                    int M, int N, int K) -> cudaError_t {
         constexpr int BN = decltype(bn)::value, EPI = decltype(epi)::value;
@@ -1239,6 +1288,80 @@ cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_hos
     }
 #undef PF_CK
     return cudaSuccess;
+}
+
+int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* tab, int tab_rows, void* attend_ws,
+                      int64_t attend_ws_bytes, const char** why, int* launches) {
+    BatchBuffers bb;
+    *launches = 0;
+    *why = nullptr;
+    if (!batch_buffers(c, ws, bb, why)) return LLM_ERR_CUDA;
+    const int n = b.n_seqs * b.n_new, qkv_w = c.q_dim + 2 * c.kv_dim;
+    CUtensorMap mout;
+    const bool out_q8 = c.wtype == LLM_Q8_0;
+    if (!(out_q8 ? q8_map(&mout, c.out.q, c.dim, c.vocab, kBnQkv) : gemm_map(&mout, c.out.q, c.dim, c.vocab, kBnQkv))) {
+        *why = "tensor map of the logits matrix";
+        return LLM_ERR_CUDA;
+    }
+    auto run = [&](auto bn, auto epi, bool q8, const CUtensorMap& ma, const CUtensorMap& mb, const DMat& wm, const GemmOut& o, int N,
+                   int K) -> cudaError_t {
+        constexpr int BN = decltype(bn)::value, EPI = decltype(epi)::value;
+        const GemmScales sc{wm.d, wm.dstride};
+        return q8 ? gemm<BN, EPI, true>(c.st, c.sms, ma, mb, sc, o, n, N, K, c.err)
+                  : gemm<BN, EPI, false>(c.st, c.sms, ma, mb, sc, o, n, N, K, c.err);
+    };
+    using Qkv = std::integral_constant<int, kBnQkv>;
+    using Narrow = std::integral_constant<int, kBnNarrow>;
+    using Wide = std::integral_constant<int, kBnWide>;
+    using EBias = std::integral_constant<int, kEpiBias>;
+    using EResid = std::integral_constant<int, kEpiResidual>;
+    using ESwi = std::integral_constant<int, kEpiSwiGLU>;
+#define BT_CK(call, what)            \
+    do {                             \
+        if ((call) != cudaSuccess) { \
+            cudaGetLastError();      \
+            *why = what;             \
+            return LLM_ERR_CUDA;     \
+        }                            \
+        ++*launches;                 \
+    } while (0)
+    const dim3 norm_grid((n + 1) / 2), norm_block(64);       // two rows per block, as the prefill's
+    auto norm = [&](const float* gain) { return launch_dep(rmsnorm_rows_f16_kernel, norm_grid, norm_block, 0, c.st, bb.X, n, c.dim, gain, c.eps, bb.Xh); };
+    BT_CK(launch_dep(embed_batch_kernel, dim3(n), dim3(256), 0, c.st, b.tokens, b.lens, b.n_new, c.vocab, c.embd, c.wtype, c.dim, bb.X, c.err),
+          "embedding");
+    const size_t side = (size_t)b.n_pages * b.page_size * c.kv_dim;      // one layer's K or V pages
+    for (int l = 0; l < c.n_layers; l++) {
+        const LayerDev& L = c.layers[l];
+        uint16_t* kp = static_cast<uint16_t*>(b.pages) + (size_t)(2 * l) * side;
+        const llm_pages pages{b.n_seqs, b.n_new, b.prefix_len, b.page_size, b.n_pages, b.max_pages, c.n_kv, c.hd, kp, kp + side,
+                              b.page_table, b.lens, b.err};
+        BT_CK(norm(L.attn_norm), "attention RMSNorm");
+        GemmOut oq{bb.QKV, L.qkv_bias, nullptr, nullptr};
+        BT_CK(run(Qkv{}, EBias{}, bb.q8, bb.mXh, bb.mw[4 * l + 0], L.qkv, oq, L.qkv.rows, c.dim), "QKV GEMM");
+        // q is rotated in place and stays F32, as in the decode step
+        llm_append ap{c.n_heads, c.rope_dims, c.neox, tab_rows, LLM_F32, LLM_F32, bb.QKV, bb.QKV + c.q_dim, bb.QKV + c.q_dim + c.kv_dim,
+                      qkv_w, qkv_w, qkv_w, bb.QKV, qkv_w, tab};
+        int rc = llm_kv_append(&pages, &ap, c.st);
+        if (rc) return rc;
+        // the prompt's rows are the handle's cache; the output is the O projection's operand
+        llm_attend at{c.n_heads, LLM_F32, LLM_F16, 1.0f / c.attn_div, bb.QKV, qkv_w, bb.Ah, c.q_dim,
+                      reinterpret_cast<const uint16_t*>(L.kc), reinterpret_cast<const uint16_t*>(L.vc), c.kv_dim, attend_ws, attend_ws_bytes};
+        rc = llm_attend_batch(&pages, &at, c.st);
+        if (rc) return rc;
+        *launches += 2 + (b.prefix_len > 0) + (b.max_pages > 0);
+        GemmOut oo{nullptr, nullptr, bb.X, nullptr};
+        BT_CK(run(Narrow{}, EResid{}, bb.q8, bb.mAh, bb.mw[4 * l + 1], L.o, oo, c.dim, c.q_dim), "O GEMM");
+        BT_CK(norm(L.ffn_norm), "FFN RMSNorm");
+        GemmOut og{nullptr, nullptr, nullptr, bb.Hh};
+        BT_CK(run(Wide{}, ESwi{}, bb.q8, bb.mXh, bb.mw[4 * l + 2], L.gu, og, 2 * L.gu.rows, c.dim), "gate/up GEMM");
+        GemmOut od{nullptr, nullptr, bb.X, nullptr};
+        BT_CK(run(Narrow{}, EResid{}, bb.q8, bb.mHh, bb.mw[4 * l + 3], L.down, od, c.dim, c.ffn), "down GEMM");
+    }
+    BT_CK(norm(c.out_norm), "final RMSNorm");
+    GemmOut ol{b.logits, nullptr, nullptr, nullptr};
+    BT_CK(run(Qkv{}, EBias{}, out_q8, bb.mXh, mout, c.out, ol, c.vocab, c.dim), "logits GEMM");
+#undef BT_CK
+    return LLM_OK;
 }
 
 }  // namespace llm

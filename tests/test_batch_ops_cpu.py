@@ -143,6 +143,13 @@ def test_null_structs_refused():
     refused(B._lib.llm_logprobs(None, None), BAD)
 
 
+def test_decode_batch_refuses_a_dead_handle():
+    b = B.llm_batch(n_seqs=1, n_new=1)
+    assert B._lib.llm_decode_batch(None, ctypes.addressof(b)) == BAD
+    assert B._lib.llm_decode_batch(0x1000, ctypes.addressof(b)) == BAD
+    assert B._lib.llm_batch_pages_bytes(None, 1, 16) == BAD
+
+
 def test_nothing_to_do():
     """No sequences, rows or positions: success without a launch (no GPU here)."""
     none = pages(n_seqs=0, k_pages=None, v_pages=None, page_table=None, lens=None)

@@ -1,0 +1,307 @@
+"""llm_decode_batch: steps of several continuations of one prompt against the
+oracle, and against the decode step run sequence by sequence ("What a Llama
+model computes, and why" §2 and §4).  The projections' operands are rounded to
+F16 as in the batched prefill, so logits are held to its tolerance; the prompt's
+rows are the handle's cache, the sequences' own rows are pages."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synth
+from harness import TOL, check_logits
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import llama_decode_forward_gb300 as L
+    return L
+
+
+def config(**kw):
+    base = dict(n_layers=2, dim=256, n_heads=8, n_kv_heads=2, head_dim=32, ffn_dim=576, vocab=1000, max_seq=300,
+                eps=1e-5, rope_base=1e6, rope_neox=1, wtype=synth.F16, tied=True, bias=True, number=81)
+    base.update(kw)
+    return synth.ModelConfig("decode_batch", **base)
+
+
+def token(cfg, s, e):
+    return (7919 * (s + 1) + 104729 * (e + 1)) % cfg.vocab
+
+
+def put(bd, cfg, lens):
+    """The step's lens, and the tokens of its rows; padding rows hold no token."""
+    n_new = bd.tokens.shape[1]
+    tok = [[token(cfg, s, n - n_new + e) if n - n_new + e >= 0 else -5 for e in range(n_new)] for s, n in enumerate(lens)]
+    bd.tokens.copy_(torch.tensor(tok, dtype=torch.int32))
+    bd.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+
+
+def scatter(bd, seed):
+    """Pages in an order that is not the sequences'."""
+    flat = bd.page_table.flatten()
+    order = torch.from_numpy(np.random.RandomState(seed).permutation(flat.numel())).cuda()
+    bd.page_table.copy_(flat[order].view_as(bd.page_table))
+
+
+def check_steps(lib, cfg, prefix, n_new, steps, page=16, copy=False):
+    """steps: each step's lens.  Every step's logits, against an oracle that runs
+    the sequences one after another from the prompt's rows."""
+    W = synth.make_weights(cfg)
+    ora, dec = oracle.OracleModel(cfg, W), lib.Decoder(cfg, W)
+    if copy:
+        lib.llm_prefill_f16_copy(dec.h)
+    if prefix:
+        toks = synth.prompt(cfg, prefix)
+        ora.prefill(toks, 0)
+        lib.llm_prefill(dec.h, toks, 0)
+    n_seqs = len(steps[0])
+    bd = lib.BatchDecoder(dec, n_seqs, max(max(s) for s in steps), prefix, n_new, page)
+    scatter(bd, 5)
+    ref = [[ora.forward(token(cfg, s, e), prefix + e) for e in range(max(st[s] for st in steps))] for s in range(n_seqs)]
+    launches = lib.llm_launch_count(dec.h)
+    for lens in steps:
+        put(bd, cfg, lens)
+        bd.step()
+        lib.llm_sync(dec.h)
+        got = bd.logits.cpu().numpy()
+        for s, n in enumerate(lens):
+            for e in range(n_new):
+                if n - n_new + e >= 0:
+                    check_logits(got[s, e], ref[s][n - n_new + e], cfg.wtype, f"sequence {s} of {n}, row {e}")
+    assert bd.errors() == 0
+    assert lib.llm_launch_count(dec.h) > launches
+    dec.close()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(rope_neox=0, bias=False, tied=False, number=82),
+                                dict(wtype=synth.Q8_0, rope_neox=0, bias=False, number=83),
+                                dict(wtype=synth.Q8_0, tied=False, rope_freqs=True, number=84),
+                                dict(n_heads=4, n_kv_heads=4, head_dim=64, bias=False, number=85),
+                                dict(dim=512, n_heads=4, n_kv_heads=1, head_dim=128, vocab=1003, number=86),
+                                dict(wtype=synth.Q8_0, n_heads=16, n_kv_heads=4, head_dim=16, vocab=999, bias=False, number=87)])
+def test_steps_match_the_oracle(lib, kw):
+    check_steps(lib, config(**kw), 150, 1, [[1, 1, 1, 1, 1], [2, 2, 2, 2, 2], [3, 3, 3, 3, 3]])
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 127, 129])
+def test_prefix_lengths(lib, prefix):
+    check_steps(lib, config(), prefix, 1, [[n] * 3 for n in range(1, 6)], page=4)
+
+
+def test_several_rows_and_padding(lib):
+    # sequences that start with 5, 3, 1 rows and none, then two that stand still
+    # behind ones that go on (their rows are written again)
+    check_steps(lib, config(), 40, 5, [[5, 3, 1, 0], [10, 8, 4, 5], [15, 8, 5, 5]], page=8)
+
+
+def test_one_sequence_and_many(lib):
+    check_steps(lib, config(), 33, 1, [[1], [2]])
+    check_steps(lib, config(), 33, 2, [[2] * 100, [4] * 100], page=2)
+    check_steps(lib, config(wtype=synth.Q8_0, bias=False, number=83), 33, 1, [[1] * 40], copy=True)
+
+
+@pytest.mark.parametrize("base", [synth.QWEN2_F16, synth.LLAMA1B_Q8], ids=["qwen2-1b-f16", "llama-3.2-1b-q8_0"])
+def test_full_width_equals_sequence_by_sequence(lib, base):
+    """Two layers of the full-width models: 24 continuations of a 200-token
+    prompt, against the decode step of the same handle, one sequence at a time."""
+    import dataclasses
+    cfg = dataclasses.replace(base, n_layers=2, max_seq=256)
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    prefix, n_seqs, n = 200, 24, 3
+    lib.llm_prefill(dec.h, synth.prompt(cfg, prefix), 0)
+    bd = lib.BatchDecoder(dec, n_seqs, 16, prefix)
+    got = []
+    for i in range(n):
+        put(bd, cfg, [i + 1] * n_seqs)
+        bd.step()
+        lib.llm_sync(dec.h)
+        got.append(bd.logits[:, 0].cpu().numpy())
+    ref = np.empty(cfg.vocab, np.float32)
+    for s in range(n_seqs):
+        for i in range(n):
+            lib.llm_decode_step(dec.h, token(cfg, s, i), prefix + i, ref)
+            check_logits(got[i][s], ref, cfg.wtype, f"sequence {s}, step {i}")
+    assert bd.errors() == 0
+    dec.close()
+
+
+def test_captured_steps_feed_on_their_own_tokens(lib):
+    """Greedy steps as a user runs them: the step, the best token's log
+    probability (llm_logprobs), that token as the next step's, the lengths one
+    further; captured once, replayed, against the same steps without a graph."""
+    cfg = config()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        dec = lib.Decoder(cfg, synth.make_weights(cfg))
+        lib.llm_prefill(dec.h, synth.prompt(cfg, 60), 0)
+        runs = []
+        for graph in (False, True):
+            bd = lib.BatchDecoder(dec, 6, 32, 60)
+            lp = lib.LogProbs(bd.logits.view(6, cfg.vocab), None, top=2)
+
+            def step():
+                bd.step()
+                lp()
+                bd.tokens.copy_(lp.top_id[:, :1])
+                bd.lens.add_(1)
+
+            put(bd, cfg, [1] * 6)
+            if graph:
+                bd.step()                       # allocates before the capture; writes what the first replay writes
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=stream):
+                    step()
+            out = []
+            for _ in range(8):
+                g.replay() if graph else step()
+                out.append((lp.top_id.clone(), lp.top_logprob.clone(), lp.entropy.clone()))
+            lib.llm_sync(dec.h)
+            assert bd.errors() == 0 and bd.lens.tolist() == [9] * 6
+            runs.append(out)
+        for a, b in zip(*runs):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+        torch.cuda.synchronize()
+        dec.close()
+
+
+def test_the_handle_goes_on(lib):
+    """A batch's steps leave the handle's cache, logits and next steps as they were."""
+    cfg = config()
+    W = synth.make_weights(cfg)
+    a, b = lib.Decoder(cfg, W), lib.Decoder(cfg, W)
+    for d in (a, b):
+        lib.llm_prefill(d.h, synth.prompt(cfg, 50), 0)
+        lib.llm_decode_step(d.h, 3, 50)
+    before = [t.clone() for layer in range(2) for t in a.kv_tensors(layer)] + [a.logits_tensor().clone()]
+    bd = lib.BatchDecoder(a, 4, 20, 51)
+    for n in range(1, 4):
+        put(bd, cfg, [n] * 4)
+        bd.step()
+    lib.llm_sync(a.h)
+    after = [t for layer in range(2) for t in a.kv_tensors(layer)] + [a.logits_tensor()]
+    assert all(torch.equal(x, y) for x, y in zip(before, after))
+    x, y = np.empty(cfg.vocab, np.float32), np.empty(cfg.vocab, np.float32)
+    for run in (lambda d, o: lib.llm_decode_step(d.h, 9, 51, o), lambda d, o: lib.llm_prefill(d.h, synth.prompt(cfg, 70), 0, o)):
+        run(a, x)
+        run(b, y)
+        assert np.array_equal(x.view(np.uint32), y.view(np.uint32))
+    a.close()
+    b.close()
+
+
+def test_rows_are_independent_of_the_rest(lib):
+    """A sequence's logits do not depend on the others: the same sequence in
+    every place of the batch, and twice on the same pages."""
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 20), 0)
+    bd = lib.BatchDecoder(dec, 5, 16, 20)
+    bd.tokens.fill_(17)
+    bd.lens.fill_(1)
+    bd.page_table[4] = bd.page_table[3]                 # the same rows, written twice alike
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert all(torch.equal(bd.logits[0], bd.logits[s]) for s in range(1, 5))
+    dec.close()
+
+
+def test_tokens_and_pages_out_of_range(lib):
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 20), 0)
+    bd = lib.BatchDecoder(dec, 3, 16, 20)
+    put(bd, cfg, [1, 1, 1])
+    bd.step()
+    lib.llm_sync(dec.h)
+    want = bd.logits.clone()
+    bd.page_table[1, 0] = bd.struct.n_pages             # a page that is not there: one sequence's, reported
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert bd.errors() == lib.LLM_PAGES_BAD_PAGE
+    assert torch.equal(bd.logits[0], want[0]) and torch.equal(bd.logits[2], want[2])
+    bd.page_table[1, 0] = 1
+    bd.err.zero_()
+    bd.lens[2] = 17                                     # behind the table
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert bd.errors() == lib.LLM_PAGES_BAD_LEN
+    assert torch.equal(bd.logits[:2], want[:2])
+    bd.lens[2] = 1
+    for bad in (-1, cfg.vocab):
+        bd.tokens[1, 0] = bad
+        bd.step()
+        with pytest.raises(lib.LlmError) as e:
+            lib.llm_sync(dec.h)
+        assert e.value.status == lib.LLM_ERR_OUT_OF_RANGE
+        with pytest.raises(lib.LlmError) as e:
+            bd.step()
+        assert e.value.status == lib.LLM_ERR_STATE
+        lib.llm_reset(dec.h)
+    bd.err.zero_()
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 20), 0)
+    put(bd, cfg, [1, 1, 1])
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert torch.equal(bd.logits, want) and bd.errors() == 0
+    dec.close()
+
+
+def test_refusals(lib):
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    bd = lib.BatchDecoder(dec, 3, 16, 20)
+    logits = bd.logits.fill_(7).clone()
+    R, U, I = lib.LLM_ERR_OUT_OF_RANGE, lib.LLM_ERR_UNSUPPORTED, lib.LLM_ERR_INVALID_ARG
+    for field, value, code in [("n_seqs", -1, R), ("n_seqs", 513, R), ("n_new", 0, R), ("n_new", 171, R), ("prefix_len", -1, R),
+                               ("prefix_len", 301, R), ("max_pages", -1, R), ("max_pages", 1 << 22, R), ("page_size", 0, R),
+                               ("page_size", 24, I), ("n_pages", -1, I), ("pages", 0, I), ("pages", bd.pages.data_ptr() + 2, I),
+                               ("page_table", 0, I), ("page_table", bd.page_table.data_ptr() + 1, I), ("lens", 0, I),
+                               ("lens", bd.lens.data_ptr() + 2, I), ("tokens", 0, I), ("tokens", bd.tokens.data_ptr() + 2, I),
+                               ("logits", 0, I), ("logits", bd.logits.data_ptr() + 4, I), ("err", bd.err.data_ptr() + 2, I)]:
+        keep = getattr(bd.struct, field)
+        setattr(bd.struct, field, value)
+        with pytest.raises(lib.LlmError) as e:
+            bd.step()
+        assert e.value.status == code, (field, value)
+        setattr(bd.struct, field, keep)
+    assert lib.binding._lib.llm_decode_batch(dec.h, None) == I
+    assert lib.binding._lib.llm_batch_pages_bytes(dec.h, 3, 24) == I
+    assert lib.binding._lib.llm_batch_pages_bytes(dec.h, -1, 16) == I
+    assert lib.llm_batch_pages_bytes(dec.h, 3, 16) == 2 * 2 * 3 * 16 * 64 * 2
+    bd.struct.n_seqs = 0
+    bd.step()                                           # nothing to do
+    lib.llm_sync(dec.h)
+    assert torch.equal(bd.logits, logits)
+    dec.close()
+    for kw, code in ((dict(wtype=synth.F32, bias=False, number=88), U), (dict(dim=512, n_heads=2, n_kv_heads=1, head_dim=256, number=89), U)):
+        cfg = config(**kw)
+        dec = lib.Decoder(cfg, synth.make_weights(cfg))
+        bd = lib.BatchDecoder(dec, 3, 16, 20)
+        with pytest.raises(lib.LlmError) as e:
+            bd.step()
+        assert e.value.status == code
+        dec.close()
+
+
+def test_allocation_failure_leaves_the_handle_usable(lib):
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 20), 0)
+    bd = lib.BatchDecoder(dec, 3, 16, 20)
+    put(bd, cfg, [1, 1, 1])
+    for n in (1, 2):                                  # the attention's workspace, then the angle table
+        lib.llm_test_fail_alloc(n)
+        with pytest.raises(lib.LlmError) as e:
+            bd.step()
+        assert e.value.status == lib.LLM_ERR_NO_MEMORY
+        lib.llm_test_fail_alloc(0)
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert bool(torch.isfinite(bd.logits).all()) and bd.errors() == 0
+    dec.close()
