@@ -120,7 +120,11 @@ struct PrefixPlan {
 };
 
 constexpr int kSoftmaxWarps = 8, kPrefixThreads = 32 * (kSoftmaxWarps + 3);
-constexpr int kPrefixRegs = 88;              // with two blocks of the suffix kernel (128 x 128): 63,744 of 65,536
+// A quarter of the SM (16,384 registers) holds up to three of this kernel's warps (7,680)
+// and then two of the suffix kernel's 128 x 32: two of its blocks run beside a block of
+// this one.  With 88 registers here only one did: 256 rows of 250 pages behind 16,000
+// shared ones 84 us, 71 us with 80.
+constexpr int kPrefixRegs = 80;
 
 constexpr int kWaitLimit = 10000000;         // probes (each suspends the warp for a while) before a wait gives up
 // A whole warp's bounded wait for a phase.  The first probe stands outside the loop
@@ -204,9 +208,8 @@ __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::
 // shared memory takes 48 cycles at this width, for 32 of work.  The MMA warps walk
 // their loops whole and one elected lane issues: counters and descriptors stay in
 // uniform registers (a loop of one lane took 90 to 140 cycles an instruction); a
-// wait costs them 75 cycles and the MMAs of a product 200 to 400.  Halving the scores keeps a thread within 88 registers, so that the
-// suffix kernel's blocks fit beside a block of this one.  SPLITQ: Q as two F16
-// parts; SPLITP: P as two.
+// wait costs them 75 cycles and the MMAs of a product 200 to 400.  Halving the scores keeps a
+// thread within kPrefixRegs.  SPLITQ: Q as two F16 parts; SPLITP: P as two.
 template <int HDP, bool SPLITQ, bool SPLITP>
 __global__ void __maxnreg__(kPrefixRegs)
     prefix_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -482,6 +485,10 @@ __global__ void __maxnreg__(kPrefixRegs)
 // worker one warp: ragged lengths leave no warp waiting.
 constexpr int kSuffixWarps = 4, kMaxSeqs = 4096;
 constexpr int kQuantum = 2;                  // pieces that are worth a worker of their own
+// A unit's own cost in pieces (its query rows, its part).  48 sequences of 1 to 512 rows
+// and 32 heads: 76 us when only pieces counted (a worker of one-piece units ran twice as
+// long as the others), 62 us.
+constexpr int kUnit = 1;
 
 // Query rows of a unit.
 __host__ __device__ constexpr int unit_rows(int srows) { return srows <= 8 ? 8 : 16; }
@@ -508,6 +515,10 @@ __device__ __forceinline__ Deal deal_of(int pieces, int units, int max_workers) 
 __device__ __forceinline__ int clipped_len(const PagesDev& p, int s) {
     return (int)max(0ll, min((long long)p.lens[s], (long long)p.max_pages << p.page_shift));
 }
+
+// What a unit of a sequence of `len` rows counts in the deal: its pieces, then kUnit
+// empty ones.
+__device__ __forceinline__ int weight(int len) { return len > 0 ? (len + 15) / 16 + kUnit : 0; }
 
 // D += A B for one m16n8k16 tile with the 16 rows of A from ldmatrix.
 __device__ __forceinline__ void mma_kn8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -556,7 +567,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
         int mine = 0;
         for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
             lens[s] = clipped_len(p, s);
-            mine += (lens[s] + 15) / 16;
+            mine += weight(lens[s]);
         }
         int sum = mine;
 #pragma unroll
@@ -570,7 +581,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
         for (int w = 0; w < warp; w++) at += sums[w];
         for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
             starts[s] = at;
-            at += (lens[s] + 15) / 16;
+            at += weight(lens[s]);
             if (blockIdx.x == 0) a.starts[s + 1] = at;
         }
         if (threadIdx.x == 0) {
@@ -592,14 +603,26 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
             ((long long)starts[mid] * units <= x0 ? lo : hi) = mid;
             s = lo;
         }
-        int np = starts[s + 1] - starts[s];
+        auto next = [&](int& s, int& j, int& pc, int& np) {      // the unit behind one, at its first piece
+            pc = 0;
+            if (++j < units) return;
+            j = 0;
+            do s++;
+            while (lens[s] == 0);
+            np = (lens[s] + 15) / 16;
+        };
+        int np = (lens[s] + 15) / 16;
         const long long in_seq = x0 - (long long)starts[s] * units;
-        int j = (int)(in_seq / np), pc = (int)(in_seq % np);
-        const int n = (int)(x1 - x0), r = lane >> 2, t = lane & 3;
+        int j = (int)(in_seq / (np + kUnit)), pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
+        if (pc >= np) {                      // it starts with empty pieces
+            left -= np + kUnit - pc;
+            if (left > 0) next(s, j, pc, np);
+        }
+        const int r = lane >> 2, t = lane & 3;
         const long long pitch = (long long)p.n_kv * p.hd;
 
         // the pages of this lane's rows r and r + 8 of the piece that is loaded next
-        int ls = s, lj = j, lpc = pc, lnp = np, page[2] = {-1, -1};
+        int ls = s, lj = j, lpc = pc, lnp = np, lleft = left, page[2] = {-1, -1};
         auto look = [&]() {
 #pragma unroll
             for (int k = 0; k < 2; k++) {
@@ -607,10 +630,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                 page[k] = e < lens[ls] ? p.table[(long long)ls * p.max_pages + (e >> p.page_shift)] : INT_MIN;
             }
         };
-        look();
         uint4 kx[2][CH], vx[2][CH];          // rows r and r + 8 of the piece on its way
         bool there_x[2];                     // neither behind the sequence's last row nor on a bad page
-        auto load = [&](bool more) {         // requests the piece, moves on and looks the next one up
+        auto load = [&]() {                  // requests the piece, moves on and looks the next one up
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 there_x[k] = page[k] >= 0 && page[k] < p.n_pages;
@@ -627,22 +649,22 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     }
                 }
             }
-            if (more) {
-                if (++lpc == lnp) {
-                    lpc = 0;
-                    if (++lj == units) {
-                        lj = 0;
-                        do lnp = starts[ls + 2] - starts[ls + 1], ls++;
-                        while (lnp == 0);
-                    }
+            lleft--;
+            if (++lpc == lnp) {
+                lleft -= kUnit;
+                if (lleft > 0) {
+                    next(ls, lj, lpc, lnp);
                 }
-                look();
             }
+            if (lleft > 0) look();
         };
-        load(n > 1);
-        for (int it = 0; it < n;) {
+        if (left > 0) {
+            look();
+            load();
+        }
+        while (left > 0) {
             // ---- one unit: pieces pc .. of its np, as far as this worker goes
-            const int tile = j % rt, g = j / rt, count = min(n - it, np - pc);
+            const int tile = j % rt, g = j / rt, count = min(left, np - pc);
             const int last = p.lens[s] - p.n_new, e_min = last + tile * RU / a.gq;
             // q as the second operand: query row r of each eight; rows behind the last repeat it (never stored)
             uint32_t qhi[NT][2 * CH][2], qlo[NT][SPLITQ ? 2 * CH : 1][2];
@@ -672,7 +694,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                 M[q][0] = M[q][1] = -1e30f;  // no key seen yet: low, but a number
                 l[q][0] = l[q][1] = 0.f;
             }
-            for (int i0 = 0; i0 < count; i0++, it++) {
+            for (int i0 = 0; i0 < count; i0++) {
                 uint32_t k0[4 * CH], k1[4 * CH], v0[4 * CH], v1[4 * CH];     // rows r (0) and r + 8 (1)
 #pragma unroll
                 for (int i = 0; i < CH; i++) {
@@ -682,7 +704,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     v1[4 * i] = vx[1][i].x; v1[4 * i + 1] = vx[1][i].y; v1[4 * i + 2] = vx[1][i].z; v1[4 * i + 3] = vx[1][i].w;
                 }
                 const bool there[2] = {there_x[0], there_x[1]};
-                if (it + 1 < n) load(it + 2 < n);
+                if (lleft > 0) load();
                 float sc[NT][4];
 #pragma unroll
                 for (int q = 0; q < NT; q++) {
@@ -804,12 +826,8 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     }
                     if (r == 0) a.suffix_ml[slot + row] = make_float2(M[q][k], l[q][k]);
                 }
-            pc = 0;
-            if (it < n && ++j == units) {
-                j = 0;
-                do np = starts[s + 2] - starts[s + 1], s++;
-                while (np == 0);
-            }
+            left -= count + kUnit;
+            if (left > 0) next(s, j, pc, np);
         }
     }
     // this grid's end is the prefix kernel's too, for the join; only the last block waits for it, so
@@ -834,7 +852,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
     const int token = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
     const int s = token / p.n_new, i = token % p.n_new, g = h / a.gq, hq = h % a.gq;
     const int len = p.lens[s];
-    if (len - p.n_new + i < 0) {             // padding
+    if (len < p.n_new - i) {                 // padding
         griddep_wait();
         return;
     }
@@ -858,9 +876,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         const Deal deal = deal_of(a.starts[p.n_seqs], p.n_kv * rt, a.suffix_workers);
         if (pieces > 0) {
             const int j = g * rt + row / ru;
-            const long long x = (long long)b * deal.units + (long long)j * pieces;
+            const long long x = (long long)b * deal.units + (long long)j * pieces;           // (pieces: kUnit empty ones among them)
             const long long w0 = owner_of(x, deal.workers, deal.total);
-            ns = (int)(owner_of(x + pieces - 1, deal.workers, deal.total) - w0) + 1;
+            ns = (int)(owner_of(x + pieces - kUnit - 1, deal.workers, deal.total) - w0) + 1;
             suf = ((long long)s * deal.units + j + w0) * step + row % ru;
         }
     }
@@ -949,7 +967,7 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
         // longest sequences could keep busy
         const int ru = unit_rows((int)srows);
         const long long units = (long long)p->n_kv_heads * ((srows + ru - 1) / ru),
-                        most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16),
+                        most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16 + kUnit),
                         blocks = (most + kQuantum * kSuffixWarps - 1) / (kQuantum * kSuffixWarps);
         const int ctas = suffix_ctas(p->head_dim <= 64 ? 64 : 128, ru / 8);
         pl.suffix_blocks = (int)std::max<long long>(1, std::min<long long>(blocks, (long long)ctas * sms));
