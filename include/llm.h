@@ -405,7 +405,7 @@ int llm_rope_table(float *cos_sin, int32_t pos0, int32_t n_pos, int32_t rope_dim
  * of one fused projection's rows).  q_out (q_out_dtype) receives the rotated q
  * and may be q itself (same type and stride); n_heads = 0: k and v only.
  * cos_sin: the angle table of positions 0 .. table_rows-1 (llm_rope_table's
- * layout, pos0 = 0). */
+ * layout, pos0 = 0); rope_dims = 0: no rotation and no table. */
 typedef struct {
     int32_t n_heads, rope_dims, rope_neox;   /* as in llm_config */
     int32_t table_rows;
@@ -422,9 +422,10 @@ typedef struct {
  * nearest even) and q into q_out.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int llm_kv_append(const llm_pages *pages, const llm_append *a, llm_stream_t stream);
 
-/* Attention of the new rows, of at most 4096 sequences.  q [rows][n_heads][head_dim] (dtype q_dtype, row
- * stride q_stride), out likewise; LLM_F32 or LLM_F16 each; 16-byte aligned,
- * strides multiples of 16 bytes.  n_heads is a multiple of n_kv_heads; head h
+/* Attention of the new rows, of at most 4096 sequences and 2^25 rows of all
+ * heads together.  q [rows][n_heads][head_dim] (dtype q_dtype, row stride
+ * q_stride), out likewise; LLM_F32 or LLM_F16 each; 16-byte aligned, strides
+ * multiples of 16 bytes.  n_heads is a multiple of n_kv_heads; head h
  * reads kv head h / (n_heads / n_kv_heads).  prefix_k, prefix_v: rows
  * 0..prefix_len-1 of the shared prefix, FP16, kv head g of row t at t *
  * prefix_stride + g * head_dim (16-byte aligned, the stride a multiple of 8 and
@@ -472,7 +473,7 @@ int64_t llm_attend_batch_workspace(const llm_pages *pages, const llm_attend *a);
  * probability 0 (logprob -infinity, no part in the entropy).  A row with no
  * other logits gives logprob -infinity and entropy 0; a row with a NaN or
  * +infinity gives NaN, its top_id by the logits that are numbers (-1 where
- * there are fewer than top).  DEVICE pointers; n_rows >= 0, vocab >= 1.
+ * there are fewer than top).  DEVICE pointers; n_rows >= 0, 1 <= vocab <= 2^30.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 typedef struct {
     int32_t n_rows, vocab, dtype, n_targets, top;

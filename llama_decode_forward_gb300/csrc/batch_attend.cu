@@ -849,6 +849,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         griddep_wait();                      // (every path: this grid must not end before those it follows)
         return;
     }
+    if (a.prefix_blocks == 0 && a.suffix_workers == 0) griddep_wait();       // the lengths, otherwise known (below)
     const int token = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
     const int s = token / p.n_new, i = token % p.n_new, g = h / a.gq, hq = h % a.gq;
     const int len = p.lens[s];
@@ -1044,6 +1045,7 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
         return fail_op(LLM_ERR_INVALID_ARG, "n_heads %d is not a multiple of n_kv_heads %d", a->n_heads, p->n_kv_heads);
     if (((long long)p->max_pages * p->page_size / 16 + 1) > (1ll << 50) / std::max(1ll, (long long)p->n_seqs * p->n_new * a->n_heads))
         return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold too many rows for that many heads");
+    if (p->prefix_len > INT_MAX - kKT) return fail_op(LLM_ERR_UNSUPPORTED, "prefix_len %d exceeds 2^31 - 65", p->prefix_len);
     if (p->n_seqs > kMaxSeqs) return fail_op(LLM_ERR_UNSUPPORTED, "n_seqs %d exceeds %d", p->n_seqs, kMaxSeqs);
     if ((long long)p->n_seqs * ((long long)p->max_pages * p->page_size / 16 + 1) > INT_MAX / 2)
         return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold more than 2^34 rows together");

@@ -124,10 +124,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         load_n<W>(x + f.a, u);
         load_n<W>(x + f.b, w);
     }
-    const int s = a.by_new.of(row), e = p.lens[s] - p.n_new + (row - s * p.n_new);
-    if (e < 0) return;                       // padding
+    const int s = a.by_new.of(row), len = p.lens[s], behind = p.n_new - (row - s * p.n_new);
+    if (len < behind) return;                // padding
+    const int e = len - behind;
     const long long pos = (long long)p.prefix_len + e;
-    if (pos >= a.table_rows) {
+    if (pos >= a.table_rows && a.half > 0) {
         flag(p.err, LLM_PAGES_BAD_LEN);
         return;
     }

@@ -873,7 +873,8 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     const long long positions = (long long)b->prefix_len + (long long)b->max_pages * b->page_size;
     if (b->max_pages < 0 || b->page_size < 1 || positions > (1 << 24))
         return fail(h, LLM_ERR_OUT_OF_RANGE, "max_pages or page_size is out of range, or positions exceed 2^24");
-    if (!b->page_table || !b->lens || !b->tokens || !b->logits || !b->pages) return fail(h, LLM_ERR_INVALID_ARG, "NULL argument");
+    if (b->n_seqs > 0 && (!b->lens || !b->tokens || !b->logits || (b->max_pages > 0 && (!b->page_table || !b->pages))))
+        return fail(h, LLM_ERR_INVALID_ARG, "a pointer of the batch is NULL");
     if ((reinterpret_cast<uintptr_t>(b->logits) & 15) || (reinterpret_cast<uintptr_t>(b->pages) & 15) ||
         ((reinterpret_cast<uintptr_t>(b->tokens) | reinterpret_cast<uintptr_t>(b->lens) | reinterpret_cast<uintptr_t>(b->page_table) |
           reinterpret_cast<uintptr_t>(b->err)) & 3))

@@ -133,6 +133,12 @@ def test_rope_table_refused(args):
     refused(B._lib.llm_rope_table(*args, None, None), BAD)
 
 
+def test_attend_refuses_a_prefix_at_the_end_of_32_bits():
+    for n, status in (((1 << 31) - 1, UNSUP), ((1 << 31) - 64, UNSUP)):
+        refused(B._lib.llm_attend_batch_workspace(ref(pages(prefix_len=n)), ref(attend())), status)
+    assert B._lib.llm_attend_batch_workspace(ref(pages(prefix_len=(1 << 31) - 65)), ref(attend())) > 0
+
+
 def test_null_structs_refused():
     refused(B._lib.llm_kv_append(None, ref(append()), None), BAD)
     refused(B._lib.llm_kv_append(ref(pages()), None, None), BAD)

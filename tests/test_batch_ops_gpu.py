@@ -154,6 +154,31 @@ def test_append_page_sizes_and_strides(lib, page):
     assert torch.equal(q, q_out)
 
 
+def test_append_without_rotation_needs_no_table(lib):
+    b = Batch(lib, [5, 17], 2, 1000, 16, 2, 64)
+    k, v = rand(1, 4, 2, 64), rand(2, 4, 2, 64)
+    before = b.k.clone(), b.v.clone()
+    op = lib.KvAppend(b.pages, None, k, v, torch.zeros(0, 0, 2, device="cuda"))
+    op()
+    check_append(b, before, None, k, v, None, torch.zeros(1017, 0, 2), False, 0)
+    assert b.pages.errors() == 0
+
+
+@pytest.mark.parametrize("n", [-1, -(1 << 31), 1 - (1 << 31)])
+def test_lengths_below_zero_are_padding(lib, n):
+    b = Batch(lib, [4, 0, 2], 2, 0, 16, 2, 64, poison=False)
+    b.lens_dev[1] = n
+    before = b.k.clone()
+    q, k, v = rand(3, 6, 4, 64), rand(1, 6, 2, 64), rand(2, 6, 2, 64)
+    lib.KvAppend(b.pages, None, k, v, rand(4, 8, 32, 2))()
+    changed = {(int(p), int(r)) for p, r in (b.k != before).any(-1).any(-1).nonzero()}
+    assert changed == {tuple(map(int, b.slot(s, e))) for s, e in ((0, 2), (0, 3), (2, 0), (2, 1))}
+    out = torch.full_like(q, 7.0)
+    lib.AttendBatch(b.pages, q, out)()
+    assert (out[2:4] == 7.0).all() and not (out[[0, 1, 4, 5]] == 7.0).any()
+    assert b.pages.errors() == 0
+
+
 def test_append_bad_places_are_flagged_and_skipped(lib):
     b = Batch(lib, [16, 20, 33, 4], 2, 0, 16, 1, 32, poison=False)
     b.table[0, 0] = b.n_pages                # a page behind the pool

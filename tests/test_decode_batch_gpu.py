@@ -274,8 +274,8 @@ def test_refusals(lib):
     assert lib.binding._lib.llm_batch_pages_bytes(dec.h, 3, 24) == I
     assert lib.binding._lib.llm_batch_pages_bytes(dec.h, -1, 16) == I
     assert lib.llm_batch_pages_bytes(dec.h, 3, 16) == 2 * 2 * 3 * 16 * 64 * 2
-    bd.struct.n_seqs = 0
-    bd.step()                                           # nothing to do
+    empty = lib.llm_batch(n_seqs=0, n_new=1, prefix_len=5, page_size=16)
+    lib.llm_decode_batch(dec.h, empty)                  # nothing to do
     lib.llm_sync(dec.h)
     assert torch.equal(bd.logits, logits)
     dec.close()
