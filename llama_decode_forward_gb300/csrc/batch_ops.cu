@@ -47,7 +47,7 @@ __device__ __forceinline__ void load_n(const float* p, float (&x)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void load_n(const __half* p, float (&x)[N]) {
-    uint32_t w[N / 2];
+    __align__(16) uint32_t w[N / 2];
     if (N == 8) *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p);
     else *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p);
 #pragma unroll
@@ -64,7 +64,7 @@ __device__ __forceinline__ void store_n(float* p, const float (&x)[N]) {
 }
 template <int N>
 __device__ __forceinline__ void store_n(__half* p, const float (&x)[N]) {
-    uint32_t w[N / 2];
+    __align__(16) uint32_t w[N / 2];
 #pragma unroll
     for (int k = 0; k < N / 2; k++) w[k] = h2_bits(__float2half_rn(x[2 * k]), __float2half_rn(x[2 * k + 1]));
     if (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
@@ -199,12 +199,16 @@ cudaError_t launch_append(cudaStream_t st, const PagesDev& pd, const AppendDev& 
 // A key (argmax_key) orders by value, then by the lower index.  A warp looks at
 // its logits one by one only when one of them reaches the floor: a key that at
 // least `top` keys of the row are known to reach.  For a warp's first logits that
-// is the top-th largest of its lanes' largest; later its own top-th key, or another
-// warp's, through shared memory.  Keys that reach it wait in shared memory; 32 of
-// them are sorted into the warp's list (lane i the i-th) at a time.  At the end the
-// few keys of a block that reach its floor are ranked by counting the larger ones.
+// is the top-th largest of its lanes' largest; later its own top-th key, or the
+// block's, through shared memory.  Keys that reach it wait in shared memory; 32 of
+// them are sorted into the warp's list (lane i the i-th) at a time.  After steps 1,
+// 4, 16, ... and at the end the keys of a block that reach its floor are ranked by
+// counting the larger ones, and the top-th becomes its floor.  512 rows of 151,936
+// with eight alternatives: 78 us without those ranks (a warp then meets some 37 keys
+// that reach its floor, in every other step), 68 us with them.
 constexpr int kLpElems = 16;                 // logits of a lane per step
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kDown = 1.f / 16384.f;       // a power of two: x * kDown is exact
 
 struct LpStat {
     float m, s, t;
@@ -323,9 +327,9 @@ __device__ __forceinline__ void put_in_order(u64* list, int n, int top, u64* bes
     }
 }
 
-// NT threads a block: 512 for few rows (the shortest chain), 128 for many (a warp
-// then sees more of its row, and finds the floor sooner; 512 rows of 151,936: 114 us
-// with 512 threads a block).
+// NT threads a block: 512 for few rows (the shortest chain), 256 for many (512 rows of
+// 151,936, before the block's floor: 79 us, and 85 us with 128 threads and two blocks a
+// row, 114 us with 512 threads).
 template <class T, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_constant__ llm_logprobs_args a) {
     constexpr int VE = 16 / sizeof(T), NV = kLpElems / VE;     // elements of a 16-byte load, loads of a lane per step
@@ -381,115 +385,148 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
         if (last > floor && lane == 0) atomicMax(&floor_all, last);
         raise(last);
     };
+    auto take = [&](u64 key, u64 f) {        // a warp's keys that reach f into the block's list
+        const uint32_t who = __ballot_sync(0xffffffffu, key != 0 && key >= f);
+        int at = 0;
+        if (lane == 0 && who) at = atomicAdd(&count, __popc(who));
+        at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
+        if ((who >> lane) & 1u) list[at] = key;
+    };
     const int first = w0 + warp * STEP;
     if (first < w1 && whole(first)) fetch(first);
-    for (int b = first; b < w1; b += NW * STEP) {
-        float v[kLpElems];
-        const bool inside = whole(b);
-        if (inside) {
+    // (every warp walks as many steps: the last of one may lie behind the block's words)
+    for (int b = first, step = 0, next = 0; w0 + step * NW * STEP < w1; b += NW * STEP, step++) {
+        if (b < w1) {
+            float v[kLpElems];
+            const bool inside = whole(b);
+            if (inside) {
 #pragma unroll
-            for (int k = 0; k < NV; k++) {
-                const uint32_t us[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                for (int k = 0; k < NV; k++) {
+                    const uint32_t us[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (sizeof(T) == 4) {
-                        v[k * VE + i] = __uint_as_float(us[i]);
-                    } else {
-                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&us[i]));
-                        v[k * VE + 2 * i] = f.x;
-                        v[k * VE + (VE == 8 ? 2 * i + 1 : 0)] = f.y;
+                    for (int i = 0; i < 4; i++) {
+                        if (sizeof(T) == 4) {
+                            v[k * VE + i] = __uint_as_float(us[i]);
+                        } else {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&us[i]));
+                            v[k * VE + 2 * i] = f.x;
+                            v[k * VE + (VE == 8 ? 2 * i + 1 : 0)] = f.y;
+                        }
                     }
                 }
+            } else {
+#pragma unroll
+                for (int k = 0; k < NV; k++)
+#pragma unroll
+                    for (int i = 0; i < VE; i++) {
+                        const int w = b + k * 32 + lane, e = w * VE - lead + i;
+                        v[k * VE + i] = w < w1 && e >= 0 && e < a.vocab ? to_f32(x[e]) : -INFINITY;
+                    }
             }
-        } else {
+            if (b + NW * STEP < w1 && whole(b + NW * STEP)) fetch(b + NW * STEP);
+            float bm = max3_nan(v[0], v[1], v[2]);
 #pragma unroll
-            for (int k = 0; k < NV; k++)
+            for (int i = 3; i < kLpElems; i += 2) bm = max3_nan(bm, v[i], i + 1 < kLpElems ? v[i + 1] : v[i]);
+            if (bm != bm) {                      // a NaN makes the row's sum one; the largest is the numbers'
+                st.s = NAN;
+                bm = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < VE; i++) {
-                    const int w = b + k * 32 + lane, e = w * VE - lead + i;
-                    v[k * VE + i] = w < w1 && e >= 0 && e < a.vocab ? to_f32(x[e]) : -INFINITY;
+                for (int i = 0; i < kLpElems; i++) bm = fmaxf(bm, v[i]);
+            }
+            if (bm > st.m) {
+                const float d = st.m - bm, c = exp2f(d * kLog2e);
+                st.t = st.s == 0.f ? 0.f : c * (st.t + st.s * d);
+                st.s *= c;
+                st.m = bm;
+            }
+            if (st.m > -INFINITY) {
+                // two pairs of sums side by side.  w = (m - x) / 2^14, cut off at 1 by the rounding's
+                // saturation: an x of -infinity gives e = 0 and a product of 0 (with a maximum for
+                // each x instead 512 rows of 151,936 took 1.3 us more)
+                float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float md = st.m * kDown;
+                const float2 up2 = make_float2(-kLog2e / kDown, -kLog2e / kDown);
+#pragma unroll
+                for (int i = 0; i < kLpElems; i += 2) {
+                    const float2 w = make_float2(__saturatef(fmaf(v[i], -kDown, md)), __saturatef(fmaf(v[i + 1], -kDown, md)));
+                    const float2 y = __fmul2_rn(w, up2);
+                    float2 e;
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
+                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
+                    s[(i >> 1) & 1] = __fadd2_rn(s[(i >> 1) & 1], e);
+                    t[(i >> 1) & 1] = __ffma2_rn(e, w, t[(i >> 1) & 1]);
                 }
-        }
-        if (b + NW * STEP < w1 && whole(b + NW * STEP)) fetch(b + NW * STEP);
-        float bm = fmaxf(v[0], v[1]);
-#pragma unroll
-        for (int i = 2; i < kLpElems; i += 2) bm = max3(bm, v[i], v[i + 1]);
-        if (bm > st.m) {
-            const float d = st.m - bm, c = exp2f(d * kLog2e);
-            st.t = st.s == 0.f ? 0.f : c * (st.t + st.s * d);
-            st.s *= c;
-            st.m = bm;
-        }
-        if (st.m > -INFINITY) {
-            // two pairs of sums side by side; -infinity - m gives e = 0, whose (x - m) is cut off at a number
-            float2 s[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            const float2 m2 = make_float2(-st.m, -st.m), log2e = make_float2(kLog2e, kLog2e);
-#pragma unroll
-            for (int i = 0; i < kLpElems; i += 2) {
-                const float2 d = __fadd2_rn(make_float2(v[i], v[i + 1]), m2), y = __fmul2_rn(d, log2e);
-                float2 e;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(y.x));
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(y.y));
-                s[(i >> 1) & 1] = __fadd2_rn(s[(i >> 1) & 1], e);
-                t[(i >> 1) & 1] = __ffma2_rn(e, make_float2(fmaxf(d.x, -1e4f), fmaxf(d.y, -1e4f)), t[(i >> 1) & 1]);
+                st.s += (s[0].x + s[0].y) + (s[1].x + s[1].y);
+                st.t = fmaf((t[0].x + t[0].y) + (t[1].x + t[1].y), -1.f / kDown, st.t);
             }
-            st.s += (s[0].x + s[0].y) + (s[1].x + s[1].y);
-            st.t += (t[0].x + t[0].y) + (t[1].x + t[1].y);
-        } else {
+            if (top == 0) continue;
+            if (step == 0) {
+                // (+ 0: a largest of -0 stands for equal +0s too.)  Many alternatives: of the lanes' two
+                // largest each, or the last lanes' poor ones would let half of the logits through
+                // (a lane without an element of the row has -infinity and counts as none)
+                uint32_t near = sort32(inside || bm > -INFINITY ? order_of(bm + 0.f) : 0u, lane);
+                if (top > 24) {
+                    float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kLpElems; i++)
-                if (v[i] != v[i]) st.s = NAN;
-        }
-        if (top == 0) continue;
-        if (b == first) {
-            // (+ 0: a largest of -0 stands for equal +0s too.)  Many alternatives: of the lanes' two
-            // largest each, or the last lanes' poor ones would let half of the logits through
-            // (a lane without an element of the row has -infinity and counts as none)
-            uint32_t near = sort32(inside || bm > -INFINITY ? order_of(bm + 0.f) : 0u, lane);
-            if (top > 24) {
-                float m1 = -INFINITY, m2 = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < kLpElems; i++) {
-                    m2 = fmaxf(m2, fminf(m1, v[i]));
-                    m1 = fmaxf(m1, v[i]);
+                    for (int i = 0; i < kLpElems; i++) {
+                        m2 = fmaxf(m2, fminf(m1, v[i]));
+                        m1 = fmaxf(m1, v[i]);
+                    }
+                    near = merge32(near, sort32(inside || m2 > -INFINITY ? order_of(m2 + 0.f) : 0u, lane), lane);
                 }
-                near = merge32(near, sort32(inside || m2 > -INFINITY ? order_of(m2 + 0.f) : 0u, lane), lane);
+                const uint32_t bound = __shfl_sync(0xffffffffu, near, top - 1);
+                raise((u64)bound << 32);
+                if (bound && lane == 0) atomicMax(&floor_all, floor);
             }
-            const uint32_t bound = __shfl_sync(0xffffffffu, near, top - 1);
-            raise((u64)bound << 32);
-            if (bound && lane == 0) atomicMax(&floor_all, floor);
+            uint32_t mask = 0;
+            if (__any_sync(0xffffffffu, bm >= floor_v)) {
+                raise(*static_cast<volatile u64*>(&floor_all));       // (only here: the other warps' floor seldom matters sooner)
+#pragma unroll
+                for (int i = 0; i < kLpElems; i++) mask |= v[i] >= floor_v ? 1u << i : 0u;
+            }
+            while (__any_sync(0xffffffffu, mask)) {
+                const int i = __ffs(mask) - 1;
+                u64 key = 0;
+                if (mask) {
+                    float z = v[0];
+#pragma unroll
+                    for (int k = 1; k < kLpElems; k++) z = k == i ? v[k] : z;
+                    const int e = (b + (i / VE) * 32 + lane) * VE - lead + i % VE;
+                    if (inside || (b + (i / VE) * 32 + lane < w1 && e >= 0 && e < a.vocab))
+                        key = argmax_key(z + 0.f, e);              // -0 + 0 = +0: equal values, equal order
+                    mask &= mask - 1;
+                }
+                const bool in = key != 0 && key >= floor;
+                const uint32_t who = __ballot_sync(0xffffffffu, in);
+                if (in) wait[warp][waiting + __popc(who & ((1u << lane) - 1))] = key;
+                waiting += __popc(who);
+                __syncwarp();
+                if (waiting >= 32) {
+                    sort_in(wait[warp][lane]);
+                    const u64 rest = wait[warp][32 + lane];
+                    __syncwarp();
+                    wait[warp][lane] = rest;
+                    waiting -= 32;
+                    __syncwarp();
+                }
+            }
         }
-        if (!__any_sync(0xffffffffu, bm >= floor_v)) continue;
-        raise(*static_cast<volatile u64*>(&floor_all));       // (only here: the other warps' floor seldom matters sooner)
-        if (!__any_sync(0xffffffffu, bm >= floor_v)) continue;
-        uint32_t mask = 0;
-#pragma unroll
-        for (int i = 0; i < kLpElems; i++) mask |= v[i] >= floor_v ? 1u << i : 0u;
-        while (__any_sync(0xffffffffu, mask)) {
-            const int i = __ffs(mask) - 1;
-            u64 key = 0;
-            if (mask) {
-                float z = v[0];
-#pragma unroll
-                for (int k = 1; k < kLpElems; k++) z = k == i ? v[k] : z;
-                const int e = (b + (i / VE) * 32 + lane) * VE - lead + i % VE;
-                if (inside || (b + (i / VE) * 32 + lane < w1 && e >= 0 && e < a.vocab))
-                    key = argmax_key(z + 0.f, e);              // -0 + 0 = +0: equal values, equal order
-                mask &= mask - 1;
-            }
-            const bool in = key != 0 && key >= floor;
-            const uint32_t who = __ballot_sync(0xffffffffu, in);
-            if (in) wait[warp][waiting + __popc(who & ((1u << lane) - 1))] = key;
-            waiting += __popc(who);
-            __syncwarp();
-            if (waiting >= 32) {
-                sort_in(wait[warp][lane]);
-                const u64 rest = wait[warp][32 + lane];
-                __syncwarp();
-                wait[warp][lane] = rest;
-                waiting -= 32;
-                __syncwarp();
-            }
+        if (step == next && w0 + (step + 1) * NW * STEP < w1) {
+            // after steps 1, 4, 16, ... the top-th largest key that the block knows becomes its floor
+            next = 4 * next + 3;
+            __syncthreads();
+            const u64 f = floor_all;
+            take(keys, f);
+            take(lane < waiting ? wait[warp][lane] : 0ull, f);
+            __syncthreads();
+            const int n = count;
+            if (threadIdx.x < 8) list[n + threadIdx.x] = 0;
+            __syncthreads();
+            if (threadIdx.x == 0) count = 0;
+            for (int i = threadIdx.x; i < n; i += NT)
+                if (rank_of(list[i], list, n) == top - 1) floor_all = list[i];
+            __syncthreads();
+            raise(floor_all);
         }
     }
     // many alternatives: the warp's own top-th key as a floor leaves the block fewer to rank
@@ -505,21 +542,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
                 if (rank_of(wait[warp][i], wait[warp], waiting) == top - 1) atomicMax(&floor_all, wait[warp][i]);
         }
     }
+    if (st.m == INFINITY) st.s = NAN;        // (+infinity less itself was cut off too)
     st = lp_join_warp<16>(st);
     if (lane == 0) stat[warp] = st;
     __syncthreads();                         // the floor is the block's now
     if (top > 0) {
         // the keys that reach it, from the lists and the waiting ones; of these the largest in order
         const u64 f = floor_all;
-        auto take = [&](u64 key) {
-            const uint32_t who = __ballot_sync(0xffffffffu, key != 0 && key >= f);
-            int at = 0;
-            if (lane == 0 && who) at = atomicAdd(&count, __popc(who));
-            at = __shfl_sync(0xffffffffu, at, 0) + __popc(who & ((1u << lane) - 1));
-            if ((who >> lane) & 1u) list[at] = key;
-        };
-        take(keys);
-        take(lane < waiting ? wait[warp][lane] : 0ull);
+        take(keys, f);
+        take(lane < waiting ? wait[warp][lane] : 0ull, f);
         __syncthreads();
         put_in_order<NT>(list, count, top, best);
     }
@@ -607,7 +638,7 @@ cudaError_t launch_logprobs(const llm_logprobs_args& a, int blocks, cudaStream_t
 
 // Few rows (not one for each SM): blocks of 512 threads, enough of them to give
 // every SM two, none with less than one step's logits, at most 16 a row (beyond 8
-// by opt-in).  More rows: blocks of 128, six or more for each SM.
+// by opt-in).  More rows: blocks of 256, three or more for each SM.
 template <class T>
 cudaError_t launch_logprobs(const llm_logprobs_args& a, cudaStream_t st) {
     const int sms = sm_count();
@@ -616,8 +647,8 @@ cudaError_t launch_logprobs(const llm_logprobs_args& a, cudaStream_t st) {
         while (blocks < 16 && (long long)a.n_rows * blocks < 2 * sms && a.vocab > blocks * 512 * kLpElems) blocks *= 2;
         return launch_logprobs<T, 512>(a, blocks, st);
     }
-    while (blocks < 16 && (long long)a.n_rows * blocks < 6 * sms && a.vocab > blocks * 128 * kLpElems) blocks *= 2;
-    return launch_logprobs<T, 128>(a, blocks, st);
+    while (blocks < 16 && (long long)a.n_rows * blocks < 3 * sms && a.vocab > blocks * 256 * kLpElems) blocks *= 2;
+    return launch_logprobs<T, 256>(a, blocks, st);
 }
 
 }  // namespace
