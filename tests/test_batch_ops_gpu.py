@@ -749,3 +749,49 @@ def test_empty_batches(lib):
     lib.LogProbs(torch.zeros(0, 50, device="cuda"), top=3)()
     torch.cuda.synchronize()
     assert pages.errors() == 0
+
+
+def test_calls_at_the_same_time(lib):
+    """Two streams run attention (a prefix each, a workspace each) and log probabilities
+    side by side; every run gives the bits of a run alone."""
+    def make(seed):
+        b = Batch(lib, [int(n) for n in np.random.RandomState(seed).randint(1, 200, 24)], 1, 3000, 16, 8, 64, seed=seed)
+        pk, pv = (rand(seed + i, 3000, 8, 64, dtype=F16) for i in (3, 4))
+        q, out = rand(seed + 5, 24, 32, 64), torch.zeros(24, 32, 64, device="cuda")
+        return lib.AttendBatch(b.pages, q, out, pk, pv), out, lib.LogProbs(rand(seed + 6, 40, 30000), None, top=4)
+    sides = [make(100), make(200)]
+    alone = []
+    for attend, out, lp in sides:
+        attend()
+        lp()
+        alone.append([t.clone() for t in (out, lp.top_id, lp.top_logprob, lp.entropy)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sides]
+    for _ in range(10):
+        for s, (attend, out, lp) in zip(streams, sides):
+            with torch.cuda.stream(s):
+                out.zero_()
+                attend()
+                lp()
+        torch.cuda.synchronize()
+        for (attend, out, lp), want in zip(sides, alone):
+            assert all(torch.equal(x, y) for x, y in zip((out, lp.top_id, lp.top_logprob, lp.entropy), want))
+
+
+@pytest.mark.parametrize("top", [1, 8, 32])
+def test_logprobs_long_rows_that_rise(lib, top):
+    """Rows of many steps whose largest logits come last, first, or all over: the floor of
+    a block rises at every rank, or never again.  Few rows take a cluster of blocks each,
+    many one block: the same tokens, and values that are each within their bound."""
+    n = 90000
+    base = torch.linspace(-5, 5, n)
+    shuffled = base[torch.randperm(n, generator=torch.Generator().manual_seed(1))]
+    x = torch.stack([base, base.flip(0), shuffled, torch.zeros(n), base.round()]).cuda()
+    few = check_logprobs(lib, x, None, top)
+    many = lib.LogProbs(x.repeat(120, 1), None, top=top)
+    many()
+    assert torch.equal(many.top_id, few.top_id.repeat(120, 1))
+    d = x.double().cpu()
+    logp = torch.log_softmax(d, -1)
+    bound = logprob_bound(d, logp, n)[1].gather(1, few.top_id.long().cpu()).repeat(120, 1)
+    assert ((many.top_logprob - few.top_logprob.repeat(120, 1)).abs().double().cpu() <= 2 * bound).all()

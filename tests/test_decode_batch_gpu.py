@@ -105,6 +105,46 @@ def test_one_sequence_and_many(lib):
     check_steps(lib, config(wtype=synth.Q8_0, bias=False, number=83), 33, 1, [[1] * 40], copy=True)
 
 
+@pytest.mark.parametrize("n_seqs,n_new", [(1, 512), (512, 1), (4, 128)])
+def test_the_most_rows(lib, n_seqs, n_new):
+    check_steps(lib, config(max_seq=600), 30, n_new, [[n_new] * n_seqs], page=32)
+
+
+def test_two_batches_on_one_prompt(lib):
+    """Two batches take turns on one handle, one of them sharing a full page between its
+    sequences; each goes on as if it were alone."""
+    cfg = config()
+    W = synth.make_weights(cfg)
+    ora, dec = oracle.OracleModel(cfg, W), lib.Decoder(cfg, W)
+    toks = synth.prompt(cfg, 25)
+    ora.prefill(toks, 0)
+    lib.llm_prefill(dec.h, toks, 0)
+    a, b = lib.BatchDecoder(dec, 2, 12, 25, page_size=4), lib.BatchDecoder(dec, 3, 8, 25, n_new=2)
+    common = [3, 1, 4, 1]                               # four rows that both sequences of a share
+    a.page_table[1, 0] = a.page_table[0, 0]
+    for e, t in enumerate(common):
+        a.tokens.fill_(t)
+        a.lens.copy_(torch.tensor([e + 1, 0], dtype=torch.int32))          # written once, by sequence 0
+        a.step()
+    for n in range(4):
+        a.tokens.copy_(torch.tensor([[token(cfg, s, 4 + n)] for s in range(2)], dtype=torch.int32))
+        a.lens.fill_(5 + n)
+        a.step()
+        put(b, cfg, [2 * n + 2] * 3)
+        b.step()
+    lib.llm_sync(dec.h)
+    for s in range(2):
+        for e, t in enumerate(common + [token(cfg, s, 4 + n) for n in range(4)]):
+            ref = ora.forward(t, 25 + e)
+        check_logits(a.logits[s, 0].cpu().numpy(), ref, cfg.wtype, f"batch a, sequence {s}")
+    for s in range(3):
+        for e in range(8):
+            ref = ora.forward(token(cfg, s, e), 25 + e)
+        check_logits(b.logits[s, 1].cpu().numpy(), ref, cfg.wtype, f"batch b, sequence {s}")
+    assert a.errors() == 0 and b.errors() == 0
+    dec.close()
+
+
 @pytest.mark.parametrize("base", [synth.QWEN2_F16, synth.LLAMA1B_Q8], ids=["qwen2-1b-f16", "llama-3.2-1b-q8_0"])
 def test_full_width_equals_sequence_by_sequence(lib, base):
     """Two layers of the full-width models: 24 continuations of a 200-token
