@@ -40,6 +40,7 @@ struct AttendDev {
     float2* suffix_ml;
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
     int prefix_blocks, suffix_workers;
+    Div by_heads, by_new, by_gq;            // the join's divisions
 };
 
 // Probabilities are kept as 2^(y - M) with M = (a recent maximum) - kHead, so
@@ -843,15 +844,15 @@ template <int LP>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a) {
     constexpr int GROUPS = 32 / LP, AHEAD = 8;
     griddep_launch();
-    const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int w = blockIdx.x * 4 + (threadIdx.x >> 5);         // (rows of all heads: at most 2^25)
     const int lane = threadIdx.x & 31, grp = lane / LP, d = 4 * (lane % LP);
-    if (w >= (long long)p.n_seqs * p.n_new * a.n_heads) {
+    if (w >= p.n_seqs * p.n_new * a.n_heads) {
         griddep_wait();                      // (every path: this grid must not end before those it follows)
         return;
     }
     if (a.prefix_blocks == 0 && a.suffix_workers == 0) griddep_wait();       // the lengths, otherwise known (below)
-    const int token = (int)(w / a.n_heads), h = (int)(w % a.n_heads);
-    const int s = token / p.n_new, i = token % p.n_new, g = h / a.gq, hq = h % a.gq;
+    const int token = a.by_heads.of(w), h = w - token * a.n_heads, s = a.by_new.of(token), i = token - s * p.n_new;
+    const int g = a.by_gq.of(h), hq = h - g * a.gq;
     const int len = p.lens[s];
     if (len < p.n_new - i) {                 // padding
         griddep_wait();
@@ -860,11 +861,11 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
     if (lane == 0 && len > clipped_len(p, s)) flag(p.err, LLM_PAGES_BAD_LEN);
     const int srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
     int np = 0, ns = 0;                      // the row's parts of the prefix and of its pages
-    long long pre = 0, suf = 0;              // the first ones' rows
+    int pre = 0, suf = 0;                    // the first ones' rows
     if (a.prefix_blocks > 0) {
         const int mt = (a.rows + 127) / 128, ntiles = (p.prefix_len + kKT - 1) / kKT, r = token * a.gq + hq, u = g * mt + r / 128;
         const long long total = (long long)mt * p.n_kv * ntiles, x = (long long)u * ntiles;
-        const long long w0 = owner_of(x, a.prefix_blocks, total);
+        const int w0 = (int)owner_of(x, a.prefix_blocks, total);
         np = 2 * ((int)(owner_of(x + ntiles - 1, a.prefix_blocks, total) - w0) + 1);       // a part of each softmax group
         pre = (u + w0) * 256 + r % 128;
     }
@@ -878,13 +879,13 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         if (pieces > 0) {
             const int j = g * rt + row / ru;
             const long long x = (long long)b * deal.units + (long long)j * pieces;           // (pieces: kUnit empty ones among them)
-            const long long w0 = owner_of(x, deal.workers, deal.total);
+            const int w0 = (int)owner_of(x, deal.workers, deal.total);
             ns = (int)(owner_of(x + pieces - kUnit - 1, deal.workers, deal.total) - w0) + 1;
-            suf = ((long long)s * deal.units + j + w0) * step + row % ru;
+            suf = (s * deal.units + j + w0) * step + row % ru;
         }
     }
     const int n = np + ns;
-    auto part = [&](int k) { return k < np ? pre + (long long)k * 128 : suf + (long long)(k - np) * step; };
+    auto part = [&](int k) { return k < np ? pre + k * 128 : suf + (k - np) * step; };
     float M = -INFINITY, L = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k0 = 0; k0 < n; k0 += GROUPS * AHEAD) {
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         for (int q = 0; q < AHEAD; q++) {
             const int k = k0 + q * GROUPS + grp;
             v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < n && d < p.hd) v[q] = *reinterpret_cast<const float4*>((k < np ? a.prefix_o : a.suffix_o) + part(k) * p.hd + d);
+            if (k < n && d < p.hd) v[q] = *reinterpret_cast<const float4*>((k < np ? a.prefix_o : a.suffix_o) + (long long)part(k) * p.hd + d);
         }
         float top = M;
 #pragma unroll
@@ -1102,6 +1103,9 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
     ad.suffix_o = reinterpret_cast<float*>(ws + pl.off_so);
     ad.suffix_ml = reinterpret_cast<float2*>(ws + pl.off_sml);
     ad.prefix_blocks = pl.prefix_blocks;
+    ad.by_heads = Div((uint32_t)a->n_heads);
+    ad.by_new = Div((uint32_t)pages->n_new);
+    ad.by_gq = Div((uint32_t)ad.gq);
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
     const bool sq = !ad.q_f16, so = !ad.out_f16;

@@ -13,17 +13,6 @@ namespace llm {
 namespace {
 
 // ------------------------------------------------------------- append --
-// Division of numbers below 2^31 by a fixed one: with 2^s >= d and m = floor(2^32
-// (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
-struct Div {
-    uint32_t d, m, s;
-    explicit Div(uint32_t by = 1) : d(by), s(0) {
-        while ((1ull << s) < by) s++;
-        m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
-    }
-    __device__ __forceinline__ int of(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s); }
-};
-
 struct AppendDev {
     int n_heads, half, neox, table_rows;
     int group;                               // elements of an item's two groups

@@ -39,6 +39,17 @@ __device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
     return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
 }
 
+// Division of numbers below 2^31 by a fixed one: with 2^s >= d and m = floor(2^32
+// (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
+struct Div {
+    uint32_t d, m, s;
+    explicit Div(uint32_t by = 1) : d(by), s(0) {
+        while ((1ull << s) < by) s++;
+        m = (uint32_t)(((1ull << 32) * ((1ull << s) - by)) / by + 1);
+    }
+    __device__ __forceinline__ int of(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> s); }
+};
+
 // max(a, b, c) in one instruction; a NaN counts as no value.
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
