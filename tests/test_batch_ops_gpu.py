@@ -795,3 +795,14 @@ def test_logprobs_long_rows_that_rise(lib, top):
     logp = torch.log_softmax(d, -1)
     bound = logprob_bound(d, logp, n)[1].gather(1, few.top_id.long().cpu()).repeat(120, 1)
     assert ((many.top_logprob - few.top_logprob.repeat(120, 1)).abs().double().cpu() <= 2 * bound).all()
+
+
+@pytest.mark.parametrize("rows,vocab,dtype", [(3, 1000003, F32), (2, 1500001, F16), (160, 50021, F32), (300, 20011, F16)])
+def test_logprobs_blocks_of_several_steps(lib, rows, vocab, dtype):
+    """A cluster whose blocks walk several steps each, rows that start anywhere in a
+    16-byte word, some tokens at -infinity, values that occur many times (F16)."""
+    x = rand(21, rows, vocab, dtype=dtype, std=3.0)
+    x[:, ::97] = -math.inf
+    t = torch.randint(0, vocab, (rows, 2), generator=torch.Generator().manual_seed(5)).int().cuda()
+    for top in (5, 32):
+        check_logprobs(lib, x, t, top)
