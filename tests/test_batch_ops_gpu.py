@@ -806,3 +806,8 @@ def test_logprobs_blocks_of_several_steps(lib, rows, vocab, dtype):
     t = torch.randint(0, vocab, (rows, 2), generator=torch.Generator().manual_seed(5)).int().cuda()
     for top in (5, 32):
         check_logprobs(lib, x, t, top)
+
+
+@pytest.mark.parametrize("prefix", [0, 70])
+def test_attend_most_sequences(lib, prefix):
+    run_attend(lib, (2, 1, 32), [s % 23 for s in range(4096)], 1, prefix, 8, F16, F32)
