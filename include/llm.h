@@ -450,11 +450,11 @@ typedef struct {
     int64_t workspace_bytes;
 } llm_attend;
 
-/* The arithmetic: F32 softmax statistics and sums of exact products.  F16
- * outputs round each probability to FP16 before it meets V, F32 outputs keep it
- * as two FP16 parts (as the decode step's attention).  An F32 q becomes two
- * parts too: 22 bits of each element (none below 2^-25), whose magnitude must
- * not exceed 65504.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+/* The arithmetic: F32 softmax statistics and sums of exact products.  Each
+ * probability meets V as two FP16 parts (as in the batched prefill's
+ * attention), whatever the output's type.  An F32 q becomes two parts too: 22
+ * bits of each element (none below 2^-25), whose magnitude must not exceed
+ * 65504.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int llm_attend_batch(const llm_pages *pages, const llm_attend *a, llm_stream_t stream);
 
 /* Bytes of workspace that a call with these sizes needs (the pointers are not

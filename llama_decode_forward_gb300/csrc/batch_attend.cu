@@ -47,6 +47,11 @@ struct AttendDev {
 // that the largest is about 2^kHead: F16 then resolves those 2^-33 of it
 // (its subnormal step 2^-24, halved by rounding), and the reference may lag
 // behind the running maximum by kLag before 2^(kHead + kLag) nears F16's 2^16.
+// Each meets V as two F16 parts, its first 22 bits, whatever the output's type:
+// with one part (11 bits) F16 outputs were 1.4 times as far from the exact ones as
+// one rounding leaves them; the second part's products cost 256 rows behind 16,000
+// shared ones 18 us of 90, 64 rows behind 32,000 6 us of 52, and nothing where the
+// pages are the larger part.
 constexpr float kHead = 8.f, kLag = 6.f;
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -200,8 +205,8 @@ __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::
 //        row per thread (its lane of tensor memory), each with a maximum, a sum and
 //        an O of its own: one group's exponentials run beside the other's waits and
 //        maxima.  A thread reads the row's 64 scores in halves, writes the
-//        probabilities over each half as F16 (with SPLITP the rounded-off rest beside
-//        them), and rescales O when the row's maximum has moved by more than kLag;
+//        probabilities over each half as two F16 parts, and rescales O when the row's
+//        maximum has moved by more than kLag;
 //   8, 9 issue a group's products each, S = Q K^T (a tile ahead, where its score
 //        buffers allow) and O += P V;
 //   10   loads 64-key tiles of K and V into a ring (TMA).
@@ -210,8 +215,8 @@ __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::
 // their loops whole and one elected lane issues: counters and descriptors stay in
 // uniform registers (a loop of one lane took 90 to 140 cycles an instruction); a
 // wait costs them 75 cycles and the MMAs of a product 200 to 400.  Halving the scores keeps a
-// thread within kPrefixRegs.  SPLITQ: Q as two F16 parts; SPLITP: P as two.
-template <int HDP, bool SPLITQ, bool SPLITP>
+// thread within kPrefixRegs.  SPLITQ: Q as two F16 parts.
+template <int HDP, bool SPLITQ>
 __global__ void __maxnreg__(kPrefixRegs)
     prefix_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                   const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a) {
@@ -302,10 +307,10 @@ __global__ void __maxnreg__(kPrefixRegs)
                 const uint32_t pa = tmem + (uint32_t)((it % kScores) * 64), more = it > first;
                 if (elect_one()) {
 #pragma unroll
-                    for (int part = 0; part < (SPLITP ? 2 : 1); part++)
+                    for (int part = 0; part < 2; part++)
 #pragma unroll
                         for (int kk = 0; kk < kKT / 16; kk++)
-                            mma_ts(o, pa + (kk / 2) * 32 + part * 16 + (kk % 2) * 8, v + (kk * 16 * 128 >> 4), io, part + kk > 0 ? 1u : more);
+                            mma_ts(o, pa + kk * 16 + part * 8, v + (kk * 16 * 128 >> 4), io, part + kk > 0 ? 1u : more);
                     mma_commit(&pvdone[it % kScores]);
                     mma_commit(&empty[it % NS]);
                 }
@@ -395,18 +400,20 @@ __global__ void __maxnreg__(kPrefixRegs)
                 };
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 auto probabilities = [&](int h, const uint32_t (&s)[32]) {
-                    uint32_t hi[16], lo[SPLITP ? 16 : 1];
                     const float2 sc2 = make_float2(a.sc, a.sc), m2 = make_float2(-M, -M);
 #pragma unroll
-                    for (int c = 0; c < 16; c++) {
-                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sc2, m2);
-                        const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-                        l2[c & 1] = __fadd2_rn(l2[c & 1], e);
-                        hi[c] = pack_hi(e.x, e.y);
-                        if (SPLITP) lo[SPLITP ? c : 0] = pack_lo(e.x, e.y, hi[c]);
+                    for (int k = 0; k < 32; k += 16) {       // one MMA's keys: eight columns of high parts, eight of low ones
+                        uint32_t p2[16];
+#pragma unroll
+                        for (int c = 0; c < 8; c++) {
+                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[k + 2 * c]), __uint_as_float(s[k + 2 * c + 1])), sc2, m2);
+                            const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+                            l2[c & 1] = __fadd2_rn(l2[c & 1], e);
+                            p2[c] = pack_hi(e.x, e.y);
+                            p2[8 + c] = pack_lo(e.x, e.y, p2[c]);
+                        }
+                        tm_st16(sb + h * 32 + k, p2);
                     }
-                    tm_st16(sb + h * 32, hi);
-                    if (SPLITP) tm_st16(sb + h * 32 + 16, lo);
                 };
                 uint32_t s[32];
                 scores(0, s);
@@ -551,7 +558,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 // a ring of TMA boxes (16 rows x 128 bytes a request) brought 3.6 TB/s, plain
 // loads 5.3 TB/s, the join and the launches included; 805 MB with heads of 128
 // values 6.2 TB/s.
-template <int HDP, int NT, bool SPLITQ, bool SPLITP>
+template <int HDP, int NT, bool SPLITQ>
 __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
     suffix_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
     constexpr int CH = HDP / 32, RU = 8 * NT;                // 16-byte chunks of a row in a lane
@@ -765,7 +772,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     for (int k = 0; k < 2; k++) {
                         const uint32_t hi = pack_hi(sc[q][2 * k], sc[q][2 * k + 1]);
                         ph[q][k] = transpose8(hi);
-                        if (SPLITP) pl[q][k] = transpose8(pack_lo(sc[q][2 * k], sc[q][2 * k + 1], hi));
+                        pl[q][k] = transpose8(pack_lo(sc[q][2 * k], sc[q][2 * k + 1], hi));
                     }
                 }
                 // a row that some new tokens see and others do not: where its V is not
@@ -806,7 +813,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 #pragma unroll
                     for (int q = 0; q < NT; q++) {
                         mma_kn8(o[q][d], a0, a1, a2, a3, ph[q][0], ph[q][1]);
-                        if (SPLITP) mma_kn8(o[q][d], a0, a1, a2, a3, pl[q][0], pl[q][1]);
+                        mma_kn8(o[q][d], a0, a1, a2, a3, pl[q][0], pl[q][1]);
                     }
                 }
             }
@@ -1009,9 +1016,9 @@ bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long 
 // pages 65 us, 51 us with the default.)
 constexpr int kCarveout = 72;
 
-template <int HDP, bool SPLITQ, bool SPLITP>
+template <int HDP, bool SPLITQ>
 cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad) {
-    auto k = prefix_kernel<HDP, SPLITQ, SPLITP>;
+    auto k = prefix_kernel<HDP, SPLITQ>;
     static OncePerDevice once;
     const cudaError_t e = once([&] {
         const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
@@ -1021,11 +1028,11 @@ cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensor
     return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
 }
 
-template <int HDP, int NT, bool SPLITQ, bool SPLITP>
+template <int HDP, int NT, bool SPLITQ>
 cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
     // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
     static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
-    auto k = suffix_kernel<HDP, NT, SPLITQ, SPLITP>;
+    auto k = suffix_kernel<HDP, NT, SPLITQ>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(32 * kSuffixWarps);
@@ -1109,7 +1116,7 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
     ad.by_gq = Div((uint32_t)ad.gq);
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
-    const bool sq = !ad.q_f16, so = !ad.out_f16;
+    const bool sq = !ad.q_f16;
     const int hd = pages->head_dim;
     cudaError_t e = cudaSuccess;
     if (prefix) {
@@ -1117,22 +1124,16 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
         if (!rows_map(&mk, a->prefix_k, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT) ||
             !rows_map(&mv, a->prefix_v, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT))
             return fail_op(LLM_ERR_CUDA, "a tensor map of the prefix");
-#define LLM_PREFIX(HDP)                                                                                          \
-    (sq ? (so ? launch_prefix<HDP, true, true>(stream, mk, mv, pd, ad)                                 \
-              : launch_prefix<HDP, true, false>(stream, mk, mv, pd, ad))                               \
-        : (so ? launch_prefix<HDP, false, true>(stream, mk, mv, pd, ad)                                \
-              : launch_prefix<HDP, false, false>(stream, mk, mv, pd, ad)))
+#define LLM_PREFIX(HDP) (sq ? launch_prefix<HDP, true>(stream, mk, mv, pd, ad) : launch_prefix<HDP, false>(stream, mk, mv, pd, ad))
         e = hd <= 64 ? LLM_PREFIX(64) : LLM_PREFIX(128);
 #undef LLM_PREFIX
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (prefix)");
     }
     if (pl.suffix_blocks > 0) {
         const int first = prefix ? 0 : 1;
-#define LLM_SUFFIX(HDP, NT)                                                                                      \
-    (sq ? (so ? launch_suffix<HDP, NT, true, true>(stream, pd, ad, first, pl.suffix_blocks)               \
-              : launch_suffix<HDP, NT, true, false>(stream, pd, ad, first, pl.suffix_blocks))             \
-        : (so ? launch_suffix<HDP, NT, false, true>(stream, pd, ad, first, pl.suffix_blocks)              \
-              : launch_suffix<HDP, NT, false, false>(stream, pd, ad, first, pl.suffix_blocks)))
+#define LLM_SUFFIX(HDP, NT)                                                               \
+    (sq ? launch_suffix<HDP, NT, true>(stream, pd, ad, first, pl.suffix_blocks) \
+        : launch_suffix<HDP, NT, false>(stream, pd, ad, first, pl.suffix_blocks))
         const bool eight = unit_rows(pages->n_new * ad.gq) == 8;
         e = hd <= 64 ? (eight ? LLM_SUFFIX(64, 1) : LLM_SUFFIX(64, 2)) : (eight ? LLM_SUFFIX(128, 1) : LLM_SUFFIX(128, 2));
 #undef LLM_SUFFIX

@@ -811,3 +811,24 @@ def test_logprobs_blocks_of_several_steps(lib, rows, vocab, dtype):
 @pytest.mark.parametrize("prefix", [0, 70])
 def test_attend_most_sequences(lib, prefix):
     run_attend(lib, (2, 1, 32), [s % 23 for s in range(4096)], 1, prefix, 8, F16, F32)
+
+
+@pytest.mark.parametrize("q_dtype", [F32, F16])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 4, 128), (8, 2, 32)])
+@pytest.mark.parametrize("prefix,lens", [(5, [1, 1, 1]), (0, [2, 7, 12]), (3, [4, 9, 1]), (70, [1, 33, 18])])
+def test_attend_f16_output_is_rounded_once(lib, prefix, lens, heads, q_dtype):
+    """An F16 output is the F32 one's value rounded once: the probabilities keep 22 bits
+    whatever the output's type, so its bound is the F32 output's and half a step of F16
+    (with few keys one F16 per probability, 2^-11 of each term, would be far outside)."""
+    n_heads, n_kv, hd = heads
+    b = Batch(lib, lens, 1, prefix, 16, n_kv, hd, seed=prefix)
+    q = rand(1, 3, n_heads, hd, dtype=q_dtype)
+    pk, pv = rand(2, max(prefix, 1), n_kv, hd, dtype=F16), rand(3, max(prefix, 1), n_kv, hd, dtype=F16)
+    out = torch.zeros(3, n_heads, hd, dtype=F16, device="cuda")
+    lib.AttendBatch(b.pages, q, out, pk, pv)()
+    for s, n in enumerate(lens):
+        keys, values = torch.cat([pk[:prefix].double(), b.gather(b.k, s, n)]), torch.cat([pv[:prefix].double(), b.gather(b.v, s, n)])
+        o, w, mag, far = attend_exact(q[s].double(), hd ** -0.5, keys, values, n_kv)
+        tol = attend_bound(o, w, mag, far, values.abs().max(), keys.shape[0], hd, q_dtype, F32)
+        err = (out[s].double() - o).abs()
+        assert (err <= tol + H16 * (o.abs() + tol) + 2.0 ** -25).all(), (s, float((err / (tol + H16 * o.abs())).max()))
