@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
                 for (int i = 0; i < kLpElems; i++) bm = fmaxf(bm, v[i]);
             }
             if (bm > st.m) {
+                // (a maximum that was very low, or none, leaves nothing: there s d may be -infinity, or NaN)
                 const float d = st.m - bm, c = exp2f(d * kLog2e);
-                st.t = st.s == 0.f ? 0.f : c * (st.t + st.s * d);
+                st.t = c == 0.f ? 0.f : c * (st.t + st.s * d);
                 st.s *= c;
                 st.m = bm;
             }

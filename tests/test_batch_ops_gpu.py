@@ -832,3 +832,33 @@ def test_attend_f16_output_is_rounded_once(lib, prefix, lens, heads, q_dtype):
         tol = attend_bound(o, w, mag, far, values.abs().max(), keys.shape[0], hd, q_dtype, F32)
         err = (out[s].double() - o).abs()
         assert (err <= tol + H16 * (o.abs() + tol) + 2.0 ** -25).all(), (s, float((err / (tol + H16 * o.abs())).max()))
+
+
+@pytest.mark.parametrize("rows,vocab", [(210, 60001), (3, 1000003), (600, 20000)])
+def test_logprobs_masks_of_long_rows(lib, rows, vocab):
+    """Tokens masked with a very low number, in rows of which every thread walks several
+    steps: its first logits may all be masked ones, the later ones not."""
+    low = torch.finfo(F32).min
+    x = rand(31, rows, vocab, std=2.0)
+    g = torch.Generator().manual_seed(32)
+    for r in range(rows):
+        kind = r % 6
+        if kind == 0:
+            x[r, :vocab - 200] = low
+        elif kind == 1:
+            x[r, :vocab * 9 // 10] = low
+        elif kind == 2:
+            x[r, (torch.rand(vocab, generator=g) < 0.98).cuda()] = low
+        elif kind == 3:
+            x[r, :vocab // 2] = -1e38
+        elif kind == 4:
+            x[r, 200:] = low
+        else:
+            x[r, :vocab - 1] = low
+    check_logprobs(lib, x, torch.full((rows, 1), vocab - 1, dtype=torch.int32, device="cuda"), 3)
+    # far from zero both ways: one token takes all
+    x[:] = low
+    x[:, vocab - 5] = 3e38
+    op = lib.LogProbs(x, torch.full((rows, 1), vocab - 5, dtype=torch.int32, device="cuda"), top=1)
+    op()
+    assert (op.entropy == 0).all() and (op.logprob == 0).all() and (op.top_id == vocab - 5).all()
