@@ -459,8 +459,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_co
                     float m1 = -INFINITY, m2 = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < kLpElems; i++) {
-                        m2 = fmaxf(m2, fminf(m1, v[i]));
-                        m1 = fmaxf(m1, v[i]);
+                        const float z = v[i] == v[i] ? v[i] : -INFINITY;       // (fminf(m1, NaN) is m1: it would count twice)
+                        m2 = fmaxf(m2, fminf(m1, z));
+                        m1 = fmaxf(m1, z);
                     }
                     near = merge32(near, sort32(inside || m2 > -INFINITY ? order_of(m2 + 0.f) : 0u, lane), lane);
                 }

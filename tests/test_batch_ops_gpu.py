@@ -862,3 +862,27 @@ def test_logprobs_masks_of_long_rows(lib, rows, vocab):
     op = lib.LogProbs(x, torch.full((rows, 1), vocab - 5, dtype=torch.int32, device="cuda"), top=1)
     op()
     assert (op.entropy == 0).all() and (op.logprob == 0).all() and (op.top_id == vocab - 5).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("vocab", [64, 500, 1000, 20000])
+@pytest.mark.parametrize("top", [8, 25, 32])
+def test_logprobs_alternatives_among_nans(lib, top, vocab, dtype):
+    """top_id counts the logits that are numbers, wherever the NaNs lie: -1 only where there
+    are fewer than `top` of them."""
+    x = rand(vocab + top, 24, vocab, dtype=dtype, std=3.0)
+    g = torch.Generator().manual_seed(top)
+    for r in range(24):
+        x[r, (torch.rand(vocab, generator=g) < (r % 8 + 1) / 10).cuda()] = math.nan
+    x[22] = math.nan
+    x[22, :20:2] = rand(5, 10, dtype=dtype)
+    # a lane's 16 logits of a step: one large, NaNs behind it, then small ones
+    x[23] = -5.0
+    x[23, :vocab // 2:4], x[23, 1:vocab // 2:4] = 10.0, math.nan
+    op = lib.LogProbs(x, None, top=top)
+    op()
+    assert op.entropy.isnan().all() and op.top_logprob.isnan().all()
+    for r, row in enumerate(x.double().cpu()):
+        order = torch.where(row.isnan(), -math.inf, row).sort(descending=True, stable=True).indices[:top]
+        want = [int(i) if not row[i].isnan() else -1 for i in order]
+        assert op.top_id[r].tolist() == want, r
