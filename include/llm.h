@@ -171,7 +171,8 @@ int llm_prefill(llm_handle *h, const int32_t *tokens_host, int32_t n, int32_t po
  * for bit and the GEMMs at the speed of F16 weights; the decode step still
  * streams the Q8_0 matrices.  Costs 2 bytes of device memory per layer
  * weight (about 2 GB for a 1B model); enabling twice keeps one copy.
- * enable == 0 frees the copy (waiting for the handle's stream first).
+ * enable == 0 frees the copy (waiting for the handle's stream first; once a
+ * step of llm_decode_batch has been captured, with llm_destroy).
  * Asynchronous on the handle's stream.  Errors: UNSUPPORTED for F16 or F32
  * weights or a model whose prefill runs token by token, NO_MEMORY (nothing
  * kept), CUDA. */
@@ -503,9 +504,14 @@ int llm_logprobs(const llm_logprobs_args *a, llm_stream_t stream);
  * [n_seqs * n_new][vocab] F32, 16-byte aligned; a padding row's are unspecified.
  * Enqueued on the handle's stream without waiting.  The handle keeps the step's
  * working memory and an angle table; a call that needs more of either than any
- * before it waits for the stream and allocates, so let one call go before a
- * capture into a CUDA graph.  llm_logits_device and the handle's cache are left
- * as they are.  Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_RANGE, STATE,
+ * before it waits for the stream and allocates, so let one call of the same
+ * sizes go before a capture into a CUDA graph (within a capture such a call is
+ * refused, STATE, and the capture goes on).  A captured step may be replayed
+ * until llm_destroy, whatever is called between: what it uses of the handle's
+ * memory (an F16 prefill copy too) is then kept until llm_destroy when a larger
+ * call or llm_prefill_f16_copy replaces it.  Replays and other calls of the
+ * handle share that memory and must not overlap in time.  llm_logits_device and the handle's
+ * cache are left as they are.  Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_RANGE, STATE,
  * NO_MEMORY, CUDA (some of the step's kernels may then have been enqueued). */
 typedef struct {
     int32_t n_seqs, n_new, prefix_len;

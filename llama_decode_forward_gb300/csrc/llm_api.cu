@@ -152,6 +152,8 @@ struct llm_handle {
     int batch_tab_rows = 0;
     void* batch_ws = nullptr;        // and the attention's workspace
     size_t batch_ws_bytes = 0;
+    bool captured = false;           // a step of llm_decode_batch was captured into a graph
+    std::vector<void*> retired;      // what was replaced after that: graphs hold its addresses, freed with the handle
     int test_logits_limit = 0;       // llm_test_logits_limit: > 0 narrows the checked logits bound
 };
 
@@ -312,6 +314,7 @@ static void free_handle(llm_handle* h) {
     cudaFree(h->f16_copy);
     cudaFree(h->batch_tab);
     cudaFree(h->batch_ws);
+    for (void* p : h->retired) cudaFree(p);
     cudaFree(h->trace);
     if (h->pinned) cudaFreeHost(h->pinned);
     cudaGetLastError();
@@ -803,12 +806,29 @@ static PrefillCtx prefill_ctx(const llm_handle* h) {
     return pc;
 }
 
+// Gives up a buffer that llm_decode_batch's kernels use: freed once the stream's work is
+// done, or kept for the graphs that may still replay a captured step on it.
+static int retire(llm_handle* h, void* p) {
+    if (!p) return LLM_OK;
+    if (h->captured) {
+        try {
+            h->retired.push_back(p);
+        } catch (...) {
+            return fail(h, LLM_ERR_NO_MEMORY, "no memory for the list of retired buffers");
+        }
+        return LLM_OK;
+    }
+    CK(h, cudaStreamSynchronize(h->st));
+    CK(h, cudaFree(p));
+    return LLM_OK;
+}
+
 extern "C" int llm_prefill_f16_copy(llm_handle* h, int enable) {
     LIVE_OR_RETURN(h);
     if (!enable) {
         if (h->f16_copy) {
-            CK(h, cudaStreamSynchronize(h->st));
-            CK(h, cudaFree(h->f16_copy));
+            const int rc = retire(h, h->f16_copy);
+            if (rc) return rc;
             h->f16_copy = nullptr;
             h->f16_copy_bytes = 0;
         }
@@ -891,26 +911,38 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     const int64_t need = llm_attend_batch_workspace(&pages, &at);
     if (need < 0) return fail(h, (int)need, "%s", llm_last_error(nullptr));
     if (b->n_seqs == 0) return LLM_OK;
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    CK(h, cudaStreamIsCapturing(h->st, &capture));
+    if (capture != cudaStreamCaptureStatusNone &&
+        (!h->prefill_ws || h->batch_ws_bytes < (size_t)need || h->batch_tab_rows < positions))
+        return fail(h, LLM_ERR_STATE, "the step would allocate during a capture; make one call of these sizes before it");
     int rc;
     if ((rc = need_prefill_ws(h, pc))) return rc;
     if (h->batch_ws_bytes < (size_t)need) {
-        CK(h, cudaStreamSynchronize(h->st));
-        cudaFree(h->batch_ws);
-        h->batch_ws = nullptr;
-        h->batch_ws_bytes = 0;
-        CK(h, dev_alloc(&h->batch_ws, (size_t)need));
+        void* p = nullptr;
+        CK(h, dev_alloc(&p, (size_t)need));
+        if ((rc = retire(h, h->batch_ws))) {
+            cudaFree(p);
+            return rc;
+        }
+        h->batch_ws = p;
         h->batch_ws_bytes = (size_t)need;
     }
     if (h->batch_tab_rows < positions) {
-        CK(h, cudaStreamSynchronize(h->st));
-        cudaFree(h->batch_tab);
-        h->batch_tab = nullptr;
-        h->batch_tab_rows = 0;
-        CK(h, dev_alloc((void**)&h->batch_tab, (size_t)positions * h->cfg.rope_dims * 4));
-        CK(h, rope_table(h->st, h->batch_tab, (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs));
+        float* p = nullptr;
+        CK(h, dev_alloc((void**)&p, (size_t)positions * h->cfg.rope_dims * 4));
+        const cudaError_t e = rope_table(h->st, p, (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs);
+        if (e != cudaSuccess || (rc = retire(h, h->batch_tab))) {
+            cudaStreamSynchronize(h->st);
+            cudaFree(p);
+            cudaGetLastError();
+            return e == cudaSuccess ? rc : fail(h, LLM_ERR_CUDA, "angle table: %s", cudaGetErrorString(e));
+        }
         h->launches++;
+        h->batch_tab = p;
         h->batch_tab_rows = (int)positions;
     }
+    if (capture != cudaStreamCaptureStatusNone) h->captured = true;
     const char* why = nullptr;
     int launches = 0;
     rc = decode_batch_rows(pc, *b, h->prefill_ws, h->batch_tab, h->batch_tab_rows, h->batch_ws, (int64_t)h->batch_ws_bytes, &why, &launches);

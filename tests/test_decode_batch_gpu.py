@@ -345,3 +345,46 @@ def test_allocation_failure_leaves_the_handle_usable(lib):
     lib.llm_sync(dec.h)
     assert bool(torch.isfinite(bd.logits).all()) and bd.errors() == 0
     dec.close()
+
+
+@pytest.mark.parametrize("copy", [False, True])
+def test_captured_step_outlives_larger_batches(lib, copy):
+    """A step captured on a handle keeps its memory when a larger batch on the same handle
+    replaces the workspace and the angle table, and when the F16 copy that it reads is given
+    up: the replay gives the same bits.  Within a capture a call that would allocate is
+    refused, and the capture goes on."""
+    cfg = config(wtype=synth.Q8_0, bias=False, number=83)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        dec = lib.Decoder(cfg, synth.make_weights(cfg))
+        if copy:
+            lib.llm_prefill_f16_copy(dec.h)
+        lib.llm_prefill(dec.h, synth.prompt(cfg, 20), 0)
+        small, large = lib.BatchDecoder(dec, 2, 16, 20), lib.BatchDecoder(dec, 64, 600, 20)
+        put(small, cfg, [3, 1])
+        put(large, cfg, [1] * 64)
+        small.step()
+        torch.cuda.synchronize()
+        want = small.logits.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            with pytest.raises(lib.LlmError) as e:
+                large.step()
+            small.step()
+        assert e.value.status == lib.LLM_ERR_STATE
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(small.logits, want)
+        large.step()
+        if copy:
+            lib.llm_prefill_f16_copy(dec.h, False)
+        torch.cuda.synchronize()
+        junk = [torch.full((1 << 19,), float("nan"), device="cuda") for _ in range(64)]     # whatever was freed is in use again
+        small.logits.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(small.logits, want)
+        assert all(bool(t.isnan().all()) for t in junk) and small.errors() == 0
+        lib.llm_sync(dec.h)
+        del graph
+        dec.close()
