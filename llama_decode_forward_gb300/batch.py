@@ -30,6 +30,11 @@ if _current_device is None or _current_stream is None:
     _current_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
 
 
+def _torch_stream(raw: int, device):
+    """The torch stream of a CUDA stream (0 and 1: the legacy default stream)."""
+    return torch.cuda.default_stream(device) if raw in (None, 0, 1) else torch.cuda.ExternalStream(raw, device=device)
+
+
 def _run(rc: int) -> None:
     if rc != _b.LLM_OK:
         raise _b.LlmError(rc, _b._lib.llm_last_error(None).decode())
@@ -184,7 +189,9 @@ class BatchDecoder:
     int32 [n_seqs, max_pages] are this object's tensors, to be written before each
     step; logits float32 [n_seqs, n_new, vocab] is the step's result.  ``pages``
     holds every layer's K and V pages; page_table starts with each sequence's own
-    pages in a row.  step() enqueues on the decoder's stream."""
+    pages in a row.  step() enqueues on the decoder's stream; where that is not the
+    current one, it runs behind what the current stream has been given (the tensors'
+    new values) and before what it is given next."""
 
     def __init__(self, decoder, n_seqs: int, max_len: int, prefix_len: int, n_new: int = 1, page_size: int = 16):
         c = _b.llm_get_config(decoder.h)
@@ -192,20 +199,42 @@ class BatchDecoder:
         max_pages = -(-max_len // page_size)
         n_pages = n_seqs * max_pages
         self.decoder = decoder
-        self.pages = torch.zeros(max(1, _b.llm_batch_pages_bytes(decoder.h, n_pages, page_size)) // 2, dtype=torch.float16,
-                                 device=dev)
-        self.page_table = torch.arange(n_pages, dtype=torch.int32, device=dev).view(n_seqs, max_pages)
-        self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
-        self.tokens = torch.zeros(n_seqs, n_new, dtype=torch.int32, device=dev)
-        self.logits = torch.empty(n_seqs, n_new, c.vocab, dtype=torch.float32, device=dev)
-        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._device, self._stream = dev, _torch_stream(decoder.stream, dev)
+        # the tensors are the decoder's stream's: filled there, and their memory, when it is
+        # given back, goes to later work of that stream only
+        with torch.cuda.stream(self._stream):
+            self.pages = torch.zeros(max(1, _b.llm_batch_pages_bytes(decoder.h, n_pages, page_size)) // 2, dtype=torch.float16,
+                                     device=dev)
+            self.page_table = torch.arange(n_pages, dtype=torch.int32, device=dev).view(n_seqs, max_pages)
+            self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+            self.tokens = torch.zeros(n_seqs, n_new, dtype=torch.int32, device=dev)
+            self.logits = torch.empty(n_seqs, n_new, c.vocab, dtype=torch.float32, device=dev)
+            self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._users = {self._stream.cuda_stream}           # the streams that the tensors' memory waits for
+        self._use_on(torch.cuda.current_stream(dev))
         self.struct = _b.llm_batch(n_seqs=n_seqs, n_new=n_new, prefix_len=prefix_len, page_size=page_size,
                                    n_pages=n_pages, max_pages=max_pages, pages=self.pages.data_ptr(),
                                    page_table=self.page_table.data_ptr(), lens=self.lens.data_ptr(),
                                    tokens=self.tokens.data_ptr(), logits=self.logits.data_ptr(), err=self.err.data_ptr())
 
+    def _use_on(self, stream) -> None:
+        """What `stream` is given from now on may use the tensors."""
+        stream.wait_stream(self._stream)
+        if stream.cuda_stream not in self._users:
+            self._users.add(stream.cuda_stream)
+            for t in (self.pages, self.page_table, self.lens, self.tokens, self.logits, self.err):
+                t.record_stream(stream)
+
     def step(self) -> None:
-        _b.llm_decode_batch(self.decoder.h, self.struct)
+        if _current_stream(self._device.index) == self._stream.cuda_stream:
+            _b.llm_decode_batch(self.decoder.h, self.struct)
+            return
+        current = torch.cuda.current_stream(self._device)
+        self._stream.wait_stream(current)
+        try:
+            _b.llm_decode_batch(self.decoder.h, self.struct)
+        finally:
+            self._use_on(current)
 
     def errors(self) -> int:
         """The LLM_PAGES_* bits seen so far (waits for the device)."""

@@ -388,3 +388,46 @@ def test_captured_step_outlives_larger_batches(lib, copy):
         lib.llm_sync(dec.h)
         del graph
         dec.close()
+
+
+@pytest.mark.parametrize("outer", [False, True])
+def test_decoder_on_its_own_stream(lib, outer):
+    """The decoder's stream is not the current one, and the current one is busy when the
+    batch is made, its tensors are written and its results are read (outer: it is a side
+    stream too): each step sees the values written before it and nothing lands later."""
+    cfg = config()
+    W = synth.make_weights(cfg)
+    prompt, steps = synth.prompt(cfg, 40), [[1, 1, 1], [2, 2, 2], [3, 3, 3]]
+    want = []
+    dec = lib.Decoder(cfg, W)
+    lib.llm_prefill(dec.h, prompt, 0)
+    bd = lib.BatchDecoder(dec, 3, 16, 40)
+    for lens in steps:
+        put(bd, cfg, lens)
+        bd.step()
+        lib.llm_sync(dec.h)
+        want.append(bd.logits.clone())
+    dec.close()
+    own = torch.cuda.Stream()
+    dec = lib.Decoder(cfg, W, stream=own.cuda_stream)
+    lib.llm_prefill(dec.h, prompt, 0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream() if outer else torch.cuda.current_stream()):
+        host = [[torch.tensor(v, dtype=torch.int32).pin_memory() for v in
+                 ([[token(cfg, s, n - 1)] for s, n in enumerate(lens)], lens)] for lens in steps]
+        got = []
+        torch.cuda._sleep(20000000)
+        bd = lib.BatchDecoder(dec, 3, 16, 40)
+        for tokens, lens in host:
+            bd.tokens.copy_(tokens, non_blocking=True)
+            bd.lens.copy_(lens, non_blocking=True)
+            torch.cuda._sleep(2000000)
+            bd.step()
+            got.append(bd.logits.clone())
+        bd.pages.fill_(0)                              # behind the last step, whose logits are already there
+        del bd                                         # memory given back while the steps are still queued
+        junk = [torch.full((1 << 16,), float("nan"), device="cuda") for _ in range(8)]
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 8
+    lib.llm_sync(dec.h)
+    dec.close()
