@@ -87,13 +87,27 @@ class PagedBatch:
 
 
 class _Op:
-    """One operator with its arguments; calling it enqueues one run."""
+    """One operator with its arguments; calling it enqueues one run.  The operator must
+    live as long as a graph that captured its runs.  A stream given by number must live
+    as long as the operator."""
+
+    def _made(self, fn, kept, structs, own, device) -> None:
+        """own: the tensors that the operator allocated, on the current stream."""
+        self._fn, self._kept, self._own, self._index = fn, (kept, structs), own, device.index
+        self._args = tuple(ctypes.addressof(x) for x in structs)
+        self._streams = {_current_stream(device.index)}    # the streams that own's memory waits for
 
     def __call__(self, stream=None) -> None:
         index = self._index
         if _current_device() != index:
             raise ValueError(f"the operator's tensors are on cuda:{index}, the current device is another")
-        rc = self._fn(*self._args, _current_stream(index) if stream is None else stream)
+        if stream is None:
+            stream = _current_stream(index)
+        if stream not in self._streams:
+            for t in self._own:
+                t.record_stream(_torch_stream(stream, t.device))
+            self._streams.add(stream)
+        rc = self._fn(*self._args, stream)
         if rc:
             _run(rc)
 
@@ -121,8 +135,7 @@ class KvAppend(_Op):
             _tensor("q_out", q_out, _DTYPES, tuple(q.shape), dev, strided=True)
             a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), q.stride(0)
             a.q_out, a.q_out_stride, a.q_out_dtype = q_out.data_ptr(), q_out.stride(0), _DTYPES[q_out.dtype]
-        self._kept, self._fn, self._index = (pages, a, q, k, v, cos_sin, q_out), _b._lib.llm_kv_append, dev.index
-        self._args = ctypes.addressof(p), ctypes.addressof(a)
+        self._made(_b._lib.llm_kv_append, (pages, q, k, v, cos_sin, q_out), (p, a), (), dev)
 
 
 class AttendBatch(_Op):
@@ -152,8 +165,7 @@ class AttendBatch(_Op):
             _run(int(n))
         self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
         a.workspace, a.workspace_bytes = self.workspace.data_ptr(), int(n)
-        self._kept, self._fn, self._index = (pages, a, q, out, prefix_k, prefix_v), _b._lib.llm_attend_batch, dev.index
-        self._args = ctypes.addressof(p), ctypes.addressof(a)
+        self._made(_b._lib.llm_attend_batch, (pages, q, out, prefix_k, prefix_v), (p, a), (self.workspace,), dev)
 
 
 class LogProbs(_Op):
@@ -178,8 +190,8 @@ class LogProbs(_Op):
                                  targets=targets.data_ptr() if n_targets else None, logprob=self.logprob.data_ptr(),
                                  entropy=self.entropy.data_ptr(), top_id=self.top_id.data_ptr(),
                                  top_logprob=self.top_logprob.data_ptr())
-        self._kept, self._fn, self._index = (a, logits, targets), _b._lib.llm_logprobs, dev.index
-        self._args = (ctypes.addressof(a),)
+        self._made(_b._lib.llm_logprobs, (logits, targets), (a,),
+                   (self.logprob, self.entropy, self.top_id, self.top_logprob), dev)
 
 
 class BatchDecoder:
@@ -246,8 +258,12 @@ def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, po
     """llm_rope_table: float32 [n_pos, rope_dims / 2, 2] of the decode step's
     angles at positions pos0 .. pos0 + n_pos - 1."""
     out = torch.empty(n_pos, rope_dims // 2, 2, dtype=torch.float32, device=device)
+    if out.device.index != _current_device():
+        raise ValueError(f"the table is on {out.device}, the current device is another")
     if rope_freqs is not None:
         _tensor("rope_freqs", rope_freqs, (torch.float32,), (rope_dims // 2,), out.device)
+    if stream is not None:
+        out.record_stream(_torch_stream(stream, out.device))
     _run(_b._lib.llm_rope_table(out.data_ptr(), pos0, n_pos, rope_dims, rope_base,
                                 rope_freqs.data_ptr() if rope_freqs is not None else None, _stream(stream)))
     return out

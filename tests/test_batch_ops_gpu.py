@@ -886,3 +886,35 @@ def test_logprobs_alternatives_among_nans(lib, top, vocab, dtype):
         order = torch.where(row.isnan(), -math.inf, row).sort(descending=True, stable=True).indices[:top]
         want = [int(i) if not row[i].isnan() else -1 for i in order]
         assert op.top_id[r].tolist() == want, r
+
+
+@pytest.mark.parametrize("by_number", [False, True])
+def test_operator_dropped_while_its_run_is_queued(lib, by_number):
+    """An operator made on one stream, run on another and dropped before the run has begun:
+    its workspace is not given to the first stream's next tensors meanwhile."""
+    b = Batch(lib, [40, 7, 90], 1, 300, 16, 2, 64)
+    q, pk, pv = rand(1, 3, 8, 64), rand(2, 300, 2, 64, dtype=F16), rand(3, 300, 2, 64, dtype=F16)
+    out = torch.zeros(3, 8, 64, device="cuda")
+    side, queued = torch.cuda.Stream(), 0
+    lib.AttendBatch(b.pages, q, out, pk, pv)()         # (the first call loads the kernels)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        out.zero_()
+        torch.cuda.synchronize()
+        op = lib.AttendBatch(b.pages, q, out, pk, pv)
+        size, at = op.workspace.numel(), op.workspace.data_ptr()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100000000)
+            if not by_number:
+                op()
+        if by_number:
+            op(stream=side.cuda_stream)
+        done = side.record_event()
+        del op
+        junk = [torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        if not done.query():
+            queued += 1
+            assert all(t.data_ptr() != at for t in junk)
+        side.synchronize()
+        check_attend(b, q, out, pk, pv)
+    assert queued > 0
