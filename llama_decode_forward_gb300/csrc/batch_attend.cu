@@ -229,8 +229,12 @@ __global__ void __maxnreg__(kPrefixRegs)
     uint64_t* sfull = empty + NS;            // [kScores] scores of a tile are in buffer b
     uint64_t* pfull = sfull + kScores;       // [kScores] its probabilities are
     uint64_t* pvdone = pfull + kScores;      // [kScores] its P V has been added
-    uint64_t* qfull = pvdone + kScores;      // a unit's Q is in tensor memory
-    uint64_t* fin = qfull + 1;               // [2] every MMA of a group has completed
+    // [2] a unit's Q is in tensor memory, units taking turns: the softmax warps may be done with a
+    // unit that has no tile of a group (one of a single tile) before that group's MMA warp has looked
+    // at it, but not with the next one, whose scores it issues.  With one barrier such a warp could
+    // miss two phases and wait for a third that needs its own scores
+    uint64_t* qfull = pvdone + kScores;
+    uint64_t* fin = qfull + 2;               // [2] every MMA of a group has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int mt = (a.rows + 127) / 128, ntiles = (p.prefix_len + kKT - 1) / kKT;
@@ -248,7 +252,8 @@ __global__ void __maxnreg__(kPrefixRegs)
             mbar_init(&pfull[b], kSoftmaxWarps / 2);
             mbar_init(&pvdone[b], 1);
         }
-        mbar_init(qfull, kSoftmaxWarps);
+        mbar_init(&qfull[0], kSoftmaxWarps);
+        mbar_init(&qfull[1], kSoftmaxWarps);
         mbar_init(&fin[0], 1);
         mbar_init(&fin[1], 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -297,7 +302,7 @@ __global__ void __maxnreg__(kPrefixRegs)
         bool ok = true;
         for (int begin = 0, tile0 = t0, unit = 0; begin < n && ok; tile0 = 0, unit++) {
             const int end = min(n, begin + ntiles - tile0), first = begin + ((begin ^ group) & 1);
-            ok = warp_wait(qfull, (uint32_t)(unit & 1), p.err);
+            ok = warp_wait(&qfull[unit & 1], (uint32_t)((unit >> 1) & 1), p.err);
             if (ok && AHEAD > 0 && first < end) ok = scores(first);
             for (int it = first; it < end && ok; it += 2) {
                 if (it + 2 * AHEAD < end && !(ok = scores(it + 2 * AHEAD))) break;
@@ -375,7 +380,7 @@ __global__ void __maxnreg__(kPrefixRegs)
             tm_wait_st();
             tm_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(qfull);
+            if (lane == 0) mbar_arrive(&qfull[(unit - u0) & 1]);
             const int first = begin + ((begin ^ group) & 1);           // the group's first tile of the unit
             for (int it = first; it < end; it += 2) {
                 const uint32_t sb = tmem + lanes + (uint32_t)((it % kScores) * 64);

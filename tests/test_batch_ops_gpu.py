@@ -918,3 +918,24 @@ def test_operator_dropped_while_its_run_is_queued(lib, by_number):
         side.synchronize()
         check_attend(b, q, out, pk, pv)
     assert queued > 0
+
+
+@pytest.mark.parametrize("prefix", [1, 64, 65, 130])
+@pytest.mark.parametrize("types", [(F32, F32), (F16, F16)])
+def test_attend_many_short_units(lib, prefix, types):
+    """Blocks of the prefix kernel that walk several (row tile, kv head) units of one, two
+    or three 64-key tiles each; every run gives the same bits."""
+    b = Batch(lib, [1 + s % 3 for s in range(2500)], 1, prefix, 16, 32, 64, poison=False)
+    q = rand(1, 2500, 32, 64, dtype=types[0])
+    pk, pv = rand(2, prefix, 32, 64, dtype=F16), rand(3, prefix, 32, 64, dtype=F16)
+    out = torch.zeros(2500, 32, 64, dtype=types[1], device="cuda")
+    op = lib.AttendBatch(b.pages, q, out, pk, pv)
+    op()
+    first = out.clone()
+    b.lens = [n if s % 97 < 2 else 0 for s, n in enumerate(b.lens)]           # rows that are looked at
+    check_attend(b, q, out, pk, pv)
+    for _ in range(20):
+        out.zero_()
+        op()
+        assert torch.equal(out, first)
+    assert b.pages.errors() == 0
