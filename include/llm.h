@@ -260,6 +260,12 @@ int llm_checked_build(void);
  * `limit` skipped.  Errors: UNSUPPORTED in other builds, OUT_OF_RANGE. */
 int llm_test_logits_limit(llm_handle *h, int32_t limit);
 
+/* Test hook: a wait that runs out.  With probes > 0 (at most 1000) the prefix
+ * attention of llm_decode_batch copies nothing and its waits for the copies
+ * give up after that many probes, as they would after their limit; 0: as
+ * usual.  Errors: OUT_OF_RANGE. */
+int llm_test_batch_wait(llm_handle *h, int32_t probes);
+
 /* Test hook: allocation failure.  The nth device or pinned-host allocation
  * the library makes from now on (in llm_create, llm_create_from_gguf or
  * llm_prefill's workspace) fails as if the device were out of memory, once;
@@ -502,7 +508,9 @@ int llm_logprobs(const llm_logprobs_args *a, llm_stream_t stream);
  * padding rows are not looked at, another one outside [0, vocab) counts as 0 and
  * sets the handle's device error (llm_sync: OUT_OF_RANGE).  logits: DEVICE
  * [n_seqs * n_new][vocab] F32, 16-byte aligned; a padding row's are unspecified.
- * Enqueued on the handle's stream without waiting.  The handle keeps the step's
+ * A bounded wait of the attention that gave up (LLM_PAGES_TIMEOUT) sets the
+ * handle's device error too (llm_sync: DEVICE_TIMEOUT), whether err is NULL or
+ * not.  Enqueued on the handle's stream without waiting.  The handle keeps the step's
  * working memory and an angle table; a call that needs more of either than any
  * before it waits for the stream and allocates, so let one call of the same
  * sizes go before a capture into a CUDA graph (within a capture such a call is

@@ -127,6 +127,7 @@ _SIGS = {
     "llm_checked_build": ([], _int),
     "llm_debug_tensor": ([_vp, _int, _int, _vp, _i32], _int),
     "llm_test_logits_limit": ([_vp, _i32], _int),
+    "llm_test_batch_wait": ([_vp, _i32], _int),
     "llm_test_guards": ([_vp], ctypes.c_int64),
     "llm_test_poke_guard": ([_vp, _int], _int),
     "llm_prefill_f16_copy": ([_vp, _int], _int),
@@ -311,6 +312,10 @@ def llm_checked_build() -> bool:
 
 def llm_test_logits_limit(h, limit: int) -> None:
     _check(_lib.llm_test_logits_limit(h, int(limit)), h)
+
+
+def llm_test_batch_wait(h, probes: int) -> None:
+    _check(_lib.llm_test_batch_wait(h, int(probes)), h)
 
 
 def llm_test_fail_alloc(nth: int) -> None:

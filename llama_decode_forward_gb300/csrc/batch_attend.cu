@@ -41,6 +41,9 @@ struct AttendDev {
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
     int prefix_blocks, suffix_workers;
     Div by_heads, by_new, by_gq;            // the join's divisions
+    int* timeout;                   // a handle's word for waits that gave up, or nullptr
+    int wait_limit;                 // probes before the prefix kernel's waits give up; below kWaitLimit
+                                    // (a test's) it makes no copies either, so that they do
 };
 
 // Probabilities are kept as 2^(y - M) with M = (a recent maximum) - kHead, so
@@ -136,11 +139,10 @@ constexpr int kWaitLimit = 10000000;         // probes (each suspends the warp f
 // A whole warp's bounded wait for a phase.  The first probe stands outside the loop
 // and every branch is the warp's: a completed phase costs 75 cycles (a loop of each
 // lane's own took 250).
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, int* err) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t par, const AttendDev& a) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
-    for (int i = 0; i < kWaitLimit; i++)
+    for (int i = 0; i < a.wait_limit; i++)
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, par))) return true;
-    flag(err, LLM_PAGES_TIMEOUT);
     return false;
 }
 
@@ -272,6 +274,7 @@ __global__ void __maxnreg__(kPrefixRegs)
     griddep_wait();
     griddep_launch();
 
+    bool ok = true;                          // no wait of this warp has given up
     if (warp == kSoftmaxWarps || warp == kSoftmaxWarps + 1) {
         // ---- the products of one group's tiles.  F16 operands, F32 accumulators, M 128.  Scores:
         // N 64, K is K-major; sums: N HDP, V has the keys (the MMA's K) as rows, so it is MN-major
@@ -283,8 +286,8 @@ __global__ void __maxnreg__(kPrefixRegs)
         const uint32_t o = tmem + G::kO + group * HDP;
         auto scores = [&](int it) {
             // they go where tile it - kScores's probabilities were
-            if (!warp_wait(&full[it % NS], (uint32_t)((it / NS) & 1), p.err)) return false;
-            if (it >= kScores && !warp_wait(&pvdone[it % kScores], (uint32_t)((it / kScores - 1) & 1), p.err)) return false;
+            if (!warp_wait(&full[it % NS], (uint32_t)((it / NS) & 1), a)) return false;
+            if (it >= kScores && !warp_wait(&pvdone[it % kScores], (uint32_t)((it / kScores - 1) & 1), a)) return false;
             tm_fence_after();
             const uint64_t k = dk + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
             if (elect_one()) {
@@ -299,14 +302,13 @@ __global__ void __maxnreg__(kPrefixRegs)
             __syncwarp();
             return true;
         };
-        bool ok = true;
         for (int begin = 0, tile0 = t0, unit = 0; begin < n && ok; tile0 = 0, unit++) {
             const int end = min(n, begin + ntiles - tile0), first = begin + ((begin ^ group) & 1);
-            ok = warp_wait(&qfull[unit & 1], (uint32_t)((unit >> 1) & 1), p.err);
+            ok = warp_wait(&qfull[unit & 1], (uint32_t)((unit >> 1) & 1), a);
             if (ok && AHEAD > 0 && first < end) ok = scores(first);
             for (int it = first; it < end && ok; it += 2) {
                 if (it + 2 * AHEAD < end && !(ok = scores(it + 2 * AHEAD))) break;
-                if (!(ok = warp_wait(&pfull[it % kScores], (uint32_t)((it / kScores) & 1), p.err))) break;
+                if (!(ok = warp_wait(&pfull[it % kScores], (uint32_t)((it / kScores) & 1), a))) break;
                 tm_fence_after();
                 const uint64_t v = dv + (uint64_t)((it % NS) * (2 * G::kTileBytes >> 4));
                 const uint32_t pa = tmem + (uint32_t)((it % kScores) * 64), more = it > first;
@@ -326,12 +328,13 @@ __global__ void __maxnreg__(kPrefixRegs)
         // every MMA issued has completed before the tensor memory is freed
         if (elect_one()) mma_commit(&fin[group]);
         __syncwarp();
-        warp_wait(&fin[group], 0, p.err);
+        ok = warp_wait(&fin[group], 0, a) && ok;
     } else if (warp == kSoftmaxWarps + 2) {
         // ---- copies
+        const int copies = a.wait_limit < kWaitLimit ? 0 : n;
         int lt = t0, lu = u0, it = 0;
-        for (; it < n; it++) {
-            if (it >= NS && !warp_wait(&empty[it % NS], (uint32_t)((it / NS - 1) & 1), p.err)) break;
+        for (; it < copies; it++) {
+            if (it >= NS && !(ok = warp_wait(&empty[it % NS], (uint32_t)((it / NS - 1) & 1), a))) break;
             uint8_t* st = ring + (it % NS) * 2 * G::kTileBytes;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&full[it % NS], 2 * G::kTileBytes);
@@ -345,19 +348,18 @@ __global__ void __maxnreg__(kPrefixRegs)
             if (++lt == ntiles) lt = 0, lu++;
         }
         // every copy has landed before the block can end (at once, unless a wait gave up)
-        for (int k = it - 1; k >= 0 && k >= it - NS; k--) warp_wait(&full[k % NS], (uint32_t)((k / NS) & 1), p.err);
+        for (int k = it - 1; k >= 0 && k >= it - NS; k--) ok = warp_wait(&full[k % NS], (uint32_t)((k / NS) & 1), a) && ok;
     } else {
         // ---- softmax
         const int group = warp >> 2, lrow = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, to = tmem + lanes + G::kO + group * HDP;
         float M = 0.f, l = 0.f;              // M: the reference less kHead
         // after a wait that gave up the warp goes on without waiting, to no result
-        bool ok = true;
         for (int begin = 0, tile0 = t0, unit = u0; begin < n; tile0 = 0, unit++) {
             // ---- a unit's tiles, `begin` to `end` of the block's: first this group's half of the
             // row's Q into tensor memory, once the last scores of the unit before are there
             const int end = min(n, begin + ntiles - tile0), r = unit % mt * 128 + lrow, g = unit / mt;
-            if (begin > 0) ok = ok && warp_wait(&sfull[(begin - 1) % kScores], (uint32_t)(((begin - 1) / kScores) & 1), p.err);
+            if (begin > 0) ok = ok && warp_wait(&sfull[(begin - 1) % kScores], (uint32_t)(((begin - 1) / kScores) & 1), a);
             tm_fence_after();
             const long long q_at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
 #pragma unroll
@@ -385,7 +387,7 @@ __global__ void __maxnreg__(kPrefixRegs)
             for (int it = first; it < end; it += 2) {
                 const uint32_t sb = tmem + lanes + (uint32_t)((it % kScores) * 64);
                 const int left = p.prefix_len - (tile0 + it - begin) * kKT;      // keys from this tile on
-                ok = ok && warp_wait(&sfull[it % kScores], (uint32_t)((it / kScores) & 1), p.err);
+                ok = ok && warp_wait(&sfull[it % kScores], (uint32_t)((it / kScores) & 1), a);
                 tm_fence_after();
                 // 32 scores, keys behind the prefix at -infinity
                 auto scores = [&](int h, uint32_t (&s)[32]) {
@@ -436,7 +438,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                         M = top;
                     }
                     l *= c;
-                    ok = ok && warp_wait(&pvdone[(it - 2) % kScores], (uint32_t)(((it - 2) / kScores) & 1), p.err);
+                    ok = ok && warp_wait(&pvdone[(it - 2) % kScores], (uint32_t)(((it - 2) / kScores) & 1), a);
                     tm_fence_after();
 #pragma unroll 1
                     for (int h = 0; h < HDP; h += 16) {
@@ -465,7 +467,7 @@ __global__ void __maxnreg__(kPrefixRegs)
             // ---- this group's part of the unit; without a tile of its own an empty one
             const int last = end - 1 - ((end - 1 - first) & 1);
             const bool any = first < end;
-            if (any) ok = ok && warp_wait(&pvdone[last % kScores], (uint32_t)((last / kScores) & 1), p.err);
+            if (any) ok = ok && warp_wait(&pvdone[last % kScores], (uint32_t)((last / kScores) & 1), a);
             tm_fence_after();
             const long long at = (((long long)unit + blockIdx.x) * 2 + group) * 128 + lrow;
 #pragma unroll 1
@@ -485,6 +487,10 @@ __global__ void __maxnreg__(kPrefixRegs)
             tm_fence_before();
             begin = end;
         }
+    }
+    if (!ok && lane == 0) {
+        flag(p.err, LLM_PAGES_TIMEOUT);
+        flag(a.timeout, kErrTimeout);
     }
     tm_fence_before();
     __syncthreads();
@@ -1074,17 +1080,7 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
 
 }  // namespace
 
-}  // namespace llm
-
-using namespace llm;
-
-extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_attend* a) {
-    int rc = check_pages(pages, false);
-    if (rc || (rc = check_attend(pages, a))) return rc;
-    return (int64_t)make_plan(pages, a, sm_count()).bytes;
-}
-
-extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
+int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit) {
     int rc = check_pages(pages, true);
     if (rc || (rc = check_attend(pages, a))) return rc;
     if (pages->n_seqs == 0) return LLM_OK;
@@ -1121,6 +1117,8 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
     ad.by_gq = Div((uint32_t)ad.gq);
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
+    ad.timeout = timeout;
+    ad.wait_limit = wait_limit > 0 ? wait_limit : kWaitLimit;
     const bool sq = !ad.q_f16;
     const int hd = pages->head_dim;
     cudaError_t e = cudaSuccess;
@@ -1149,4 +1147,18 @@ extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm
                     : hd <= 64 ? launch_dep(join_kernel<16>, grid, dim3(128), 0, stream, pd, ad)
                                : launch_dep(join_kernel<32>, grid, dim3(128), 0, stream, pd, ad),
                     "llm_attend_batch (join)");
+}
+
+}  // namespace llm
+
+using namespace llm;
+
+extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_attend* a) {
+    int rc = check_pages(pages, false);
+    if (rc || (rc = check_attend(pages, a))) return rc;
+    return (int64_t)make_plan(pages, a, sm_count()).bytes;
+}
+
+extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
+    return attend_batch(pages, a, stream, nullptr, 0);
 }

@@ -97,7 +97,7 @@ static void guarded_free(Guarded& g) {
 struct HostPinned {
     int token_in;
     int argmax;
-    int err;
+    int err[2];
 };
 
 struct llm_handle {
@@ -134,7 +134,7 @@ struct llm_handle {
     unsigned long long* best = nullptr;
     unsigned* counters = nullptr;
     int n_counters = 0;
-    int* err = nullptr;
+    int* err = nullptr;                 // [2] device error words: the steps' and the prefill's, the batch's attention
     int* tok_in = nullptr;
     int* tok_out = nullptr;
     HostPinned* pinned = nullptr;
@@ -154,6 +154,7 @@ struct llm_handle {
     size_t batch_ws_bytes = 0;
     bool captured = false;           // a step of llm_decode_batch was captured into a graph
     std::vector<void*> retired;      // what was replaced after that: graphs hold its addresses, freed with the handle
+    int test_batch_wait = 0;         // llm_test_batch_wait: > 0 limits the batch attention's waits
     int test_logits_limit = 0;       // llm_test_logits_limit: > 0 narrows the checked logits bound
 };
 
@@ -534,7 +535,7 @@ extern "C" int llm_create(const llm_config* cfg, const llm_weights* w, llm_strea
     h->delta_words = (size_t)2 * L * 2 * d;
     const size_t o_tv = take(h->tv_words * 8), o_part = take(h->part_words * 8), o_delta = take(h->delta_words * 8),
                  o_epoch = take(4), o_logits = take((size_t)c.vocab * 4), o_best = take(8),
-                 o_ctr = take((size_t)h->n_counters * 4), o_err = take(4), o_tin = take(4), o_tout = take(4);
+                 o_ctr = take((size_t)h->n_counters * 4), o_err = take(8), o_tin = take(4), o_tout = take(4);
     CKC(guarded_alloc(h->act_mem, a, h->st));
     h->act = h->act_mem.ptr();
     CKC(cudaMemsetAsync(h->act, 0, a, h->st));
@@ -729,15 +730,15 @@ static int device_error_status(llm_handle* h, int e) {
 }
 
 static int read_device_error(llm_handle* h) {
-    CK(h, cudaMemcpyAsync(&h->pinned->err, h->err, 4, cudaMemcpyDeviceToHost, h->st));
+    CK(h, cudaMemcpyAsync(h->pinned->err, h->err, 8, cudaMemcpyDeviceToHost, h->st));
     CK(h, cudaStreamSynchronize(h->st));
-    return device_error_status(h, h->pinned->err);
+    return device_error_status(h, h->pinned->err[0] | h->pinned->err[1]);
 }
 
 extern "C" int llm_reset(llm_handle* h) {
     LIVE_OR_RETURN(h);
     CK(h, cudaStreamSynchronize(h->st));
-    CK(h, cudaMemsetAsync(h->err, 0, 4, h->st));
+    CK(h, cudaMemsetAsync(h->err, 0, 8, h->st));
     CK(h, cudaMemsetAsync(h->counters, 0, (size_t)h->n_counters * 4, h->st));
     CK(h, cudaMemsetAsync(h->best, 0, 8, h->st));
     // a step that stopped early may have left words with the next step's tag
@@ -802,7 +803,7 @@ static PrefillCtx prefill_ctx(const llm_handle* h) {
     pc.eps = h->cfg.eps; pc.theta_scale = h->theta_scale; pc.attn_div = h->attn_div;
     pc.layers = h->layers.data(); pc.embd = h->embd; pc.out = h->out; pc.out_norm = h->out_norm;
     pc.rope_freqs = h->rope_freqs; pc.logits = h->logits; pc.argmax_dev = h->tok_out; pc.best = h->best; pc.err = h->err;
-    pc.f16_copy = h->f16_copy;
+    pc.f16_copy = h->f16_copy; pc.batch_err = h->err + 1; pc.batch_wait_limit = h->test_batch_wait;
     return pc;
 }
 
@@ -1116,6 +1117,13 @@ extern "C" int llm_debug_tensor(llm_handle* h, int layer, int which, float* host
     return LLM_OK;
 }
 
+extern "C" int llm_test_batch_wait(llm_handle* h, int32_t probes) {
+    LIVE_OR_RETURN(h);
+    if (probes < 0 || probes > 1000) return fail(h, LLM_ERR_OUT_OF_RANGE, "%d probes not in [0, 1000]", probes);
+    h->test_batch_wait = probes;
+    return LLM_OK;
+}
+
 extern "C" int llm_test_logits_limit(llm_handle* h, int32_t limit) {
     LIVE_OR_RETURN(h);
 #ifdef LLM_CHECKED
@@ -1319,9 +1327,9 @@ extern "C" int llm_decode_step_noalloc(llm_handle* h, const int32_t* token_dev, 
     void* args[] = {&p};
     CK(h, cudaLaunchCooperativeKernel(h->kernel, dim3(h->sms), dim3(kBlock), args, h->smem, h->st));
     h->launches++;
-    CK(h, cudaMemcpyAsync(&h->pinned->err, base + sl.err, 4, cudaMemcpyDeviceToHost, h->st));
+    CK(h, cudaMemcpyAsync(h->pinned->err, base + sl.err, 4, cudaMemcpyDeviceToHost, h->st));
     CK(h, cudaStreamSynchronize(h->st));
-    const int e = h->pinned->err;
+    const int e = h->pinned->err[0];
     if (e) {
         // a step that stopped early may have left words with the next step's tag
         CK(h, cudaMemsetAsync(base + sl.tv, 0, sl.tv_bytes, h->st));

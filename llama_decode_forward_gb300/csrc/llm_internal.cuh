@@ -199,6 +199,9 @@ struct PrefillCtx {
     int* argmax_dev;                         // the last token's argmax
     unsigned long long* best;                // argmax key, zero before and after
     int* err;                                // device error word
+    int* batch_err;                          // the same of the batch's attention (kErrTimeout), apart from err, which the
+                                             // GEMMs' waits look at
+    int batch_wait_limit;                    // > 0: a test's limit of its waits
     const __half* f16_copy;                  // Q8_0: the F16 copy of the layer matrices, or nullptr
 };
 bool prefill_supported(const PrefillCtx& c);
@@ -215,6 +218,9 @@ cudaError_t rope_table(cudaStream_t st, float* tab, int n, int pos0, int rope_di
 // Records the calling thread's reason (llm_last_error(NULL)) of a failed call
 // without a handle; returns `status`.
 int fail_op(int status, const char* fmt, ...);
+// llm_attend_batch, with a word that waits which gave up set to kErrTimeout (or nullptr) and
+// a test's limit of the waits' probes (0: the usual one).
+int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit);
 // A step of a batch (llm_decode_batch): `ws` holds prefill_workspace_bytes(c), tab the
 // angles of positions 0 .. tab_rows-1, attend_ws the attention's workspace.  Returns a
 // status; a CUDA error's text and the failing step are in *why (otherwise the reason is

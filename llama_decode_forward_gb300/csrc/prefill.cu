@@ -1346,7 +1346,7 @@ int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* 
         // the prompt's rows are the handle's cache; the output is the O projection's operand
         llm_attend at{c.n_heads, LLM_F32, LLM_F16, 1.0f / c.attn_div, bb.QKV, qkv_w, bb.Ah, c.q_dim,
                       reinterpret_cast<const uint16_t*>(L.kc), reinterpret_cast<const uint16_t*>(L.vc), c.kv_dim, attend_ws, attend_ws_bytes};
-        rc = llm_attend_batch(&pages, &at, c.st);
+        rc = attend_batch(&pages, &at, c.st, c.batch_err, c.batch_wait_limit);
         if (rc) return rc;
         *launches += 2 + (b.prefix_len > 0) + (b.max_pages > 0);
         GemmOut oo{nullptr, nullptr, bb.X, nullptr};

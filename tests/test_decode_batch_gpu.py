@@ -431,3 +431,42 @@ def test_decoder_on_its_own_stream(lib, outer):
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(junk) == 8
     lib.llm_sync(dec.h)
     dec.close()
+
+
+@pytest.mark.parametrize("kw", [{}, dict(wtype=synth.Q8_0, bias=False, number=83),
+                                dict(dim=512, n_heads=4, n_kv_heads=1, head_dim=128, vocab=1003, number=86)])
+def test_wait_that_gives_up_reaches_the_handle(lib, kw):
+    """A wait of the prefix attention that runs out (nothing is copied, its limit is short)
+    is the handle's device error, with the batch's own error word and without one."""
+    cfg = config(**kw)
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 150), 0)
+    bd = lib.BatchDecoder(dec, 3, 16, 150)
+    put(bd, cfg, [1, 1, 1])
+    bd.step()
+    lib.llm_sync(dec.h)
+    want = bd.logits.clone()
+    err = bd.struct.err
+    for word in (None, err):
+        bd.struct.err = word
+        lib.llm_test_batch_wait(dec.h, 20)
+        bd.step()
+        lib.llm_test_batch_wait(dec.h, 0)
+        with pytest.raises(lib.LlmError) as e:
+            lib.llm_sync(dec.h)
+        assert e.value.status == lib.LLM_ERR_DEVICE_TIMEOUT
+        assert bd.errors() == (lib.LLM_PAGES_TIMEOUT if word else 0)
+        with pytest.raises(lib.LlmError) as e:
+            bd.step()
+        assert e.value.status == lib.LLM_ERR_STATE
+        lib.llm_reset(dec.h)
+        lib.llm_prefill(dec.h, synth.prompt(cfg, 150), 0)
+        bd.err.zero_()
+        bd.step()
+        lib.llm_sync(dec.h)
+        assert torch.equal(bd.logits, want) and bd.errors() == 0
+    for bad in (-1, 1001):
+        with pytest.raises(lib.LlmError) as e:
+            lib.llm_test_batch_wait(dec.h, bad)
+        assert e.value.status == lib.LLM_ERR_OUT_OF_RANGE
+    dec.close()
