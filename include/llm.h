@@ -459,9 +459,9 @@ typedef struct {
 
 /* The arithmetic: F32 softmax statistics and sums of exact products.  Each
  * probability meets V as two FP16 parts (as in the batched prefill's
- * attention), whatever the output's type.  An F32 q becomes two parts too: 22
- * bits of each element (none below 2^-25), whose magnitude must not exceed
- * 65504.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+ * attention), whatever the output's type.  An F32 q becomes two parts too, after
+ * a power of two of its row and head: 22 bits of each element down to 2^-39 of
+ * the largest.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int llm_attend_batch(const llm_pages *pages, const llm_attend *a, llm_stream_t stream);
 
 /* Bytes of workspace that a call with these sizes needs (the pointers are not

@@ -56,6 +56,7 @@ struct AttendDev {
 // shared ones 18 us of 90, 64 rows behind 32,000 6 us of 52, and nothing where the
 // pages are the larger part.
 constexpr float kHead = 8.f, kLag = 6.f;
+constexpr float kLow = -3e38f;               // a maximum where there is no key: low, but a number
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -93,6 +94,22 @@ __device__ __forceinline__ void load_q8(const AttendDev& a, long long at, float 
     }
 }
 
+// An F32 row of q is multiplied by a power of two that brings its largest element to
+// 2^14 .. 2^15, so that its two F16 parts hold 22 bits of every element down to 2^-39 of
+// the largest, whatever the row's magnitude; its scores are multiplied by the inverse.
+struct PowerOfTwo {
+    float up, down;                 // the factor of q and that of the scores
+};
+__device__ __forceinline__ float largest8(const float (&x)[8], float m) {
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) m = max3(m, fabsf(x[k]), fabsf(x[k + 1]));
+    return m;
+}
+__device__ __forceinline__ PowerOfTwo power_of(int exponent) {         // the largest element's
+    const int e = max(15, exponent);         // (15: the factor stays below 2^127; infinity has 255)
+    return {__uint_as_float((uint32_t)(268 - e) << 23), __uint_as_float((uint32_t)(e - 14) << 23)};
+}
+
 // Element offset of row r (of kv head g's rows) in q.
 __device__ __forceinline__ long long q_offset(const AttendDev& a, int hd, int g, int r) {
     return (long long)(r / a.gq) * a.q_stride + (long long)(g * a.gq + r % a.gq) * hd;
@@ -125,7 +142,9 @@ struct PrefixPlan {
     // more than half of an SM's shared memory: a second block there would only wait
     // for the first one's tensor memory
     static constexpr int kStages = HDP == 64 ? 8 : 5;
-    static constexpr int kSmem = kStages * 2 * kTileBytes + 512 + 1024;
+    // behind the ring: the barriers and the tensor memory's address, then a byte per softmax thread
+    static constexpr int kBars = 8 * (2 * kStages + 3 * kScores + 4) + 16;
+    static constexpr int kSmem = kStages * 2 * kTileBytes + kBars + 256 + 1024;
 };
 
 constexpr int kSoftmaxWarps = 8, kPrefixThreads = 32 * (kSoftmaxWarps + 3);
@@ -238,6 +257,7 @@ __global__ void __maxnreg__(kPrefixRegs)
     uint64_t* qfull = pvdone + kScores;
     uint64_t* fin = qfull + 2;               // [2] every MMA of a group has completed
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 2);
+    uint8_t* q_exponent = reinterpret_cast<uint8_t*>(full) + G::kBars;     // [256] of the largest element that each softmax thread has loaded
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int mt = (a.rows + 127) / 128, ntiles = (p.prefix_len + kKT - 1) / kKT;
     const long long total = (long long)mt * p.n_kv * ntiles;
@@ -353,7 +373,7 @@ __global__ void __maxnreg__(kPrefixRegs)
         // ---- softmax
         const int group = warp >> 2, lrow = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, to = tmem + lanes + G::kO + group * HDP;
-        float M = 0.f, l = 0.f;              // M: the reference less kHead
+        float M = 0.f, l = 0.f, sc = a.sc;   // M: the reference less kHead; sc: the factor of the row's scores
         // after a wait that gave up the warp goes on without waiting, to no result
         for (int begin = 0, tile0 = t0, unit = u0; begin < n; tile0 = 0, unit++) {
             // ---- a unit's tiles, `begin` to `end` of the block's: first this group's half of the
@@ -362,6 +382,25 @@ __global__ void __maxnreg__(kPrefixRegs)
             if (begin > 0) ok = ok && warp_wait(&sfull[(begin - 1) % kScores], (uint32_t)(((begin - 1) / kScores) & 1), a);
             tm_fence_after();
             const long long q_at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
+            float up = 1.f;
+            if (SPLITQ) {
+                // the largest of this group's columns, and the other group's
+                float m = 0.f;
+#pragma unroll
+                for (int c = 0; c < HDP / 16; c++) {
+                    float x[8];
+                    if (r < a.rows && group * (HDP / 2) + c * 8 < p.hd) {
+                        load_q8(a, q_at + group * (HDP / 2) + c * 8, x);
+                        m = largest8(x, m);
+                    }
+                }
+                const int e = (int)(__float_as_uint(m) >> 23);
+                q_exponent[threadIdx.x] = (uint8_t)e;
+                asm volatile("bar.sync 9, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
+                const PowerOfTwo two = power_of(max(e, (int)q_exponent[threadIdx.x ^ 128]));
+                up = two.up;
+                sc = a.sc * two.down;
+            }
 #pragma unroll
             for (int h = 0; h < HDP / 64; h++) {
                 const int c0 = group * (HDP / 2) + h * 32;             // 32 columns from here
@@ -370,6 +409,9 @@ __global__ void __maxnreg__(kPrefixRegs)
                 for (int c = 0; c < 4; c++) {
                     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     if (r < a.rows && c0 + c * 8 < p.hd) load_q8(a, q_at + c0 + c * 8, x);
+                    if (SPLITQ)
+#pragma unroll
+                        for (int k = 0; k < 8; k++) x[k] *= up;
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
                         hi[4 * c + k] = pack_hi(x[2 * k], x[2 * k + 1]);
@@ -407,7 +449,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                 };
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 auto probabilities = [&](int h, const uint32_t (&s)[32]) {
-                    const float2 sc2 = make_float2(a.sc, a.sc), m2 = make_float2(-M, -M);
+                    const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-M, -M);
 #pragma unroll
                     for (int k = 0; k < 32; k += 16) {       // one MMA's keys: eight columns of high parts, eight of low ones
                         uint32_t p2[16];
@@ -427,7 +469,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                 float mx = largest(s);
                 scores(1, s);
                 mx = fmaxf(mx, largest(s));
-                const float top = fmaxf(mx * a.sc, -1e30f) - kHead;
+                const float top = fmaxf(mx * sc, kLow) - kHead;
                 if (it == first) {
                     M = top;
                     l = 0.f;
@@ -482,7 +524,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                             *reinterpret_cast<uint4*>(a.prefix_o + at * p.hd + h + k) =
                                 any ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
             }
-            if (r < a.rows) a.prefix_ml[at] = any ? make_float2(M, l) : make_float2(-1e30f, 0.f);
+            if (r < a.rows) a.prefix_ml[at] = any ? make_float2(M, l) : make_float2(kLow, 0.f);
             // O has been read before the next unit's first P V, which waits for these warps' probabilities
             tm_fence_before();
             begin = end;
@@ -689,15 +731,37 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
             // q as the second operand: query row r of each eight; rows behind the last repeat it (never stored)
             uint32_t qhi[NT][2 * CH][2], qlo[NT][SPLITQ ? 2 * CH : 1][2];
             int e[NT][2];                    // the last cached row that query rows 2t and 2t + 1 see
+            float qs[NT][2];                 // and the factor of their scores
 #pragma unroll
             for (int q = 0; q < NT; q++) {
                 const long long at = q_offset(a, p.hd, g, s * srows + min(tile * RU + q * 8 + r, srows - 1));
 #pragma unroll
                 for (int k = 0; k < 2; k++) e[q][k] = last + min(tile * RU + q * 8 + 2 * t + k, srows - 1) / a.gq;
+                float up = 1.f;
+                qs[q][0] = qs[q][1] = a.sc;
+                if (SPLITQ) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < CH; i++) {
+                        float x[8];
+                        if (8 * (t + 4 * i) < p.hd) {
+                            load_q8(a, at + 8 * (t + 4 * i), x);
+                            m = largest8(x, m);
+                        }
+                    }
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    const PowerOfTwo two = power_of((int)(__float_as_uint(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2))) >> 23));
+                    up = two.up;
+#pragma unroll
+                    for (int k = 0; k < 2; k++) qs[q][k] = a.sc * __shfl_sync(0xffffffffu, two.down, 4 * (2 * t + k));
+                }
 #pragma unroll
                 for (int i = 0; i < CH; i++) {
                     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                     if (8 * (t + 4 * i) < p.hd) load_q8(a, at + 8 * (t + 4 * i), x);
+                    if (SPLITQ)
+#pragma unroll
+                        for (int k = 0; k < 8; k++) x[k] *= up;
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
                         const uint32_t hi = pack_hi(x[2 * k], x[2 * k + 1]);
@@ -711,7 +775,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
             for (int q = 0; q < NT; q++) {
 #pragma unroll
                 for (int d = 0; d < 2 * CH; d++) o[q][d][0] = o[q][d][1] = o[q][d][2] = o[q][d][3] = 0.f;
-                M[q][0] = M[q][1] = -1e30f;  // no key seen yet: low, but a number
+                M[q][0] = M[q][1] = kLow;    // no key seen yet
                 l[q][0] = l[q][1] = 0.f;
             }
             for (int i0 = 0; i0 < count; i0++) {
@@ -754,7 +818,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                         float m = fmaxf(sc[q][k], sc[q][2 + k]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        top[k] = fmaxf(m * a.sc, -1e30f) - kHead;
+                        top[k] = fmaxf(m * qs[q][k], kLow) - kHead;
                         move |= top[k] > M[q][k] + kLag;
                     }
                     if (__any_sync(0xffffffffu, move)) {
@@ -776,7 +840,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     }
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        sc[q][k] = exp2_fast(fmaf(sc[q][k], a.sc, -M[q][k & 1]));
+                        sc[q][k] = exp2_fast(fmaf(sc[q][k], qs[q][k & 1], -M[q][k & 1]));
                         l[q][k & 1] += sc[q][k];          // this thread's cached rows; all are added at the end
                     }
 #pragma unroll

@@ -939,3 +939,41 @@ def test_attend_many_short_units(lib, prefix, types):
         op()
         assert torch.equal(out, first)
     assert b.pages.errors() == 0
+
+
+@pytest.mark.parametrize("out_dtype", [F32, F16])
+@pytest.mark.parametrize("heads,lens,n_new", [((8, 2, 64), [40, 7, 1], 1), ((12, 2, 64), [40, 7, 5], 5), ((4, 4, 128), [3, 70], 2)])
+@pytest.mark.parametrize("size", [1e7, 1e30, 3e38 / 256, 1e-9, 1e-36])
+def test_attend_f32_queries_of_any_magnitude(lib, size, heads, lens, n_new, out_dtype):
+    """F32 queries far above F16's largest number and far below its smallest, rows of
+    different magnitudes in one tile: the bound is the one of queries near 1."""
+    n_heads, n_kv, hd = heads
+    b = Batch(lib, lens, n_new, 130, 16, n_kv, hd)
+    q = rand(1, len(lens) * n_new, n_heads, hd) * size
+    q[:, 1::2] *= 2.0 ** -20                          # flat scores next to pointed ones
+    q[:, 0, ::3] *= 2.0 ** -12                        # small elements beside large ones
+    pk, pv = rand(2, 130, n_kv, hd, dtype=F16), rand(3, 130, n_kv, hd, dtype=F16)
+    out = torch.zeros(*q.shape, dtype=out_dtype, device="cuda")
+    scale = float(np.float32(hd ** -0.5 / size))
+    lib.AttendBatch(b.pages, q, out, pk, pv, scale=scale)()
+    check_attend(b, q, out, pk, pv, scale)
+    assert b.pages.errors() == 0
+
+
+def test_attend_f32_queries_not_finite(lib):
+    """A query that is not finite gives NaN in its own row and head, nowhere else; one of
+    zeros the mean of the values."""
+    b = Batch(lib, [20, 5], 1, 70, 16, 2, 64)
+    q = rand(1, 2, 4, 64)
+    q[0, 1, 3], q[1, 2, 63] = math.inf, math.nan
+    q[1, 3] = 0.0
+    pk, pv = rand(2, 70, 2, 64, dtype=F16), rand(3, 70, 2, 64, dtype=F16)
+    out = torch.zeros(2, 4, 64, device="cuda")
+    lib.AttendBatch(b.pages, q, out, pk, pv)()
+    assert out[0, 1].isnan().all() and out[1, 2].isnan().all()
+    q[0, 1] = q[1, 2] = 1.0
+    again = torch.zeros_like(out)
+    lib.AttendBatch(b.pages, q, again, pk, pv)()
+    check_attend(b, q, again, pk, pv)
+    for row, h in ((0, 0), (0, 2), (0, 3), (1, 0), (1, 1), (1, 3)):
+        assert torch.equal(out[row, h], again[row, h])
