@@ -3,9 +3,9 @@
 // own sequence's pages.
 //
 // The softmax splits over the keys: a part keeps, per query row, a reference
-// M, l = sum 2^(y_t - M) and O = sum 2^(y_t - M) v_t over its keys (y =
+// Y, l = sum 2^(y_t - Y) and O = sum 2^(y_t - Y) v_t over its keys (y =
 // scale log2(e) q.k), and parts join as out = sum_i w_i O_i / sum_i w_i l_i,
-// w_i = 2^(M_i - max M).  Three kernels, chained by programmatic dependent
+// w_i = 2^(Y_i - max Y).  Three kernels, chained by programmatic dependent
 // launches:
 //   prefix_kernel  every query row of the batch against the shared rows: the
 //                  rows (new token, head of the kv head's group) of all
@@ -35,7 +35,7 @@ struct AttendDev {
     long long out_stride;
     int out_f16;
     float* prefix_o;                // [n_kv * row tiles + blocks][2 groups][128][hd]
-    float2* prefix_ml;              // [n_kv * row tiles + blocks][2][128]: M, l
+    float2* prefix_ml;              // [n_kv * row tiles + blocks][2][128]: Y, l
     float* suffix_o;                // [units of all sequences + workers][up to 16 rows][hd]
     float2* suffix_ml;
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
@@ -46,17 +46,22 @@ struct AttendDev {
                                     // (a test's) it makes no copies either, so that they do
 };
 
-// Probabilities are kept as 2^(y - M) with M = (a recent maximum) - kHead, so
-// that the largest is about 2^kHead: F16 then resolves those 2^-33 of it
-// (its subnormal step 2^-24, halved by rounding), and the reference may lag
-// behind the running maximum by kLag before 2^(kHead + kLag) nears F16's 2^16.
+// Probabilities are kept as 2^(y - Y + kHead) with Y = (scale log2(e)) R and R a recent
+// maximum of the scores, so that the largest is about 2^kHead: F16 then resolves those
+// 2^-33 of it (its subnormal step 2^-24, halved by rounding), and R may lag behind the
+// running maximum by kLag / (scale log2(e)) before 2^(kHead + kLag) nears F16's 2^16.
+// The scores' difference is taken first and then scaled: as fma(score, scale, kHead - Y)
+// every exponent would keep the half step by which Y was rounded, and with |y| above 2^27
+// the largest probability be infinite or zero.  (256 rows behind 16,000 shared ones 80 us
+// that way, 85 us this way; a branch that keeps the difference to rows that need it took
+// as long.)  Parts give Y to the join; their common 2^kHead cancels there.
 // Each meets V as two F16 parts, its first 22 bits, whatever the output's type:
 // with one part (11 bits) F16 outputs were 1.4 times as far from the exact ones as
 // one rounding leaves them; the second part's products cost 256 rows behind 16,000
 // shared ones 18 us of 90, 64 rows behind 32,000 6 us of 52, and nothing where the
 // pages are the larger part.
 constexpr float kHead = 8.f, kLag = 6.f;
-constexpr float kLow = -3e38f;               // a maximum where there is no key: low, but a number
+constexpr float kLow = -3e38f;               // R, or Y, where there is no key: low, but a number
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -373,7 +378,7 @@ __global__ void __maxnreg__(kPrefixRegs)
         // ---- softmax
         const int group = warp >> 2, lrow = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, to = tmem + lanes + G::kO + group * HDP;
-        float M = 0.f, l = 0.f, sc = a.sc;   // M: the reference less kHead; sc: the factor of the row's scores
+        float R = 0.f, l = 0.f, sc = a.sc;   // sc: the factor of the row's scores
         // after a wait that gave up the warp goes on without waiting, to no result
         for (int begin = 0, tile0 = t0, unit = u0; begin < n; tile0 = 0, unit++) {
             // ---- a unit's tiles, `begin` to `end` of the block's: first this group's half of the
@@ -449,13 +454,14 @@ __global__ void __maxnreg__(kPrefixRegs)
                 };
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 auto probabilities = [&](int h, const uint32_t (&s)[32]) {
-                    const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-M, -M);
+                    const float2 sc2 = make_float2(sc, sc), r2 = make_float2(-R, -R), head2 = make_float2(kHead, kHead);
 #pragma unroll
                     for (int k = 0; k < 32; k += 16) {       // one MMA's keys: eight columns of high parts, eight of low ones
                         uint32_t p2[16];
 #pragma unroll
                         for (int c = 0; c < 8; c++) {
-                            const float2 y = __ffma2_rn(make_float2(__uint_as_float(s[k + 2 * c]), __uint_as_float(s[k + 2 * c + 1])), sc2, m2);
+                            const float2 d = __fadd2_rn(make_float2(__uint_as_float(s[k + 2 * c]), __uint_as_float(s[k + 2 * c + 1])), r2);
+                            const float2 y = __ffma2_rn(d, sc2, head2);
                             const float2 e = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                             l2[c & 1] = __fadd2_rn(l2[c & 1], e);
                             p2[c] = pack_hi(e.x, e.y);
@@ -469,15 +475,15 @@ __global__ void __maxnreg__(kPrefixRegs)
                 float mx = largest(s);
                 scores(1, s);
                 mx = fmaxf(mx, largest(s));
-                const float top = fmaxf(mx * sc, kLow) - kHead;
+                mx = fmaxf(mx, kLow);
                 if (it == first) {
-                    M = top;
+                    R = mx;
                     l = 0.f;
-                } else if (__any_sync(0xffffffffu, top > M + kLag)) {
+                } else if (__any_sync(0xffffffffu, (mx - R) * sc > kLag)) {
                     float c = 1.f;
-                    if (top > M + kLag) {
-                        c = exp2_fast(M - top);
-                        M = top;
+                    if ((mx - R) * sc > kLag) {
+                        c = exp2_fast((R - mx) * sc);
+                        R = mx;
                     }
                     l *= c;
                     ok = ok && warp_wait(&pvdone[(it - 2) % kScores], (uint32_t)(((it - 2) / kScores) & 1), a);
@@ -524,7 +530,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                             *reinterpret_cast<uint4*>(a.prefix_o + at * p.hd + h + k) =
                                 any ? make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]) : make_uint4(0, 0, 0, 0);
             }
-            if (r < a.rows) a.prefix_ml[at] = any ? make_float2(M, l) : make_float2(kLow, 0.f);
+            if (r < a.rows) a.prefix_ml[at] = any ? make_float2(fmaxf(R * sc, kLow), l) : make_float2(kLow, 0.f);
             // O has been read before the next unit's first P V, which waits for these warps' probabilities
             tm_fence_before();
             begin = end;
@@ -770,12 +776,12 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     }
                 }
             }
-            float o[NT][2 * CH][4], M[NT][2], l[NT][2];
+            float o[NT][2 * CH][4], R[NT][2], l[NT][2];
 #pragma unroll
             for (int q = 0; q < NT; q++) {
 #pragma unroll
                 for (int d = 0; d < 2 * CH; d++) o[q][d][0] = o[q][d][1] = o[q][d][2] = o[q][d][3] = 0.f;
-                M[q][0] = M[q][1] = kLow;    // no key seen yet
+                R[q][0] = R[q][1] = kLow;    // no key seen yet
                 l[q][0] = l[q][1] = 0.f;
             }
             for (int i0 = 0; i0 < count; i0++) {
@@ -818,16 +824,17 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                         float m = fmaxf(sc[q][k], sc[q][2 + k]);
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                        top[k] = fmaxf(m * qs[q][k], kLow) - kHead;
-                        move |= top[k] > M[q][k] + kLag;
+                        top[k] = fmaxf(m, kLow);
+                        move |= (top[k] - R[q][k]) * qs[q][k] > kLag;
                     }
                     if (__any_sync(0xffffffffu, move)) {
                         float c[2];
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
-                            const float up = fmaxf(M[q][k], top[k]);
-                            c[k] = exp2_fast(M[q][k] - up);
-                            M[q][k] = up;
+                            // (a row's own maximum decides: its bits do not depend on its neighbours)
+                            const float up = (top[k] - R[q][k]) * qs[q][k] > kLag ? top[k] : R[q][k];
+                            c[k] = exp2_fast((R[q][k] - up) * qs[q][k]);
+                            R[q][k] = up;
                             l[q][k] *= c[k];
                         }
 #pragma unroll
@@ -840,7 +847,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     }
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        sc[q][k] = exp2_fast(fmaf(sc[q][k], qs[q][k & 1], -M[q][k & 1]));
+                        sc[q][k] = exp2_fast(fmaf(sc[q][k] - R[q][k & 1], qs[q][k & 1], kHead));
                         l[q][k & 1] += sc[q][k];          // this thread's cached rows; all are added at the end
                     }
 #pragma unroll
@@ -908,7 +915,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                         const int d = 8 * (r >> 1) + 32 * (i / 4) + 2 * (i % 4) + (r & 1);
                         if (d < p.hd) dst[d] = o[q][i / 2][2 * (i & 1) + k];
                     }
-                    if (r == 0) a.suffix_ml[slot + row] = make_float2(M[q][k], l[q][k]);
+                    if (r == 0) a.suffix_ml[slot + row] = make_float2(fmaxf(R[q][k] * qs[q][k], kLow), l[q][k]);
                 }
             left -= count + kUnit;
             if (left > 0) next(s, j, pc, np);

@@ -977,3 +977,23 @@ def test_attend_f32_queries_not_finite(lib):
     check_attend(b, q, again, pk, pv)
     for row, h in ((0, 0), (0, 2), (0, 3), (1, 0), (1, 1), (1, 3)):
         assert torch.equal(out[row, h], again[row, h])
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("q_dtype,q_size,k_size", [(F32, 1e30, 1), (F32, 1e9, 1), (F16, 30000, 4000), (F32, 2e3, 4000)])
+@pytest.mark.parametrize("prefix,lens", [(90, [1]), (0, [70]), (700, [40])])
+def test_attend_scores_far_from_zero(lib, prefix, lens, q_dtype, q_size, k_size, sign):
+    """Scores of 10^8 to 10^32, all on one side of zero: the largest takes all."""
+    b = Batch(lib, lens, 1, prefix, 16, 1, 64)
+    q = torch.full((1, 2, 64), float(q_size), dtype=q_dtype, device="cuda")
+    pk, pv = (rand(2, max(prefix, 1), 1, 64).abs() + 0.1).mul(sign * k_size).half(), rand(3, max(prefix, 1), 1, 64, dtype=F16)
+    b.k.copy_((b.k.abs() + 0.1) * sign * k_size)
+    out = torch.zeros(1, 2, 64, device="cuda")
+    lib.AttendBatch(b.pages, q, out, pk, pv)()
+    keys, values = torch.cat([pk[:prefix].double(), b.gather(b.k, 0, lens[0])]), torch.cat([pv[:prefix].double(), b.gather(b.v, 0, lens[0])])
+    total = keys[:, 0].sum(-1)
+    best = total.argmax()
+    # the second best is far behind, whatever 64 additions of F32 leave of the scores (2^-17)
+    assert total.sort().values[-2] < total[best] - total[best].abs() * 2.0 ** -16
+    # one probability of 1 as two F16 parts, one division: 2^-22 and a few roundings
+    assert ((out[0].double() - values[best, 0]).abs() <= 2.0 ** -20 * values[best, 0].abs()).all()
