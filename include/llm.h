@@ -267,22 +267,23 @@ int llm_test_logits_limit(llm_handle *h, int32_t limit);
 int llm_test_batch_wait(llm_handle *h, int32_t probes);
 
 /* Test hook: allocation failure.  The nth device or pinned-host allocation
- * the library makes from now on (in llm_create, llm_create_from_gguf or
- * llm_prefill's workspace) fails as if the device were out of memory, once;
+ * the library makes from now on (in llm_create, llm_create_from_gguf,
+ * llm_prefill's workspace or llm_decode_batch's memory) fails as if the device were out of memory, once;
  * 0 disarms.  The failing call returns LLM_ERR_NO_MEMORY and releases what it
  * had allocated.  Process-wide.  Errors: INVALID_ARG for nth < 0. */
 int llm_test_fail_alloc(int32_t nth);
 
-/* Test hook: guard bands.  The KV cache, the activation buffer and the
- * prefill workspace are allocated with 4096 bytes more on each side, filled
- * with 0xA5.  Returns how many of those bytes differ from 0xA5 (0: no kernel
+/* Test hook: guard bands.  The KV cache, the activation buffer, the prefill
+ * workspace and llm_decode_batch's workspace and angle table are allocated
+ * with 4096 bytes more on each side, filled with 0xA5.  Returns how many of those bytes differ from 0xA5 (0: no kernel
  * wrote past either end of these buffers), or a negative status.
  * Synchronous. */
 int64_t llm_test_guards(llm_handle *h);
 
 /* Test hook: overwrites the guard byte adjacent to one end of a guarded
  * buffer (band 2b: before buffer b, 2b+1: after it; b = 0 KV cache,
- * 1 activations, 2 prefill workspace once allocated), so that a test can see
+ * 1 activations, then what is allocated of: prefill workspace, the batch's
+ * workspace, its angle table), so that a test can see
  * llm_test_guards report it.  Synchronous.  Errors: OUT_OF_RANGE. */
 int llm_test_poke_guard(llm_handle *h, int band);
 

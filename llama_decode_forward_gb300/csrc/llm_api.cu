@@ -64,8 +64,8 @@ static cudaError_t host_alloc(void** p, size_t bytes) {
     return cudaMallocHost(p, bytes);
 }
 
-// Guard bands: the KV cache, the activations and the prefill workspace are
-// allocated with kGuardBytes more on each side, filled with kGuardByte; the
+// Guard bands: the KV cache, the activations, the prefill workspace and the
+// batch's workspace and angle table are allocated with kGuardBytes more on each side, filled with kGuardByte; the
 // buffer proper starts kGuardBytes into the allocation (256-byte alignment
 // kept).  llm_test_guards counts guard bytes that changed: a kernel that
 // wrote past either end of one of these buffers shows up there.
@@ -148,10 +148,9 @@ struct llm_handle {
     size_t prefill_ws_bytes = 0;
     __half* f16_copy = nullptr;      // llm_prefill_f16_copy: F16 copy of the Q8_0 layer matrices
     size_t f16_copy_bytes = 0;
-    float* batch_tab = nullptr;      // llm_decode_batch: angles of positions 0 .. batch_tab_rows-1
+    Guarded batch_tab;               // llm_decode_batch: angles of positions 0 .. batch_tab_rows-1
     int batch_tab_rows = 0;
-    void* batch_ws = nullptr;        // and the attention's workspace
-    size_t batch_ws_bytes = 0;
+    Guarded batch_ws;                // and the attention's workspace
     bool captured = false;           // a step of llm_decode_batch was captured into a graph
     std::vector<void*> retired;      // what was replaced after that: graphs hold its addresses, freed with the handle
     int test_batch_wait = 0;         // llm_test_batch_wait: > 0 limits the batch attention's waits
@@ -313,8 +312,8 @@ static void free_handle(llm_handle* h) {
     cudaFree(h->kv_maps);
     guarded_free(h->ws_mem);
     cudaFree(h->f16_copy);
-    cudaFree(h->batch_tab);
-    cudaFree(h->batch_ws);
+    guarded_free(h->batch_tab);
+    guarded_free(h->batch_ws);
     for (void* p : h->retired) cudaFree(p);
     cudaFree(h->trace);
     if (h->pinned) cudaFreeHost(h->pinned);
@@ -915,38 +914,41 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
     CK(h, cudaStreamIsCapturing(h->st, &capture));
     if (capture != cudaStreamCaptureStatusNone &&
-        (!h->prefill_ws || h->batch_ws_bytes < (size_t)need || h->batch_tab_rows < positions))
+        (!h->prefill_ws || h->batch_ws.bytes < (size_t)need || h->batch_tab_rows < positions))
         return fail(h, LLM_ERR_STATE, "the step would allocate during a capture; make one call of these sizes before it");
     int rc;
     if ((rc = need_prefill_ws(h, pc))) return rc;
-    if (h->batch_ws_bytes < (size_t)need) {
-        void* p = nullptr;
-        CK(h, dev_alloc(&p, (size_t)need));
-        if ((rc = retire(h, h->batch_ws))) {
-            cudaFree(p);
-            return rc;
+    // a larger buffer takes the place of one of these, once it is ready
+    auto replace = [&](Guarded& old, size_t bytes, auto fill) -> int {
+        Guarded g;
+        cudaError_t e = guarded_alloc(g, bytes, h->st);
+        if (e == cudaSuccess) e = fill(g.ptr());
+        const int rc = e == cudaSuccess ? retire(h, old.raw) : LLM_OK;
+        if (e == cudaSuccess && rc == LLM_OK) {
+            old = g;
+            return LLM_OK;
         }
-        h->batch_ws = p;
-        h->batch_ws_bytes = (size_t)need;
-    }
+        cudaStreamSynchronize(h->st);
+        guarded_free(g);
+        cudaGetLastError();
+        if (rc) return rc;
+        return fail(h, e == cudaErrorMemoryAllocation ? LLM_ERR_NO_MEMORY : LLM_ERR_CUDA, "allocating %zu bytes for a batch's steps: %s",
+                    bytes, cudaGetErrorString(e));
+    };
+    if (h->batch_ws.bytes < (size_t)need && (rc = replace(h->batch_ws, (size_t)need, [](uint8_t*) { return cudaSuccess; }))) return rc;
     if (h->batch_tab_rows < positions) {
-        float* p = nullptr;
-        CK(h, dev_alloc((void**)&p, (size_t)positions * h->cfg.rope_dims * 4));
-        const cudaError_t e = rope_table(h->st, p, (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs);
-        if (e != cudaSuccess || (rc = retire(h, h->batch_tab))) {
-            cudaStreamSynchronize(h->st);
-            cudaFree(p);
-            cudaGetLastError();
-            return e == cudaSuccess ? rc : fail(h, LLM_ERR_CUDA, "angle table: %s", cudaGetErrorString(e));
-        }
+        rc = replace(h->batch_tab, (size_t)positions * h->cfg.rope_dims * 4, [&](uint8_t* p) {
+            return rope_table(h->st, reinterpret_cast<float*>(p), (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs);
+        });
+        if (rc) return rc;
         h->launches++;
-        h->batch_tab = p;
         h->batch_tab_rows = (int)positions;
     }
     if (capture != cudaStreamCaptureStatusNone) h->captured = true;
     const char* why = nullptr;
     int launches = 0;
-    rc = decode_batch_rows(pc, *b, h->prefill_ws, h->batch_tab, h->batch_tab_rows, h->batch_ws, (int64_t)h->batch_ws_bytes, &why, &launches);
+    rc = decode_batch_rows(pc, *b, h->prefill_ws, reinterpret_cast<float*>(h->batch_tab.ptr()), h->batch_tab_rows, h->batch_ws.ptr(),
+                           (int64_t)h->batch_ws.bytes, &why, &launches);
     h->launches += launches;
     return rc ? fail(h, rc, "batch step: %s", why ? why : llm_last_error(nullptr)) : LLM_OK;
 }
@@ -1151,18 +1153,21 @@ extern "C" int llm_test_fail_alloc(int32_t nth) {
 }
 
 // The guarded buffers of a handle, in the order llm_test_poke_guard numbers
-// their bands: KV cache, activations, prefill workspace (when allocated).
+// their bands: KV cache, activations, then what is allocated of the prefill
+// workspace, the batch's workspace and its angle table.
+constexpr int kGuardedBuffers = 5;
 static int guarded_buffers(const llm_handle* h, const Guarded** out) {
     int n = 0;
     out[n++] = &h->kv_mem;
     out[n++] = &h->act_mem;
-    if (h->ws_mem.raw) out[n++] = &h->ws_mem;
+    for (const Guarded* g : {&h->ws_mem, &h->batch_ws, &h->batch_tab})
+        if (g->raw) out[n++] = g;
     return n;
 }
 
 extern "C" int64_t llm_test_guards(llm_handle* h) {
     LIVE_OR_RETURN(h);
-    const Guarded* g[3];
+    const Guarded* g[kGuardedBuffers];
     const int n = guarded_buffers(h, g);
     std::vector<uint8_t> band(kGuardBytes);
     int64_t changed = 0;
@@ -1178,7 +1183,7 @@ extern "C" int64_t llm_test_guards(llm_handle* h) {
 
 extern "C" int llm_test_poke_guard(llm_handle* h, int band) {
     LIVE_OR_RETURN(h);
-    const Guarded* g[3];
+    const Guarded* g[kGuardedBuffers];
     const int n = guarded_buffers(h, g);
     if (band < 0 || band >= 2 * n) return fail(h, LLM_ERR_OUT_OF_RANGE, "guard band %d of %d", band, 2 * n);
     const Guarded& b = *g[band / 2];

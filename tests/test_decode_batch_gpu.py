@@ -470,3 +470,26 @@ def test_wait_that_gives_up_reaches_the_handle(lib, kw):
             lib.llm_test_batch_wait(dec.h, bad)
         assert e.value.status == lib.LLM_ERR_OUT_OF_RANGE
     dec.close()
+
+
+def test_guard_bands_of_the_batch(lib):
+    """Steps of the smallest and of larger batches, with padding and a growing workspace,
+    leave every guard byte as written; a byte changed next to either end of the step's own
+    buffers is reported."""
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    lib.llm_prefill(dec.h, synth.prompt(cfg, 150), 0)
+    for n_seqs, n_new, prefix, lens in ((1, 1, 150, [16]), (3, 5, 0, [5, 2, 40]), (64, 8, 129, [8] * 63 + [300])):
+        bd = lib.BatchDecoder(dec, n_seqs, max(lens), prefix, n_new)
+        put(bd, cfg, lens)
+        bd.pages.fill_(0.25)
+        bd.step()
+        lib.llm_sync(dec.h)
+        assert bd.errors() == 0 and lib.llm_test_guards(dec.h) == 0
+    for band in range(10):                    # cache, activations, prefill workspace, the batch's workspace and angles
+        lib.llm_test_poke_guard(dec.h, band)
+        assert lib.llm_test_guards(dec.h) == band + 1
+    with pytest.raises(lib.LlmError) as e:
+        lib.llm_test_poke_guard(dec.h, 10)
+    assert e.value.status == lib.LLM_ERR_OUT_OF_RANGE
+    dec.close()
