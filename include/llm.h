@@ -266,8 +266,8 @@ int llm_test_logits_limit(llm_handle *h, int32_t limit);
  * usual.  Errors: OUT_OF_RANGE. */
 int llm_test_batch_wait(llm_handle *h, int32_t probes);
 
-/* Test hook: allocation failure.  The nth device or pinned-host allocation
- * the library makes from now on (in llm_create, llm_create_from_gguf,
+/* Test hook: allocation failure.  The nth device or pinned-host allocation (or
+ * host table of the batched prefill and of llm_decode_batch) the library makes from now on (in llm_create, llm_create_from_gguf,
  * llm_prefill's workspace or llm_decode_batch's memory) fails as if the device were out of memory, once;
  * 0 disarms.  The failing call returns LLM_ERR_NO_MEMORY and releases what it
  * had allocated.  Process-wide.  Errors: INVALID_ARG for nth < 0. */

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <new>
 #include <string>
 #include <unordered_set>
 #include <vector>
@@ -34,7 +35,8 @@ using namespace llm;
 
 // ------------------------------------------------------------ allocations --
 // Every device and pinned-host allocation of the library goes through these
-// two functions.  llm_test_fail_alloc(n) arms a countdown: the n-th
+// two functions, and the batched prefill's and batch step's host tables through
+// check_host_memory.  llm_test_fail_alloc(n) arms a countdown: the n-th
 // allocation from then on fails with cudaErrorMemoryAllocation without
 // calling CUDA (and disarms the countdown), so tests can make each allocation
 // of llm_create or llm_prefill fail in turn.
@@ -47,6 +49,10 @@ static bool injected_failure() {
 }
 
 namespace llm {
+void check_host_memory() {
+    if (injected_failure()) throw std::bad_alloc();
+}
+
 cudaError_t dev_alloc(void** p, size_t bytes) {
     if (injected_failure()) {
         *p = nullptr;
@@ -165,7 +171,11 @@ static int fail(llm_handle* h, int status, const char* fmt, ...) {
         va_start(ap, fmt);
         vsnprintf(buf, sizeof buf, fmt, ap);
         va_end(ap);
-        h->last_error = buf;
+        try {
+            h->last_error = buf;
+        } catch (...) {                    // no memory for the reason: no exception leaves a C entry
+            h->last_error.clear();
+        }
     }
     return status;
 }
@@ -947,8 +957,13 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     if (capture != cudaStreamCaptureStatusNone) h->captured = true;
     const char* why = nullptr;
     int launches = 0;
-    rc = decode_batch_rows(pc, *b, h->prefill_ws, reinterpret_cast<float*>(h->batch_tab.ptr()), h->batch_tab_rows, h->batch_ws.ptr(),
-                           (int64_t)h->batch_ws.bytes, &why, &launches);
+    try {
+        rc = decode_batch_rows(pc, *b, h->prefill_ws, reinterpret_cast<float*>(h->batch_tab.ptr()), h->batch_tab_rows, h->batch_ws.ptr(),
+                               (int64_t)h->batch_ws.bytes, &why, &launches);
+    } catch (const std::bad_alloc&) {
+        rc = LLM_ERR_NO_MEMORY;
+        why = "allocating the tensor maps";
+    }
     h->launches += launches;
     return rc ? fail(h, rc, "batch step: %s", why ? why : llm_last_error(nullptr)) : LLM_OK;
 }
@@ -969,7 +984,12 @@ extern "C" int llm_prefill(llm_handle* h, const int32_t* tokens_host, int32_t n,
         // F16 weights: tensor-core batches of up to kPrefillRows tokens
         if ((rc = need_prefill_ws(h, pc))) return rc;
         const char* what = "";
-        const cudaError_t e = prefill_f16(pc, h->prefill_ws, tokens_host, n, pos0, &what);
+        cudaError_t e;
+        try {
+            e = prefill_f16(pc, h->prefill_ws, tokens_host, n, pos0, &what);
+        } catch (const std::bad_alloc&) {
+            return fail(h, LLM_ERR_NO_MEMORY, "prefill: allocating the tensor maps");
+        }
         if (e != cudaSuccess) {
             cudaGetLastError();
             return fail(h, LLM_ERR_CUDA, "prefill (%s): %s", what, cudaGetErrorString(e));

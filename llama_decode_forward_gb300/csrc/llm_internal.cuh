@@ -215,6 +215,8 @@ cudaError_t prefill_make_f16_copy(const PrefillCtx& c, __half* dst, int* launche
 inline float rope_theta_scale(float base, int rope_dims) { return (float)pow((double)base, -2.0 / (double)rope_dims); }
 cudaError_t rope_table(cudaStream_t st, float* tab, int n, int pos0, int rope_dims, float theta_scale,
                        const float* freqs);
+// Throws std::bad_alloc where llm_test_fail_alloc's turn has come.
+void check_host_memory();
 // Records the calling thread's reason (llm_last_error(NULL)) of a failed call
 // without a handle; returns `status`.
 int fail_op(int status, const char* fmt, ...);

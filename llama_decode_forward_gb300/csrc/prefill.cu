@@ -1158,7 +1158,7 @@ struct BatchBuffers {
     bool q8;                                 // the layers' weights are expanded from the quants in the GEMMs
 };
 
-// The weight operands are the F16 matrices, the F16 copy of the Q8_0 ones, or the
+// (Throws std::bad_alloc.)  The weight operands are the F16 matrices, the F16 copy of the Q8_0 ones, or the
 // int8 quants of the Q8_0 ones (expanded to F16 tile by tile inside the GEMM), per
 // layer: QKV, O, gate/up (single rows), down; box heights = the GEMMs' tile widths.
 bool batch_buffers(const PrefillCtx& c, void* ws, BatchBuffers& b, const char** msg) {
@@ -1178,6 +1178,7 @@ bool batch_buffers(const PrefillCtx& c, void* ws, BatchBuffers& b, const char** 
         return false;
     }
     b.q8 = c.wtype == LLM_Q8_0 && !c.f16_copy;
+    check_host_memory();
     b.mw.resize((size_t)4 * c.n_layers);
     static constexpr int kBox[4] = {kBnQkv, kBnNarrow, kBnWide, kBnNarrow};
     for (int l = 0; l < c.n_layers; l++) {

@@ -493,3 +493,29 @@ def test_guard_bands_of_the_batch(lib):
         lib.llm_test_poke_guard(dec.h, 10)
     assert e.value.status == lib.LLM_ERR_OUT_OF_RANGE
     dec.close()
+
+
+def test_host_allocation_failure_is_a_status(lib):
+    """The tables that a prefill and a batch step make on the host: their allocation
+    failing is NO_MEMORY with a reason, and the next call works."""
+    cfg = config()
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    toks, logits = synth.prompt(cfg, 20), np.empty(cfg.vocab, np.float32)
+    lib.llm_prefill(dec.h, toks, 0, logits)
+    bd = lib.BatchDecoder(dec, 3, 16, 20)
+    put(bd, cfg, [1, 1, 1])
+    bd.step()
+    lib.llm_sync(dec.h)
+    want = bd.logits.clone()
+    again = np.empty(cfg.vocab, np.float32)
+    for call in (bd.step, lambda: lib.llm_prefill(dec.h, toks, 0, again)):
+        lib.llm_test_fail_alloc(1)                    # (the device memory is there: the table is the first)
+        with pytest.raises(lib.LlmError) as e:
+            call()
+        lib.llm_test_fail_alloc(0)
+        assert e.value.status == lib.LLM_ERR_NO_MEMORY and "tensor maps" in str(e.value)
+        call()
+    bd.step()
+    lib.llm_sync(dec.h)
+    assert torch.equal(bd.logits, want) and np.array_equal(again.view(np.uint32), logits.view(np.uint32))
+    dec.close()
