@@ -997,3 +997,39 @@ def test_attend_scores_far_from_zero(lib, prefix, lens, q_dtype, q_size, k_size,
     assert total.sort().values[-2] < total[best] - total[best].abs() * 2.0 ** -16
     # one probability of 1 as two F16 parts, one division: 2^-22 and a few roundings
     assert ((out[0].double() - values[best, 0]).abs() <= 2.0 ** -20 * values[best, 0].abs()).all()
+
+
+def test_calls_of_several_threads(lib):
+    """Host threads that make their first calls together, each on a stream of its own:
+    every one gets its own results."""
+    import threading
+    def make(seed):
+        b = Batch(lib, [40, 3, 100], 1, 130, 16, 2, 64, seed=seed)
+        return b, rand(seed + 5, 3, 4, 64), rand(seed + 6, 130, 2, 64, dtype=F16), rand(seed + 7, 130, 2, 64, dtype=F16), torch.zeros(3, 4, 64, device="cuda")
+    sides, errors = [make(10 * i) for i in range(6)], []
+    gate = threading.Barrier(6)
+    torch.cuda.synchronize()
+
+    def work(side):
+        try:
+            b, q, pk, pv, out = side
+            with torch.cuda.stream(torch.cuda.Stream()):
+                op = lib.AttendBatch(b.pages, q, out, pk, pv)
+                lp = lib.LogProbs(q.view(3, 256), top=3)
+                gate.wait()
+                for _ in range(20):
+                    op()
+                    lp()
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(lp.top_id.long(), q.view(3, 256).topk(3).indices)
+        except Exception as e:                         # (an exception of a thread would otherwise be lost)
+            errors.append(e)
+            gate.abort()
+    threads = [threading.Thread(target=work, args=(s,)) for s in sides]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for b, q, pk, pv, out in sides:
+        check_attend(b, q, out, pk, pv)
