@@ -587,12 +587,6 @@ __device__ __forceinline__ int clipped_len(const PagesDev& p, int s) {
 // empty ones.
 __device__ __forceinline__ int weight(int len) { return len > 0 ? (len + 15) / 16 + kUnit : 0; }
 
-// D += A B for one m16n8k16 tile with the 16 rows of A from ldmatrix.
-__device__ __forceinline__ void mma_kn8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 // An 8 x 8 matrix of F16 pairs, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -801,10 +795,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                     sc[q][0] = sc[q][1] = sc[q][2] = sc[q][3] = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < 2 * CH; ks++) {
-                        mma_kn8(sc[q], k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], qhi[q][ks][0], qhi[q][ks][1]);
-                        if (SPLITQ)
-                            mma_kn8(sc[q], k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1], qlo[q][SPLITQ ? ks : 0][0],
-                                    qlo[q][SPLITQ ? ks : 0][1]);
+                        const uint32_t k[4] = {k0[2 * ks], k1[2 * ks], k0[2 * ks + 1], k1[2 * ks + 1]};
+                        mma16816(sc[q], k, qhi[q][ks][0], qhi[q][ks][1]);
+                        if (SPLITQ) mma16816(sc[q], k, qlo[q][SPLITQ ? ks : 0][0], qlo[q][SPLITQ ? ks : 0][1]);
                     }
                 }
                 // rows that are not there, and those that some query rows do not see
@@ -891,11 +884,11 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
                 }
 #pragma unroll
                 for (int d = 0; d < 2 * CH; d++) {
-                    const uint32_t a0 = transpose8(v0[2 * d]), a1 = transpose8(v0[2 * d + 1]), a2 = transpose8(v1[2 * d]), a3 = transpose8(v1[2 * d + 1]);
+                    const uint32_t v[4] = {transpose8(v0[2 * d]), transpose8(v0[2 * d + 1]), transpose8(v1[2 * d]), transpose8(v1[2 * d + 1])};
 #pragma unroll
                     for (int q = 0; q < NT; q++) {
-                        mma_kn8(o[q][d], a0, a1, a2, a3, ph[q][0], ph[q][1]);
-                        mma_kn8(o[q][d], a0, a1, a2, a3, pl[q][0], pl[q][1]);
+                        mma16816(o[q][d], v, ph[q][0], ph[q][1]);
+                        mma16816(o[q][d], v, pl[q][0], pl[q][1]);
                     }
                 }
             }

@@ -502,14 +502,6 @@ cudaError_t launch_dep(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
-constexpr long long kSpinLimit = 200000000ll;   // mbarrier polls before a wait gives up
-__device__ __forceinline__ bool wait_parity(uint64_t* bar, uint32_t par, int* err) {
-    for (long long i = 0; i < kSpinLimit; i++)
-        if (mbar_test_wait(bar, par)) return true;
-    atomicOr(err, kErrTimeout);
-    return false;
-}
-
 // (not volatile: a pure function of its operands, so the compiler may
 // interleave independent accumulation chains)
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -45,6 +45,14 @@ constexpr int kGABytes = kGBM * kGBK * 2;
 // of 224 were slower)
 constexpr int kBnQkv = 128, kBnNarrow = 64, kBnWide = 256;
 
+constexpr long long kSpinLimit = 200000000ll;   // mbarrier polls before a wait gives up
+__device__ __forceinline__ bool wait_parity(uint64_t* bar, uint32_t par, int* err) {
+    for (long long i = 0; i < kSpinLimit; i++)
+        if (mbar_test_wait(bar, par)) return true;
+    atomicOr(err, kErrTimeout);
+    return false;
+}
+
 // The same wait with the threads suspended between probes (about 1 us at
 // most per probe): for warps that wait through a whole main loop, whose
 // polling would otherwise take shared-memory bandwidth from the tensor cores.
