@@ -519,8 +519,9 @@ int llm_logprobs(const llm_logprobs_args *a, llm_stream_t stream);
  * until llm_destroy, whatever is called between: what it uses of the handle's
  * memory (an F16 prefill copy too) is then kept until llm_destroy when a larger
  * call or llm_prefill_f16_copy replaces it.  Replays and other calls of the
- * handle share that memory and must not overlap in time.  llm_logits_device and the handle's
- * cache are left as they are.  Errors: INVALID_ARG, UNSUPPORTED, OUT_OF_RANGE, STATE,
+ * handle share that memory and must not overlap in time.  llm_logits_device and
+ * the handle's cache are left as they are.  Errors: INVALID_ARG (also where the
+ * current device is not the handle's), UNSUPPORTED, OUT_OF_RANGE, STATE,
  * NO_MEMORY, CUDA (some of the step's kernels may then have been enqueued). */
 typedef struct {
     int32_t n_seqs, n_new, prefix_len;

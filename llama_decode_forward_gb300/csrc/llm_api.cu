@@ -894,6 +894,9 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     LIVE_OR_RETURN(h);
     if (!b) return fail(h, LLM_ERR_INVALID_ARG, "the batch is NULL");
     if (h->broken) return fail(h, LLM_ERR_STATE, "handle has a device error; call llm_reset");
+    int device = -1;
+    CK(h, cudaGetDevice(&device));
+    if (device != h->device) return fail(h, LLM_ERR_INVALID_ARG, "the handle is device %d's, the current one is %d", h->device, device);
     const PrefillCtx pc = prefill_ctx(h);
     if (!prefill_supported(pc)) return fail(h, LLM_ERR_UNSUPPORTED, "this model's prefill runs the decode step token by token");
     if (b->n_seqs < 0 || b->n_new < 1 || (long long)b->n_seqs * b->n_new > kPrefillRows)
