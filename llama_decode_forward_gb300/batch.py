@@ -9,6 +9,7 @@ the same tensors, or captures the calls into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 import torch
 
@@ -55,6 +56,13 @@ def _tensor(name, t, dtypes, shape, device, strided=False):
     return t
 
 
+def _int32(**sizes) -> None:
+    """Refuses a size that a C int32 does not hold (ctypes would cut it off)."""
+    for name, n in sizes.items():
+        if not -2 ** 31 <= operator.index(n) < 2 ** 31:
+            raise ValueError(f"{name} {n} is not a 32-bit integer")
+
+
 class PagedBatch:
     """n_seqs sequences of n_new new tokens each behind a shared prefix of
     prefix_len rows (llm_pages).  k_pages, v_pages: float16 [n_pages,
@@ -64,6 +72,7 @@ class PagedBatch:
     (LLM_PAGES_*); errors() reads it."""
 
     def __init__(self, k_pages, v_pages, page_table, lens, n_new: int = 1, prefix_len: int = 0, err=None):
+        _int32(n_new=n_new, prefix_len=prefix_len)
         _tensor("k_pages", k_pages, (torch.float16,), (None,) * 4, None)
         dev = k_pages.device
         _tensor("v_pages", v_pages, (torch.float16,), tuple(k_pages.shape), dev)
@@ -75,6 +84,7 @@ class PagedBatch:
         self.k_pages, self.v_pages, self.page_table, self.lens, self.err = k_pages, v_pages, page_table, lens, err
         self.device = dev
         n_pages, page_size, n_kv, hd = k_pages.shape
+        _int32(n_pages=n_pages, page_size=page_size, sequences=lens.shape[0], max_pages=page_table.shape[1])
         self.rows = lens.shape[0] * n_new
         self.struct = _b.llm_pages(n_seqs=lens.shape[0], n_new=n_new, prefix_len=prefix_len, page_size=page_size,
                                    n_pages=n_pages, max_pages=page_table.shape[1], n_kv_heads=n_kv, head_dim=hd,
@@ -126,6 +136,7 @@ class KvAppend(_Op):
         _tensor("k", k, _DTYPES, kv, dev, strided=True)
         _tensor("v", v, (k.dtype,), kv, dev, strided=True)
         _tensor("cos_sin", cos_sin, (torch.float32,), (None, None, 2), dev)
+        _int32(positions=cos_sin.shape[0], rope_dims=2 * cos_sin.shape[1])
         a = _b.llm_append(n_heads=0, rope_dims=2 * cos_sin.shape[1], rope_neox=int(rope_neox),
                           table_rows=cos_sin.shape[0], dtype=_DTYPES[k.dtype], q_out_dtype=_b.LLM_F32,
                           k=k.data_ptr(), v=v.data_ptr(), k_stride=k.stride(0), v_stride=v.stride(0),
@@ -176,11 +187,13 @@ class LogProbs(_Op):
     top_logprob."""
 
     def __init__(self, logits, targets=None, top: int = 0):
+        _int32(top=top)
         _tensor("logits", logits, _DTYPES, (None, None), None, strided=True)
         n, dev = logits.shape[0], logits.device
         if targets is not None:
             _tensor("targets", targets, (torch.int32,), (n, None), dev)
         n_targets = 0 if targets is None else targets.shape[1]
+        _int32(rows=n, vocab=logits.shape[1], n_targets=n_targets)
         self.logprob = torch.empty(n, n_targets, dtype=torch.float32, device=dev)
         self.entropy = torch.empty(n, dtype=torch.float32, device=dev)
         self.top_id = torch.empty(n, max(top, 0), dtype=torch.int32, device=dev)
@@ -206,10 +219,14 @@ class BatchDecoder:
     new values) and before what it is given next."""
 
     def __init__(self, decoder, n_seqs: int, max_len: int, prefix_len: int, n_new: int = 1, page_size: int = 16):
+        _int32(n_seqs=n_seqs, max_len=max_len, prefix_len=prefix_len, n_new=n_new, page_size=page_size)
+        if page_size < 1:
+            raise ValueError(f"page_size {page_size} is not positive")
         c = _b.llm_get_config(decoder.h)
         dev = torch.device("cuda", torch.cuda.current_device())
         max_pages = -(-max_len // page_size)
         n_pages = n_seqs * max_pages
+        _int32(n_pages=n_pages)
         self.decoder = decoder
         self._device, self._stream = dev, _torch_stream(decoder.stream, dev)
         # the tensors are the decoder's stream's: filled there, and their memory, when it is
@@ -257,6 +274,7 @@ def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, po
                stream=None) -> torch.Tensor:
     """llm_rope_table: float32 [n_pos, rope_dims / 2, 2] of the decode step's
     angles at positions pos0 .. pos0 + n_pos - 1."""
+    _int32(n_pos=n_pos, rope_dims=rope_dims, pos0=pos0)
     out = torch.empty(n_pos, rope_dims // 2, 2, dtype=torch.float32, device=device)
     if out.device.index != _current_device():
         raise ValueError(f"the table is on {out.device}, the current device is another")

@@ -177,3 +177,25 @@ def test_binding_refuses_wrong_tensors():
         L.LogProbs(torch.zeros(2, 10))
     with pytest.raises(TypeError):
         L.LogProbs(torch.zeros(2, 10, dtype=torch.float64))
+
+
+def test_binding_refuses_sizes_that_32_bits_do_not_hold():
+    """A C int32 would keep the low bits of these: 2^32 + 5 would be 5."""
+    torch = pytest.importorskip("torch")
+    x, one = torch.zeros(2, 16, 2, 64, dtype=torch.float16), torch.ones(1, dtype=torch.int32)
+    big = (1 << 32) + 5
+    for kw in (dict(prefix_len=big), dict(n_new=big), dict(prefix_len=-big)):
+        with pytest.raises(ValueError, match="32-bit"):
+            L.PagedBatch(x, x, one.view(1, 1), one, **kw)
+    with pytest.raises(ValueError, match="32-bit"):
+        L.LogProbs(torch.zeros(2, 10), top=big)
+    for args in ((big, 64, 1e4), (4, big, 1e4)):
+        with pytest.raises(ValueError, match="32-bit"):
+            L.rope_table(*args)
+    with pytest.raises(ValueError, match="32-bit"):
+        L.rope_table(4, 64, 1e4, pos0=1 << 31)
+    for args in ((big, 16, 0), (1, big, 0), (1, 16, big), (1, 16, 0, big), (1, 16, 0, 1, big)):
+        with pytest.raises(ValueError, match="32-bit"):
+            L.BatchDecoder(None, *args)
+    with pytest.raises(ValueError, match="positive"):
+        L.BatchDecoder(None, 1, 16, 0, 1, 0)
