@@ -358,8 +358,11 @@ const char *llm_last_error(const llm_handle *h);
  * These calls take a stream and no handle (llm_decode_batch takes a handle and
  * uses its stream): they only enqueue, allocate nothing, keep no state between
  * calls and may be captured into a CUDA graph.  The device pointers must be
- * valid on the current device, which the stream belongs to.  A failed call has
- * enqueued nothing; llm_last_error(NULL) gives the calling thread's reason.
+ * valid on the current device, which the stream belongs to.  A call that fails
+ * with INVALID_ARG or UNSUPPORTED has enqueued nothing; one that fails with CUDA
+ * may have enqueued some of its kernels, so its workspace and outputs stay in use
+ * until the stream has been waited for.  llm_last_error(NULL) gives the calling
+ * thread's reason.
  *
  * Rows.  A call handles n_seqs sequences of n_new new tokens each; new token i
  * of sequence s is row s*n_new + i of q, k, v and the outputs.  lens[s] counts
