@@ -405,8 +405,8 @@ enum { LLM_PAGES_BAD_PAGE = 1, LLM_PAGES_BAD_LEN = 2, LLM_PAGES_TIMEOUT = 4 };
  * Example 6: a float that starts at the position and is multiplied by
  * rope_base^(-2/rope_dims) once per pair; divided by rope_freqs[j] when not
  * NULL), so a cache written with this table holds the same bits.  cos_sin
- * (DEVICE, n_pos * rope_dims floats), rope_freqs (DEVICE).  Errors:
- * INVALID_ARG, CUDA. */
+ * (DEVICE, n_pos * rope_dims floats), rope_freqs (DEVICE); rope_dims is at most
+ * 1024.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int llm_rope_table(float *cos_sin, int32_t pos0, int32_t n_pos, int32_t rope_dims, float rope_base,
                    const float *rope_freqs, llm_stream_t stream);
 

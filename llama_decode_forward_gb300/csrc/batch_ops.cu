@@ -651,8 +651,10 @@ using namespace llm;
 extern "C" int llm_rope_table(float* cos_sin, int32_t pos0, int32_t n_pos, int32_t rope_dims, float rope_base,
                               const float* rope_freqs, llm_stream_t stream) {
     if (!cos_sin || pos0 < 0 || n_pos < 0 || (long long)pos0 + n_pos > INT_MAX || rope_dims < 2 || rope_dims % 2 ||
-        !(rope_base > 0.f))
+        !(rope_base > 0.f) || !aligned(cos_sin, 4) || !aligned(rope_freqs, 4))
         return fail_op(LLM_ERR_INVALID_ARG, "llm_rope_table: bad argument");
+    // (an angle is a chain of rope_dims / 2 products at most)
+    if (rope_dims > 1024) return fail_op(LLM_ERR_UNSUPPORTED, "llm_rope_table: rope_dims %d exceeds 1024", rope_dims);
     if ((long long)n_pos * (rope_dims / 2) > INT_MAX - 256) return fail_op(LLM_ERR_UNSUPPORTED, "llm_rope_table: the table is too large");
     if (n_pos == 0) return LLM_OK;
     return launched(rope_table(stream, cos_sin, n_pos, pos0, rope_dims, rope_theta_scale(rope_base, rope_dims), rope_freqs), "llm_rope_table");

@@ -199,3 +199,9 @@ def test_binding_refuses_sizes_that_32_bits_do_not_hold():
             L.BatchDecoder(None, *args)
     with pytest.raises(ValueError, match="positive"):
         L.BatchDecoder(None, 1, 16, 0, 1, 0)
+
+
+@pytest.mark.parametrize("args,freqs,status", [((P + 2, 0, 4, 64, 1e4), None, BAD), ((P, 0, 4, 64, 1e4), P + 1, BAD),
+                                               ((P, 0, 1, 1026, 1e4), None, UNSUP), ((P, 0, 1, 1 << 30, 1e4), None, UNSUP)])
+def test_rope_table_refuses_what_its_kernel_cannot_take(args, freqs, status):
+    refused(B._lib.llm_rope_table(*args, freqs, None), status)
