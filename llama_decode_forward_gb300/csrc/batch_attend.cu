@@ -1136,6 +1136,12 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
     if (p->n_kv_heads > 65535) return fail_op(LLM_ERR_UNSUPPORTED, "n_kv_heads %d exceeds 65535", p->n_kv_heads);
     if ((long long)p->n_seqs * p->n_new * a->n_heads > INT_MAX / 64)
         return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^25 rows of all heads");
+    // a block's share of the prefix's tiles and a warp's of the pages' pieces are counted in 32 bits
+    const long long gq = a->n_heads / p->n_kv_heads, srows = p->n_new * gq, ru = unit_rows((int)srows);
+    if ((srows * p->n_seqs + 127) / 128 * p->n_kv_heads * ((p->prefix_len + (long long)kKT - 1) / kKT) > 1ll << 38)
+        return fail_op(LLM_ERR_UNSUPPORTED, "the prefix is too long for that many rows and heads");
+    if ((srows + ru - 1) / ru * p->n_kv_heads * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16 + kUnit) > 1ll << 41)
+        return fail_op(LLM_ERR_UNSUPPORTED, "the sequences' pages hold too many rows for that many heads");
     if (!type_bytes(a->q_dtype) || !type_bytes(a->out_dtype))
         return fail_op(LLM_ERR_UNSUPPORTED, "q or out is neither LLM_F32 nor LLM_F16");
     if (!(a->scale >= 0.f) || !(a->scale < INFINITY)) return fail_op(LLM_ERR_INVALID_ARG, "scale is not a finite number >= 0");

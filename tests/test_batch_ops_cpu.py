@@ -205,3 +205,11 @@ def test_binding_refuses_sizes_that_32_bits_do_not_hold():
                                                ((P, 0, 1, 1026, 1e4), None, UNSUP), ((P, 0, 1, 1 << 30, 1e4), None, UNSUP)])
 def test_rope_table_refuses_what_its_kernel_cannot_take(args, freqs, status):
     refused(B._lib.llm_rope_table(*args, freqs, None), status)
+
+
+@pytest.mark.parametrize("kw,heads", [
+    (dict(n_seqs=2, prefix_len=(1 << 31) - 65, n_kv_heads=16384, head_dim=8), 16384),            # 2^39 tiles of the prefix
+    (dict(n_seqs=1, n_new=512, max_pages=(1 << 27) - 1, n_kv_heads=16384, head_dim=8), 16384),   # 2^46 pieces of the pages
+])
+def test_attend_refuses_shares_beyond_32_bits(kw, heads):
+    refused(B._lib.llm_attend_batch_workspace(ref(pages(**kw)), ref(attend(n_heads=heads))), UNSUP)
