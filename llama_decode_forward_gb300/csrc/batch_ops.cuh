@@ -39,7 +39,8 @@ __device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
     return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
 }
 
-// Division of numbers below 2^31 by a fixed one: with 2^s >= d and m = floor(2^32
+// Division of numbers below 2^31 by a fixed one (Granlund and Montgomery, "Division by
+// Invariant Integers using Multiplication", 1994): with 2^s >= d and m = floor(2^32
 // (2^s - d) / d) + 1, n / d = (floor(m n / 2^32) + n) >> s.
 struct Div {
     uint32_t d, m, s;
