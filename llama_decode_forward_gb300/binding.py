@@ -254,6 +254,9 @@ def llm_prefill_f16_copy(h, enable: bool = True) -> None:
 
 
 def llm_batch_pages_bytes(h, n_pages: int, page_size: int) -> int:
+    for name, v in (("n_pages", n_pages), ("page_size", page_size)):
+        if not -2 ** 31 <= int(v) < 2 ** 31:           # (ctypes would cut it off)
+            raise ValueError(f"{name} {v} is not a 32-bit integer")
     n = int(_lib.llm_batch_pages_bytes(h, int(n_pages), int(page_size)))
     if n < 0:
         raise LlmError(n, "n_pages or page_size")

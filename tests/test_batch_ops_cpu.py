@@ -199,6 +199,9 @@ def test_binding_refuses_sizes_that_32_bits_do_not_hold():
             L.BatchDecoder(None, *args)
     with pytest.raises(ValueError, match="positive"):
         L.BatchDecoder(None, 1, 16, 0, 1, 0)
+    for args in ((big, 16), (3, big)):
+        with pytest.raises(ValueError, match="32-bit"):
+            L.llm_batch_pages_bytes(None, *args)
 
 
 @pytest.mark.parametrize("args,freqs,status", [((P + 2, 0, 4, 64, 1e4), None, BAD), ((P, 0, 4, 64, 1e4), P + 1, BAD),
