@@ -171,8 +171,8 @@ int llm_prefill(llm_handle *h, const int32_t *tokens_host, int32_t n, int32_t po
  * for bit and the GEMMs at the speed of F16 weights; the decode step still
  * streams the Q8_0 matrices.  Costs 2 bytes of device memory per layer
  * weight (about 2 GB for a 1B model); enabling twice keeps one copy.
- * enable == 0 frees the copy (waiting for the handle's stream first; once a
- * step of llm_decode_batch has been captured, with llm_destroy).
+ * enable == 0 frees the copy (waiting for the handle's stream first; with
+ * llm_destroy if a step of llm_decode_batch was captured that reads it).
  * Asynchronous on the handle's stream.  Errors: UNSUPPORTED for F16 or F32
  * weights or a model whose prefill runs token by token, NO_MEMORY (nothing
  * kept), CUDA. */

@@ -71,9 +71,9 @@ static cudaError_t host_alloc(void** p, size_t bytes) {
 }
 
 // Guard bands: the KV cache, the activations, the prefill workspace and the
-// batch's workspace and angle table are allocated with kGuardBytes more on each side, filled with kGuardByte; the
-// buffer proper starts kGuardBytes into the allocation (256-byte alignment
-// kept).  llm_test_guards counts guard bytes that changed: a kernel that
+// batch's workspace and angle table are allocated with kGuardBytes more on
+// each side, filled with kGuardByte; the buffer proper starts kGuardBytes into
+// the allocation (256-byte alignment kept).  llm_test_guards counts guard bytes that changed: a kernel that
 // wrote past either end of one of these buffers shows up there.
 constexpr size_t kGuardBytes = 4096;
 constexpr int kGuardByte = 0xA5;
@@ -157,8 +157,9 @@ struct llm_handle {
     Guarded batch_tab;               // llm_decode_batch: angles of positions 0 .. batch_tab_rows-1
     int batch_tab_rows = 0;
     Guarded batch_ws;                // and the attention's workspace
-    bool captured = false;           // a step of llm_decode_batch was captured into a graph
-    std::vector<void*> retired;      // what was replaced after that: graphs hold its addresses, freed with the handle
+    // a step of llm_decode_batch was captured into a graph on the present one of these
+    bool ws_captured = false, tab_captured = false, copy_captured = false;
+    std::vector<void*> retired;      // those that were replaced: graphs hold their addresses, freed with the handle
     int test_batch_wait = 0;         // llm_test_batch_wait: > 0 limits the batch attention's waits
     int test_logits_limit = 0;       // llm_test_logits_limit: > 0 narrows the checked logits bound
 };
@@ -817,15 +818,16 @@ static PrefillCtx prefill_ctx(const llm_handle* h) {
 }
 
 // Gives up a buffer that llm_decode_batch's kernels use: freed once the stream's work is
-// done, or kept for the graphs that may still replay a captured step on it.
-static int retire(llm_handle* h, void* p) {
+// done, or kept for the graphs that may still replay a step captured on it.
+static int retire(llm_handle* h, void* p, bool& captured) {
     if (!p) return LLM_OK;
-    if (h->captured) {
+    if (captured) {
         try {
             h->retired.push_back(p);
         } catch (...) {
             return fail(h, LLM_ERR_NO_MEMORY, "no memory for the list of retired buffers");
         }
+        captured = false;
         return LLM_OK;
     }
     CK(h, cudaStreamSynchronize(h->st));
@@ -837,7 +839,7 @@ extern "C" int llm_prefill_f16_copy(llm_handle* h, int enable) {
     LIVE_OR_RETURN(h);
     if (!enable) {
         if (h->f16_copy) {
-            const int rc = retire(h, h->f16_copy);
+            const int rc = retire(h, h->f16_copy, h->copy_captured);
             if (rc) return rc;
             h->f16_copy = nullptr;
             h->f16_copy_bytes = 0;
@@ -932,11 +934,11 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     int rc;
     if ((rc = need_prefill_ws(h, pc))) return rc;
     // a larger buffer takes the place of one of these, once it is ready
-    auto replace = [&](Guarded& old, size_t bytes, auto fill) -> int {
+    auto replace = [&](Guarded& old, bool& captured, size_t bytes, auto fill) -> int {
         Guarded g;
         cudaError_t e = guarded_alloc(g, bytes, h->st);
         if (e == cudaSuccess) e = fill(g.ptr());
-        const int rc = e == cudaSuccess ? retire(h, old.raw) : LLM_OK;
+        const int rc = e == cudaSuccess ? retire(h, old.raw, captured) : LLM_OK;
         if (e == cudaSuccess && rc == LLM_OK) {
             old = g;
             return LLM_OK;
@@ -948,16 +950,21 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
         return fail(h, e == cudaErrorMemoryAllocation ? LLM_ERR_NO_MEMORY : LLM_ERR_CUDA, "allocating %zu bytes for a batch's steps: %s",
                     bytes, cudaGetErrorString(e));
     };
-    if (h->batch_ws.bytes < (size_t)need && (rc = replace(h->batch_ws, (size_t)need, [](uint8_t*) { return cudaSuccess; }))) return rc;
+    if (h->batch_ws.bytes < (size_t)need &&
+        (rc = replace(h->batch_ws, h->ws_captured, (size_t)need, [](uint8_t*) { return cudaSuccess; })))
+        return rc;
     if (h->batch_tab_rows < positions) {
-        rc = replace(h->batch_tab, (size_t)positions * h->cfg.rope_dims * 4, [&](uint8_t* p) {
+        rc = replace(h->batch_tab, h->tab_captured, (size_t)positions * h->cfg.rope_dims * 4, [&](uint8_t* p) {
             return rope_table(h->st, reinterpret_cast<float*>(p), (int)positions, 0, h->cfg.rope_dims, h->theta_scale, h->rope_freqs);
         });
         if (rc) return rc;
         h->launches++;
         h->batch_tab_rows = (int)positions;
     }
-    if (capture != cudaStreamCaptureStatusNone) h->captured = true;
+    if (capture != cudaStreamCaptureStatusNone) {
+        h->ws_captured = h->tab_captured = true;
+        h->copy_captured = h->copy_captured || h->f16_copy;
+    }
     const char* why = nullptr;
     int launches = 0;
     try {

@@ -519,3 +519,36 @@ def test_host_allocation_failure_is_a_status(lib):
     lib.llm_sync(dec.h)
     assert torch.equal(bd.logits, want) and np.array_equal(again.view(np.uint32), logits.view(np.uint32))
     dec.close()
+
+
+def test_copy_that_no_graph_reads_is_freed(lib):
+    """After a captured step's copy was kept, a new copy that no captured step reads is
+    given back at once."""
+    cfg = config(wtype=synth.Q8_0, bias=False, number=83, dim=512, n_heads=16, ffn_dim=4096, n_layers=4)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        dec = lib.Decoder(cfg, synth.make_weights(cfg))
+        lib.llm_prefill_f16_copy(dec.h)
+        bd = lib.BatchDecoder(dec, 2, 16, 0)
+        put(bd, cfg, [1, 1])
+        bd.step()
+        torch.cuda.synchronize()
+        want = bd.logits.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            bd.step()
+        lib.llm_prefill_f16_copy(dec.h, False)         # kept for the graph
+        torch.cuda.synchronize()
+        free = torch.cuda.mem_get_info()[0]
+        for _ in range(3):
+            lib.llm_prefill_f16_copy(dec.h)
+            bd.step()
+            lib.llm_prefill_f16_copy(dec.h, False)
+        torch.cuda.synchronize()
+        assert torch.cuda.mem_get_info()[0] == free
+        bd.logits.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bd.logits, want)
+        del graph
+        dec.close()
