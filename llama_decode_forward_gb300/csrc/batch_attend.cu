@@ -52,14 +52,14 @@ struct AttendDev {
 // running maximum by kLag / (scale log2(e)) before 2^(kHead + kLag) nears F16's 2^16.
 // The scores' difference is taken first and then scaled: as fma(score, scale, kHead - Y)
 // every exponent would keep the half step by which Y was rounded, and with |y| above 2^27
-// the largest probability be infinite or zero.  (256 rows behind 16,000 shared ones 80 us
-// that way, 85 us this way; a branch that keeps the difference to rows that need it took
-// as long.)  Parts give Y to the join; their common 2^kHead cancels there.
+// the largest probability be infinite or zero.  (256 rows behind 16,000 shared ones 79 us
+// that way, 81.5 us this way; a branch that keeps the difference to rows that need it
+// took no less.)  Parts give Y to the join; their common 2^kHead cancels there.
 // Each meets V as two F16 parts, its first 22 bits, whatever the output's type:
 // with one part (11 bits) F16 outputs were 1.4 times as far from the exact ones as
-// one rounding leaves them; the second part's products cost 256 rows behind 16,000
-// shared ones 18 us of 90, 64 rows behind 32,000 6 us of 52, and nothing where the
-// pages are the larger part.
+// one rounding leaves them; the second part costs 256 rows behind 16,000 shared ones
+// 10 us of 81, 64 rows behind 32,000 3.5 us of 51, and next to nothing where the pages
+// are the larger part.
 constexpr float kHead = 8.f, kLag = 6.f;
 constexpr float kLow = -3e38f;               // R, or Y, where there is no key: low, but a number
 
@@ -156,7 +156,7 @@ constexpr int kSoftmaxWarps = 8, kPrefixThreads = 32 * (kSoftmaxWarps + 3);
 // A quarter of the SM (16,384 registers) holds up to three of this kernel's warps (7,680)
 // and then two of the suffix kernel's 128 x 32: two of its blocks run beside a block of
 // this one.  With 88 registers here only one did: 256 rows of 250 pages behind 16,000
-// shared ones 84 us, 71 us with 80.
+// shared ones 91 us, 81 us with 80.
 constexpr int kPrefixRegs = 80;
 
 constexpr int kWaitLimit = 10000000;         // probes (each suspends the warp for a while) before a wait gives up
@@ -401,7 +401,7 @@ __global__ void __maxnreg__(kPrefixRegs)
                 }
                 const int e = (int)(__float_as_uint(m) >> 23);
                 q_exponent[threadIdx.x] = (uint8_t)e;
-                asm volatile("bar.sync 9, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(32 * kSoftmaxWarps) : "memory");
                 const PowerOfTwo two = power_of(max(e, (int)q_exponent[threadIdx.x ^ 128]));
                 up = two.up;
                 sc = a.sc * two.down;
@@ -498,14 +498,9 @@ __global__ void __maxnreg__(kPrefixRegs)
                         tm_st16(to + h, o);
                     }
                 }
-                // the exponentials of the block's tiles take turns (a warp of each group shares a
-                // scheduler's one exponential unit): left alone both groups ran them at the same time
-                // and waited for the rest at the same time, 700 cycles a tile
-                if (it > 0) asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 3) + 4 * group) : "memory");
                 probabilities(1, s);
                 scores(0, s);                // read a second time: 64 scores at once would not leave the registers
                 probabilities(0, s);
-                if (it + 1 < n) asm volatile("bar.arrive %0, 64;" ::"r"(1 + (warp & 3) + 4 * (group ^ 1)) : "memory");
                 l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
                 tm_wait_st();
                 tm_fence_before();
@@ -553,7 +548,7 @@ __global__ void __maxnreg__(kPrefixRegs)
 constexpr int kSuffixWarps = 4, kMaxSeqs = 4096;
 constexpr int kQuantum = 2;                  // pieces that are worth a worker of their own
 // A unit's own cost in pieces (its query rows, its part).  48 sequences of 1 to 512 rows
-// and 32 heads: 76 us when only pieces counted (a worker of one-piece units ran twice as
+// and 32 heads: 66 to 77 us when only pieces counted (a worker of one-piece units ran twice as
 // long as the others), 62 us.
 constexpr int kUnit = 1;
 

@@ -88,8 +88,8 @@ __device__ __forceinline__ Groups groups_of(int i, int half, int neox) {
 // beside that load.  N: elements of an item's two groups, 8 where head_dim and
 // rope_dims are multiples of 16, else 4 where rope_dims is one of 8, else 0: eight
 // elements taken pair by pair.  Bound by the stream of rows, and close behind it by
-// instructions: 8000 rows of 4 KB (F16) took 27 us with groups of four and
-// divisions by sizes, 26 us without those.
+// instructions: 8000 rows of 4 KB (F16) take 20.8 us (4.8 TB/s) with groups of eight,
+// 26.4 us with groups of four.
 constexpr int kAppendThreads = 128;
 constexpr int append_item(int n) { return n ? 2 * n : 8; }
 template <class T, class U, int N>
@@ -193,7 +193,7 @@ cudaError_t launch_append(cudaStream_t st, const PagesDev& pd, const AppendDev& 
 // them are sorted into the warp's list (lane i the i-th) at a time.  After steps 1,
 // 4, 16, ... and at the end the keys of a block that reach its floor are ranked by
 // counting the larger ones, and the top-th becomes its floor.  512 rows of 151,936
-// with eight alternatives: 78 us without those ranks (a warp then meets some 37 keys
+// with eight alternatives: 77 us without those ranks (a warp then meets some 37 keys
 // that reach its floor, in every other step), 68 us with them.
 constexpr int kLpElems = 16;                 // logits of a lane per step
 constexpr float kLog2e = 1.4426950408889634f;
@@ -317,8 +317,7 @@ __device__ __forceinline__ void put_in_order(u64* list, int n, int top, u64* bes
 }
 
 // NT threads a block: 512 for few rows (the shortest chain), 256 for many (512 rows of
-// 151,936, before the block's floor: 79 us, and 85 us with 128 threads and two blocks a
-// row, 114 us with 512 threads).
+// 151,936: 68 us, 74 us with 128 threads and two blocks a row, 77 us with 512 threads).
 template <class T, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const __grid_constant__ llm_logprobs_args a) {
     constexpr int VE = 16 / sizeof(T), NV = kLpElems / VE;     // elements of a 16-byte load, loads of a lane per step
