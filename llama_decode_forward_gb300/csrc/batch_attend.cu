@@ -382,9 +382,9 @@ __global__ void __maxnreg__(kPrefixRegs)
         // after a wait that gave up the warp goes on without waiting, to no result
         for (int begin = 0, tile0 = t0, unit = u0; begin < n; tile0 = 0, unit++) {
             // ---- a unit's tiles, `begin` to `end` of the block's: first this group's half of the
-            // row's Q into tensor memory, once the last scores of the unit before are there
+            // row's Q into tensor memory, once the last scores of both groups are there: they read all of it
             const int end = min(n, begin + ntiles - tile0), r = unit % mt * 128 + lrow, g = unit / mt;
-            if (begin > 0) ok = ok && warp_wait(&sfull[(begin - 1) % kScores], (uint32_t)(((begin - 1) / kScores) & 1), a);
+            for (int it = max(0, begin - 2); it < begin; it++) ok = ok && warp_wait(&sfull[it % kScores], (uint32_t)((it / kScores) & 1), a);
             tm_fence_after();
             const long long q_at = r < a.rows ? q_offset(a, p.hd, g, r) : 0;
             float up = 1.f;

@@ -1033,3 +1033,31 @@ def test_calls_of_several_threads(lib):
     assert not errors, errors
     for b, q, pk, pv, out in sides:
         check_attend(b, q, out, pk, pv)
+
+
+@pytest.mark.parametrize("heads,n_seqs,prefix", [((16, 16, 128), 700, 150), ((16, 16, 128), 700, 200), ((32, 8, 64), 600, 330), ((8, 8, 64), 2000, 190)])
+@pytest.mark.parametrize("q_dtype", [F16, F32])
+def test_attend_units_behind_one_another(lib, heads, n_seqs, prefix, q_dtype):
+    """Blocks of the prefix kernel that go from unit to unit, with even and odd numbers of
+    tiles: the queries of the next unit must not take their place before both groups' last
+    scores have read the present ones.  Every run gives the same bits, and the right ones."""
+    n_heads, n_kv, hd = heads
+    b = Batch(lib, [1] * n_seqs, 1, prefix, 16, n_kv, hd, poison=False)
+    q = rand(1, n_seqs, n_heads, hd, dtype=q_dtype)
+    pk, pv = rand(2, prefix, n_kv, hd, dtype=F16), rand(3, prefix, n_kv, hd, dtype=F16)
+    out = torch.zeros(n_seqs, n_heads, hd, dtype=F16, device="cuda")
+    op = lib.AttendBatch(b.pages, q, out, pk, pv)
+    op()
+    first = out.clone()
+    # all rows against 64 bits, one key of its own each
+    own_k, own_v = (t[b.table[:, 0].long(), 0].double() for t in (b.k, b.v))
+    qd = q.double().view(n_seqs, n_kv, n_heads // n_kv, hd)
+    s = torch.cat([torch.einsum("nghd,tgd->nght", qd, pk.double()), (qd * own_k[:, :, None]).sum(-1, keepdim=True)], -1) * hd ** -0.5
+    p = s.softmax(-1)
+    o = torch.einsum("nght,tgd->nghd", p[..., :-1], pv.double()) + p[..., -1:] * own_v[:, :, None]
+    o = o.view(n_seqs, n_heads, hd)
+    # one rounding to F16, and 2^-13 for what attend_bound counts of these sizes (it is below 2^-14)
+    assert ((out.double() - o).abs() <= H16 * o.abs() + 2.0 ** -13).all()
+    for _ in range(100):
+        op()
+        assert torch.equal(out, first)
