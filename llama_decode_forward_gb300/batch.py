@@ -63,7 +63,39 @@ def _int32(**sizes) -> None:
             raise ValueError(f"{name} {n} is not a 32-bit integer")
 
 
-class PagedBatch:
+def _capturing() -> bool:
+    return torch.cuda.is_current_stream_capturing()
+
+
+class _Owner:
+    """An object with tensors of its own (own, allocated on the current stream) that its
+    user may hand to any stream.  (A capture in which a stream first uses them must begin
+    after the work of the stream that they were made on, as that of torch.cuda.graph
+    does.)"""
+
+    def _owns(self, own, device) -> None:
+        self._own, self._index = own, device.index
+        self._streams = {_current_stream(device.index)}    # the streams that own's memory waits for when it is given back
+        self._free = None                                  # and what others wait for: earlier tensors there, own's fill
+        if own and not _capturing():
+            self._free = torch.cuda.Event()
+            self._free.record(torch.cuda.current_stream(device))
+
+    def _use_on(self, stream: int) -> None:
+        if stream in self._streams:
+            return
+        self._streams.add(stream)
+        if not self._own:
+            return
+        s = _torch_stream(stream, self._own[0].device)
+        with torch.cuda.stream(s):
+            if self._free is not None and not _capturing():
+                s.wait_event(self._free)
+        for t in self._own:
+            t.record_stream(s)
+
+
+class PagedBatch(_Owner):
     """n_seqs sequences of n_new new tokens each behind a shared prefix of
     prefix_len rows (llm_pages).  k_pages, v_pages: float16 [n_pages,
     page_size, n_kv_heads, head_dim]; page_table int32 [n_seqs, max_pages];
@@ -78,9 +110,11 @@ class PagedBatch:
         _tensor("v_pages", v_pages, (torch.float16,), tuple(k_pages.shape), dev)
         _tensor("lens", lens, (torch.int32,), (None,), dev)
         _tensor("page_table", page_table, (torch.int32,), (lens.shape[0], None), dev)
-        if err is None:
+        made = err is None
+        if made:
             err = torch.zeros(1, dtype=torch.int32, device=dev)
         _tensor("err", err, (torch.int32,), (1,), dev)
+        self._owns((err,) if made else (), dev)
         self.k_pages, self.v_pages, self.page_table, self.lens, self.err = k_pages, v_pages, page_table, lens, err
         self.device = dev
         n_pages, page_size, n_kv, hd = k_pages.shape
@@ -96,16 +130,17 @@ class PagedBatch:
         return int(self.err.item())
 
 
-class _Op:
+class _Op(_Owner):
     """One operator with its arguments; calling it enqueues one run.  The operator must
     live as long as a graph that captured its runs.  A stream given by number must live
     as long as the operator."""
 
-    def _made(self, fn, kept, structs, own, device) -> None:
-        """own: the tensors that the operator allocated, on the current stream."""
-        self._fn, self._kept, self._own, self._index = fn, (kept, structs), own, device.index
+    def _made(self, fn, pages, kept, structs, own, device) -> None:
+        self._owns(own, device)
+        if pages is not None:
+            pages._use_on(_current_stream(device.index))
+        self._fn, self._pages, self._kept = fn, pages, (kept, structs)
         self._args = tuple(ctypes.addressof(x) for x in structs)
-        self._streams = {_current_stream(device.index)}    # the streams that own's memory waits for
 
     def __call__(self, stream=None) -> None:
         index = self._index
@@ -114,9 +149,9 @@ class _Op:
         if stream is None:
             stream = _current_stream(index)
         if stream not in self._streams:
-            for t in self._own:
-                t.record_stream(_torch_stream(stream, t.device))
-            self._streams.add(stream)
+            if self._pages is not None:
+                self._pages._use_on(stream)
+            self._use_on(stream)
         rc = self._fn(*self._args, stream)
         if rc:
             _run(rc)
@@ -146,7 +181,7 @@ class KvAppend(_Op):
             _tensor("q_out", q_out, _DTYPES, tuple(q.shape), dev, strided=True)
             a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), q.stride(0)
             a.q_out, a.q_out_stride, a.q_out_dtype = q_out.data_ptr(), q_out.stride(0), _DTYPES[q_out.dtype]
-        self._made(_b._lib.llm_kv_append, (pages, q, k, v, cos_sin, q_out), (p, a), (), dev)
+        self._made(_b._lib.llm_kv_append, pages, (q, k, v, cos_sin, q_out), (p, a), (), dev)
 
 
 class AttendBatch(_Op):
@@ -176,7 +211,7 @@ class AttendBatch(_Op):
             _run(int(n))
         self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
         a.workspace, a.workspace_bytes = self.workspace.data_ptr(), int(n)
-        self._made(_b._lib.llm_attend_batch, (pages, q, out, prefix_k, prefix_v), (p, a), (self.workspace,), dev)
+        self._made(_b._lib.llm_attend_batch, pages, (q, out, prefix_k, prefix_v), (p, a), (self.workspace,), dev)
 
 
 class LogProbs(_Op):
@@ -203,7 +238,7 @@ class LogProbs(_Op):
                                  targets=targets.data_ptr() if n_targets else None, logprob=self.logprob.data_ptr(),
                                  entropy=self.entropy.data_ptr(), top_id=self.top_id.data_ptr(),
                                  top_logprob=self.top_logprob.data_ptr())
-        self._made(_b._lib.llm_logprobs, (logits, targets), (a,),
+        self._made(_b._lib.llm_logprobs, None, (logits, targets), (a,),
                    (self.logprob, self.entropy, self.top_id, self.top_logprob), dev)
 
 
@@ -280,8 +315,10 @@ def rope_table(n_pos: int, rope_dims: int, rope_base: float, rope_freqs=None, po
         raise ValueError(f"the table is on {out.device}, the current device is another")
     if rope_freqs is not None:
         _tensor("rope_freqs", rope_freqs, (torch.float32,), (rope_dims // 2,), out.device)
-    if stream is not None:
-        out.record_stream(_torch_stream(stream, out.device))
+    if stream is not None and stream != _current_stream(out.device.index):
+        other = _torch_stream(stream, out.device)
+        other.wait_stream(torch.cuda.current_stream(out.device))
+        out.record_stream(other)
     _run(_b._lib.llm_rope_table(out.data_ptr(), pos0, n_pos, rope_dims, rope_base,
                                 rope_freqs.data_ptr() if rope_freqs is not None else None, _stream(stream)))
     return out

@@ -1055,9 +1055,47 @@ def test_attend_units_behind_one_another(lib, heads, n_seqs, prefix, q_dtype):
     s = torch.cat([torch.einsum("nghd,tgd->nght", qd, pk.double()), (qd * own_k[:, :, None]).sum(-1, keepdim=True)], -1) * hd ** -0.5
     p = s.softmax(-1)
     o = torch.einsum("nght,tgd->nghd", p[..., :-1], pv.double()) + p[..., -1:] * own_v[:, :, None]
-    o = o.view(n_seqs, n_heads, hd)
-    # one rounding to F16, and 2^-13 for what attend_bound counts of these sizes (it is below 2^-14)
-    assert ((out.double() - o).abs() <= H16 * o.abs() + 2.0 ** -13).all()
+    o = o.reshape(n_seqs, n_heads, hd)
+    values = torch.cat([pv.double().flatten(), own_v.flatten()]).abs().max()
+    w = torch.einsum("nght,tgd->nghd", p[..., :-1], pv.double().abs()) + p[..., -1:] * own_v[:, :, None].abs()
+    mag = torch.cat([torch.einsum("nghd,tgd->nght", qd.abs(), pk.double().abs()), (qd * own_k[:, :, None]).abs().sum(-1, keepdim=True)], -1).amax(-1) * hd ** -0.5
+    far = s.amax(-1) - s.amin(-1)
+    tol = attend_bound(o, w.reshape(o.shape), mag.reshape(n_seqs, n_heads, 1), far.reshape(n_seqs, n_heads, 1), values, prefix + 1, hd, q_dtype, F16)
+    assert ((out.double() - o).abs() <= tol).all()
     for _ in range(100):
         op()
         assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("by_number", [False, True])
+def test_operator_made_on_a_busy_stream(lib, by_number):
+    """An operator's own tensors lie where tensors of its stream's queued work lay; its first
+    run on another stream waits for that work.  (Its inputs are ready: the user saw to them.)"""
+    b = Batch(lib, [40, 7, 90], 1, 300, 16, 2, 64)
+    q, pk, pv = rand(1, 3, 8, 64), rand(2, 300, 2, 64, dtype=F16), rand(3, 300, 2, 64, dtype=F16)
+    logits = rand(4, 40, 5000)
+    out = torch.zeros(3, 8, 64, device="cuda")
+    size = lib.AttendBatch(b.pages, q, out, pk, pv).workspace.numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        out.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        torch.cuda._sleep(20000000)
+        for n in (size, 40 * 3 * 4, 40 * 4):           # queued: what will have written where the operators' tensors lie
+            junk = torch.empty(n, dtype=torch.uint8, device="cuda")
+            junk.fill_(0x7F)
+            del junk
+        pages = lib.PagedBatch(b.k, b.v, b.table, b.lens_dev, prefix_len=300)
+        op, lp = lib.AttendBatch(pages, q, out, pk, pv), lib.LogProbs(logits, top=3)
+        if by_number:
+            op(stream=side.cuda_stream)
+            lp(stream=side.cuda_stream)
+        else:
+            with torch.cuda.stream(side):
+                op()
+                lp()
+        side.synchronize()
+        torch.cuda.synchronize()
+        check_attend(b, q, out, pk, pv)
+        assert torch.equal(lp.top_id.long(), logits.topk(3).indices) and pages.errors() == 0
