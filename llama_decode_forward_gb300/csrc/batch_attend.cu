@@ -957,8 +957,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         if (pieces > 0) {
             const int j = g * rt + row / ru;
             const long long x = (long long)b * deal.units + (long long)j * pieces;           // (pieces: kUnit empty ones among them)
-            const int w0 = (int)owner_of(x, deal.workers, deal.total);
-            ns = (int)(owner_of(x + pieces - kUnit - 1, deal.workers, deal.total) - w0) + 1;
+            // (the bounds hold by themselves; they keep the reads within the workspace where another
+            // call has written into it, which the caller must not let happen)
+            const int w0 = max(0, min((int)owner_of(x, deal.workers, deal.total), a.suffix_workers - 1));
+            ns = max(0, min((int)owner_of(x + pieces - kUnit - 1, deal.workers, deal.total) - w0 + 1, a.suffix_workers - w0));
             suf = (s * deal.units + j + w0) * step + row % ru;
         }
     }
