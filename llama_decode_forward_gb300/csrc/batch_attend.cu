@@ -604,8 +604,8 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 //   now counting dims.
 // The stream of rows is the bound.  At 64 continuations of 2048 rows each (268 MB)
 // a ring of TMA boxes (16 rows x 128 bytes a request) brought 3.6 TB/s, plain
-// loads 5.3 TB/s, the join and the launches included; 805 MB with heads of 128
-// values 6.2 TB/s.
+// loads 5.5 TB/s, the join and the launches included; 805 MB with heads of 128
+// values 6.4 TB/s.
 template <int HDP, int NT, bool SPLITQ>
 __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
     suffix_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
@@ -1085,7 +1085,7 @@ bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long 
 // Percent of an SM's memory as shared memory for the prefix kernel and a suffix
 // kernel that runs beside it: an SM that holds a block of one takes none of the
 // other under another division.  (A suffix kernel alone wants the cache: 268 MB of
-// pages 65 us, 51 us with the default.)
+// pages 65 us, 49 us with the default.)
 constexpr int kCarveout = 72;
 
 template <int HDP, bool SPLITQ>
