@@ -127,6 +127,7 @@ class PagedBatch(_Owner):
 
     def errors(self) -> int:
         """The LLM_PAGES_* bits seen so far (waits for the device)."""
+        torch.cuda.synchronize(self.device)
         return int(self.err.item())
 
 
@@ -302,6 +303,7 @@ class BatchDecoder:
 
     def errors(self) -> int:
         """The LLM_PAGES_* bits seen so far (waits for the device)."""
+        torch.cuda.synchronize(self._device)
         return int(self.err.item())
 
 

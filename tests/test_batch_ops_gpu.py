@@ -1099,3 +1099,20 @@ def test_operator_made_on_a_busy_stream(lib, by_number):
         torch.cuda.synchronize()
         check_attend(b, q, out, pk, pv)
         assert torch.equal(lp.top_id.long(), logits.topk(3).indices) and pages.errors() == 0
+
+
+def test_errors_wait_for_every_stream(lib):
+    """A bad page met on a stream that is not the current one is seen."""
+    b = Batch(lib, [20], 1, 0, 16, 1, 64, poison=False)
+    b.table[0, 1] = -1
+    q, out = rand(1, 1, 2, 64), torch.zeros(1, 2, 64, device="cuda")
+    op = lib.AttendBatch(b.pages, q, out)
+    op()
+    assert b.pages.errors() == lib.LLM_PAGES_BAD_PAGE
+    b.pages.err.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100000000)
+        op()
+    assert b.pages.errors() == lib.LLM_PAGES_BAD_PAGE
