@@ -385,7 +385,8 @@ const char *llm_last_error(const llm_handle *h);
  * rows); LLM_PAGES_BAD_LEN, a row at or behind max_pages*page_size (skipped
  * likewise) or, in llm_kv_append, behind the angle table (the whole row is
  * skipped); LLM_PAGES_TIMEOUT, a bounded wait inside a kernel gave up (the
- * outputs are invalid).  A row of attention left without any key is zero. */
+ * outputs are invalid).  A row of attention left without any key is zero.
+ * (LLM_PAGES_FULL and LLM_PAGES_BAD_SEQ: llm_pages_update.) */
 typedef struct {
     int32_t n_seqs, n_new;               /* >= 0, >= 1 */
     int32_t prefix_len;                  /* >= 0: rows all sequences share, before their pages */
@@ -397,7 +398,7 @@ typedef struct {
     const int32_t *lens;                 /* DEVICE [n_seqs] */
     int32_t *err;                        /* DEVICE, or NULL */
 } llm_pages;
-enum { LLM_PAGES_BAD_PAGE = 1, LLM_PAGES_BAD_LEN = 2, LLM_PAGES_TIMEOUT = 4 };
+enum { LLM_PAGES_BAD_PAGE = 1, LLM_PAGES_BAD_LEN = 2, LLM_PAGES_TIMEOUT = 4, LLM_PAGES_FULL = 8, LLM_PAGES_BAD_SEQ = 16 };
 
 /* cos and sin of the rotation angles of positions pos0 .. pos0+n_pos-1:
  * cos_sin[(p * rope_dims/2 + j) * 2] = cos, + 1 = sin of pair j at position
@@ -471,6 +472,128 @@ int llm_attend_batch(const llm_pages *pages, const llm_attend *a, llm_stream_t s
 /* Bytes of workspace that a call with these sizes needs (the pointers are not
  * looked at), or a negative llm_status. */
 int64_t llm_attend_batch_workspace(const llm_pages *pages, const llm_attend *a);
+
+/* Reads the new rows' k and v back: k_out, v_out (dtype LLM_F32 or LLM_F16, rows
+ * as in llm_append) receive row e of each new token's pages; a padding row, or one
+ * at a bad place, is left as it was.  With n_new = a sequence's length its rows come
+ * out in a row, as a prefix for llm_attend_batch.  Errors: INVALID_ARG, UNSUPPORTED,
+ * CUDA. */
+typedef struct {
+    int32_t dtype;
+    void *k_out, *v_out;
+    int64_t k_stride, v_stride;
+} llm_read;
+int llm_kv_read(const llm_pages *pages, const llm_read *a, llm_stream_t stream);
+
+/* Pages of 4-bit values: 5 bits a value instead of 16.  The _q4 calls are
+ * llm_kv_append, llm_attend_batch and llm_kv_read on such pages: k_pages and v_pages
+ * are n_pages pages of llm_q4_page_bytes() bytes each, 16-byte aligned, and
+ * everything else is as there.  page_size is at least 8, head_dim a multiple of 16 (UNSUPPORTED
+ * otherwise).
+ * A row of a kv head is cut into groups of 32 consecutive elements (the last one may
+ * be shorter).  A group is held as FP16 d and m and a number n in 0..15 for each
+ * element, which stands for the FP16 nearest to d n + m (rounded once):
+ *   m = the FP16 nearest to the group's least element, d = the FP16 nearest to
+ *   (largest - least) / 15, n = (x - m) / d rounded to the nearest integer (half to even) and
+ *   cut off at 0 and 15; n = 0 where d = 0.  Elements are k after its rotation, and v, in F32;
+ *   differences and quotients are rounded to F32.
+ * A group with an element that is not finite, or whose m or d is not finite in FP16, stands for
+ * NaN throughout.
+ * A page is [n_kv_heads][page_size][head_dim / 2] bytes of numbers (element 2i in
+ * the lower half of byte i, 2i + 1 in the upper one), then [n_kv_heads][page_size]
+ * [groups] pairs of FP16 d, m, and zero to twelve bytes that nothing reads or writes. */
+int64_t llm_q4_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_dim);   /* or a negative llm_status */
+int llm_kv_append_q4(const llm_pages *pages, const llm_append *a, llm_stream_t stream);
+int llm_kv_read_q4(const llm_pages *pages, const llm_read *a, llm_stream_t stream);
+int llm_attend_batch_q4(const llm_pages *pages, const llm_attend *a, llm_stream_t stream);
+int64_t llm_attend_batch_q4_workspace(const llm_pages *pages, const llm_attend *a);
+
+/* A pool of pages and the sequences that hold them: sequence s (of n_seqs, at most
+ * 4096) has lens[s] rows, in pages page_table[s*max_pages + 0 ..
+ * ceil(lens[s] / page_size) - 1].  refs[j] counts page j's holders: one for each
+ * entry of a sequence that names it, and whatever the caller adds for itself; 0: the page
+ * is free.  Pages of any layout: page j of layer l is page_bytes bytes at
+ * k_pages + l * layer_stride + j * page_bytes (v_pages likewise; all multiples of 16).
+ * row_bytes > 0: row i of a page is its bytes i * row_bytes .. (FP16 pages:
+ * n_kv_heads * head_dim * 2), so that a page's first rows can be copied alone;
+ * 0: pages are copied whole.  n_layers = 0: tables only. */
+typedef struct {
+    int32_t n_seqs, page_size, n_pages, max_pages;   /* page_size: a power of two */
+    int32_t *page_table, *lens, *refs;               /* DEVICE */
+    int32_t *err;                                    /* DEVICE, or NULL */
+    int32_t n_layers;
+    void *k_pages, *v_pages;                         /* DEVICE, 16-byte aligned */
+    int64_t page_bytes, row_bytes, layer_stride;
+} llm_pool;
+
+/* Forks, reorders, cuts, extends and ends sequences, all in one step: sequence s goes
+ * on from the rows that sequence parents[s] had before the call (-1: from none; parents
+ * NULL: each from itself), of which it keeps the first rows[s], and has rows[s] rows then
+ * (rows NULL: as many as its parent had); those behind the kept ones are room for rows
+ * to be written.  rows[s] = 0 ends a sequence.
+ *   Pages whose rows are all kept are shared.  A page of which a sequence keeps only the
+ * first rows (it will write the next ones) stays with the first sequence in order that keeps it so, if no one
+ * holds it whole and refs counts no holder of the caller's; the others get a copy of the kept rows in a fresh page.  Fresh pages
+ * are the free ones (as of the new state) with the lowest numbers, given out in order of the sequences and of their
+ * rows.  page_table, lens and refs become the new state's; entries that a sequence
+ * gives up become -1.
+ *   Where the free pages do not suffice (LLM_PAGES_FULL), a parent is not in
+ * [-1, n_seqs) (LLM_PAGES_BAD_SEQ), a length is below 0 or above max_pages*page_size
+ * (LLM_PAGES_BAD_LEN), an entry that is given up or taken over names no page or a page
+ * would be left with fewer holders than none (LLM_PAGES_BAD_PAGE), *err says so and nothing is changed.
+ * parents, rows: DEVICE [n_seqs].  workspace: DEVICE, 256-byte aligned, as for
+ * llm_attend_batch.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int llm_pages_update(const llm_pool *pool, const int32_t *parents, const int32_t *rows, void *workspace,
+                     int64_t workspace_bytes, llm_stream_t stream);
+int64_t llm_pages_update_workspace(const llm_pool *pool);
+
+/* Moves the pages in use to the first places of the pool: with n_live pages in use,
+ * those at n_live or behind, in order, are copied to the free ones before n_live, in
+ * order.  n_live (DEVICE, one value) receives their count, moved [n_pages] each page's new
+ * number (-1: free), table_out (page_table's shape) the new numbers of the entries in
+ * use (no other entry is written), refs_out [n_pages] the new counts.  table_out may be page_table and refs_out may be refs; otherwise those are left as they
+ * are (and name the pages that still hold what they held).  An entry in use that names no page in use is
+ * taken over as it is and sets LLM_PAGES_BAD_PAGE; a length above max_pages*page_size
+ * counts as that and sets LLM_PAGES_BAD_LEN.  DEVICE pointers; workspace as above.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int llm_pages_compact(const llm_pool *pool, int32_t *table_out, int32_t *refs_out, int32_t *moved, int32_t *n_live,
+                      void *workspace, int64_t workspace_bytes, llm_stream_t stream);
+int64_t llm_pages_compact_workspace(const llm_pool *pool);
+
+/* Penalties, biases and masks on n_rows rows of vocab logits (LLM_F32 or LLM_F16, row
+ * r at r * stride elements, any alignment of the type) into out (out_dtype,
+ * out_stride), which may be logits itself (same type and stride; what does not change is
+ * then neither read nor written) and must not overlap it otherwise.  For row r and token t, in F32, rounded once to out_dtype:
+ *   c = how often t is in history[r*history_stride + i], i in [max(0, n - window), n),
+ *       n = history_lens[r] cut off at 0 and max_history; window = 0: all of it
+ *   y = logit; if c > 0: y = (y > 0 ? y / repetition[r] : y * repetition[r]) -
+ *       (frequency[r] * c + presence[r])
+ *   y = y + bias of t: of row r's entries bias_ids[r*n_bias + j] = t the last one's
+ *       bias[r*n_bias + j]
+ *   y = -infinity if bit t % 32 of word t / 32 of the row's mask is 0
+ * history NULL: no penalties; repetition, frequency or presence NULL: 1, 0, 0.
+ * Tokens outside [0, vocab) in the history or the biases (-1, say) count for nothing.
+ * Row r's mask is masks + mask_of[r] * mask_stride words (mask_of NULL: mask r); a
+ * number outside [0, n_masks): no mask.  DEVICE pointers; n_rows >= 0, 1 <= vocab <=
+ * 2^30.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+typedef struct {
+    int32_t n_rows, vocab, dtype, out_dtype;
+    const void *logits;
+    int64_t stride;
+    void *out;
+    int64_t out_stride;
+    const int32_t *history, *history_lens;
+    int64_t history_stride;
+    int32_t max_history, window;
+    const float *repetition, *frequency, *presence;
+    const int32_t *bias_ids;
+    const float *bias;
+    int32_t n_bias, n_masks;
+    const uint32_t *masks;
+    int64_t mask_stride;
+    const int32_t *mask_of;
+} llm_adjust;
+int llm_logits_adjust(const llm_adjust *a, llm_stream_t stream);
 
 /* n_rows rows of vocab logits (LLM_F32 or LLM_F16; row r at r * stride
  * elements, any alignment of the type).  For each row, with p = softmax(row):

@@ -7,7 +7,8 @@ builds the library if needed and fails if it cannot be built or loaded.
 from .binding import *  # noqa: F401,F403
 from .binding import Decoder, DeviceWeights, LlmError, LIBRARY_PATH, declared_symbols  # noqa: F401
 
-_BATCH = ("AttendBatch", "BatchDecoder", "KvAppend", "LogProbs", "PagedBatch", "rope_table")
+_BATCH = ("AdjustLogits", "AttendBatch", "BatchDecoder", "KvAppend", "KvRead", "LogProbs", "PagePool", "PagedBatch", "PagedBatchQ4",
+          "PagesCompact", "PagesUpdate", "q4_pages", "rope_table")
 
 
 def __getattr__(name):

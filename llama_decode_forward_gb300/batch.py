@@ -1,5 +1,7 @@
 """Batched decoding over CUDA tensors: the operators llm_kv_append,
-llm_attend_batch and llm_logprobs of include/llm.h.
+llm_attend_batch, llm_kv_read (on pages in float16 or of 4-bit values),
+llm_pages_update, llm_pages_compact, llm_logits_adjust and llm_logprobs of
+include/llm.h.
 
 Each class checks its tensors once, keeps them (and the C arguments made of
 them) and enqueues one call of its operator whenever it is called, on the
@@ -106,8 +108,11 @@ class PagedBatch(_Owner):
     def __init__(self, k_pages, v_pages, page_table, lens, n_new: int = 1, prefix_len: int = 0, err=None):
         _int32(n_new=n_new, prefix_len=prefix_len)
         _tensor("k_pages", k_pages, (torch.float16,), (None,) * 4, None)
+        self._set(k_pages, v_pages, page_table, lens, *k_pages.shape[1:], n_new, prefix_len, err)
+
+    def _set(self, k_pages, v_pages, page_table, lens, page_size, n_kv, hd, n_new, prefix_len, err) -> None:
         dev = k_pages.device
-        _tensor("v_pages", v_pages, (torch.float16,), tuple(k_pages.shape), dev)
+        _tensor("v_pages", v_pages, (k_pages.dtype,), tuple(k_pages.shape), dev)
         _tensor("lens", lens, (torch.int32,), (None,), dev)
         _tensor("page_table", page_table, (torch.int32,), (lens.shape[0], None), dev)
         made = err is None
@@ -117,7 +122,7 @@ class PagedBatch(_Owner):
         self._owns((err,) if made else (), dev)
         self.k_pages, self.v_pages, self.page_table, self.lens, self.err = k_pages, v_pages, page_table, lens, err
         self.device = dev
-        n_pages, page_size, n_kv, hd = k_pages.shape
+        n_pages = k_pages.shape[0]
         _int32(n_pages=n_pages, page_size=page_size, sequences=lens.shape[0], max_pages=page_table.shape[1])
         self.rows = lens.shape[0] * n_new
         self.struct = _b.llm_pages(n_seqs=lens.shape[0], n_new=n_new, prefix_len=prefix_len, page_size=page_size,
@@ -129,6 +134,32 @@ class PagedBatch(_Owner):
         """The LLM_PAGES_* bits seen so far (waits for the device)."""
         torch.cuda.synchronize(self.device)
         return int(self.err.item())
+
+
+class PagedBatchQ4(PagedBatch):
+    """The same over pages of 4-bit values (include/llm.h): k_pages, v_pages uint8
+    [n_pages, bytes of a page], as q4_pages() makes them."""
+
+    def __init__(self, k_pages, v_pages, page_table, lens, page_size: int, n_kv_heads: int, head_dim: int, n_new: int = 1,
+                 prefix_len: int = 0, err=None):
+        _int32(n_new=n_new, prefix_len=prefix_len)
+        _tensor("k_pages", k_pages, (torch.uint8,), (None, _q4_page_bytes(page_size, n_kv_heads, head_dim)), None)
+        self._set(k_pages, v_pages, page_table, lens, page_size, n_kv_heads, head_dim, n_new, prefix_len, err)
+
+
+def _q4_page_bytes(page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    _int32(page_size=page_size, n_kv_heads=n_kv_heads, head_dim=head_dim)
+    n = _b._lib.llm_q4_page_bytes(page_size, n_kv_heads, head_dim)
+    if n < 0:
+        _run(int(n))
+    return int(n)
+
+
+def q4_pages(n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, n_layers: int | None = None, device="cuda") -> torch.Tensor:
+    """Pages of 4-bit values, all zero: uint8 [n_pages, bytes of a page], with n_layers
+    [n_layers, n_pages, bytes of a page]."""
+    shape = (n_pages, _q4_page_bytes(page_size, n_kv_heads, head_dim))
+    return torch.zeros(shape if n_layers is None else (n_layers, *shape), dtype=torch.uint8, device=device)
 
 
 class _Op(_Owner):
@@ -182,7 +213,23 @@ class KvAppend(_Op):
             _tensor("q_out", q_out, _DTYPES, tuple(q.shape), dev, strided=True)
             a.n_heads, a.q, a.q_stride = q.shape[1], q.data_ptr(), q.stride(0)
             a.q_out, a.q_out_stride, a.q_out_dtype = q_out.data_ptr(), q_out.stride(0), _DTYPES[q_out.dtype]
-        self._made(_b._lib.llm_kv_append, pages, (q, k, v, cos_sin, q_out), (p, a), (), dev)
+        fn = _b._lib.llm_kv_append_q4 if isinstance(pages, PagedBatchQ4) else _b._lib.llm_kv_append
+        self._made(fn, pages, (q, k, v, cos_sin, q_out), (p, a), (), dev)
+
+
+class KvRead(_Op):
+    """llm_kv_read: the new rows' k and v into k_out, v_out [rows, n_kv_heads,
+    head_dim] (float32 or float16, free in the row stride)."""
+
+    def __init__(self, pages: PagedBatch, k_out, v_out):
+        p, dev = pages.struct, pages.device
+        kv = (pages.rows, p.n_kv_heads, p.head_dim)
+        _tensor("k_out", k_out, _DTYPES, kv, dev, strided=True)
+        _tensor("v_out", v_out, (k_out.dtype,), kv, dev, strided=True)
+        a = _b.llm_read(dtype=_DTYPES[k_out.dtype], k_out=k_out.data_ptr(), v_out=v_out.data_ptr(), k_stride=k_out.stride(0),
+                        v_stride=v_out.stride(0))
+        fn = _b._lib.llm_kv_read_q4 if isinstance(pages, PagedBatchQ4) else _b._lib.llm_kv_read
+        self._made(fn, pages, (k_out, v_out), (p, a), (), dev)
 
 
 class AttendBatch(_Op):
@@ -207,12 +254,167 @@ class AttendBatch(_Op):
             if prefix_k.stride(0) != prefix_v.stride(0):
                 raise ValueError("prefix_k and prefix_v have different row strides")
             a.prefix_k, a.prefix_v, a.prefix_stride = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.stride(0)
-        n = _b._lib.llm_attend_batch_workspace(ctypes.byref(p), ctypes.byref(a))
+        q4 = isinstance(pages, PagedBatchQ4)
+        n = (_b._lib.llm_attend_batch_q4_workspace if q4 else _b._lib.llm_attend_batch_workspace)(ctypes.byref(p), ctypes.byref(a))
         if n < 0:
             _run(int(n))
         self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
         a.workspace, a.workspace_bytes = self.workspace.data_ptr(), int(n)
-        self._made(_b._lib.llm_attend_batch, pages, (q, out, prefix_k, prefix_v), (p, a), (self.workspace,), dev)
+        self._made(_b._lib.llm_attend_batch_q4 if q4 else _b._lib.llm_attend_batch, pages, (q, out, prefix_k, prefix_v), (p, a), (self.workspace,), dev)
+
+
+class PagePool(_Owner):
+    """Sequences and the pages that they hold (llm_pool), for PagesUpdate and
+    PagesCompact.  k_pages, v_pages: float16 [n_pages, page_size, n_kv_heads, head_dim],
+    or uint8 [n_pages, bytes of a page] (then page_size is wanted), each also with the
+    layers before that, free in the layers' stride; None: tables only.  page_table
+    int32 [n_seqs, max_pages], lens int32 [n_seqs], refs int32 [n_pages]; ``err``
+    collects errors as in PagedBatch, whose page_table, lens and err these may be."""
+
+    def __init__(self, k_pages, v_pages, page_table, lens, refs, page_size: int | None = None, err=None):
+        _tensor("refs", refs, (torch.int32,), (None,), None)
+        dev, n_pages = refs.device, refs.shape[0]
+        _tensor("lens", lens, (torch.int32,), (None,), dev)
+        _tensor("page_table", page_table, (torch.int32,), (lens.shape[0], None), dev)
+        made = err is None
+        if made:
+            err = torch.zeros(1, dtype=torch.int32, device=dev)
+        _tensor("err", err, (torch.int32,), (1,), dev)
+        s = _b.llm_pool(n_seqs=lens.shape[0], n_pages=n_pages, max_pages=page_table.shape[1], page_table=page_table.data_ptr(),
+                        lens=lens.data_ptr(), refs=refs.data_ptr(), err=err.data_ptr())
+        if k_pages is not None:
+            page = 3 if isinstance(k_pages, torch.Tensor) and k_pages.dtype == torch.float16 else 1
+            layers = isinstance(k_pages, torch.Tensor) and k_pages.dim() == page + 2
+            shape = ((None,) if layers else ()) + (n_pages,) + (None,) * page
+            _tensor("k_pages", k_pages, (torch.float16, torch.uint8), shape, dev, strided=layers)
+            _tensor("v_pages", v_pages, (k_pages.dtype,), tuple(k_pages.shape), dev, strided=layers)
+            if layers and k_pages.stride(0) != v_pages.stride(0):
+                raise ValueError("k_pages and v_pages have different layer strides")
+            size = k_pages.element_size()
+            one = k_pages.shape[1 + layers:].numel() * size
+            if page == 3:
+                if page_size not in (None, k_pages.shape[1 + layers]):
+                    raise ValueError(f"page_size {page_size}: the pages have {k_pages.shape[1 + layers]} rows")
+                page_size = k_pages.shape[1 + layers]
+                s.row_bytes = one // max(page_size, 1)
+            s.n_layers = k_pages.shape[0] if layers else 1
+            s.k_pages, s.v_pages, s.page_bytes = k_pages.data_ptr(), v_pages.data_ptr(), one
+            s.layer_stride = k_pages.stride(0) * size if layers else n_pages * one
+        if page_size is None:
+            raise ValueError("page_size is wanted for pages of bytes, and without pages")
+        _int32(n_seqs=s.n_seqs, page_size=page_size, pages=n_pages, max_pages=page_table.shape[1], layers=s.n_layers)
+        s.page_size = page_size
+        self._owns((err,) if made else (), dev)
+        self.k_pages, self.v_pages, self.page_table, self.lens, self.refs, self.err = k_pages, v_pages, page_table, lens, refs, err
+        self.device, self.struct = dev, s
+
+    def errors(self) -> int:
+        """The LLM_PAGES_* bits seen so far (waits for the device)."""
+        torch.cuda.synchronize(self.device)
+        return int(self.err.item())
+
+
+class PagesUpdate(_Op):
+    """llm_pages_update: sequence s goes on from parents[s] (int32 [n_seqs]; None: itself)
+    and has rows[s] rows then (int32 [n_seqs]; None: as many as its parent).  The
+    operator owns its workspace, as AttendBatch does."""
+
+    def __init__(self, pool: PagePool, parents=None, rows=None):
+        p, dev = pool.struct, pool.device
+        for name, t in (("parents", parents), ("rows", rows)):
+            if t is not None:
+                _tensor(name, t, (torch.int32,), (p.n_seqs,), dev)
+        n = _b._lib.llm_pages_update_workspace(ctypes.byref(p))
+        if n < 0:
+            _run(int(n))
+        self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
+        self._made(_b._lib.llm_pages_update, pool, (parents, rows), (p,), (self.workspace,), dev)
+        self._args += tuple(t.data_ptr() if t is not None else None for t in (parents, rows)) + (self.workspace.data_ptr(), int(n))
+
+
+class PagesCompact(_Op):
+    """llm_pages_compact: the pages in use to the front of the pool.  table_out and
+    refs_out (None: the pool's own tensors, in place) receive the new tables; moved int32
+    [n_pages] and n_live int32 [1] (None: made here) each page's new number and how
+    many are in use."""
+
+    def __init__(self, pool: PagePool, table_out=None, refs_out=None, moved=None, n_live=None):
+        p, dev = pool.struct, pool.device
+        own = []
+        table_out = pool.page_table if table_out is None else table_out
+        refs_out = pool.refs if refs_out is None else refs_out
+        if moved is None:
+            moved = torch.empty_like(pool.refs)
+            own.append(moved)
+        if n_live is None:
+            n_live = torch.empty(1, dtype=torch.int32, device=dev)
+            own.append(n_live)
+        for name, t, shape in (("table_out", table_out, tuple(pool.page_table.shape)), ("refs_out", refs_out, (p.n_pages,)),
+                               ("moved", moved, (p.n_pages,)), ("n_live", n_live, (1,))):
+            _tensor(name, t, (torch.int32,), shape, dev)
+        n = _b._lib.llm_pages_compact_workspace(ctypes.byref(p))
+        if n < 0:
+            _run(int(n))
+        self.workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=dev)
+        self.table_out, self.refs_out, self.moved, self.n_live = table_out, refs_out, moved, n_live
+        self._made(_b._lib.llm_pages_compact, pool, (table_out, refs_out, moved, n_live), (p,), (self.workspace, *own), dev)
+        self._args += tuple(t.data_ptr() for t in (table_out, refs_out, moved, n_live, self.workspace)) + (int(n),)
+
+
+class AdjustLogits(_Op):
+    """llm_logits_adjust: penalties for repeated tokens, biases and masks on logits
+    [rows, vocab] (float32 or float16, free in the row stride) into out (likewise; None:
+    logits itself).  history int32 [rows, max_history] with history_lens int32 [rows]
+    and, float32 [rows] or None each, repetition, frequency and presence; window: how many
+    of the last tokens count (0: all).  bias_ids int32 and bias float32 [rows, n_bias].
+    masks int32 [n_masks, at least vocab / 32] (bit 0: banned), mask_of int32 [rows] the
+    mask of each row (None: its own)."""
+
+    def __init__(self, logits, out=None, history=None, history_lens=None, window: int = 0, repetition=None, frequency=None,
+                 presence=None, bias_ids=None, bias=None, masks=None, mask_of=None):
+        _int32(window=window)
+        _tensor("logits", logits, _DTYPES, (None, None), None, strided=True)
+        dev, (n, vocab) = logits.device, logits.shape
+        out = logits if out is None else out
+        _tensor("out", out, _DTYPES, (n, vocab), dev, strided=True)
+        _int32(rows=n, vocab=vocab)
+        a = _b.llm_adjust(n_rows=n, vocab=vocab, dtype=_DTYPES[logits.dtype], out_dtype=_DTYPES[out.dtype], logits=logits.data_ptr(),
+                          stride=logits.stride(0), out=out.data_ptr(), out_stride=out.stride(0), window=window)
+        if history is None and any(t is not None for t in (history_lens, repetition, frequency, presence)):
+            raise ValueError("penalties without a history")
+        if history is not None:
+            _tensor("history", history, (torch.int32,), (n, None), dev, strided=True)
+            _tensor("history_lens", history_lens, (torch.int32,), (n,), dev)
+            _int32(max_history=history.shape[1])
+            a.history, a.history_stride, a.max_history = history.data_ptr(), history.stride(0), history.shape[1]
+            a.history_lens = history_lens.data_ptr()
+            for name, t in (("repetition", repetition), ("frequency", frequency), ("presence", presence)):
+                if t is not None:
+                    _tensor(name, t, (torch.float32,), (n,), dev)
+                    setattr(a, name, t.data_ptr())
+        if (bias_ids is None) != (bias is None):
+            raise ValueError("bias_ids and bias belong together")
+        if bias_ids is not None:
+            _tensor("bias_ids", bias_ids, (torch.int32,), (n, None), dev)
+            _tensor("bias", bias, (torch.float32,), tuple(bias_ids.shape), dev)
+            _int32(n_bias=bias_ids.shape[1])
+            a.bias_ids, a.bias, a.n_bias = bias_ids.data_ptr(), bias.data_ptr(), bias_ids.shape[1]
+        if masks is None and mask_of is not None:
+            raise ValueError("mask_of without masks")
+        if masks is not None:
+            _tensor("masks", masks, (torch.int32,), (None, None), dev, strided=True)
+            if masks.shape[1] < -(-vocab // 32):
+                raise ValueError(f"masks of {masks.shape[1]} words, {-(-vocab // 32)} are wanted")
+            if mask_of is None and masks.shape[0] < n:
+                raise ValueError(f"{masks.shape[0]} masks for {n} rows")
+            _int32(n_masks=masks.shape[0])
+            a.masks, a.n_masks, a.mask_stride = masks.data_ptr(), masks.shape[0], masks.stride(0)
+            if mask_of is not None:
+                _tensor("mask_of", mask_of, (torch.int32,), (n,), dev)
+                a.mask_of = mask_of.data_ptr()
+        self.out = out
+        self._made(_b._lib.llm_logits_adjust, None,
+                   (logits, out, history, history_lens, repetition, frequency, presence, bias_ids, bias, masks, mask_of), (a,), (), dev)
 
 
 class LogProbs(_Op):
@@ -281,6 +483,16 @@ class BatchDecoder:
                                    n_pages=n_pages, max_pages=max_pages, pages=self.pages.data_ptr(),
                                    page_table=self.page_table.data_ptr(), lens=self.lens.data_ptr(),
                                    tokens=self.tokens.data_ptr(), logits=self.logits.data_ptr(), err=self.err.data_ptr())
+
+    def pool(self, refs, err=None) -> "PagePool":
+        """The decoder's pages as a pool, with refs int32 [n_pages] the pages' holders: what the
+        sequences hold is then up to PagesUpdate, which page_table and lens are written by."""
+        if refs.shape[0] != self.struct.n_pages:
+            raise ValueError(f"{refs.shape[0]} counts of holders for {self.struct.n_pages} pages")
+        c = _b.llm_get_config(self.decoder.h)
+        kv = self.pages[:2 * c.n_layers * refs.shape[0] * self.struct.page_size * c.n_kv_heads * c.head_dim]
+        kv = kv.view(c.n_layers, 2, refs.shape[0], self.struct.page_size, c.n_kv_heads, c.head_dim)
+        return PagePool(kv[:, 0], kv[:, 1], self.page_table, self.lens, refs, err=err)
 
     def _use_on(self, stream) -> None:
         """What `stream` is given from now on may use the tensors."""

@@ -20,7 +20,7 @@ LLM_ERR_INVALID_ARG, LLM_ERR_UNSUPPORTED, LLM_ERR_OUT_OF_RANGE = -1, -2, -3
 LLM_ERR_CUDA, LLM_ERR_NO_MEMORY, LLM_ERR_DEVICE_TIMEOUT, LLM_ERR_STATE, LLM_ERR_NONFINITE = -4, -5, -6, -7, -8
 LLM_ERR_CHECK = -9
 LLM_NUMERICS_EXACT, LLM_NUMERICS_LLAMACPP = 0, 1
-LLM_PAGES_BAD_PAGE, LLM_PAGES_BAD_LEN, LLM_PAGES_TIMEOUT = 1, 2, 4
+LLM_PAGES_BAD_PAGE, LLM_PAGES_BAD_LEN, LLM_PAGES_TIMEOUT, LLM_PAGES_FULL, LLM_PAGES_BAD_SEQ = 1, 2, 4, 8, 16
 LLM_DEBUG_Q, LLM_DEBUG_K, LLM_DEBUG_V, LLM_DEBUG_ATTN_OUT, LLM_DEBUG_FFN_SWIGLU, LLM_DEBUG_FFN_OUT = range(6)
 
 
@@ -61,6 +61,28 @@ class llm_attend(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("prefix_k", ctypes.c_void_p),
                 ("prefix_v", ctypes.c_void_p), ("prefix_stride", ctypes.c_int64), ("workspace", ctypes.c_void_p),
                 ("workspace_bytes", ctypes.c_int64)]
+
+
+class llm_read(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("k_out", ctypes.c_void_p), ("v_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64)]
+
+
+class llm_pool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "page_size", "n_pages", "max_pages")] + \
+               [(n, ctypes.c_void_p) for n in ("page_table", "lens", "refs", "err")] + \
+               [("n_layers", ctypes.c_int32), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("page_bytes", "row_bytes", "layer_stride")]
+
+
+class llm_adjust(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_rows", "vocab", "dtype", "out_dtype")] + \
+               [("logits", ctypes.c_void_p), ("stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("history", ctypes.c_void_p), ("history_lens", ctypes.c_void_p),
+                ("history_stride", ctypes.c_int64), ("max_history", ctypes.c_int32), ("window", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("repetition", "frequency", "presence", "bias_ids", "bias")] + \
+               [("n_bias", ctypes.c_int32), ("n_masks", ctypes.c_int32), ("masks", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64), ("mask_of", ctypes.c_void_p)]
 
 
 class llm_logprobs_args(ctypes.Structure):
@@ -135,6 +157,17 @@ _SIGS = {
     "llm_kv_append": ([_vp, _vp, _vp], _int),
     "llm_attend_batch_workspace": ([_vp, _vp], ctypes.c_int64),
     "llm_attend_batch": ([_vp, _vp, _vp], _int),
+    "llm_kv_read": ([_vp, _vp, _vp], _int),
+    "llm_q4_page_bytes": ([_i32, _i32, _i32], ctypes.c_int64),
+    "llm_kv_append_q4": ([_vp, _vp, _vp], _int),
+    "llm_kv_read_q4": ([_vp, _vp, _vp], _int),
+    "llm_attend_batch_q4": ([_vp, _vp, _vp], _int),
+    "llm_attend_batch_q4_workspace": ([_vp, _vp], ctypes.c_int64),
+    "llm_pages_update": ([_vp, _vp, _vp, _vp, ctypes.c_int64, _vp], _int),
+    "llm_pages_update_workspace": ([_vp], ctypes.c_int64),
+    "llm_pages_compact": ([_vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int64, _vp], _int),
+    "llm_pages_compact_workspace": ([_vp], ctypes.c_int64),
+    "llm_logits_adjust": ([_vp, _vp], _int),
     "llm_logprobs": ([_vp, _vp], _int),
     "llm_batch_pages_bytes": ([_vp, _i32, _i32], ctypes.c_int64),
     "llm_decode_batch": ([_vp, _vp], _int),

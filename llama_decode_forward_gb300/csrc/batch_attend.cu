@@ -41,6 +41,7 @@ struct AttendDev {
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
     int prefix_blocks, suffix_workers;
     Div by_heads, by_new, by_gq;            // the join's divisions
+    Q4Dev q4;                               // pages of 4-bit values
     int* timeout;                   // a handle's word for waits that gave up, or nullptr
     int wait_limit;                 // probes before the prefix kernel's waits give up; below kWaitLimit
                                     // (a test's) it makes no copies either, so that they do
@@ -582,6 +583,40 @@ __device__ __forceinline__ int clipped_len(const PagesDev& p, int s) {
 // empty ones.
 __device__ __forceinline__ int weight(int len) { return len > 0 ? (len + 15) / 16 + kUnit : 0; }
 
+// The sequences' row counts, and the sums of their weights before each.
+__device__ __forceinline__ void count_pieces(const PagesDev& p, const AttendDev& a, int* starts, int* lens) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int sums[kSuffixWarps];
+    const int each = (p.n_seqs + 32 * kSuffixWarps - 1) / (32 * kSuffixWarps), s0 = threadIdx.x * each;
+    int mine = 0;
+    for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
+        lens[s] = clipped_len(p, s);
+        mine += weight(lens[s]);
+    }
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
+    }
+    if (lane == 31) sums[warp] = sum;
+    __syncthreads();
+    int at = sum - mine;
+    for (int w = 0; w < warp; w++) at += sums[w];
+    for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
+        starts[s] = at;
+        at += weight(lens[s]);
+        if (blockIdx.x == 0) a.starts[s + 1] = at;
+    }
+    if (threadIdx.x == 0) {
+        int all = 0;
+        for (int w = 0; w < kSuffixWarps; w++) all += sums[w];
+        starts[p.n_seqs] = all;
+        if (blockIdx.x == 0) a.starts[0] = 0;
+    }
+    __syncthreads();
+}
+
 // An 8 x 8 matrix of F16 pairs, transposed across the warp.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
@@ -617,38 +652,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
     const int srows = p.n_new * a.gq, rt = (srows + RU - 1) / RU, units = p.n_kv * rt;
     int* starts = seqs;                      // [n_seqs + 1]
     int* lens = starts + p.n_seqs + 1;       // [n_seqs]
-    {
-        // prefix sums of the sequences' pieces
-        __shared__ int sums[kSuffixWarps];
-        const int each = (p.n_seqs + 32 * kSuffixWarps - 1) / (32 * kSuffixWarps), s0 = threadIdx.x * each;
-        int mine = 0;
-        for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
-            lens[s] = clipped_len(p, s);
-            mine += weight(lens[s]);
-        }
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += v;
-        }
-        if (lane == 31) sums[warp] = sum;
-        __syncthreads();
-        int at = sum - mine;
-        for (int w = 0; w < warp; w++) at += sums[w];
-        for (int s = s0; s < min(p.n_seqs, s0 + each); s++) {
-            starts[s] = at;
-            at += weight(lens[s]);
-            if (blockIdx.x == 0) a.starts[s + 1] = at;
-        }
-        if (threadIdx.x == 0) {
-            int all = 0;
-            for (int w = 0; w < kSuffixWarps; w++) all += sums[w];
-            starts[p.n_seqs] = all;
-            if (blockIdx.x == 0) a.starts[0] = 0;
-        }
-        __syncthreads();
-    }
+    count_pieces(p, a, starts, lens);
     const Deal deal = deal_of(starts[p.n_seqs], units, (int)gridDim.x * kSuffixWarps);
     const int me = blockIdx.x * kSuffixWarps + warp;
     if (me < deal.workers) {
@@ -914,6 +918,398 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
     if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();
 }
 
+// ---------------------------------------------- suffix, 4-bit pages --
+// The suffix kernel for pages of 4-bit values: the same units, pieces, deal and parts.
+// A value is made where it is used: numbers become F16 by their bits (0x6400 | n is
+// 1024 + n, 0x6400 | 16 n is 1024 + 16 n; one exact operation takes the 1024 away) and
+// one fused multiply-add rounds d n + m to the F16 that it stands for.
+// - K is the products' first operand: lane (r, t) holds dims 64 c + 16 t + {0 .. 15} of
+//   cached rows r and r + 8, two words of numbers.  Their half-words pair dims 0 and 4, 1
+//   and 5, ... of a word, so q is loaded in that order.
+// - V^T is the other product's first operand, and needs pairs of cached rows: lane (r, t)
+//   loads dims 8 V r .. of rows 2t, 2t + 1 (and those eight behind), and a byte permutation
+//   joins the two rows' numbers, so no transpose is needed.  An MMA's rows r and r + 8 are
+//   dims 8 V r + 2 i and + 1.
+// A step is H pieces (32 cached rows for heads of up to 64 values: half of the bytes and
+// of the maxima's exchanges for each), requested while the one before is multiplied.
+// Eight rows in a row lie in one page (page_size >= 8): an octet.
+__host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? 4 : 3) : (nt == 1 ? 3 : 2); }
+
+// Four pairs of numbers of a word, as F16 pairs: (x & 15, (x >> 16) & 15) and so on.
+__device__ __forceinline__ __half2 q4_low(uint32_t x) {            // numbers at bits 0 and 16
+    const uint32_t y = (x & 0x000F000Fu) | 0x64006400u;
+    return __hsub2(*reinterpret_cast<const __half2*>(&y), __float2half2_rn(1024.f));
+}
+__device__ __forceinline__ __half2 q4_high(uint32_t x) {           // numbers at bits 4 and 20
+    const uint32_t y = (x & 0x00F000F0u) | 0x64006400u;
+    return __hfma2(*reinterpret_cast<const __half2*>(&y), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+}
+__device__ __forceinline__ uint32_t q4_value(__half2 n, __half2 d, __half2 m) {
+    const __half2 v = __hfma2(n, d, m);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+
+template <int HDP, int NT, bool SPLITQ>
+__global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
+    suffix_q4_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
+    constexpr int C = HDP / 64, KS = HDP / 16, RU = 8 * NT;  // chunks of 64 dims, MMA steps of a dot product (and MMA tiles of the sums)
+    constexpr int H = HDP == 64 ? 2 : 1, OCT = 2 * H;        // pieces and octets of a step
+    extern __shared__ int seqs[];
+    if (first) griddep_wait();
+    griddep_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int srows = p.n_new * a.gq, rt = (srows + RU - 1) / RU, units = p.n_kv * rt;
+    int* starts = seqs;
+    int* lens = starts + p.n_seqs + 1;
+    count_pieces(p, a, starts, lens);
+    const Deal deal = deal_of(starts[p.n_seqs], units, (int)gridDim.x * kSuffixWarps);
+    const int me = blockIdx.x * kSuffixWarps + warp;
+    if (me < deal.workers) {
+        const long long x0 = deal.total * me / deal.workers, x1 = deal.total * (me + 1) / deal.workers;
+        int s = 0;
+        for (int lo = 0, hi = p.n_seqs; hi - lo > 1;) {
+            const int mid = (lo + hi) / 2;
+            ((long long)starts[mid] * units <= x0 ? lo : hi) = mid;
+            s = lo;
+        }
+        auto next = [&](int& s, int& j, int& pc, int& np) {      // the unit behind one, at its first piece
+            pc = 0;
+            if (++j < units) return;
+            j = 0;
+            do s++;
+            while (lens[s] == 0);
+            np = (lens[s] + 15) / 16;
+        };
+        int np = (lens[s] + 15) / 16;
+        const long long in_seq = x0 - (long long)starts[s] * units;
+        int j = (int)(in_seq / (np + kUnit)), pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
+        if (pc >= np) {                      // it starts with empty pieces
+            left -= np + kUnit - pc;
+            if (left > 0) next(s, j, pc, np);
+        }
+        const int r = lane >> 2, t = lane & 3, pitch = p.hd / 2, pairs = 4 * a.q4.groups;
+        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k), *vp = reinterpret_cast<const uint8_t*>(p.v);
+
+        // octet lane % OCT's page of the step that is loaded next; -1: nothing to read
+        int ls = s, lj = j, lpc = pc, lnp = np, lleft = left, page = -1;
+        auto look = [&]() {
+            const int e = lpc * 16 + 8 * (lane % OCT), end = min(lens[ls], 16 * (lpc + min(lleft, H)));
+            page = -1;
+            if (e < end) {
+                page = p.table[(long long)ls * p.max_pages + (e >> p.page_shift)];
+                if (page < 0 || page >= p.n_pages) {
+                    flag(p.err, LLM_PAGES_BAD_PAGE);
+                    page = -1;
+                }
+            }
+        };
+        uint32_t kw[OCT][2 * C], kd[OCT][C], vw[OCT][2][C], vd[OCT][2];      // numbers and pairs of the step on its way
+        uint32_t there_x;                    // bit o: this lane's row r of octet o is there
+        auto load = [&]() {                  // requests the step, moves on and looks the next one up
+            const int e0 = lpc * 16, end = min(lens[ls], 16 * (lpc + min(lleft, H))), g = lj / rt;
+            there_x = 0;
+#pragma unroll
+            for (int o = 0; o < OCT; o++) {
+                const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o, in = e & ((1 << p.page_shift) - 1);
+                const long long numbers = q4_numbers(p, a.q4, pg, g, in), dm = q4_pairs(p, a.q4, pg, g, in);
+                const bool kr = pg >= 0 && e + r < end;
+                there_x |= kr ? 1u << o : 0u;
+#pragma unroll
+                for (int c = 0; c < C; c++) {
+                    kw[o][2 * c] = kw[o][2 * c + 1] = kd[o][c] = 0;
+                    if (kr && 64 * c + 16 * t < p.hd) {
+                        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(kp + numbers + r * pitch + 32 * c + 8 * t));
+                        kw[o][2 * c] = w.x;
+                        kw[o][2 * c + 1] = w.y;
+                        kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(kp + dm + r * pairs + 4 * (2 * c + (t >> 1))));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int row = 2 * t + k;
+#pragma unroll
+                    for (int c = 0; c < C; c++) vw[o][k][c] = 0;
+                    vd[o][k] = 0;
+                    if (pg >= 0 && e + row < end && 8 * C * r < p.hd) {
+                        const uint8_t* w = vp + numbers + row * pitch + 4 * C * r;
+                        if (C == 1) {
+                            vw[o][k][0] = __ldcs(reinterpret_cast<const uint32_t*>(w));
+                        } else {
+                            const uint2 y = __ldcs(reinterpret_cast<const uint2*>(w));
+                            vw[o][k][0] = y.x;
+                            vw[o][k][C - 1] = y.y;
+                        }
+                        vd[o][k] = __ldcs(reinterpret_cast<const uint32_t*>(vp + dm + row * pairs + 4 * (C * r >> 2)));
+                    }
+                }
+            }
+            const int n = min(min(lleft, H), lnp - lpc);
+            lleft -= n;
+            lpc += n;
+            if (lpc == lnp) {
+                lleft -= kUnit;
+                if (lleft > 0) next(ls, lj, lpc, lnp);
+            }
+            if (lleft > 0) look();
+        };
+        if (left > 0) {
+            look();
+            load();
+        }
+        while (left > 0) {
+            // ---- one unit: pieces pc .. of its np, as far as this worker goes
+            const int tile = j % rt, g = j / rt, count = min(left, np - pc);
+            const int last = p.lens[s] - p.n_new, e_min = last + tile * RU / a.gq;
+            // q as the second operand: query row r of each eight; rows behind the last repeat it (never stored)
+            uint32_t qhi[NT][KS][2], qlo[NT][SPLITQ ? KS : 1][2];
+            int e[NT][2];                    // the last cached row that query rows 2t and 2t + 1 see
+            float qs[NT][2];                 // and the factor of their scores
+#pragma unroll
+            for (int q = 0; q < NT; q++) {
+                const long long at = q_offset(a, p.hd, g, s * srows + min(tile * RU + q * 8 + r, srows - 1));
+#pragma unroll
+                for (int k = 0; k < 2; k++) e[q][k] = last + min(tile * RU + q * 8 + 2 * t + k, srows - 1) / a.gq;
+                float up = 1.f;
+                qs[q][0] = qs[q][1] = a.sc;
+                if (SPLITQ) {
+                    float m = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2 * C; i++) {
+                        float x[8];
+                        const int d = 64 * (i / 2) + 16 * t + 8 * (i % 2);
+                        if (d < p.hd) {
+                            load_q8(a, at + d, x);
+                            m = largest8(x, m);
+                        }
+                    }
+                    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                    const PowerOfTwo two = power_of((int)(__float_as_uint(fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2))) >> 23));
+                    up = two.up;
+#pragma unroll
+                    for (int k = 0; k < 2; k++) qs[q][k] = a.sc * __shfl_sync(0xffffffffu, two.down, 4 * (2 * t + k));
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * C; i++) {
+                    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    const int d = 64 * (i / 2) + 16 * t + 8 * (i % 2);
+                    if (d < p.hd) load_q8(a, at + d, x);
+                    if (SPLITQ)
+#pragma unroll
+                        for (int k = 0; k < 8; k++) x[k] *= up;
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {                // dims k and k + 4
+                        const uint32_t hi = pack_hi(x[k], x[k + 4]);
+                        qhi[q][2 * i + k / 2][k % 2] = hi;
+                        if (SPLITQ) qlo[q][SPLITQ ? 2 * i + k / 2 : 0][k % 2] = pack_lo(x[k], x[k + 4], hi);
+                    }
+                }
+            }
+            float o[NT][KS][4], R[NT][2], l[NT][2];
+#pragma unroll
+            for (int q = 0; q < NT; q++) {
+#pragma unroll
+                for (int d = 0; d < KS; d++) o[q][d][0] = o[q][d][1] = o[q][d][2] = o[q][d][3] = 0.f;
+                R[q][0] = R[q][1] = kLow;    // no key seen yet
+                l[q][0] = l[q][1] = 0.f;
+            }
+            for (int i0 = 0; i0 < count; i0 += H) {
+                uint32_t k_w[OCT][2 * C], k_d[OCT][C], v_w[OCT][2][C], v_d[OCT][2];
+#pragma unroll
+                for (int oc = 0; oc < OCT; oc++) {
+#pragma unroll
+                    for (int c = 0; c < C; c++) {
+                        k_w[oc][2 * c] = kw[oc][2 * c];
+                        k_w[oc][2 * c + 1] = kw[oc][2 * c + 1];
+                        k_d[oc][c] = kd[oc][c];
+                        v_w[oc][0][c] = vw[oc][0][c];
+                        v_w[oc][1][c] = vw[oc][1][c];
+                    }
+                    v_d[oc][0] = vd[oc][0];
+                    v_d[oc][1] = vd[oc][1];
+                }
+                const uint32_t there = there_x;
+                if (lleft > 0) load();
+                // ---- scores
+                float sc[H][NT][4];
+#pragma unroll
+                for (int h = 0; h < H; h++) {
+#pragma unroll
+                    for (int q = 0; q < NT; q++) sc[h][q][0] = sc[h][q][1] = sc[h][q][2] = sc[h][q][3] = 0.f;
+#pragma unroll
+                    for (int c = 0; c < C; c++) {
+                        __half2 d[2], m[2];
+#pragma unroll
+                        for (int x = 0; x < 2; x++) {
+                            d[x] = __low2half2(half2_of(k_d[2 * h + x][c]));
+                            m[x] = __high2half2(half2_of(k_d[2 * h + x][c]));
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            uint32_t y[2][4];
+#pragma unroll
+                            for (int x = 0; x < 2; x++) {
+                                const uint32_t w = k_w[2 * h + x][2 * c + i];
+                                y[x][0] = q4_value(q4_low(w), d[x], m[x]);
+                                y[x][1] = q4_value(q4_high(w), d[x], m[x]);
+                                y[x][2] = q4_value(q4_low(w >> 8), d[x], m[x]);
+                                y[x][3] = q4_value(q4_high(w >> 8), d[x], m[x]);
+                            }
+#pragma unroll
+                            for (int u = 0; u < 2; u++) {
+                                const uint32_t k[4] = {y[0][2 * u], y[1][2 * u], y[0][2 * u + 1], y[1][2 * u + 1]};
+                                const int ks = 4 * c + 2 * i + u;
+#pragma unroll
+                                for (int q = 0; q < NT; q++) {
+                                    mma16816(sc[h][q], k, qhi[q][ks][0], qhi[q][ks][1]);
+                                    if (SPLITQ) mma16816(sc[h][q], k, qlo[q][SPLITQ ? ks : 0][0], qlo[q][SPLITQ ? ks : 0][1]);
+                                }
+                            }
+                        }
+                    }
+                }
+                // rows that are not there, and those that some query rows do not see
+                const int e0 = (pc + i0) * 16;
+#pragma unroll
+                for (int h = 0; h < H; h++)
+#pragma unroll
+                    for (int q = 0; q < NT; q++)
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (!((there >> (2 * h + (k >> 1))) & 1u) || e0 + 16 * h + r + (k >> 1) * 8 > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                uint32_t ph[H][NT][2], pl[H][NT][2];
+#pragma unroll
+                for (int q = 0; q < NT; q++) {
+                    float top[2];
+                    bool move = false;
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        float m = fmaxf(sc[0][q][k], sc[0][q][2 + k]);
+                        if (H == 2) m = max3(m, sc[H - 1][q][k], sc[H - 1][q][2 + k]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        top[k] = fmaxf(m, kLow);
+                        move |= (top[k] - R[q][k]) * qs[q][k] > kLag;
+                    }
+                    if (__any_sync(0xffffffffu, move)) {
+                        float c[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            // (a row's own maximum decides: its bits do not depend on its neighbours)
+                            const float up = (top[k] - R[q][k]) * qs[q][k] > kLag ? top[k] : R[q][k];
+                            c[k] = exp2_fast((R[q][k] - up) * qs[q][k]);
+                            R[q][k] = up;
+                            l[q][k] *= c[k];
+                        }
+#pragma unroll
+                        for (int d = 0; d < KS; d++) {
+                            o[q][d][0] *= c[0];
+                            o[q][d][1] *= c[1];
+                            o[q][d][2] *= c[0];
+                            o[q][d][3] *= c[1];
+                        }
+                    }
+#pragma unroll
+                    for (int h = 0; h < H; h++) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            sc[h][q][k] = exp2_fast(fmaf(sc[h][q][k] - R[q][k & 1], qs[q][k & 1], kHead));
+                            l[q][k & 1] += sc[h][q][k];          // this thread's cached rows; all are added at the end
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const uint32_t hi = pack_hi(sc[h][q][2 * k], sc[h][q][2 * k + 1]);
+                            ph[h][q][k] = transpose8(hi);
+                            pl[h][q][k] = transpose8(pack_lo(sc[h][q][2 * k], sc[h][q][2 * k + 1], hi));
+                        }
+                    }
+                }
+                // ---- sums
+#pragma unroll
+                for (int h = 0; h < H; h++) {
+                    uint32_t v[KS][4];       // tile i: dims 2i and 2i + 1 of this lane's, of rows 2t, 2t + 1 and of the eight behind
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        const uint32_t da = v_d[2 * h + x][0], db = v_d[2 * h + x][1];
+                        const __half2 d = half2_of(__byte_perm(da, db, 0x5410)), m = half2_of(__byte_perm(da, db, 0x7632));
+#pragma unroll
+                        for (int i = 0; i < KS; i++) {
+                            const uint32_t b = i % 4, w = __byte_perm(v_w[2 * h + x][0][i / 4], v_w[2 * h + x][1][i / 4], b | (4 + b) << 8 | (4 + b) << 12 | b << 4);
+                            v[i][2 * x] = q4_value(q4_low(w), d, m);
+                            v[i][2 * x + 1] = q4_value(q4_high(w), d, m);
+                        }
+                    }
+                    // a row that some new tokens see and others do not: where its V is not
+                    // finite, 0 * V would reach those that do not, so it is added to the
+                    // others alone and taken out of the product
+                    if (p.n_new > 1 && e0 + 16 * h + 15 > e_min) {
+#pragma unroll
+                        for (int x = 0; x < 2; x++)
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                bool wild = false;
+#pragma unroll
+                                for (int i = 0; i < KS; i++)
+#pragma unroll
+                                    for (int z = 0; z < 2; z++) wild |= ((v[i][2 * x + z] >> (16 * k)) & 0x7C00u) == 0x7C00u;
+                                const uint32_t who = __ballot_sync(0xffffffffu, wild);
+                                for (int tt = 0; tt < 4 && who; tt++) {
+                                    if (!(who & (0x11111111u << tt))) continue;
+#pragma unroll
+                                    for (int q = 0; q < NT; q++) {
+                                        const float pa = __shfl_sync(0xffffffffu, sc[h][q][2 * x], 4 * (2 * tt + k) + t),
+                                                    pb = __shfl_sync(0xffffffffu, sc[h][q][2 * x + 1], 4 * (2 * tt + k) + t);
+#pragma unroll
+                                        for (int i = 0; i < KS; i++)
+#pragma unroll
+                                            for (int z = 0; z < 2; z++) {
+                                                const uint32_t w = __shfl_sync(0xffffffffu, v[i][2 * x + z], 4 * r + tt);
+                                                const float y = __half2float(__ushort_as_half((unsigned short)(w >> (16 * k))));
+                                                if (pa != 0.f) o[q][i][2 * z] = fmaf(pa, y, o[q][i][2 * z]);
+                                                if (pb != 0.f) o[q][i][2 * z + 1] = fmaf(pb, y, o[q][i][2 * z + 1]);
+                                            }
+                                    }
+                                    if (t == tt)
+#pragma unroll
+                                        for (int i = 0; i < KS; i++)
+#pragma unroll
+                                            for (int z = 0; z < 2; z++) v[i][2 * x + z] &= k ? 0x0000FFFFu : 0xFFFF0000u;
+                                }
+                            }
+                    }
+#pragma unroll
+                    for (int i = 0; i < KS; i++)
+#pragma unroll
+                        for (int q = 0; q < NT; q++) {
+                            mma16816(o[q][i], v[i], ph[h][q][0], ph[h][q][1]);
+                            mma16816(o[q][i], v[i], pl[h][q][0], pl[h][q][1]);
+                        }
+                }
+            }
+            // ---- this worker's part of the unit
+            const long long slot = ((long long)s * units + j + me) * min(srows, RU);
+#pragma unroll
+            for (int q = 0; q < NT; q++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) l[q][k] += __shfl_xor_sync(0xffffffffu, l[q][k], d);
+                    const int row = q * 8 + 2 * t + k;
+                    if (tile * RU + row >= srows) continue;
+                    float* dst = a.suffix_o + (slot + row) * p.hd + 8 * C * r;
+                    if (8 * C * r < p.hd)
+#pragma unroll
+                        for (int i = 0; i < KS; i += 2)
+                            *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[q][i][k], o[q][i][2 + k], o[q][i + 1][k], o[q][i + 1][2 + k]);
+                    if (r == 0) a.suffix_ml[slot + row] = make_float2(fmaxf(R[q][k] * qs[q][k], kLow), l[q][k]);
+                }
+            left -= count + kUnit;
+            if (left > 0) next(s, j, pc, np);
+        }
+    }
+    if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();   // (as the suffix kernel above)
+}
+
 // --------------------------------------------------------------- join --
 // One warp per (row, head): the prefix's parts, then the sequence's.  LP lanes
 // hold the hd values of a part, four each, and the warp's 32 / LP groups take
@@ -1034,7 +1430,7 @@ struct Plan {
     size_t off_pml, off_so, off_sml, off_starts, bytes;
 };
 
-Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
+Plan make_plan(const llm_pages* p, const llm_attend* a, int sms, bool q4) {
     Plan pl{};
     const int gq = a->n_heads / p->n_kv_heads;
     const long long srows = (long long)p->n_new * gq, rows = srows * p->n_seqs;
@@ -1051,7 +1447,7 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms) {
         const long long units = (long long)p->n_kv_heads * ((srows + ru - 1) / ru),
                         most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16 + kUnit),
                         blocks = (most + kQuantum * kSuffixWarps - 1) / (kQuantum * kSuffixWarps);
-        const int ctas = suffix_ctas(p->head_dim <= 64 ? 64 : 128, ru / 8);
+        const int hdp = p->head_dim <= 64 ? 64 : 128, ctas = q4 ? suffix_q4_ctas(hdp, ru / 8) : suffix_ctas(hdp, ru / 8);
         pl.suffix_blocks = (int)std::max<long long>(1, std::min<long long>(blocks, (long long)ctas * sms));
         pl.suffix_rows = (units * p->n_seqs + pl.suffix_blocks * kSuffixWarps) * std::min<long long>(srows, ru);
     }
@@ -1101,10 +1497,10 @@ cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensor
 }
 
 template <int HDP, int NT, bool SPLITQ>
-cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
+cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks, bool q4) {
     // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
     static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
-    auto k = suffix_kernel<HDP, NT, SPLITQ>;
+    auto k = q4 ? suffix_q4_kernel<HDP, NT, SPLITQ> : suffix_kernel<HDP, NT, SPLITQ>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(32 * kSuffixWarps);
@@ -1147,8 +1543,12 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
 
 }  // namespace
 
-int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit) {
-    int rc = check_pages(pages, true);
+namespace {
+
+// llm_attend_batch; q4: over pages of 4-bit values.
+int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit, bool q4) {
+    Q4Dev f{};
+    int rc = q4 ? check_pages_q4(pages, true, &f) : check_pages(pages, true);
     if (rc || (rc = check_attend(pages, a))) return rc;
     if (pages->n_seqs == 0) return LLM_OK;
     const long long rows = (long long)pages->n_seqs * pages->n_new, width = (long long)a->n_heads * pages->head_dim,
@@ -1161,7 +1561,7 @@ int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t strea
                    (rc = check_rows("prefix_v", a->prefix_v, LLM_F16, a->prefix_stride, kv, 2))))
         return rc;
     if (prefix && a->prefix_stride >= (1ll << 39)) return fail_op(LLM_ERR_UNSUPPORTED, "prefix_stride is too large");
-    const Plan pl = make_plan(pages, a, sm_count());
+    const Plan pl = make_plan(pages, a, sm_count(), q4);
     if (pl.bytes > 0 && (!a->workspace || !aligned(a->workspace, 256) || a->workspace_bytes < (int64_t)pl.bytes))
         return fail_op(LLM_ERR_INVALID_ARG, "workspace: NULL, not 256-byte aligned, or below %zu bytes", pl.bytes);
     const PagesDev pd = pages_dev(pages);
@@ -1184,6 +1584,7 @@ int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t strea
     ad.by_gq = Div((uint32_t)ad.gq);
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
+    ad.q4 = f;
     ad.timeout = timeout;
     ad.wait_limit = wait_limit > 0 ? wait_limit : kWaitLimit;
     const bool sq = !ad.q_f16;
@@ -1202,8 +1603,8 @@ int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t strea
     if (pl.suffix_blocks > 0) {
         const int first = prefix ? 0 : 1;
 #define LLM_SUFFIX(HDP, NT)                                                               \
-    (sq ? launch_suffix<HDP, NT, true>(stream, pd, ad, first, pl.suffix_blocks) \
-        : launch_suffix<HDP, NT, false>(stream, pd, ad, first, pl.suffix_blocks))
+    (sq ? launch_suffix<HDP, NT, true>(stream, pd, ad, first, pl.suffix_blocks, q4) \
+        : launch_suffix<HDP, NT, false>(stream, pd, ad, first, pl.suffix_blocks, q4))
         const bool eight = unit_rows(pages->n_new * ad.gq) == 8;
         e = hd <= 64 ? (eight ? LLM_SUFFIX(64, 1) : LLM_SUFFIX(64, 2)) : (eight ? LLM_SUFFIX(128, 1) : LLM_SUFFIX(128, 2));
 #undef LLM_SUFFIX
@@ -1216,16 +1617,29 @@ int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t strea
                     "llm_attend_batch (join)");
 }
 
+int64_t attend_workspace(const llm_pages* pages, const llm_attend* a, bool q4) {
+    Q4Dev f{};
+    int rc = q4 ? check_pages_q4(pages, false, &f) : check_pages(pages, false);
+    if (rc || (rc = check_attend(pages, a))) return rc;
+    return (int64_t)make_plan(pages, a, sm_count(), q4).bytes;
+}
+
+}  // namespace
+
+int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit) {
+    return attend(pages, a, stream, timeout, wait_limit, false);
+}
+
 }  // namespace llm
 
 using namespace llm;
 
-extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_attend* a) {
-    int rc = check_pages(pages, false);
-    if (rc || (rc = check_attend(pages, a))) return rc;
-    return (int64_t)make_plan(pages, a, sm_count()).bytes;
-}
+extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_attend* a) { return attend_workspace(pages, a, false); }
+extern "C" int64_t llm_attend_batch_q4_workspace(const llm_pages* pages, const llm_attend* a) { return attend_workspace(pages, a, true); }
 
 extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
     return attend_batch(pages, a, stream, nullptr, 0);
+}
+extern "C" int llm_attend_batch_q4(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
+    return attend(pages, a, stream, nullptr, 0, true);
 }

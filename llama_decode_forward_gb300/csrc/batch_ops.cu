@@ -23,6 +23,8 @@ struct AppendDev {
     void* q_out;
     long long q_out_stride;
     const float2* cs;
+    Q4Dev q4;                                // pages of 4-bit values
+    Div by_q4;                               // division by a head's runs of eight elements
 };
 
 // N (4 or 8) consecutive elements, as F32.
@@ -82,6 +84,101 @@ __device__ __forceinline__ Groups groups_of(int i, int half, int neox) {
     return neox ? Groups{N * i, half + N * i, N * i} : Groups{2 * N * i, 2 * N * i + N, N * i};
 }
 
+// One element turned: its pair's other one, and whether it is the first of the two.
+__device__ __forceinline__ float turned(float x, float other, float2 r, bool first) {
+    return first ? __fsub_rn(__fmul_rn(x, r.x), __fmul_rn(other, r.y)) : __fadd_rn(__fmul_rn(other, r.y), __fmul_rn(x, r.x));
+}
+
+// Run `item` of eight elements of a new row's k and v (all heads of k, then those of v)
+// into a page of 4-bit values.  Four threads hold a group of 32 elements (the last of a
+// head may be shorter); they share its least and its largest value by two shuffles.  The
+// whole block calls this, with one row.
+template <class T>
+__device__ __forceinline__ void append_q4(const PagesDev& p, const AppendDev& a, int row, int item) {
+    const int h = a.by_q4.of(item), i = item - h * (4 * a.q4.groups);
+    const bool live = h < 2 * p.n_kv && 8 * i < p.hd, is_v = h >= p.n_kv;
+    const int g = is_v ? h - p.n_kv : h, d0 = 8 * i, half = is_v ? 0 : a.half;
+    const T* x = is_v ? static_cast<const T*>(a.v) + row * a.v_stride : static_cast<const T*>(a.k) + row * a.k_stride;
+    x += g * p.hd;
+    const bool turns = d0 < 2 * half, fast = a.neox ? a.group == 8 : a.group >= 4;
+    float u[8], other[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) u[k] = 0.f;
+    if (live) {
+        load_n<8>(x + d0, u);
+        if (turns && fast && a.neox) load_n<8>(x + (d0 < half ? d0 + half : d0 - half), other);
+    }
+    const int s = a.by_new.of(row), len = p.lens[s], behind = p.n_new - (row - s * p.n_new);
+    if (len < behind) return;                // padding (the whole block: one row)
+    const int e = len - behind;
+    const long long pos = (long long)p.prefix_len + e;
+    if (pos >= a.table_rows && a.half > 0) {
+        flag(p.err, LLM_PAGES_BAD_LEN);
+        return;
+    }
+    const int page = page_of(p, s, e);
+    if (page < 0) return;
+    const float2* cs = a.cs + pos * a.half;
+    if (live && turns) {
+        if (fast && a.neox) {
+            const bool first = d0 < half;
+            const int j = first ? d0 : d0 - half;
+#pragma unroll
+            for (int k = 0; k < 8; k += 2) {
+                const float4 r = __ldg(reinterpret_cast<const float4*>(cs + j + k));
+                u[k] = turned(u[k], other[k], make_float2(r.x, r.y), first);
+                u[k + 1] = turned(u[k + 1], other[k + 1], make_float2(r.z, r.w), first);
+            }
+        } else if (fast) {
+#pragma unroll
+            for (int k = 0; k < 8; k += 4) {
+                const float4 r = __ldg(reinterpret_cast<const float4*>(cs + (d0 + k) / 2));
+                turn(u[k], u[k + 1], make_float2(r.x, r.y));
+                turn(u[k + 2], u[k + 3], make_float2(r.z, r.w));
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const int d = d0 + k;
+                if (d >= 2 * half) continue;
+                const bool first = a.neox ? d < half : d % 2 == 0;
+                const int j = a.neox ? (first ? d : d - half) : d / 2, o = a.neox ? (first ? d + half : d - half) : d ^ 1;
+                u[k] = turned(u[k], to_f32(x[o]), cs[j], first);
+            }
+        }
+    }
+    float low = INFINITY, high = -INFINITY;
+    bool wild = false;
+    if (live) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            low = fminf(low, u[k]);
+            high = fmaxf(high, u[k]);
+            wild |= !(fabsf(u[k]) < INFINITY);
+        }
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        wild |= __shfl_xor_sync(0xffffffffu, (int)wild, o) != 0;
+    }
+    if (!live) return;
+    __half d = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f)), m = __float2half_rn(low);
+    wild |= __hisinf(d) || __hisinf(m);
+    if (wild) d = m = __ushort_as_half(0x7FFFu);                 // NaN: so is each value of the group
+    const float df = __half2float(d), mf = __half2float(m);
+    uint32_t w = 0;
+    if (!wild && df > 0.f) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(u[k], mf), df)), 0.f), 15.f) << (4 * k);
+    }
+    uint8_t* pages = reinterpret_cast<uint8_t*>(is_v ? p.v : p.k);
+    const int in = e & ((1 << p.page_shift) - 1);
+    *reinterpret_cast<uint32_t*>(pages + q4_numbers(p, a.q4, page, g, in) + 4 * i) = w;
+    if (i % 4 == 0) *reinterpret_cast<uint32_t*>(pages + q4_pairs(p, a.q4, page, g, in) + i) = h2_bits(d, m);
+}
+
 // One thread per item of a head of q, k or v; a row has blocks of its own for q and
 // for k and v, so its sequence, place and angles are the block's.  The elements are
 // loaded before the row's place is known: the chain length -> page -> store runs
@@ -92,13 +189,18 @@ __device__ __forceinline__ Groups groups_of(int i, int half, int neox) {
 // 26.4 us with groups of four.
 constexpr int kAppendThreads = 128;
 constexpr int append_item(int n) { return n ? 2 * n : 8; }
-template <class T, class U, int N>
+// Q4: k and v go into pages of 4-bit values, in items of eight elements.
+template <class T, class U, int N, bool Q4>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ PagesDev p,
                                                                 const __grid_constant__ AppendDev a) {
     griddep_entry();
     const int row = a.by_row_blocks.of(blockIdx.x), block = blockIdx.x - row * a.row_blocks, per_head = p.hd / append_item(N);
     const bool is_q = block < a.q_blocks;
     const int item = (is_q ? block : block - a.q_blocks) * kAppendThreads + (int)threadIdx.x;
+    if (Q4 && !is_q) {
+        append_q4<T>(p, a, row, item);
+        return;
+    }
     const int h = a.by_head.of(item), i = item - h * per_head;
     if (h >= (is_q ? a.n_heads : 2 * p.n_kv)) return;
     const bool is_v = !is_q && h >= p.n_kv;
@@ -171,10 +273,51 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
 }
 
-template <class T, class U>
+template <class T, class U, bool Q4>
 cudaError_t launch_append(cudaStream_t st, const PagesDev& pd, const AppendDev& ad, long long rows) {
-    auto k = ad.group == 8 ? append_kernel<T, U, 8> : ad.group == 4 ? append_kernel<T, U, 4> : append_kernel<T, U, 0>;
+    auto k = ad.group == 8 ? append_kernel<T, U, 8, Q4> : ad.group == 4 ? append_kernel<T, U, 4, Q4> : append_kernel<T, U, 0, Q4>;
     return launch_dep(k, dim3((unsigned)(rows * ad.row_blocks)), dim3(kAppendThreads), 0, st, pd, ad);
+}
+
+// --------------------------------------------------------------- read --
+// The values of the new rows' k and v: one thread per eight elements.  Bound by the
+// stream of rows.
+struct ReadDev {
+    void *k, *v;
+    long long k_stride, v_stride;
+    int row_blocks;
+    Div by_row_blocks, by_head, by_new;      // by row_blocks, a head's runs of eight elements, n_new
+    Q4Dev q4;
+};
+
+// The eight values that a word of numbers stands for with the pair d, m: the F16 nearest to d n + m.
+__device__ __forceinline__ void q4_values(uint32_t w, uint32_t pair, float (&x)[8]) {
+    const __half2 dm = *reinterpret_cast<const __half2*>(&pair);
+#pragma unroll
+    for (int k = 0; k < 8; k++) x[k] = __half2float(__hfma(__uint2half_rn((w >> (4 * k)) & 15u), __low2half(dm), __high2half(dm)));
+}
+
+template <class U, bool Q4>
+__global__ void __launch_bounds__(kAppendThreads) read_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ ReadDev a) {
+    griddep_entry();
+    const int row = a.by_row_blocks.of(blockIdx.x), item = (blockIdx.x - row * a.row_blocks) * kAppendThreads + (int)threadIdx.x;
+    const int h = a.by_head.of(item), i = item - h * (p.hd / 8);
+    if (h >= 2 * p.n_kv) return;
+    const bool is_v = h >= p.n_kv;
+    const int g = is_v ? h - p.n_kv : h, s = a.by_new.of(row), len = p.lens[s], behind = p.n_new - (row - s * p.n_new);
+    if (len < behind) return;                // padding
+    const int e = len - behind, page = page_of(p, s, e);
+    if (page < 0) return;
+    const int in = e & ((1 << p.page_shift) - 1);
+    float x[8];
+    if (Q4) {
+        const uint8_t* pages = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k);
+        q4_values(*reinterpret_cast<const uint32_t*>(pages + q4_numbers(p, a.q4, page, g, in) + 4 * i),
+                  *reinterpret_cast<const uint32_t*>(pages + q4_pairs(p, a.q4, page, g, in) + 4 * (i / 4)), x);
+    } else {
+        load_n<8>((is_v ? p.v : p.k) + ((((long long)page << p.page_shift) + in) * p.n_kv + g) * p.hd + 8 * i, x);
+    }
+    store_n<8>(static_cast<U*>(is_v ? a.v : a.k) + row * (is_v ? a.v_stride : a.k_stride) + g * p.hd + 8 * i, x);
 }
 
 // --------------------------------------------------- log probabilities --
@@ -659,8 +802,13 @@ extern "C" int llm_rope_table(float* cos_sin, int32_t pos0, int32_t n_pos, int32
     return launched(rope_table(stream, cos_sin, n_pos, pos0, rope_dims, rope_theta_scale(rope_base, rope_dims), rope_freqs), "llm_rope_table");
 }
 
-extern "C" int llm_kv_append(const llm_pages* pages, const llm_append* a, llm_stream_t stream) {
-    int rc = check_pages(pages, true);
+namespace llm {
+namespace {
+
+// llm_kv_append; q4: into pages of 4-bit values.
+int append(const llm_pages* pages, const llm_append* a, bool q4, llm_stream_t stream) {
+    Q4Dev f{};
+    int rc = q4 ? check_pages_q4(pages, true, &f) : check_pages(pages, true);
     if (rc) return rc;
     if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the append arguments are NULL");
     if (a->n_heads < 0 || a->table_rows < 0) return fail_op(LLM_ERR_INVALID_ARG, "n_heads or table_rows is negative");
@@ -681,16 +829,54 @@ extern "C" int llm_kv_append(const llm_pages* pages, const llm_append* a, llm_st
     const PagesDev pd = pages_dev(pages);
     const int half = a->rope_dims / 2, group = pages->head_dim % 16 == 0 && half % 8 == 0 ? 8 : half % 4 == 0 ? 4 : 0;
     const long long per_head = pages->head_dim / append_item(group), q_blocks = (a->n_heads * per_head + kAppendThreads - 1) / kAppendThreads,
-                    row_blocks = q_blocks + (2 * pages->n_kv_heads * per_head + kAppendThreads - 1) / kAppendThreads;
+                    kv_items = 2ll * pages->n_kv_heads * (q4 ? 4 * f.groups : per_head),
+                    row_blocks = q_blocks + (kv_items + kAppendThreads - 1) / kAppendThreads;
     if (qw > INT_MAX || rows * row_blocks > INT_MAX)
         return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^31 blocks of %d threads", kAppendThreads);
     const AppendDev ad{a->n_heads, half, a->rope_neox, a->table_rows, group, (int)q_blocks, (int)row_blocks,
                        Div((uint32_t)row_blocks), Div((uint32_t)per_head), Div((uint32_t)pages->n_new), a->q, a->k, a->v, a->q_stride,
-                       a->k_stride, a->v_stride, a->q_out, a->q_out_stride, reinterpret_cast<const float2*>(a->cos_sin)};
+                       a->k_stride, a->v_stride, a->q_out, a->q_out_stride, reinterpret_cast<const float2*>(a->cos_sin), f,
+                       Div((uint32_t)(q4 ? 4 * f.groups : 1))};
     const bool h = a->dtype == LLM_F16, qh = a->n_heads > 0 && a->q_out_dtype == LLM_F16;
-    return launched(h ? (qh ? launch_append<__half, __half>(stream, pd, ad, rows) : launch_append<__half, float>(stream, pd, ad, rows))
-                      : (qh ? launch_append<float, __half>(stream, pd, ad, rows) : launch_append<float, float>(stream, pd, ad, rows)),
-                    "llm_kv_append");
+#define LLM_APPEND(T, U) (q4 ? launch_append<T, U, true>(stream, pd, ad, rows) : launch_append<T, U, false>(stream, pd, ad, rows))
+    return launched(h ? (qh ? LLM_APPEND(__half, __half) : LLM_APPEND(__half, float)) : (qh ? LLM_APPEND(float, __half) : LLM_APPEND(float, float)),
+                    q4 ? "llm_kv_append_q4" : "llm_kv_append");
+#undef LLM_APPEND
+}
+
+// llm_kv_read; q4: from pages of 4-bit values.
+int read_rows(const llm_pages* pages, const llm_read* a, bool q4, llm_stream_t stream) {
+    Q4Dev f{};
+    int rc = q4 ? check_pages_q4(pages, true, &f) : check_pages(pages, true);
+    if (rc) return rc;
+    if (!a) return fail_op(LLM_ERR_INVALID_ARG, "the read arguments are NULL");
+    if (pages->n_seqs == 0) return LLM_OK;
+    const long long rows = (long long)pages->n_seqs * pages->n_new, kv = (long long)pages->n_kv_heads * pages->head_dim;
+    if ((rc = check_rows("k_out", a->k_out, a->dtype, a->k_stride, kv, rows)) || (rc = check_rows("v_out", a->v_out, a->dtype, a->v_stride, kv, rows)))
+        return rc;
+    const long long row_blocks = (2 * kv / 8 + kAppendThreads - 1) / kAppendThreads;
+    if (rows * row_blocks > INT_MAX) return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^31 blocks of %d threads", kAppendThreads);
+    const PagesDev pd = pages_dev(pages);
+    const ReadDev rd{a->k_out, a->v_out, a->k_stride, a->v_stride, (int)row_blocks, Div((uint32_t)row_blocks), Div((uint32_t)(pages->head_dim / 8)),
+                     Div((uint32_t)pages->n_new), f};
+    const bool h = a->dtype == LLM_F16;
+    auto k = q4 ? (h ? read_kernel<__half, true> : read_kernel<float, true>) : (h ? read_kernel<__half, false> : read_kernel<float, false>);
+    return launched(launch_dep(k, dim3((unsigned)(rows * row_blocks)), dim3(kAppendThreads), 0, stream, pd, rd), q4 ? "llm_kv_read_q4" : "llm_kv_read");
+}
+
+}  // namespace
+}  // namespace llm
+
+extern "C" int llm_kv_append(const llm_pages* pages, const llm_append* a, llm_stream_t stream) { return append(pages, a, false, stream); }
+extern "C" int llm_kv_append_q4(const llm_pages* pages, const llm_append* a, llm_stream_t stream) { return append(pages, a, true, stream); }
+extern "C" int llm_kv_read(const llm_pages* pages, const llm_read* a, llm_stream_t stream) { return read_rows(pages, a, false, stream); }
+extern "C" int llm_kv_read_q4(const llm_pages* pages, const llm_read* a, llm_stream_t stream) { return read_rows(pages, a, true, stream); }
+
+extern "C" int64_t llm_q4_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_dim) {
+    const llm_pages p{0, 1, 0, page_size, 0, 0, n_kv_heads, head_dim, nullptr, nullptr, nullptr, nullptr, nullptr};
+    Q4Dev f{};
+    const int rc = check_pages_q4(&p, false, &f);
+    return rc ? rc : f.page_bytes;
 }
 
 extern "C" int llm_logprobs(const llm_logprobs_args* a, llm_stream_t stream) {

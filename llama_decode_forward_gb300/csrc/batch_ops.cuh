@@ -23,9 +23,8 @@ __device__ __forceinline__ void flag(int* err, int bit) {
     if (err) atomicOr(err, bit);
 }
 
-// First row (of the pool's n_pages * page_size rows) and validity of the page
-// that holds row e >= 0 of sequence s; a bad place is flagged and gives -1.
-__device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
+// The page that holds row e >= 0 of sequence s; a bad place is flagged and gives -1.
+__device__ __forceinline__ int page_of(const PagesDev& p, int s, int e) {
     const int i = e >> p.page_shift;
     if (i >= p.max_pages) {
         flag(p.err, LLM_PAGES_BAD_LEN);
@@ -36,7 +35,28 @@ __device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
         flag(p.err, LLM_PAGES_BAD_PAGE);
         return -1;
     }
-    return ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
+    return page;
+}
+// Its row of the pool's n_pages * page_size rows, or -1.
+__device__ __forceinline__ long long page_row(const PagesDev& p, int s, int e) {
+    const int page = page_of(p, s, e);
+    return page < 0 ? -1 : ((long long)page << p.page_shift) + (e & ((1 << p.page_shift) - 1));
+}
+
+// Pages of 4-bit values (include/llm.h): [n_kv][page_size][hd / 2] bytes of numbers, then
+// [n_kv][page_size][groups] pairs d, m, in whole words of 16 bytes.
+struct Q4Dev {
+    int groups;                              // of a head's row
+    long long page_bytes, scales;            // bytes of a page, and where its pairs begin
+};
+constexpr int kQ4Group = 32;
+
+// Byte offsets of a row's numbers and of its pairs: row `in` (of the page) of kv head g.
+__device__ __forceinline__ long long q4_numbers(const PagesDev& p, const Q4Dev& f, int page, int g, int in) {
+    return page * f.page_bytes + ((long long)(g << p.page_shift) + in) * (p.hd / 2);
+}
+__device__ __forceinline__ long long q4_pairs(const PagesDev& p, const Q4Dev& f, int page, int g, int in) {
+    return page * f.page_bytes + f.scales + ((long long)(g << p.page_shift) + in) * (4 * f.groups);
 }
 
 // Division of numbers below 2^31 by a fixed one (Granlund and Montgomery, "Division by
@@ -91,6 +111,20 @@ inline int check_pages(const llm_pages* p, bool pointers) {
     if (!aligned(p->k_pages, 16) || !aligned(p->v_pages, 16) || !aligned(p->page_table, 4) || !aligned(p->lens, 4) ||
         !aligned(p->err, 4))
         return fail_op(LLM_ERR_INVALID_ARG, "a pointer of the pages is not aligned");
+    return LLM_OK;
+}
+
+// The same for pages of 4-bit values, and their layout.
+inline int check_pages_q4(const llm_pages* p, bool pointers, Q4Dev* f) {
+    const int rc = check_pages(p, pointers);
+    if (rc) return rc;
+    if (p->head_dim % 16) return fail_op(LLM_ERR_UNSUPPORTED, "pages of 4-bit values: head_dim %d is not a multiple of 16", p->head_dim);
+    if (p->page_size < 8) return fail_op(LLM_ERR_UNSUPPORTED, "pages of 4-bit values: page_size %d is below 8", p->page_size);
+    const long long rows = (long long)p->page_size * p->n_kv_heads;
+    if (rows > INT_MAX / 64) return fail_op(LLM_ERR_UNSUPPORTED, "a page of 4-bit values has more than 2^25 rows of all heads");
+    f->groups = (p->head_dim + kQ4Group - 1) / kQ4Group;
+    f->scales = rows * (p->head_dim / 2);
+    f->page_bytes = (f->scales + rows * 4 * f->groups + 15) / 16 * 16;
     return LLM_OK;
 }
 
