@@ -40,6 +40,7 @@ struct AttendDev {
     float2* suffix_ml;
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
     int prefix_blocks, suffix_workers;
+    int unit_rows;                          // query rows of a unit of the pages' kernel
     Div by_heads, by_new, by_gq;            // the join's divisions
     Q4Dev q4;                               // pages of 4-bit values
     int* timeout;                   // a handle's word for waits that gave up, or nullptr
@@ -919,7 +920,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 }
 
 // ---------------------------------------------- suffix, 4-bit pages --
-// The suffix kernel for pages of 4-bit values: the same units, pieces, deal and parts.
+// The suffix kernel for pages of 4-bit values: the same pieces, deal and parts.
 // A value is made where it is used: numbers become F16 by their bits (0x6400 | n is
 // 1024 + n, 0x6400 | 16 n is 1024 + 16 n; one exact operation takes the 1024 away) and
 // one fused multiply-add rounds d n + m to the F16 that it stands for.
@@ -927,34 +928,47 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 //   cached rows r and r + 8, two words of numbers.  Their half-words pair dims 0 and 4, 1
 //   and 5, ... of a word, so q is loaded in that order.
 // - V^T is the other product's first operand, and needs pairs of cached rows: lane (r, t)
-//   loads dims 8 V r .. of rows 2t, 2t + 1 (and those eight behind), and a byte permutation
+//   loads dims 8 C r .. of rows 2t, 2t + 1 (and those eight behind), and a byte permutation
 //   joins the two rows' numbers, so no transpose is needed.  An MMA's rows r and r + 8 are
-//   dims 8 V r + 2 i and + 1.
-// A step is H pieces (32 cached rows for heads of up to 64 values: half of the bytes and
-// of the maxima's exchanges for each), requested while the one before is multiplied.
-// Eight rows in a row lie in one page (page_size >= 8): an octet.
-__host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? 4 : 3) : (nt == 1 ? 3 : 2); }
+//   dims 8 C r + 2 i and + 1.
+// A step is H pieces.  Eight rows in a row lie in one page (page_size >= 8): an octet.  The
+// next step's K is requested as soon as the scores have used this one's, its V behind the
+// sums, into the same registers.
+// PACK: up to four query rows.  The eight columns of a product hold each of them twice;
+// the second four take the probabilities' second parts, so one product adds both.
+// FULL: head_dim is HDP, so that the distances of rows and pairs are constants.
+constexpr int kCtas64 = 4, kCtas128 = 4, kPieces128 = 1;
+__host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? kCtas64 : nt == 2 ? 3 : 2) : (nt == 1 ? kCtas128 : 2); }
 
-// Four pairs of numbers of a word, as F16 pairs: (x & 15, (x >> 16) & 15) and so on.
-__device__ __forceinline__ __half2 q4_low(uint32_t x) {            // numbers at bits 0 and 16
-    const uint32_t y = (x & 0x000F000Fu) | 0x64006400u;
-    return __hsub2(*reinterpret_cast<const __half2*>(&y), __float2half2_rn(1024.f));
+// Query rows of a unit: more than 16 are taken at once (up to 24, where the registers allow) as
+// long as one unit then does, since every unit makes the values anew.
+__host__ __device__ constexpr int unit_rows_q4(int srows, int hd) { return srows <= 8 ? 8 : srows > 16 && srows <= 24 && hd <= 64 ? 24 : 16; }
+
+// Pairs of numbers of a word, as F16 pairs.  (x & m | c in one instruction: left to itself the compiler takes
+// two, each with a constant of its own; a step of 32 rows then had 145 logical operations, of 777.)
+__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(m), "r"(c));
+    return y;
 }
-__device__ __forceinline__ __half2 q4_high(uint32_t x) {           // numbers at bits 4 and 20
-    const uint32_t y = (x & 0x00F000F0u) | 0x64006400u;
-    return __hfma2(*reinterpret_cast<const __half2*>(&y), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+__device__ __forceinline__ __half2 q4_low(uint32_t x, uint32_t c) {            // numbers at bits 0 and 16
+    return __hsub2(half2_of(and_or(x, 0x000F000Fu, c)), __float2half2_rn(1024.f));
+}
+__device__ __forceinline__ __half2 q4_high(uint32_t x, uint32_t c) {           // numbers at bits 4 and 20
+    return __hfma2(half2_of(and_or(x, 0x00F000F0u, c)), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
 }
 __device__ __forceinline__ uint32_t q4_value(__half2 n, __half2 d, __half2 m) {
     const __half2 v = __hfma2(n, d, m);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
-__device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 
-template <int HDP, int NT, bool SPLITQ>
+template <int HDP, int NT, bool SPLITQ, bool PACK, bool FULL>
 __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
     suffix_q4_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
-    constexpr int C = HDP / 64, KS = HDP / 16, RU = 8 * NT;  // chunks of 64 dims, MMA steps of a dot product (and MMA tiles of the sums)
-    constexpr int H = HDP == 64 ? 2 : 1, OCT = 2 * H;        // pieces and octets of a step
+    static_assert(!PACK || NT == 1, "four query rows");
+    constexpr int C = HDP / 64, KS = HDP / 16, RU = 8 * NT;  // chunks of 64 dims; MMA steps of a dot product, and MMA tiles of the sums
+    constexpr int H = HDP == 64 ? 2 : kPieces128, OCT = 2 * H;   // pieces and octets of a step
     extern __shared__ int seqs[];
     if (first) griddep_wait();
     griddep_launch();
@@ -973,30 +987,45 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             ((long long)starts[mid] * units <= x0 ? lo : hi) = mid;
             s = lo;
         }
-        auto next = [&](int& s, int& j, int& pc, int& np) {      // the unit behind one, at its first piece
+        // the unit behind one (row tile `tile` of kv head g of sequence s), at its first piece
+        auto next = [&](int& s, int& g, int& tile, int& pc, int& np) {
             pc = 0;
-            if (++j < units) return;
-            j = 0;
+            if (++tile < rt) return;
+            tile = 0;
+            if (++g < p.n_kv) return;
+            g = 0;
             do s++;
             while (lens[s] == 0);
             np = (lens[s] + 15) / 16;
         };
         int np = (lens[s] + 15) / 16;
         const long long in_seq = x0 - (long long)starts[s] * units;
-        int j = (int)(in_seq / (np + kUnit)), pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
+        const int j0 = (int)(in_seq / (np + kUnit));
+        int g = j0 / rt, tile = j0 % rt, pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
         if (pc >= np) {                      // it starts with empty pieces
             left -= np + kUnit - pc;
-            if (left > 0) next(s, j, pc, np);
+            if (left > 0) next(s, g, tile, pc, np);
         }
-        const int r = lane >> 2, t = lane & 3, pitch = p.hd / 2, pairs = 4 * a.q4.groups;
-        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k), *vp = reinterpret_cast<const uint8_t*>(p.v);
+        const int r = lane >> 2, t = lane & 3;
+        const uint32_t pitch = (FULL ? HDP : (uint32_t)p.hd) / 2, pairs = FULL ? HDP / 8 : 4u * a.q4.groups, page_bytes = (uint32_t)a.q4.page_bytes,
+                       mask = (1u << p.page_shift) - 1;
+        // this lane's places among the rows of an octet of page 0
+        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k) + r * pitch + 8 * t,
+                      *kdp = reinterpret_cast<const uint8_t*>(p.k) + a.q4.scales + r * pairs + 4 * (t >> 1),
+                      *vp = reinterpret_cast<const uint8_t*>(p.v) + 2 * t * pitch + 4 * C * r,
+                      *vdp = reinterpret_cast<const uint8_t*>(p.v) + a.q4.scales + 2 * t * pairs + 4 * (C * r >> 2);
+        const bool k_in[2] = {FULL || 16 * t < p.hd, FULL || 64 + 16 * t < p.hd}, v_in = FULL || 8 * C * r < p.hd;
+        const float second = t >= 2 ? -1.f : 0.f;                // PACK: which part of the probabilities this lane's columns take
+        uint32_t k1024;                      // (a register: see and_or)
+        asm volatile("mov.u32 %0, 0x64006400;" : "=r"(k1024));
 
-        // octet lane % OCT's page of the step that is loaded next; -1: nothing to read
-        int ls = s, lj = j, lpc = pc, lnp = np, lleft = left, page = -1;
+        // the step that is loaded next: octet lane % OCT's page (-1: nothing to read there), looked up ahead
+        int ls = s, lg = g, ltile = tile, lpc = pc, lnp = np, lleft = left, page = -1, lend = 0;
         auto look = [&]() {
-            const int e = lpc * 16 + 8 * (lane % OCT), end = min(lens[ls], 16 * (lpc + min(lleft, H)));
+            const int e = lpc * 16 + 8 * (lane % OCT);
+            lend = min(lens[ls], 16 * (lpc + min(lleft, H)));
             page = -1;
-            if (e < end) {
+            if (e < lend) {
                 page = p.table[(long long)ls * p.max_pages + (e >> p.page_shift)];
                 if (page < 0 || page >= p.n_pages) {
                     flag(p.err, LLM_PAGES_BAD_PAGE);
@@ -1004,43 +1033,99 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                 }
             }
         };
-        uint32_t kw[OCT][2 * C], kd[OCT][C], vw[OCT][2][C], vd[OCT][2];      // numbers and pairs of the step on its way
-        uint32_t there_x;                    // bit o: this lane's row r of octet o is there
-        auto load = [&]() {                  // requests the step, moves on and looks the next one up
-            const int e0 = lpc * 16, end = min(lens[ls], 16 * (lpc + min(lleft, H))), g = lj / rt;
-            there_x = 0;
+        uint32_t kw[OCT][2 * C], kd[OCT][C], vw[OCT][2][C], vd[OCT][2];      // numbers and pairs
+#pragma unroll
+        for (int o = 0; o < OCT; o++) {
+#pragma unroll
+            for (int c = 0; c < C; c++) kw[o][2 * c] = kw[o][2 * c + 1] = kd[o][c] = vw[o][0][c] = vw[o][1][c] = 0;
+            vd[o][0] = vd[o][1] = 0;
+        }
+        uint32_t there = 0;                  // bit o: this lane's row r of octet o is there (K)
+        bool whole = false;                  // all rows of the step are
+        // row e's place in page pg, from a lane's place in page 0
+        auto place = [&](const uint8_t* lane_at, int pg, int e, uint32_t row_bytes) {
+            const uint32_t row = (uint32_t)(lg << p.page_shift) + ((uint32_t)e & mask);
+            return lane_at + (unsigned long long)(uint32_t)pg * page_bytes + (unsigned long long)row * row_bytes;
+        };
+        auto load_k = [&]() {
+            const int e0 = lpc * 16;
+            whole = e0 + 16 * H <= lend && __all_sync(0xffffffffu, page >= 0);
+            if (whole && p.page_shift >= 4) {            // a page for each sixteen rows
+                there = 0xFFFFFFFFu;
+                const uint8_t *w[H], *d[H];
+#pragma unroll
+                for (int h = 0; h < H; h++) {
+                    const int pg = __shfl_sync(0xffffffffu, page, 2 * h);
+                    w[h] = place(kp, pg, e0 + 16 * h, pitch);
+                    d[h] = place(kdp, pg, e0 + 16 * h, pairs);
+                }
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    if (k_in[c])
+#pragma unroll
+                        for (int o = 0; o < OCT; o++) {
+                            const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w[o / 2] + o % 2 * (8 * pitch) + 32 * c));
+                            kw[o][2 * c] = x.x;
+                            kw[o][2 * c + 1] = x.y;
+                            kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(d[o / 2] + o % 2 * (8 * pairs) + 8 * c));
+                        }
+                return;
+            }
+            there = 0;
 #pragma unroll
             for (int o = 0; o < OCT; o++) {
-                const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o, in = e & ((1 << p.page_shift) - 1);
-                const long long numbers = q4_numbers(p, a.q4, pg, g, in), dm = q4_pairs(p, a.q4, pg, g, in);
-                const bool kr = pg >= 0 && e + r < end;
-                there_x |= kr ? 1u << o : 0u;
+                const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o;
+                const bool in = pg >= 0 && e + r < lend;
+                if (in) there |= 1u << o;
+                const uint8_t *w = place(kp, pg, e, pitch), *d = place(kdp, pg, e, pairs);
 #pragma unroll
                 for (int c = 0; c < C; c++) {
                     kw[o][2 * c] = kw[o][2 * c + 1] = kd[o][c] = 0;
-                    if (kr && 64 * c + 16 * t < p.hd) {
-                        const uint2 w = __ldcs(reinterpret_cast<const uint2*>(kp + numbers + r * pitch + 32 * c + 8 * t));
-                        kw[o][2 * c] = w.x;
-                        kw[o][2 * c + 1] = w.y;
-                        kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(kp + dm + r * pairs + 4 * (2 * c + (t >> 1))));
+                    if (in && k_in[c]) {
+                        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w + 32 * c));
+                        kw[o][2 * c] = x.x;
+                        kw[o][2 * c + 1] = x.y;
+                        kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(d + 8 * c));
                     }
                 }
+            }
+        };
+        auto load_v = [&]() {                // then moves on and looks the next step up
+            const int e0 = lpc * 16;
+            auto one = [&](int o, int k, const uint8_t* w, const uint8_t* d) {
+                if (C == 1) {
+                    vw[o][k][0] = __ldcs(reinterpret_cast<const uint32_t*>(w));
+                } else {
+                    const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w));
+                    vw[o][k][0] = x.x;
+                    vw[o][k][C - 1] = x.y;
+                }
+                vd[o][k] = __ldcs(reinterpret_cast<const uint32_t*>(d));
+            };
+            if (whole && p.page_shift >= 4) {
+                const uint8_t *w[H], *d[H];
 #pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    const int row = 2 * t + k;
+                for (int h = 0; h < H; h++) {
+                    const int pg = __shfl_sync(0xffffffffu, page, 2 * h);
+                    w[h] = place(vp, pg, e0 + 16 * h, pitch);
+                    d[h] = place(vdp, pg, e0 + 16 * h, pairs);
+                }
+                if (v_in)
 #pragma unroll
-                    for (int c = 0; c < C; c++) vw[o][k][c] = 0;
-                    vd[o][k] = 0;
-                    if (pg >= 0 && e + row < end && 8 * C * r < p.hd) {
-                        const uint8_t* w = vp + numbers + row * pitch + 4 * C * r;
-                        if (C == 1) {
-                            vw[o][k][0] = __ldcs(reinterpret_cast<const uint32_t*>(w));
-                        } else {
-                            const uint2 y = __ldcs(reinterpret_cast<const uint2*>(w));
-                            vw[o][k][0] = y.x;
-                            vw[o][k][C - 1] = y.y;
-                        }
-                        vd[o][k] = __ldcs(reinterpret_cast<const uint32_t*>(vp + dm + row * pairs + 4 * (C * r >> 2)));
+                    for (int o = 0; o < OCT; o++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++) one(o, k, w[o / 2] + (o % 2 * 8 + k) * pitch, d[o / 2] + (o % 2 * 8 + k) * pairs);
+            } else {
+#pragma unroll
+                for (int o = 0; o < OCT; o++) {
+                    const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o;
+                    const uint8_t *w = place(vp, pg, e, pitch), *d = place(vdp, pg, e, pairs);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+#pragma unroll
+                        for (int c = 0; c < C; c++) vw[o][k][c] = 0;
+                        vd[o][k] = 0;
+                        if (v_in && pg >= 0 && e + 2 * t + k < lend) one(o, k, w + k * pitch, d + k * pairs);
                     }
                 }
             }
@@ -1049,17 +1134,18 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             lpc += n;
             if (lpc == lnp) {
                 lleft -= kUnit;
-                if (lleft > 0) next(ls, lj, lpc, lnp);
+                if (lleft > 0) next(ls, lg, ltile, lpc, lnp);
             }
             if (lleft > 0) look();
         };
         if (left > 0) {
             look();
-            load();
+            load_k();
+            load_v();
         }
         while (left > 0) {
             // ---- one unit: pieces pc .. of its np, as far as this worker goes
-            const int tile = j % rt, g = j / rt, count = min(left, np - pc);
+            const int count = min(left, np - pc);
             const int last = p.lens[s] - p.n_new, e_min = last + tile * RU / a.gq;
             // q as the second operand: query row r of each eight; rows behind the last repeat it (never stored)
             uint32_t qhi[NT][KS][2], qlo[NT][SPLITQ ? KS : 1][2];
@@ -1067,9 +1153,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             float qs[NT][2];                 // and the factor of their scores
 #pragma unroll
             for (int q = 0; q < NT; q++) {
-                const long long at = q_offset(a, p.hd, g, s * srows + min(tile * RU + q * 8 + r, srows - 1));
+                const long long at = q_offset(a, p.hd, g, s * srows + min(tile * RU + q * 8 + (PACK ? r & 3 : r), srows - 1));
 #pragma unroll
-                for (int k = 0; k < 2; k++) e[q][k] = last + min(tile * RU + q * 8 + 2 * t + k, srows - 1) / a.gq;
+                for (int k = 0; k < 2; k++) e[q][k] = last + min(tile * RU + q * 8 + (PACK ? (2 * t + k) & 3 : 2 * t + k), srows - 1) / a.gq;
                 float up = 1.f;
                 qs[q][0] = qs[q][1] = a.sc;
                 if (SPLITQ) {
@@ -1114,22 +1200,6 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                 l[q][0] = l[q][1] = 0.f;
             }
             for (int i0 = 0; i0 < count; i0 += H) {
-                uint32_t k_w[OCT][2 * C], k_d[OCT][C], v_w[OCT][2][C], v_d[OCT][2];
-#pragma unroll
-                for (int oc = 0; oc < OCT; oc++) {
-#pragma unroll
-                    for (int c = 0; c < C; c++) {
-                        k_w[oc][2 * c] = kw[oc][2 * c];
-                        k_w[oc][2 * c + 1] = kw[oc][2 * c + 1];
-                        k_d[oc][c] = kd[oc][c];
-                        v_w[oc][0][c] = vw[oc][0][c];
-                        v_w[oc][1][c] = vw[oc][1][c];
-                    }
-                    v_d[oc][0] = vd[oc][0];
-                    v_d[oc][1] = vd[oc][1];
-                }
-                const uint32_t there = there_x;
-                if (lleft > 0) load();
                 // ---- scores
                 float sc[H][NT][4];
 #pragma unroll
@@ -1141,19 +1211,19 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                         __half2 d[2], m[2];
 #pragma unroll
                         for (int x = 0; x < 2; x++) {
-                            d[x] = __low2half2(half2_of(k_d[2 * h + x][c]));
-                            m[x] = __high2half2(half2_of(k_d[2 * h + x][c]));
+                            d[x] = __low2half2(half2_of(kd[2 * h + x][c]));
+                            m[x] = __high2half2(half2_of(kd[2 * h + x][c]));
                         }
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
                             uint32_t y[2][4];
 #pragma unroll
                             for (int x = 0; x < 2; x++) {
-                                const uint32_t w = k_w[2 * h + x][2 * c + i];
-                                y[x][0] = q4_value(q4_low(w), d[x], m[x]);
-                                y[x][1] = q4_value(q4_high(w), d[x], m[x]);
-                                y[x][2] = q4_value(q4_low(w >> 8), d[x], m[x]);
-                                y[x][3] = q4_value(q4_high(w >> 8), d[x], m[x]);
+                                const uint32_t w = kw[2 * h + x][2 * c + i];
+                                y[x][0] = q4_value(q4_low(w, k1024), d[x], m[x]);
+                                y[x][1] = q4_value(q4_high(w, k1024), d[x], m[x]);
+                                y[x][2] = q4_value(q4_low(w >> 8, k1024), d[x], m[x]);
+                                y[x][3] = q4_value(q4_high(w >> 8, k1024), d[x], m[x]);
                             }
 #pragma unroll
                             for (int u = 0; u < 2; u++) {
@@ -1168,15 +1238,19 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                         }
                     }
                 }
-                // rows that are not there, and those that some query rows do not see
                 const int e0 = (pc + i0) * 16;
+                // rows that are not there, and those that some query rows do not see
+                if (!whole || e0 + 16 * H - 1 > e_min) {
 #pragma unroll
-                for (int h = 0; h < H; h++)
+                    for (int h = 0; h < H; h++)
 #pragma unroll
-                    for (int q = 0; q < NT; q++)
+                        for (int q = 0; q < NT; q++)
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            if (!((there >> (2 * h + (k >> 1))) & 1u) || e0 + 16 * h + r + (k >> 1) * 8 > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                            for (int k = 0; k < 4; k++)
+                                if (!((there >> (2 * h + (k >> 1))) & 1u) || e0 + 16 * h + r + (k >> 1) * 8 > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                }
+                const bool more = lleft > 0;
+                if (more) load_k();
                 uint32_t ph[H][NT][2], pl[H][NT][2];
 #pragma unroll
                 for (int q = 0; q < NT; q++) {
@@ -1219,8 +1293,13 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                         for (int k = 0; k < 2; k++) {
                             const uint32_t hi = pack_hi(sc[h][q][2 * k], sc[h][q][2 * k + 1]);
-                            ph[h][q][k] = transpose8(hi);
-                            pl[h][q][k] = transpose8(pack_lo(sc[h][q][2 * k], sc[h][q][2 * k + 1], hi));
+                            if (PACK) {      // the first part, or what it leaves
+                                const float2 f = __half22float2(half2_of(hi));
+                                ph[h][q][k] = transpose8(pack_hi(fmaf(f.x, second, sc[h][q][2 * k]), fmaf(f.y, second, sc[h][q][2 * k + 1])));
+                            } else {
+                                ph[h][q][k] = transpose8(hi);
+                                pl[h][q][k] = transpose8(pack_lo(sc[h][q][2 * k], sc[h][q][2 * k + 1], hi));
+                            }
                         }
                     }
                 }
@@ -1230,13 +1309,13 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                     uint32_t v[KS][4];       // tile i: dims 2i and 2i + 1 of this lane's, of rows 2t, 2t + 1 and of the eight behind
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
-                        const uint32_t da = v_d[2 * h + x][0], db = v_d[2 * h + x][1];
+                        const uint32_t da = vd[2 * h + x][0], db = vd[2 * h + x][1];
                         const __half2 d = half2_of(__byte_perm(da, db, 0x5410)), m = half2_of(__byte_perm(da, db, 0x7632));
 #pragma unroll
                         for (int i = 0; i < KS; i++) {
-                            const uint32_t b = i % 4, w = __byte_perm(v_w[2 * h + x][0][i / 4], v_w[2 * h + x][1][i / 4], b | (4 + b) << 8 | (4 + b) << 12 | b << 4);
-                            v[i][2 * x] = q4_value(q4_low(w), d, m);
-                            v[i][2 * x + 1] = q4_value(q4_high(w), d, m);
+                            const uint32_t b = i % 4, w = __byte_perm(vw[2 * h + x][0][i / 4], vw[2 * h + x][1][i / 4], b | b << 4 | (4 + b) << 8 | (4 + b) << 12);
+                            v[i][2 * x] = q4_value(q4_low(w, k1024), d, m);
+                            v[i][2 * x + 1] = q4_value(q4_high(w, k1024), d, m);
                         }
                     }
                     // a row that some new tokens see and others do not: where its V is not
@@ -1257,8 +1336,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                                     if (!(who & (0x11111111u << tt))) continue;
 #pragma unroll
                                     for (int q = 0; q < NT; q++) {
-                                        const float pa = __shfl_sync(0xffffffffu, sc[h][q][2 * x], 4 * (2 * tt + k) + t),
-                                                    pb = __shfl_sync(0xffffffffu, sc[h][q][2 * x + 1], 4 * (2 * tt + k) + t);
+                                        float pa = __shfl_sync(0xffffffffu, sc[h][q][2 * x], 4 * (2 * tt + k) + t),
+                                              pb = __shfl_sync(0xffffffffu, sc[h][q][2 * x + 1], 4 * (2 * tt + k) + t);
+                                        if (PACK && t >= 2) pa = pb = 0.f;       // (the first four columns' are whole)
 #pragma unroll
                                         for (int i = 0; i < KS; i++)
 #pragma unroll
@@ -1282,12 +1362,18 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                         for (int q = 0; q < NT; q++) {
                             mma16816(o[q][i], v[i], ph[h][q][0], ph[h][q][1]);
-                            mma16816(o[q][i], v[i], pl[h][q][0], pl[h][q][1]);
+                            if (!PACK) mma16816(o[q][i], v[i], pl[h][q][0], pl[h][q][1]);
                         }
                 }
+                if (more) load_v();
             }
             // ---- this worker's part of the unit
-            const long long slot = ((long long)s * units + j + me) * min(srows, RU);
+            const long long slot = ((long long)s * units + (g * rt + tile) + me) * min(srows, RU);
+            if (PACK)
+#pragma unroll
+                for (int i = 0; i < KS; i++)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) o[0][i][k] += __shfl_xor_sync(0xffffffffu, o[0][i][k], 2);
 #pragma unroll
             for (int q = 0; q < NT; q++)
 #pragma unroll
@@ -1295,16 +1381,16 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) l[q][k] += __shfl_xor_sync(0xffffffffu, l[q][k], d);
                     const int row = q * 8 + 2 * t + k;
-                    if (tile * RU + row >= srows) continue;
+                    if (tile * RU + row >= srows || (PACK && t >= 2)) continue;
                     float* dst = a.suffix_o + (slot + row) * p.hd + 8 * C * r;
-                    if (8 * C * r < p.hd)
+                    if (v_in)
 #pragma unroll
                         for (int i = 0; i < KS; i += 2)
                             *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[q][i][k], o[q][i][2 + k], o[q][i + 1][k], o[q][i + 1][2 + k]);
                     if (r == 0) a.suffix_ml[slot + row] = make_float2(fmaxf(R[q][k] * qs[q][k], kLow), l[q][k]);
                 }
             left -= count + kUnit;
-            if (left > 0) next(s, j, pc, np);
+            if (left > 0) next(s, g, tile, pc, np);
         }
     }
     if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();   // (as the suffix kernel above)
@@ -1333,7 +1419,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
         return;
     }
     if (lane == 0 && len > clipped_len(p, s)) flag(p.err, LLM_PAGES_BAD_LEN);
-    const int srows = p.n_new * a.gq, ru = unit_rows(srows), rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
+    const int srows = p.n_new * a.gq, ru = a.unit_rows, rt = (srows + ru - 1) / ru, row = i * a.gq + hq;
     int np = 0, ns = 0;                      // the row's parts of the prefix and of its pages
     int pre = 0, suf = 0;                    // the first ones' rows
     if (a.prefix_blocks > 0) {
@@ -1425,7 +1511,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Pages
 
 // --------------------------------------------------------------- host --
 struct Plan {
-    int prefix_blocks, suffix_blocks;
+    int prefix_blocks, suffix_blocks, unit_rows;
     long long prefix_rows, suffix_rows;      // parts of one row each
     size_t off_pml, off_so, off_sml, off_starts, bytes;
 };
@@ -1443,7 +1529,8 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms, bool q4) {
     if (p->max_pages > 0) {
         // workers for as many blocks as an SM holds at once, but no more than the
         // longest sequences could keep busy
-        const int ru = unit_rows((int)srows);
+        const int ru = q4 ? unit_rows_q4((int)srows, p->head_dim) : unit_rows((int)srows);
+        pl.unit_rows = ru;
         const long long units = (long long)p->n_kv_heads * ((srows + ru - 1) / ru),
                         most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16 + kUnit),
                         blocks = (most + kQuantum * kSuffixWarps - 1) / (kQuantum * kSuffixWarps);
@@ -1496,11 +1583,15 @@ cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensor
     return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
 }
 
-template <int HDP, int NT, bool SPLITQ>
-cudaError_t launch_suffix(cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks, bool q4) {
+typedef void (*PagesKernel)(PagesDev, AttendDev, int);
+template <int HDP, int NT>
+PagesKernel pages_kernel(bool splitq) { return splitq ? suffix_kernel<HDP, NT, true> : suffix_kernel<HDP, NT, false>; }
+template <int HDP, int NT, bool PACK, bool FULL>
+PagesKernel pages_q4_kernel(bool splitq) { return splitq ? suffix_q4_kernel<HDP, NT, true, PACK, FULL> : suffix_q4_kernel<HDP, NT, false, PACK, FULL>; }
+
+cudaError_t launch_suffix(PagesKernel k, cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
     // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
     static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
-    auto k = q4 ? suffix_q4_kernel<HDP, NT, SPLITQ> : suffix_kernel<HDP, NT, SPLITQ>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(32 * kSuffixWarps);
@@ -1584,6 +1675,7 @@ int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int
     ad.by_gq = Div((uint32_t)ad.gq);
     ad.starts = reinterpret_cast<int*>(ws + pl.off_starts);
     ad.suffix_workers = pl.suffix_blocks * kSuffixWarps;
+    ad.unit_rows = pl.unit_rows;
     ad.q4 = f;
     ad.timeout = timeout;
     ad.wait_limit = wait_limit > 0 ? wait_limit : kWaitLimit;
@@ -1602,12 +1694,23 @@ int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int
     }
     if (pl.suffix_blocks > 0) {
         const int first = prefix ? 0 : 1;
-#define LLM_SUFFIX(HDP, NT)                                                               \
-    (sq ? launch_suffix<HDP, NT, true>(stream, pd, ad, first, pl.suffix_blocks, q4) \
-        : launch_suffix<HDP, NT, false>(stream, pd, ad, first, pl.suffix_blocks, q4))
-        const bool eight = unit_rows(pages->n_new * ad.gq) == 8;
-        e = hd <= 64 ? (eight ? LLM_SUFFIX(64, 1) : LLM_SUFFIX(64, 2)) : (eight ? LLM_SUFFIX(128, 1) : LLM_SUFFIX(128, 2));
-#undef LLM_SUFFIX
+        PagesKernel k;
+        const int tiles = pl.unit_rows / 8;
+        if (!q4) {
+            k = hd <= 64 ? (tiles == 1 ? pages_kernel<64, 1>(sq) : pages_kernel<64, 2>(sq)) : (tiles == 1 ? pages_kernel<128, 1>(sq) : pages_kernel<128, 2>(sq));
+        } else if (pages->n_new * ad.gq <= 4) {
+            k = hd == 64    ? pages_q4_kernel<64, 1, true, true>(sq)
+                : hd < 64   ? pages_q4_kernel<64, 1, true, false>(sq)
+                : hd == 128 ? pages_q4_kernel<128, 1, true, true>(sq)
+                            : pages_q4_kernel<128, 1, true, false>(sq);
+        } else if (hd <= 64) {
+            k = tiles == 1   ? pages_q4_kernel<64, 1, false, false>(sq)
+                : tiles == 2 ? pages_q4_kernel<64, 2, false, false>(sq)
+                             : pages_q4_kernel<64, 3, false, false>(sq);
+        } else {
+            k = tiles == 1 ? pages_q4_kernel<128, 1, false, false>(sq) : pages_q4_kernel<128, 2, false, false>(sq);
+        }
+        e = launch_suffix(k, stream, pd, ad, first, pl.suffix_blocks);
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (suffix)");
     }
     const dim3 grid((unsigned)((rows * a->n_heads + 3) / 4));
