@@ -931,13 +931,28 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 //   loads dims 8 C r .. of rows 2t, 2t + 1 (and those eight behind), and a byte permutation
 //   joins the two rows' numbers, so no transpose is needed.  An MMA's rows r and r + 8 are
 //   dims 8 C r + 2 i and + 1.
-// A step is H pieces.  Eight rows in a row lie in one page (page_size >= 8): an octet.  The
-// next step's K is requested as soon as the scores have used this one's, its V behind the
-// sums, into the same registers.
+// A step is H pieces.  Eight rows in a row lie in one page (page_size >= 8): an octet.  Each
+// warp has a ring of steps in shared memory, filled by asynchronous 16-byte copies: an
+// octet's numbers lie in a row, and so do its pairs, so a step of 32 rows of heads of 64
+// values takes five copies of a warp where loads into registers took 24.
 // PACK: up to four query rows.  The eight columns of a product hold each of them twice;
 // the second four take the probabilities' second parts, so one product adds both.
 // FULL: head_dim is HDP, so that the distances of rows and pairs are constants.
-constexpr int kCtas64 = 4, kCtas128 = 4, kPieces128 = 1;
+constexpr int kQ4Stages = 3;
+constexpr int kCtas64 = 4, kCtas128 = 4, kPieces64 = 2, kPieces128 = 1;
+__host__ __device__ constexpr int q4_pieces(int hdp) { return hdp == 64 ? kPieces64 : kPieces128; }
+// Shared memory of a block's rings.
+__host__ __device__ constexpr int q4_rings(int hdp) { return kSuffixWarps * kQ4Stages * 2 * (2 * q4_pieces(hdp)) * 5 * hdp; }
+
+// A 16-byte asynchronous copy to shared memory, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+// Waits until at most N groups of this thread's copies are on their way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? kCtas64 : nt == 2 ? 3 : 2) : (nt == 1 ? kCtas128 : 2); }
 
 // Query rows of a unit: more than 16 are taken at once (up to 24, where the registers allow) as
@@ -968,8 +983,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
     suffix_q4_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
     static_assert(!PACK || NT == 1, "four query rows");
     constexpr int C = HDP / 64, KS = HDP / 16, RU = 8 * NT;  // chunks of 64 dims; MMA steps of a dot product, and MMA tiles of the sums
-    constexpr int H = HDP == 64 ? 2 : kPieces128, OCT = 2 * H;   // pieces and octets of a step
-    extern __shared__ int seqs[];
+    constexpr int H = q4_pieces(HDP), OCT = 2 * H;           // pieces and octets of a step
+    constexpr int S = kQ4Stages, NUMBERS = OCT * 4 * HDP, PAIRS = OCT * HDP, STAGE = 2 * (NUMBERS + PAIRS);
+    extern __shared__ __align__(16) int seqs[];
     if (first) griddep_wait();
     griddep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1009,11 +1025,17 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
         const int r = lane >> 2, t = lane & 3;
         const uint32_t pitch = (FULL ? HDP : (uint32_t)p.hd) / 2, pairs = FULL ? HDP / 8 : 4u * a.q4.groups, page_bytes = (uint32_t)a.q4.page_bytes,
                        mask = (1u << p.page_shift) - 1;
-        // this lane's places among the rows of an octet of page 0
-        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k) + r * pitch + 8 * t,
-                      *kdp = reinterpret_cast<const uint8_t*>(p.k) + a.q4.scales + r * pairs + 4 * (t >> 1),
-                      *vp = reinterpret_cast<const uint8_t*>(p.v) + 2 * t * pitch + 4 * C * r,
-                      *vdp = reinterpret_cast<const uint8_t*>(p.v) + a.q4.scales + 2 * t * pairs + 4 * (C * r >> 2);
+        // the warp's ring of steps: numbers of K, of V, pairs of K, of V
+        uint8_t* ring = reinterpret_cast<uint8_t*>(seqs) + ((2 * p.n_seqs + 1) * 4 + 15) / 16 * 16 + warp * (S * STAGE);
+        // 16-byte words of an octet's numbers, two octets of heads of up to 64 values to a copy of the whole warp; those of
+        // its pairs, K's and V's of four octets (two, of heads of up to 128)
+        constexpr int NW = HDP / 4, NO = 32 / NW, PW = HDP / 16, PO = 16 / PW;
+        const int n_oct = lane / NW, n_word = lane % NW, p_oct = lane % 16 / PW, p_word = lane % PW;
+        const bool n_in = FULL || 4 * n_word < p.hd, p_in = FULL || 4 * p_word < (int)pairs * 2;
+        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k) + 16 * n_word, *vp = reinterpret_cast<const uint8_t*>(p.v) + 16 * n_word,
+                      *dp = reinterpret_cast<const uint8_t*>(lane < 16 ? p.k : p.v) + a.q4.scales + 16 * p_word;
+        uint8_t* n_to = ring + n_oct * (8 * pitch) + 16 * n_word;
+        uint8_t* p_to = ring + 2 * NUMBERS + (lane < 16 ? 0 : PAIRS) + p_oct * (8 * pairs) + 16 * p_word;
         const bool k_in[2] = {FULL || 16 * t < p.hd, FULL || 64 + 16 * t < p.hd}, v_in = FULL || 8 * C * r < p.hd;
         const float second = t >= 2 ? -1.f : 0.f;                // PACK: which part of the probabilities this lane's columns take
         uint32_t k1024;                      // (a register: see and_or)
@@ -1033,101 +1055,28 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                 }
             }
         };
-        uint32_t kw[OCT][2 * C], kd[OCT][C], vw[OCT][2][C], vd[OCT][2];      // numbers and pairs
+        uint32_t pages_ok = 0;               // four bits for each step in the ring: its octets that have a page
+        // requests the step into a place of the ring, moves on and looks the next one up.  An octet without a page is zero;
+        // rows of its page that are not the sequence's come along
+        auto load = [&](int to) {
+            const int e0 = lpc * 16, first_row = lg << p.page_shift;
+            pages_ok |= (__ballot_sync(0xffffffffu, page >= 0) & ((1u << OCT) - 1)) << (4 * to);
 #pragma unroll
-        for (int o = 0; o < OCT; o++) {
-#pragma unroll
-            for (int c = 0; c < C; c++) kw[o][2 * c] = kw[o][2 * c + 1] = kd[o][c] = vw[o][0][c] = vw[o][1][c] = 0;
-            vd[o][0] = vd[o][1] = 0;
-        }
-        uint32_t there = 0;                  // bit o: this lane's row r of octet o is there (K)
-        bool whole = false;                  // all rows of the step are
-        // row e's place in page pg, from a lane's place in page 0
-        auto place = [&](const uint8_t* lane_at, int pg, int e, uint32_t row_bytes) {
-            const uint32_t row = (uint32_t)(lg << p.page_shift) + ((uint32_t)e & mask);
-            return lane_at + (unsigned long long)(uint32_t)pg * page_bytes + (unsigned long long)row * row_bytes;
-        };
-        auto load_k = [&]() {
-            const int e0 = lpc * 16;
-            whole = e0 + 16 * H <= lend && __all_sync(0xffffffffu, page >= 0);
-            if (whole && p.page_shift >= 4) {            // a page for each sixteen rows
-                there = 0xFFFFFFFFu;
-                const uint8_t *w[H], *d[H];
-#pragma unroll
-                for (int h = 0; h < H; h++) {
-                    const int pg = __shfl_sync(0xffffffffu, page, 2 * h);
-                    w[h] = place(kp, pg, e0 + 16 * h, pitch);
-                    d[h] = place(kdp, pg, e0 + 16 * h, pairs);
-                }
-#pragma unroll
-                for (int c = 0; c < C; c++)
-                    if (k_in[c])
-#pragma unroll
-                        for (int o = 0; o < OCT; o++) {
-                            const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w[o / 2] + o % 2 * (8 * pitch) + 32 * c));
-                            kw[o][2 * c] = x.x;
-                            kw[o][2 * c + 1] = x.y;
-                            kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(d[o / 2] + o % 2 * (8 * pairs) + 8 * c));
-                        }
-                return;
-            }
-            there = 0;
-#pragma unroll
-            for (int o = 0; o < OCT; o++) {
-                const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o;
-                const bool in = pg >= 0 && e + r < lend;
-                if (in) there |= 1u << o;
-                const uint8_t *w = place(kp, pg, e, pitch), *d = place(kdp, pg, e, pairs);
-#pragma unroll
-                for (int c = 0; c < C; c++) {
-                    kw[o][2 * c] = kw[o][2 * c + 1] = kd[o][c] = 0;
-                    if (in && k_in[c]) {
-                        const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w + 32 * c));
-                        kw[o][2 * c] = x.x;
-                        kw[o][2 * c + 1] = x.y;
-                        kd[o][c] = __ldcs(reinterpret_cast<const uint32_t*>(d + 8 * c));
-                    }
+            for (int i = 0; i < OCT; i += NO) {
+                const int pg = __shfl_sync(0xffffffffu, page, i + n_oct);
+                const unsigned long long off = (unsigned long long)(uint32_t)max(pg, 0) * page_bytes +
+                                               (unsigned long long)(uint32_t)(first_row + ((e0 + 8 * (i + n_oct)) & (int)mask)) * pitch;
+                if (n_in) {
+                    cp_async16_or_zero(n_to + to * STAGE + i * (8 * pitch), kp + off, pg >= 0);
+                    cp_async16_or_zero(n_to + to * STAGE + NUMBERS + i * (8 * pitch), vp + off, pg >= 0);
                 }
             }
-        };
-        auto load_v = [&]() {                // then moves on and looks the next step up
-            const int e0 = lpc * 16;
-            auto one = [&](int o, int k, const uint8_t* w, const uint8_t* d) {
-                if (C == 1) {
-                    vw[o][k][0] = __ldcs(reinterpret_cast<const uint32_t*>(w));
-                } else {
-                    const uint2 x = __ldcs(reinterpret_cast<const uint2*>(w));
-                    vw[o][k][0] = x.x;
-                    vw[o][k][C - 1] = x.y;
-                }
-                vd[o][k] = __ldcs(reinterpret_cast<const uint32_t*>(d));
-            };
-            if (whole && p.page_shift >= 4) {
-                const uint8_t *w[H], *d[H];
 #pragma unroll
-                for (int h = 0; h < H; h++) {
-                    const int pg = __shfl_sync(0xffffffffu, page, 2 * h);
-                    w[h] = place(vp, pg, e0 + 16 * h, pitch);
-                    d[h] = place(vdp, pg, e0 + 16 * h, pairs);
-                }
-                if (v_in)
-#pragma unroll
-                    for (int o = 0; o < OCT; o++)
-#pragma unroll
-                        for (int k = 0; k < 2; k++) one(o, k, w[o / 2] + (o % 2 * 8 + k) * pitch, d[o / 2] + (o % 2 * 8 + k) * pairs);
-            } else {
-#pragma unroll
-                for (int o = 0; o < OCT; o++) {
-                    const int pg = __shfl_sync(0xffffffffu, page, o), e = e0 + 8 * o;
-                    const uint8_t *w = place(vp, pg, e, pitch), *d = place(vdp, pg, e, pairs);
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-#pragma unroll
-                        for (int c = 0; c < C; c++) vw[o][k][c] = 0;
-                        vd[o][k] = 0;
-                        if (v_in && pg >= 0 && e + 2 * t + k < lend) one(o, k, w + k * pitch, d + k * pairs);
-                    }
-                }
+            for (int i = 0; i < OCT; i += PO) {
+                const int oc = i + p_oct, pg = __shfl_sync(0xffffffffu, page, oc % OCT);
+                const unsigned long long off = (unsigned long long)(uint32_t)max(pg, 0) * page_bytes +
+                                               (unsigned long long)(uint32_t)(first_row + ((e0 + 8 * oc) & (int)mask)) * pairs;
+                if (p_in && oc < OCT) cp_async16_or_zero(p_to + to * STAGE + i * (8 * pairs), dp + off, pg >= 0);
             }
             const int n = min(min(lleft, H), lnp - lpc);
             lleft -= n;
@@ -1138,11 +1087,13 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             }
             if (lleft > 0) look();
         };
-        if (left > 0) {
-            look();
-            load_k();
-            load_v();
+        if (left > 0) look();
+#pragma unroll
+        for (int i = 0; i < S - 1; i++) {
+            if (lleft > 0) load(i);
+            cp_async_commit();
         }
+        int cur = 0;                         // the step's place in the ring
         while (left > 0) {
             // ---- one unit: pieces pc .. of its np, as far as this worker goes
             const int count = min(left, np - pc);
@@ -1200,6 +1151,14 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                 l[q][0] = l[q][1] = 0.f;
             }
             for (int i0 = 0; i0 < count; i0 += H) {
+                cp_async_wait<S - 2>();
+                __syncwarp();                // the step is there, and every lane has read the one before
+                if (lleft > 0) load(cur == 0 ? S - 1 : cur - 1);
+                cp_async_commit();
+                const uint8_t* st = ring + cur * STAGE;
+                const uint32_t has_page = (pages_ok >> (4 * cur)) & ((1u << OCT) - 1);
+                pages_ok &= ~(15u << (4 * cur));
+                cur = cur == S - 1 ? 0 : cur + 1;
                 // ---- scores
                 float sc[H][NT][4];
 #pragma unroll
@@ -1209,17 +1168,24 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                     for (int c = 0; c < C; c++) {
                         __half2 d[2], m[2];
+                        uint2 kw[2] = {make_uint2(0, 0), make_uint2(0, 0)};
 #pragma unroll
                         for (int x = 0; x < 2; x++) {
-                            d[x] = __low2half2(half2_of(kd[2 * h + x][c]));
-                            m[x] = __high2half2(half2_of(kd[2 * h + x][c]));
+                            const int row = 8 * (2 * h + x) + r;
+                            uint32_t dm = 0;
+                            if (k_in[c]) {
+                                kw[x] = *reinterpret_cast<const uint2*>(st + row * pitch + 32 * c + 8 * t);
+                                dm = *reinterpret_cast<const uint32_t*>(st + 2 * NUMBERS + row * pairs + 4 * (2 * c + (t >> 1)));
+                            }
+                            d[x] = __low2half2(half2_of(dm));
+                            m[x] = __high2half2(half2_of(dm));
                         }
 #pragma unroll
                         for (int i = 0; i < 2; i++) {
                             uint32_t y[2][4];
 #pragma unroll
                             for (int x = 0; x < 2; x++) {
-                                const uint32_t w = kw[2 * h + x][2 * c + i];
+                                const uint32_t w = i == 0 ? kw[x].x : kw[x].y;
                                 y[x][0] = q4_value(q4_low(w, k1024), d[x], m[x]);
                                 y[x][1] = q4_value(q4_high(w, k1024), d[x], m[x]);
                                 y[x][2] = q4_value(q4_low(w >> 8, k1024), d[x], m[x]);
@@ -1238,7 +1204,8 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                         }
                     }
                 }
-                const int e0 = (pc + i0) * 16;
+                const int e0 = (pc + i0) * 16, end = min(lens[s], e0 + 16 * min(H, count - i0));
+                const bool whole = e0 + 16 * H <= end && has_page == (1u << OCT) - 1;
                 // rows that are not there, and those that some query rows do not see
                 if (!whole || e0 + 16 * H - 1 > e_min) {
 #pragma unroll
@@ -1246,11 +1213,11 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                         for (int q = 0; q < NT; q++)
 #pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                if (!((there >> (2 * h + (k >> 1))) & 1u) || e0 + 16 * h + r + (k >> 1) * 8 > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                            for (int k = 0; k < 4; k++) {
+                                const int at = e0 + 16 * h + r + (k >> 1) * 8;
+                                if (!((has_page >> (2 * h + (k >> 1))) & 1u) || at >= end || at > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                            }
                 }
-                const bool more = lleft > 0;
-                if (more) load_k();
                 uint32_t ph[H][NT][2], pl[H][NT][2];
 #pragma unroll
                 for (int q = 0; q < NT; q++) {
@@ -1309,11 +1276,29 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                     uint32_t v[KS][4];       // tile i: dims 2i and 2i + 1 of this lane's, of rows 2t, 2t + 1 and of the eight behind
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
-                        const uint32_t da = vd[2 * h + x][0], db = vd[2 * h + x][1];
-                        const __half2 d = half2_of(__byte_perm(da, db, 0x5410)), m = half2_of(__byte_perm(da, db, 0x7632));
+                        uint32_t vw[2][C], vd[2];
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const int row = 8 * (2 * h + x) + 2 * t + k;
+                            vd[k] = 0;
+#pragma unroll
+                            for (int c = 0; c < C; c++) vw[k][c] = 0;
+                            if (!v_in) continue;
+                            const uint8_t* w = st + NUMBERS + row * pitch + 4 * C * r;
+                            if (C == 1) {
+                                vw[k][0] = *reinterpret_cast<const uint32_t*>(w);
+                            } else {
+                                const uint2 y = *reinterpret_cast<const uint2*>(w);
+                                vw[k][0] = y.x;
+                                vw[k][C - 1] = y.y;
+                            }
+                            vd[k] = *reinterpret_cast<const uint32_t*>(st + 2 * NUMBERS + PAIRS + row * pairs + 4 * (C * r >> 2));
+                            if (!whole && e0 + row >= end) vd[k] = 0;      // (whatever is there: its values are 0 then)
+                        }
+                        const __half2 d = half2_of(__byte_perm(vd[0], vd[1], 0x5410)), m = half2_of(__byte_perm(vd[0], vd[1], 0x7632));
 #pragma unroll
                         for (int i = 0; i < KS; i++) {
-                            const uint32_t b = i % 4, w = __byte_perm(vw[2 * h + x][0][i / 4], vw[2 * h + x][1][i / 4], b | b << 4 | (4 + b) << 8 | (4 + b) << 12);
+                            const uint32_t b = i % 4, w = __byte_perm(vw[0][i / 4], vw[1][i / 4], b | b << 4 | (4 + b) << 8 | (4 + b) << 12);
                             v[i][2 * x] = q4_value(q4_low(w, k1024), d, m);
                             v[i][2 * x + 1] = q4_value(q4_high(w, k1024), d, m);
                         }
@@ -1365,7 +1350,6 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                             if (!PACK) mma16816(o[q][i], v[i], pl[h][q][0], pl[h][q][1]);
                         }
                 }
-                if (more) load_v();
             }
             // ---- this worker's part of the unit
             const long long slot = ((long long)s * units + (g * rt + tile) + me) * min(srows, RU);
@@ -1570,40 +1554,66 @@ bool rows_map(CUtensorMap* m, const uint16_t* base, int hd, int n_kv, long long 
 // other under another division.  (A suffix kernel alone wants the cache: 268 MB of
 // pages 65 us, 49 us with the default.)
 constexpr int kCarveout = 72;
+// The page kernel's rings want all of it, beside the prefix kernel or alone.
+constexpr int kCarveoutQ4 = 100;
+
+void launch_attributes(cudaLaunchAttribute (&at)[2], int carveout) {
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
+    at[1].val.sharedMemCarveout = carveout;
+}
 
 template <int HDP, bool SPLITQ>
-cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad) {
+cudaError_t launch_prefix(cudaStream_t st, const CUtensorMap& mk, const CUtensorMap& mv, const PagesDev& pd, const AttendDev& ad, int carveout) {
     auto k = prefix_kernel<HDP, SPLITQ>;
     static OncePerDevice once;
-    const cudaError_t e = once([&] {
-        const cudaError_t r = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem);
-        return r != cudaSuccess ? r : cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveout);
-    });
+    const cudaError_t e = once([&] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PrefixPlan<HDP>::kSmem); });
     if (e != cudaSuccess) return e;
-    return launch_dep(k, dim3((unsigned)ad.prefix_blocks), dim3(kPrefixThreads), (size_t)PrefixPlan<HDP>::kSmem, st, mk, mv, pd, ad);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ad.prefix_blocks);
+    cfg.blockDim = dim3(kPrefixThreads);
+    cfg.dynamicSmemBytes = (size_t)PrefixPlan<HDP>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    launch_attributes(at, carveout);
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k, mk, mv, pd, ad);
 }
+
+// Shared memory of a block of the pages' kernel: row counts and sums of the sequences, the rings.
+constexpr int suffix_smem(int n_seqs, int hdp, bool q4) { return q4 ? ((2 * n_seqs + 1) * 4 + 15) / 16 * 16 + q4_rings(hdp) : (2 * n_seqs + 1) * 4; }
+// (within the 48 KB that need no opt-in)
+static_assert(suffix_smem(kMaxSeqs, 128, false) <= 47 * 1024, "shared memory of the sequences");
 
 typedef void (*PagesKernel)(PagesDev, AttendDev, int);
 template <int HDP, int NT>
 PagesKernel pages_kernel(bool splitq) { return splitq ? suffix_kernel<HDP, NT, true> : suffix_kernel<HDP, NT, false>; }
+// (*e: whether it may have the shared memory that it needs)
 template <int HDP, int NT, bool PACK, bool FULL>
-PagesKernel pages_q4_kernel(bool splitq) { return splitq ? suffix_q4_kernel<HDP, NT, true, PACK, FULL> : suffix_q4_kernel<HDP, NT, false, PACK, FULL>; }
+PagesKernel pages_q4_kernel(bool splitq, cudaError_t* e) {
+    const PagesKernel one = suffix_q4_kernel<HDP, NT, false, PACK, FULL>, two = suffix_q4_kernel<HDP, NT, true, PACK, FULL>;
+    static OncePerDevice once;
+    *e = once([&] {
+        const int most = suffix_smem(kMaxSeqs, HDP, true);
+        const cudaError_t r = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        return r != cudaSuccess ? r : cudaFuncSetAttribute(two, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    });
+    return splitq ? two : one;
+}
 
-cudaError_t launch_suffix(PagesKernel k, cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks) {
-    // row counts and sums of at most kMaxSeqs sequences: within the 48 KB that need no opt-in
-    static_assert((2 * kMaxSeqs + 1) * 4 <= 47 * 1024, "shared memory of the sequences");
+// carveout 0: the driver's choice.
+cudaError_t launch_suffix(PagesKernel k, cudaStream_t st, const PagesDev& pd, const AttendDev& ad, int first, int blocks, int smem, int carveout) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(32 * kSuffixWarps);
-    cfg.dynamicSmemBytes = (size_t)(2 * pd.n_seqs + 1) * 4;
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = st;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributePreferredSharedMemoryCarveout;
-    at[1].val.sharedMemCarveout = kCarveout;
+    launch_attributes(at, carveout);
     cfg.attrs = at;
-    cfg.numAttrs = first ? 1 : 2;
+    cfg.numAttrs = carveout ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, k, pd, ad, first);
 }
 
@@ -1681,13 +1691,14 @@ int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int
     ad.wait_limit = wait_limit > 0 ? wait_limit : kWaitLimit;
     const bool sq = !ad.q_f16;
     const int hd = pages->head_dim;
+    const int carveout = q4 ? kCarveoutQ4 : kCarveout;
     cudaError_t e = cudaSuccess;
     if (prefix) {
         CUtensorMap mk, mv;
         if (!rows_map(&mk, a->prefix_k, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT) ||
             !rows_map(&mv, a->prefix_v, hd, pages->n_kv_heads, pages->prefix_len, a->prefix_stride, kKT))
             return fail_op(LLM_ERR_CUDA, "a tensor map of the prefix");
-#define LLM_PREFIX(HDP) (sq ? launch_prefix<HDP, true>(stream, mk, mv, pd, ad) : launch_prefix<HDP, false>(stream, mk, mv, pd, ad))
+#define LLM_PREFIX(HDP) (sq ? launch_prefix<HDP, true>(stream, mk, mv, pd, ad, carveout) : launch_prefix<HDP, false>(stream, mk, mv, pd, ad, carveout))
         e = hd <= 64 ? LLM_PREFIX(64) : LLM_PREFIX(128);
 #undef LLM_PREFIX
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (prefix)");
@@ -1699,18 +1710,20 @@ int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int
         if (!q4) {
             k = hd <= 64 ? (tiles == 1 ? pages_kernel<64, 1>(sq) : pages_kernel<64, 2>(sq)) : (tiles == 1 ? pages_kernel<128, 1>(sq) : pages_kernel<128, 2>(sq));
         } else if (pages->n_new * ad.gq <= 4) {
-            k = hd == 64    ? pages_q4_kernel<64, 1, true, true>(sq)
-                : hd < 64   ? pages_q4_kernel<64, 1, true, false>(sq)
-                : hd == 128 ? pages_q4_kernel<128, 1, true, true>(sq)
-                            : pages_q4_kernel<128, 1, true, false>(sq);
+            k = hd == 64    ? pages_q4_kernel<64, 1, true, true>(sq, &e)
+                : hd < 64   ? pages_q4_kernel<64, 1, true, false>(sq, &e)
+                : hd == 128 ? pages_q4_kernel<128, 1, true, true>(sq, &e)
+                            : pages_q4_kernel<128, 1, true, false>(sq, &e);
         } else if (hd <= 64) {
-            k = tiles == 1   ? pages_q4_kernel<64, 1, false, false>(sq)
-                : tiles == 2 ? pages_q4_kernel<64, 2, false, false>(sq)
-                             : pages_q4_kernel<64, 3, false, false>(sq);
+            k = tiles == 1   ? pages_q4_kernel<64, 1, false, false>(sq, &e)
+                : tiles == 2 ? pages_q4_kernel<64, 2, false, false>(sq, &e)
+                             : pages_q4_kernel<64, 3, false, false>(sq, &e);
         } else {
-            k = tiles == 1 ? pages_q4_kernel<128, 1, false, false>(sq) : pages_q4_kernel<128, 2, false, false>(sq);
+            k = tiles == 1 ? pages_q4_kernel<128, 1, false, false>(sq, &e) : pages_q4_kernel<128, 2, false, false>(sq, &e);
         }
-        e = launch_suffix(k, stream, pd, ad, first, pl.suffix_blocks);
+        if (e == cudaSuccess)
+            e = launch_suffix(k, stream, pd, ad, first, pl.suffix_blocks, suffix_smem(pages->n_seqs, hd <= 64 ? 64 : 128, q4),
+                              q4 || !first ? carveout : 0);
         if (e != cudaSuccess) return launched(e, "llm_attend_batch (suffix)");
     }
     const dim3 grid((unsigned)((rows * a->n_heads + 3) / 4));
