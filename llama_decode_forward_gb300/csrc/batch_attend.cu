@@ -1274,31 +1274,34 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
 #pragma unroll
                 for (int h = 0; h < H; h++) {
                     uint32_t v[KS][4];       // tile i: dims 2i and 2i + 1 of this lane's, of rows 2t, 2t + 1 and of the eight behind
+                    uint32_t vw[4][C], vd[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const int row = 16 * h + 8 * (k / 2) + 2 * t + k % 2;
+                        const uint8_t* w = st + NUMBERS + row * pitch + 4 * C * r;
+                        vd[k] = 0;
+#pragma unroll
+                        for (int c = 0; c < C; c++) vw[k][c] = 0;
+                        if (!v_in) continue;
+                        if (C == 1) {
+                            vw[k][0] = *reinterpret_cast<const uint32_t*>(w);
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2*>(w);
+                            vw[k][0] = y.x;
+                            vw[k][C - 1] = y.y;
+                        }
+                        vd[k] = *reinterpret_cast<const uint32_t*>(st + 2 * NUMBERS + PAIRS + row * pairs + 4 * (C * r >> 2));
+                    }
+                    if (!whole)              // rows behind the last: whatever is there, their values are 0
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (e0 + 16 * h + 8 * (k / 2) + 2 * t + k % 2 >= end) vd[k] = 0;
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
-                        uint32_t vw[2][C], vd[2];
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const int row = 8 * (2 * h + x) + 2 * t + k;
-                            vd[k] = 0;
-#pragma unroll
-                            for (int c = 0; c < C; c++) vw[k][c] = 0;
-                            if (!v_in) continue;
-                            const uint8_t* w = st + NUMBERS + row * pitch + 4 * C * r;
-                            if (C == 1) {
-                                vw[k][0] = *reinterpret_cast<const uint32_t*>(w);
-                            } else {
-                                const uint2 y = *reinterpret_cast<const uint2*>(w);
-                                vw[k][0] = y.x;
-                                vw[k][C - 1] = y.y;
-                            }
-                            vd[k] = *reinterpret_cast<const uint32_t*>(st + 2 * NUMBERS + PAIRS + row * pairs + 4 * (C * r >> 2));
-                            if (!whole && e0 + row >= end) vd[k] = 0;      // (whatever is there: its values are 0 then)
-                        }
-                        const __half2 d = half2_of(__byte_perm(vd[0], vd[1], 0x5410)), m = half2_of(__byte_perm(vd[0], vd[1], 0x7632));
+                        const __half2 d = half2_of(__byte_perm(vd[2 * x], vd[2 * x + 1], 0x5410)), m = half2_of(__byte_perm(vd[2 * x], vd[2 * x + 1], 0x7632));
 #pragma unroll
                         for (int i = 0; i < KS; i++) {
-                            const uint32_t b = i % 4, w = __byte_perm(vw[0][i / 4], vw[1][i / 4], b | b << 4 | (4 + b) << 8 | (4 + b) << 12);
+                            const uint32_t b = i % 4, w = __byte_perm(vw[2 * x][i / 4], vw[2 * x + 1][i / 4], b | b << 4 | (4 + b) << 8 | (4 + b) << 12);
                             v[i][2 * x] = q4_value(q4_low(w, k1024), d, m);
                             v[i][2 * x + 1] = q4_value(q4_high(w, k1024), d, m);
                         }
