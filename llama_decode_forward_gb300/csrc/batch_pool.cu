@@ -45,33 +45,56 @@ struct CompactWork {
     int *from, *to;                          // [n_pages]
 };
 
-__device__ __forceinline__ uint32_t plan_rank() {
+// A plan runs as one block (ONE), whose working arrays are in shared memory, or as a cluster
+// of kPlanBlocks.
+template <bool ONE>
+__device__ __forceinline__ int plan_rank() {
+    if (ONE) return 0;
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+    return (int)r;
 }
+// (of the cluster's global memory too: what a block wrote before it is seen behind it by the others, which read around L1)
+template <bool ONE>
 __device__ __forceinline__ void plan_barrier() {
-    // (global memory as well: what a block wrote before it is seen behind it by the others, which read around L1)
-    __threadfence();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (ONE) __syncthreads();
+    else asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+template <bool ONE>
+__device__ __forceinline__ int read(const int* p) { return ONE ? *static_cast<const volatile int*>(p) : __ldcg(p); }
+template <bool ONE>
+__device__ __forceinline__ void write(int* p, int v) {
+    if (ONE) *static_cast<volatile int*>(p) = v;
+    else __stcg(p, v);
+}
+// A shared-memory word of block `rank`.
+template <bool ONE>
 __device__ __forceinline__ int plan_peer(const int* p, uint32_t rank) {
+    if (ONE) return *static_cast<const volatile int*>(p);
     uint32_t a;
     int v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
+template <bool ONE>
 __device__ __forceinline__ long long plan_peer(const long long* p, uint32_t rank) {
+    if (ONE) return *static_cast<const volatile long long*>(p);
     uint32_t a;
     long long v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void plan_or(int* p, uint32_t rank, int bits) {
+// ORs bits into block 0's word.
+template <bool ONE>
+__device__ __forceinline__ void plan_or(int* p, int bits) {
+    if (ONE) {
+        atomicOr(p, bits);
+        return;
+    }
     uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(p)));
     asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(bits) : "memory");
 }
 
@@ -100,93 +123,99 @@ __device__ __forceinline__ N block_scan(N x, N* tmp, N* all) {
 }
 
 // The run of `n` things that block `rank` handles: whole warps' words of 32.
-__device__ __forceinline__ void share_of(int n, int rank, int* lo, int* hi) {
+__device__ __forceinline__ void share_of(int n, int rank, int blocks, int* lo, int* hi) {
     const long long w = (n + 31ll) / 32;
-    *lo = (int)min((long long)n, w * rank / kPlanBlocks * 32);
-    *hi = (int)min((long long)n, w * (rank + 1) / kPlanBlocks * 32);
+    *lo = (int)min((long long)n, w * rank / blocks * 32);
+    *hi = (int)min((long long)n, w * (rank + 1) / blocks * 32);
 }
 
 __device__ __forceinline__ int pages_of(long long rows, int shift) { return (int)((rows + (1ll << shift) - 1) >> shift); }
 
 // ------------------------------------------------------------- update --
-// Phases: 0 copies of the counts; 1 what each sequence gives up and takes; 2 which
-// pages stay, how many are wanted and free; 3 the free ones in order, the counts.
-__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
+// Phases: 0 copies of the counts, and what each sequence keeps (a thread each); 1 the pages that
+// it gives up and takes (a warp each); 2 which pages stay, how many are wanted and free; 3
+// the free ones in order, the counts.
+template <bool ONE>
+__global__ void __launch_bounds__(kPlanThreads, 1)
     update_plan_kernel(const __grid_constant__ PoolDev p, const __grid_constant__ UpdateWork w, const int* __restrict__ parents,
                        const int* __restrict__ rows) {
+    constexpr int BLOCKS = ONE ? 1 : kPlanBlocks;
+    extern __shared__ int arrays[];          // ONE: refs, first
     __shared__ int tmp[kPlanWarps], bad[2], copied, unheld;
     __shared__ long long tmp_wide[kPlanWarps], wanted;           // (the pages that all sequences want may pass 32 bits)
-    const int rank = (int)plan_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gwarp = rank * kPlanWarps + warp, gtid = rank * kPlanThreads + (int)threadIdx.x;
+    __shared__ int4 todo[kPlanThreads];      // of the block's sequences: whole pages, pages held, parent (-2: nothing to do)
+    const int rank = plan_rank<ONE>(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gtid = rank * kPlanThreads + (int)threadIdx.x;
     const int shift = p.page_shift, ps = 1 << shift;
+    int *refs = ONE ? arrays : w.refs, *first = ONE ? arrays + p.n_pages : w.first;
     if (threadIdx.x == 0) bad[0] = bad[1] = 0;
     griddep_entry();
-    for (int j = gtid; j < p.n_pages; j += kPlanBlocks * kPlanThreads) {
-        __stcg(w.refs + j, p.refs[j]);
-        __stcg(w.first + j, INT_MAX);
-    }
-    plan_barrier();
-
-    const long long room = (long long)p.max_pages << shift;
-    for (int s = gwarp; s < p.n_seqs; s += kPlanBlocks * kPlanWarps) {
-        const int parent = parents ? parents[s] : s, was = p.lens[s];
-        int wrong = 0;
+    // the block's sequences: a thread has at most one (n_seqs <= BLOCKS * kPlanThreads)
+    const int each = (p.n_seqs + BLOCKS - 1) / BLOCKS, s0 = rank * each, s = s0 + (int)threadIdx.x;
+    const int mine_n = min(each, p.n_seqs - s0);
+    const bool one = (int)threadIdx.x < mine_n;
+    int parent = -1, was = 0, had = 0, now = 0, part = -1, wrong = 0;
+    if (one) {
+        parent = parents ? parents[s] : s;
+        was = p.lens[s];
+        now = rows ? rows[s] : 0;
         if (parent < -1 || parent >= p.n_seqs) wrong = LLM_PAGES_BAD_SEQ;
-        const int had = wrong || parent < 0 ? 0 : p.lens[parent], now = rows ? rows[s] : had;
+        had = wrong || parent < 0 ? 0 : p.lens[parent];
+        if (!rows) now = had;
+        const long long room = (long long)p.max_pages << shift;
         if (was < 0 || was > room || had < 0 || had > room || now < 0 || now > room) wrong |= LLM_PAGES_BAD_LEN;
-        if (wrong) {
-            if (lane == 0) plan_or(&bad[0], 0, wrong);
-            continue;
-        }
-        const int keep = min(had, now), full = keep >> shift, tail = keep & (ps - 1), held = pages_of(was, shift);
-        const int* mine = p.table + (long long)s * p.max_pages;
-        const int* theirs = p.table + (long long)max(parent, 0) * p.max_pages;
-        // (a sequence that goes on from itself keeps its whole pages: only the others change hands)
-        for (int i = (parent == s ? full : 0) + lane; i < held; i += 32) {
-            const int j = mine[i];
-            if (j < 0 || j >= p.n_pages) wrong = LLM_PAGES_BAD_PAGE;
-            else atomicSub(w.refs + j, 1);
-        }
-        if (parent != s)
-            for (int i = lane; i < full; i += 32) {
-                const int j = theirs[i];
-                __stcg(w.source + (long long)s * p.max_pages + i, j);
-                if (j < 0 || j >= p.n_pages) wrong = LLM_PAGES_BAD_PAGE;
-                else atomicAdd(w.refs + j, 1);
-            }
-        if (lane == 0) {
-            int part = -1;
-            if (tail > 0) {
-                part = theirs[full];
-                if (part < 0 || part >= p.n_pages) wrong = LLM_PAGES_BAD_PAGE;
-                else atomicMin(w.first + part, s);
-            }
-            __stcg(w.rows + s, make_int4(full, tail, part, now));
-            __stcg(w.pages + s, make_int4(held, parent, 0, 0));
-        }
-        if (wrong) plan_or(&bad[0], 0, wrong);
     }
-    plan_barrier();
+    const int keep = wrong ? 0 : min(had, now), full = keep >> shift, tail = keep & (ps - 1), held = wrong ? 0 : pages_of(was, shift);
+    if (one) {
+        todo[threadIdx.x] = make_int4(full, held, wrong ? -2 : parent, 0);
+        if (tail > 0) part = p.table[(long long)parent * p.max_pages + full];
+    }
+    for (int j = gtid; j < p.n_pages; j += BLOCKS * kPlanThreads) {
+        write<ONE>(refs + j, p.refs[j]);
+        write<ONE>(first + j, INT_MAX);
+    }
+    plan_barrier<ONE>();                     // (bad[] is zero, too)
 
-    const int wrong = plan_peer(&bad[0], 0);
+    if (tail > 0) {
+        if (part < 0 || part >= p.n_pages) wrong |= LLM_PAGES_BAD_PAGE;
+        else atomicMin(first + part, s);
+    }
+    for (int i0 = warp; i0 < mine_n; i0 += kPlanWarps) {
+        const int4 q = todo[i0];
+        if (q.z == -2) continue;
+        const int* mine = p.table + (long long)(s0 + i0) * p.max_pages;
+        // (a sequence that goes on from itself keeps its whole pages: only the others change hands)
+        for (int i = (q.z == s0 + i0 ? q.x : 0) + lane; i < q.y; i += 32) {
+            const int j = mine[i];
+            if (j < 0 || j >= p.n_pages) wrong |= LLM_PAGES_BAD_PAGE;
+            else atomicSub(refs + j, 1);
+        }
+        if (q.z == s0 + i0) continue;
+        const int* theirs = p.table + (long long)max(q.z, 0) * p.max_pages;
+        for (int i = lane; i < q.x; i += 32) {
+            const int j = theirs[i];
+            w.source[(long long)(s0 + i0) * p.max_pages + i] = j;
+            if (j < 0 || j >= p.n_pages) wrong |= LLM_PAGES_BAD_PAGE;
+            else atomicAdd(refs + j, 1);
+        }
+    }
+    if (wrong) plan_or<ONE>(&bad[0], wrong);
+    plan_barrier<ONE>();
+
+    wrong = plan_peer<ONE>(&bad[0], 0);
     if (wrong) {                             // every block alike: nothing has been changed
         if (gtid == 0) {
             flag(p.err, wrong);
             w.header[0] = 0;
         }
-        plan_barrier();                      // (a block's shared memory stays until it has been read)
+        plan_barrier<ONE>();                 // (a block's shared memory stays until it has been read)
         return;
     }
-    // sequences, in runs: a thread has at most one (n_seqs <= kPlanBlocks * kPlanThreads)
-    const int each = (p.n_seqs + kPlanBlocks - 1) / kPlanBlocks, s = rank * each + (int)threadIdx.x;
-    const bool one = (int)threadIdx.x < each && s < p.n_seqs;
     int need = 0, copy = 0, stays = 0;
     if (one) {
-        const int4 q = __ldcg(w.rows + s);
         // a page kept in part stays where no one holds it whole, with the first sequence that keeps it
-        stays = q.y > 0 && __ldcg(w.refs + q.z) == 0 && __ldcg(w.first + q.z) == s;
-        copy = q.y > 0 && !stays;
-        need = pages_of(q.w, shift) - q.x - stays;
+        stays = tail > 0 && read<ONE>(refs + part) == 0 && read<ONE>(first + part) == s;
+        copy = tail > 0 && !stays;
+        need = pages_of(now, shift) - full - stays;
     }
     long long all_need;
     int all_copy;
@@ -194,20 +223,20 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     const int copy_before = block_scan(copy, tmp, &all_copy);
     // pages, in runs of 32: free ones are held by no sequence, in whole or in part
     int lo, hi;
-    share_of(p.n_pages, rank, &lo, &hi);
+    share_of(p.n_pages, rank, BLOCKS, &lo, &hi);
     const int words = (hi - lo + 31) / 32, w0 = (int)((long long)words * warp / kPlanWarps), w1 = (int)((long long)words * (warp + 1) / kPlanWarps);
     int mine = 0, below = 0;
     for (int k = w0; k < w1; k++) {
         const int j = lo + 32 * k + lane;
         bool none = false;
         if (j < hi) {
-            const int held = __ldcg(w.refs + j);
+            const int held = read<ONE>(refs + j);
             below |= held < 0;
-            none = held == 0 && __ldcg(w.first + j) == INT_MAX;
+            none = held == 0 && read<ONE>(first + j) == INT_MAX;
         }
         mine += __popc(__ballot_sync(0xffffffffu, none));
     }
-    if (below) plan_or(&bad[1], 0, LLM_PAGES_BAD_PAGE);          // fewer counted holders than there are
+    if (below) plan_or<ONE>(&bad[1], LLM_PAGES_BAD_PAGE);        // fewer counted holders than there are
     int all_free;
     const int free_before = __shfl_sync(0xffffffffu, block_scan(lane == 0 ? mine : 0, tmp, &all_free), 0);
     if (threadIdx.x == 0) {
@@ -215,13 +244,13 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         copied = all_copy;
         unheld = all_free;
     }
-    plan_barrier();
+    plan_barrier<ONE>();
 
     long long need0 = 0, needs = 0;
     int copy0 = 0, at = free_before, copies = 0, frees = 0;
-    for (int b = 0; b < kPlanBlocks; b++) {
-        const long long n = plan_peer(&wanted, b);
-        const int c = plan_peer(&copied, b), f = plan_peer(&unheld, b);
+    for (int b = 0; b < BLOCKS; b++) {
+        const long long n = plan_peer<ONE>(&wanted, b);
+        const int c = plan_peer<ONE>(&copied, b), f = plan_peer<ONE>(&unheld, b);
         if (b < rank) {
             need0 += n;
             copy0 += c;
@@ -231,8 +260,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         copies += c;
         frees += f;
     }
-    const int stop = plan_peer(&bad[1], 0) | (needs > frees ? LLM_PAGES_FULL : 0);
-    plan_barrier();                          // (the same)
+    const int stop = plan_peer<ONE>(&bad[1], 0) | (needs > frees ? LLM_PAGES_FULL : 0);
+    if (!ONE) plan_barrier<ONE>();           // (the same)
     if (gtid == 0) {
         if (stop) flag(p.err, stop);
         w.header[0] = stop == 0;
@@ -240,8 +269,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     }
     if (stop) return;
     if (one) {
-        const int4 q = __ldcg(w.pages + s);
-        w.pages[s] = make_int4(q.x, q.y, stays, (int)(need0 + need_before));
+        w.rows[s] = make_int4(full, tail, part, now);
+        w.pages[s] = make_int4(held, parent, stays, (int)(need0 + need_before));
         if (copy) w.copies[copy0 + copy_before] = s;
     }
     for (int k = w0; k < w1; k++) {
@@ -249,8 +278,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         int held = 0;
         bool part = false;
         if (j < hi) {
-            held = __ldcg(w.refs + j);
-            part = __ldcg(w.first + j) != INT_MAX;
+            held = read<ONE>(refs + j);
+            part = read<ONE>(first + j) != INT_MAX;
         }
         const bool none = j < hi && held == 0 && !part;
         const uint32_t who = __ballot_sync(0xffffffffu, none);
@@ -317,14 +346,16 @@ __global__ void __launch_bounds__(kMoveThreads) update_move_kernel(const __grid_
 // Phases: 1 how many pages are in use; 2 the pages in use by their rank, and the free
 // places before the last of them; 3 the pairs: the pages in use behind the first
 // n_live places, ascending, go to the free ones among those, ascending.
-__global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThreads, 1)
+template <bool ONE>
+__global__ void __launch_bounds__(kPlanThreads, 1)
     compact_plan_kernel(const __grid_constant__ PoolDev p, const __grid_constant__ CompactWork w, int* refs_out, int* moved, int* n_live) {
+    constexpr int BLOCKS = ONE ? 1 : kPlanBlocks;
     __shared__ int tmp[kPlanWarps], live_here, free_before_end;
-    const int rank = (int)plan_rank(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = plan_rank<ONE>(), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gtid = rank * kPlanThreads + (int)threadIdx.x;
     griddep_entry();
     int lo, hi;
-    share_of(p.n_pages, rank, &lo, &hi);
+    share_of(p.n_pages, rank, BLOCKS, &lo, &hi);
     const int words = (hi - lo + 31) / 32, w0 = (int)((long long)words * warp / kPlanWarps), w1 = (int)((long long)words * (warp + 1) / kPlanWarps);
     int mine = 0;
     for (int k = w0; k < w1; k++) {
@@ -337,10 +368,10 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         live_here = all;
         free_before_end = 0;
     }
-    plan_barrier();
+    plan_barrier<ONE>();
     int live = 0;
-    for (int b = 0; b < kPlanBlocks; b++) {
-        const int n = plan_peer(&live_here, b);
+    for (int b = 0; b < BLOCKS; b++) {
+        const int n = plan_peer<ONE>(&live_here, b);
         if (b < rank) at += n;
         live += n;
     }
@@ -370,11 +401,11 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     int all_holes;
     block_scan(holes, tmp, &all_holes);
     if (threadIdx.x == 0) free_before_end = all_holes;
-    plan_barrier();
+    plan_barrier<ONE>();
     int pairs = 0;
-    for (int b = 0; b < kPlanBlocks; b++) pairs += plan_peer(&free_before_end, b);
-    plan_barrier();                          // (a block's shared memory stays until it has been read)
-    for (int k = gtid; k < pairs; k += kPlanBlocks * kPlanThreads) {
+    for (int b = 0; b < BLOCKS; b++) pairs += plan_peer<ONE>(&free_before_end, b);
+    plan_barrier<ONE>();                          // (a block's shared memory stays until it has been read)
+    for (int k = gtid; k < pairs; k += BLOCKS * kPlanThreads) {
         const int from = __ldcg(w.from + live - pairs + k), to = __ldcg(w.to + k), r = __ldcg(refs_out + from);
         moved[from] = to;
         refs_out[to] = r;
@@ -456,6 +487,32 @@ int move_blocks(const llm_pool* p, long long most_pairs) {
     return (int)std::max(1ll, std::min((long long)8 * sm_count(), std::max(items, warps)));
 }
 
+// One block plans for pools whose counts fit its shared memory: a barrier of a cluster takes some 0.5 us more.
+constexpr int kOnePages = 16384, kOneSeqs = kPlanThreads;
+constexpr long long kOneEntries = 1 << 16;
+bool one_block(const llm_pool* p) {
+    return p->n_pages <= kOnePages && p->n_seqs <= kOneSeqs && (long long)p->n_seqs * p->max_pages <= kOneEntries;
+}
+
+// A plan: one block, or a cluster.
+template <class... KArgs, class... Args>
+cudaError_t launch_plan(void (*one)(KArgs...), void (*cluster)(KArgs...), bool is_one, size_t smem, cudaStream_t st, Args... args) {
+    if (is_one) return launch_dep(one, dim3(1), dim3(kPlanThreads), smem, st, args...);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(kPlanBlocks);
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = kPlanBlocks;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, cluster, static_cast<KArgs>(args)...);
+}
+
 size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 size_t update_work(const llm_pool* p, uint8_t* ws, UpdateWork* w) {
@@ -511,7 +568,10 @@ extern "C" int llm_pages_update(const llm_pool* pool, const int32_t* parents, co
     if ((rc = check_workspace(workspace, workspace_bytes, update_work(pool, static_cast<uint8_t*>(workspace), &w)))) return rc;
     if (pool->n_seqs == 0) return LLM_OK;
     const PoolDev d = pool_dev(pool);
-    cudaError_t e = launch_dep(update_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads), 0, stream, d, w, parents, rows);
+    static OncePerDevice once;
+    cudaError_t e = once([] { return cudaFuncSetAttribute(update_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kOnePages * 8); });
+    if (e == cudaSuccess)
+        e = launch_plan(update_plan_kernel<true>, update_plan_kernel<false>, one_block(pool), (size_t)pool->n_pages * 8, stream, d, w, parents, rows);
     if (e == cudaSuccess)
         e = launch_dep(update_move_kernel, dim3((unsigned)move_blocks(pool, pool->n_seqs)), dim3(kMoveThreads), 0, stream, d, w, parts_of(pool));
     return launched(e, "llm_pages_update");
@@ -535,7 +595,7 @@ extern "C" int llm_pages_compact(const llm_pool* pool, int32_t* table_out, int32
     CompactWork w;
     if ((rc = check_workspace(workspace, workspace_bytes, compact_work(pool, static_cast<uint8_t*>(workspace), &w)))) return rc;
     const PoolDev d = pool_dev(pool);
-    cudaError_t e = launch_dep(compact_plan_kernel, dim3(kPlanBlocks), dim3(kPlanThreads), 0, stream, d, w, refs_out, moved, n_live);
+    cudaError_t e = launch_plan(compact_plan_kernel<true>, compact_plan_kernel<false>, one_block(pool), 0, stream, d, w, refs_out, moved, n_live);
     if (e == cudaSuccess)
         e = launch_dep(compact_move_kernel, dim3((unsigned)move_blocks(pool, pool->n_pages / 2)), dim3(kMoveThreads), 0, stream, d, w,
                        static_cast<const int*>(moved), table_out, parts_of(pool));
