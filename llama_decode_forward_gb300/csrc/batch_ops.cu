@@ -57,7 +57,10 @@ template <int N>
 __device__ __forceinline__ void store_n(__half* p, const float (&x)[N]) {
     __align__(16) uint32_t w[N / 2];
 #pragma unroll
-    for (int k = 0; k < N / 2; k++) w[k] = h2_bits(__float2half_rn(x[2 * k]), __float2half_rn(x[2 * k + 1]));
+    for (int k = 0; k < N / 2; k++) {
+        const __half2 h = __floats2half2_rn(x[2 * k], x[2 * k + 1]);       // (one instruction; two conversions run on a slower unit)
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
     if (N == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
     else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(w);
 }
@@ -89,18 +92,74 @@ __device__ __forceinline__ float turned(float x, float other, float2 r, bool fir
     return first ? __fsub_rn(__fmul_rn(x, r.x), __fmul_rn(other, r.y)) : __fadd_rn(__fmul_rn(other, r.y), __fmul_rn(x, r.x));
 }
 
+// Eight elements of a group of 32, whose others the three other lanes of this one's four hold
+// (live: false for those behind a shorter last group): their numbers, and the group's d and m.
+__device__ __forceinline__ uint32_t quantize8(const float (&u)[8], bool live, uint32_t* pair) {
+    float low = INFINITY, high = -INFINITY, size = 0.f;
+    if (live) {
+        low = min3(u[0], u[1], u[2]);
+        high = max3(u[0], u[1], u[2]);
+        size = max3_nan(fabsf(u[0]), fabsf(u[1]), fabsf(u[2]));
+#pragma unroll
+        for (int k = 3; k < 8; k += 2) {
+            const float x = u[k + 1 < 8 ? k + 1 : k];
+            low = min3(low, u[k], x);
+            high = max3(high, u[k], x);
+            size = max3_nan(size, fabsf(u[k]), fabsf(x));
+        }
+    }
+    bool wild = !(size < INFINITY);          // an element is not finite
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
+        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
+        wild |= __shfl_xor_sync(0xffffffffu, (int)wild, o) != 0;
+    }
+    __half d = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f)), m = __float2half_rn(low);
+    wild |= __hisinf(d) || __hisinf(m);
+    if (wild) d = m = __ushort_as_half(0x7FFFu);                 // NaN: so is each value of the group
+    *pair = h2_bits(d, m);
+    const float df = __half2float(d), mf = __half2float(m);
+    uint32_t w = 0;
+    if (!wild && df > 0.f) {
+        // n is the quotient's nearest integer.  A product with the reciprocal (1 / d and the product off by a rounding
+        // each, of a number below 24: 15 and what d's rounding adds, at most by half where d is the smallest F16) is within
+        // 2.9e-6 of it, and the quotient's own rounding 1.5e-6; so only one that lies near a half is divided.  1.5 2^23 + y
+        // holds y's nearest integer in its last bits.
+        constexpr float kWhole = 12582912.f;
+        const float inv = __frcp_rn(df);
+        float near = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float x = __fsub_rn(u[k], mf), t = __fmaf_rn(x, inv, kWhole);
+            near = fmaxf(near, fabsf(__fmaf_rn(x, inv, __fsub_rn(kWhole, t))));
+            w += (__float_as_uint(fminf(fmaxf(t, kWhole), kWhole + 15.f)) - __float_as_uint(kWhole)) << (4 * k);
+        }
+        if (near > 0.5f - 1e-5f) {
+            w = 0;
+#pragma unroll 1
+            for (int k = 0; k < 8; k++) {
+                float x = u[0];
+#pragma unroll
+                for (int j = 1; j < 8; j++) x = j == k ? u[j] : x;
+                w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x, mf), df)), 0.f), 15.f) << (4 * k);
+            }
+        }
+    }
+    return w;
+}
+
 // Run `item` of eight elements of a new row's k and v (all heads of k, then those of v)
 // into a page of 4-bit values.  Four threads hold a group of 32 elements (the last of a
-// head may be shorter); they share its least and its largest value by two shuffles.  The
-// whole block calls this, with one row.
+// head may be shorter).  The whole block calls this, with one row.  (A thread for eight elements of both
+// was slower: with few heads half of a block had nothing to do.)
 template <class T>
 __device__ __forceinline__ void append_q4(const PagesDev& p, const AppendDev& a, int row, int item) {
-    const int h = a.by_q4.of(item), i = item - h * (4 * a.q4.groups);
-    const bool live = h < 2 * p.n_kv && 8 * i < p.hd, is_v = h >= p.n_kv;
-    const int g = is_v ? h - p.n_kv : h, d0 = 8 * i, half = is_v ? 0 : a.half;
-    const T* x = is_v ? static_cast<const T*>(a.v) + row * a.v_stride : static_cast<const T*>(a.k) + row * a.k_stride;
-    x += g * p.hd;
-    const bool turns = d0 < 2 * half, fast = a.neox ? a.group == 8 : a.group >= 4;
+    const int h = a.by_q4.of(item), i = item - h * (4 * a.q4.groups), d0 = 8 * i;
+    const bool is_v = h >= p.n_kv;
+    const int g = is_v ? h - p.n_kv : h, half = is_v ? 0 : a.half;
+    const bool live = h < 2 * p.n_kv && d0 < p.hd, turns = d0 < 2 * half, fast = a.neox ? a.group == 8 : a.group >= 4;
+    const T* x = (is_v ? static_cast<const T*>(a.v) + row * a.v_stride : static_cast<const T*>(a.k) + row * a.k_stride) + g * p.hd;
     float u[8], other[8];
 #pragma unroll
     for (int k = 0; k < 8; k++) u[k] = 0.f;
@@ -118,7 +177,7 @@ __device__ __forceinline__ void append_q4(const PagesDev& p, const AppendDev& a,
     }
     const int page = page_of(p, s, e);
     if (page < 0) return;
-    const float2* cs = a.cs + pos * a.half;
+    const float2* cs = a.cs + pos * half;
     if (live && turns) {
         if (fast && a.neox) {
             const bool first = d0 < half;
@@ -147,36 +206,13 @@ __device__ __forceinline__ void append_q4(const PagesDev& p, const AppendDev& a,
             }
         }
     }
-    float low = INFINITY, high = -INFINITY;
-    bool wild = false;
-    if (live) {
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            low = fminf(low, u[k]);
-            high = fmaxf(high, u[k]);
-            wild |= !(fabsf(u[k]) < INFINITY);
-        }
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        low = fminf(low, __shfl_xor_sync(0xffffffffu, low, o));
-        high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, o));
-        wild |= __shfl_xor_sync(0xffffffffu, (int)wild, o) != 0;
-    }
+    uint32_t pair;
+    const uint32_t w = quantize8(u, live, &pair);
     if (!live) return;
-    __half d = __float2half_rn(__fdiv_rn(__fsub_rn(high, low), 15.f)), m = __float2half_rn(low);
-    wild |= __hisinf(d) || __hisinf(m);
-    if (wild) d = m = __ushort_as_half(0x7FFFu);                 // NaN: so is each value of the group
-    const float df = __half2float(d), mf = __half2float(m);
-    uint32_t w = 0;
-    if (!wild && df > 0.f) {
-#pragma unroll
-        for (int k = 0; k < 8; k++) w |= (uint32_t)fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(u[k], mf), df)), 0.f), 15.f) << (4 * k);
-    }
     uint8_t* pages = reinterpret_cast<uint8_t*>(is_v ? p.v : p.k);
     const int in = e & ((1 << p.page_shift) - 1);
     *reinterpret_cast<uint32_t*>(pages + q4_numbers(p, a.q4, page, g, in) + 4 * i) = w;
-    if (i % 4 == 0) *reinterpret_cast<uint32_t*>(pages + q4_pairs(p, a.q4, page, g, in) + i) = h2_bits(d, m);
+    if (i % 4 == 0) *reinterpret_cast<uint32_t*>(pages + q4_pairs(p, a.q4, page, g, in) + i) = pair;
 }
 
 // One thread per item of a head of q, k or v; a row has blocks of its own for q and
@@ -280,13 +316,14 @@ cudaError_t launch_append(cudaStream_t st, const PagesDev& pd, const AppendDev& 
 }
 
 // --------------------------------------------------------------- read --
-// The values of the new rows' k and v: one thread per eight elements.  Bound by the
-// stream of rows.
+// The values of the new rows' k and v: one thread per eight elements of both, whose place it
+// works out once.  Bound by the chain length -> page -> row, and the stream of rows.  (8000 rows of 8 heads
+// of 64 values: 11 us with a thread for each of k and v and blocks of one row.)
 struct ReadDev {
     void *k, *v;
     long long k_stride, v_stride;
-    int row_blocks;
-    Div by_row_blocks, by_head, by_new;      // by row_blocks, a head's runs of eight elements, n_new
+    int items;                               // of all rows
+    Div by_row, by_head, by_new;             // by a row's items, a head's, n_new
     Q4Dev q4;
 };
 
@@ -300,24 +337,29 @@ __device__ __forceinline__ void q4_values(uint32_t w, uint32_t pair, float (&x)[
 template <class U, bool Q4>
 __global__ void __launch_bounds__(kAppendThreads) read_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ ReadDev a) {
     griddep_entry();
-    const int row = a.by_row_blocks.of(blockIdx.x), item = (blockIdx.x - row * a.row_blocks) * kAppendThreads + (int)threadIdx.x;
-    const int h = a.by_head.of(item), i = item - h * (p.hd / 8);
-    if (h >= 2 * p.n_kv) return;
-    const bool is_v = h >= p.n_kv;
-    const int g = is_v ? h - p.n_kv : h, s = a.by_new.of(row), len = p.lens[s], behind = p.n_new - (row - s * p.n_new);
+    const int item = (int)blockIdx.x * kAppendThreads + (int)threadIdx.x;
+    if (item >= a.items) return;
+    const int row = a.by_row.of(item), in_row = item - row * (p.n_kv * (p.hd / 8)), g = a.by_head.of(in_row), i = in_row - g * (p.hd / 8);
+    const int s = a.by_new.of(row), len = p.lens[s], behind = p.n_new - (row - s * p.n_new);
     if (len < behind) return;                // padding
     const int e = len - behind, page = page_of(p, s, e);
     if (page < 0) return;
     const int in = e & ((1 << p.page_shift) - 1);
-    float x[8];
+    float k[8], v[8];
     if (Q4) {
-        const uint8_t* pages = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k);
-        q4_values(*reinterpret_cast<const uint32_t*>(pages + q4_numbers(p, a.q4, page, g, in) + 4 * i),
-                  *reinterpret_cast<const uint32_t*>(pages + q4_pairs(p, a.q4, page, g, in) + 4 * (i / 4)), x);
+        const uint8_t *kp = reinterpret_cast<const uint8_t*>(p.k), *vp = reinterpret_cast<const uint8_t*>(p.v);
+        const long long n = q4_numbers(p, a.q4, page, g, in) + 4 * i, d = q4_pairs(p, a.q4, page, g, in) + 4 * (i / 4);
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(kp + n), kd = *reinterpret_cast<const uint32_t*>(kp + d),
+                       vw = *reinterpret_cast<const uint32_t*>(vp + n), vd = *reinterpret_cast<const uint32_t*>(vp + d);
+        q4_values(kw, kd, k);
+        q4_values(vw, vd, v);
     } else {
-        load_n<8>((is_v ? p.v : p.k) + ((((long long)page << p.page_shift) + in) * p.n_kv + g) * p.hd + 8 * i, x);
+        const long long at = ((((long long)page << p.page_shift) + in) * p.n_kv + g) * p.hd + 8 * i;
+        load_n<8>(p.k + at, k);
+        load_n<8>(p.v + at, v);
     }
-    store_n<8>(static_cast<U*>(is_v ? a.v : a.k) + row * (is_v ? a.v_stride : a.k_stride) + g * p.hd + 8 * i, x);
+    store_n<8>(static_cast<U*>(a.k) + row * a.k_stride + g * p.hd + 8 * i, k);
+    store_n<8>(static_cast<U*>(a.v) + row * a.v_stride + g * p.hd + 8 * i, v);
 }
 
 // --------------------------------------------------- log probabilities --
@@ -854,14 +896,14 @@ int read_rows(const llm_pages* pages, const llm_read* a, bool q4, llm_stream_t s
     const long long rows = (long long)pages->n_seqs * pages->n_new, kv = (long long)pages->n_kv_heads * pages->head_dim;
     if ((rc = check_rows("k_out", a->k_out, a->dtype, a->k_stride, kv, rows)) || (rc = check_rows("v_out", a->v_out, a->dtype, a->v_stride, kv, rows)))
         return rc;
-    const long long row_blocks = (2 * kv / 8 + kAppendThreads - 1) / kAppendThreads;
-    if (rows * row_blocks > INT_MAX) return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^31 blocks of %d threads", kAppendThreads);
+    const long long items = rows * (kv / 8);
+    if (items > INT_MAX - kAppendThreads) return fail_op(LLM_ERR_UNSUPPORTED, "more than 2^34 values");
     const PagesDev pd = pages_dev(pages);
-    const ReadDev rd{a->k_out, a->v_out, a->k_stride, a->v_stride, (int)row_blocks, Div((uint32_t)row_blocks), Div((uint32_t)(pages->head_dim / 8)),
+    const ReadDev rd{a->k_out, a->v_out, a->k_stride, a->v_stride, (int)items, Div((uint32_t)(kv / 8)), Div((uint32_t)(pages->head_dim / 8)),
                      Div((uint32_t)pages->n_new), f};
     const bool h = a->dtype == LLM_F16;
     auto k = q4 ? (h ? read_kernel<__half, true> : read_kernel<float, true>) : (h ? read_kernel<__half, false> : read_kernel<float, false>);
-    return launched(launch_dep(k, dim3((unsigned)(rows * row_blocks)), dim3(kAppendThreads), 0, stream, pd, rd), q4 ? "llm_kv_read_q4" : "llm_kv_read");
+    return launched(launch_dep(k, dim3((unsigned)((items + kAppendThreads - 1) / kAppendThreads)), dim3(kAppendThreads), 0, stream, pd, rd), q4 ? "llm_kv_read_q4" : "llm_kv_read");
 }
 
 }  // namespace

@@ -51,12 +51,13 @@ struct Q4Dev {
 };
 constexpr int kQ4Group = 32;
 
-// Byte offsets of a row's numbers and of its pairs: row `in` (of the page) of kv head g.
+// Byte offsets of a row's numbers and of its pairs: row `in` (of the page) of kv head g.  (page_bytes is below 2^32 and
+// a page has at most 2^25 rows of all heads: each product is one instruction.)
 __device__ __forceinline__ long long q4_numbers(const PagesDev& p, const Q4Dev& f, int page, int g, int in) {
-    return page * f.page_bytes + ((long long)(g << p.page_shift) + in) * (p.hd / 2);
+    return (long long)((unsigned long long)(uint32_t)page * (uint32_t)f.page_bytes + (unsigned long long)(uint32_t)((g << p.page_shift) + in) * (uint32_t)(p.hd / 2));
 }
 __device__ __forceinline__ long long q4_pairs(const PagesDev& p, const Q4Dev& f, int page, int g, int in) {
-    return page * f.page_bytes + f.scales + ((long long)(g << p.page_shift) + in) * (4 * f.groups);
+    return (long long)((unsigned long long)(uint32_t)page * (uint32_t)f.page_bytes + (unsigned long long)(uint32_t)((g << p.page_shift) + in) * (uint32_t)(4 * f.groups)) + f.scales;
 }
 
 // Division of numbers below 2^31 by a fixed one (Granlund and Montgomery, "Division by
@@ -78,7 +79,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return y;
 }
 
-// The same, but NaN if one of them is.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float y;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// max3, but NaN if one of them is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
     float y;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));

@@ -18,7 +18,7 @@ namespace llm {
 namespace {
 
 constexpr int kPlanBlocks = 8, kPlanThreads = 1024, kPlanWarps = kPlanThreads / 32;
-constexpr int kMoveThreads = 256, kMoveVecs = 2;                       // 16-byte words of a thread per item
+constexpr int kMoveThreads = 256, kMoveVecs = 4;                       // 16-byte words of a thread per item
 constexpr int kMoveBytes = kMoveThreads * kMoveVecs * 16;
 
 struct PoolDev {
