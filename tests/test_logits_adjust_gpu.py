@@ -219,3 +219,25 @@ def test_binding_refuses_what_does_not_belong_together(lib):  # noqa: F811
         lib.AdjustLogits(x["logits"], window=-1)()
     with pytest.raises(lib.LlmError):                          # the same memory as another type
         lib.AdjustLogits(x["logits"], x["logits"].view(F16)[:, :100])()
+
+
+@pytest.mark.parametrize("biases,window", [(4094, 0), (4096, 0), (6000, 7)])
+@pytest.mark.parametrize("types", [(F32, F32), (F16, F16)])
+def test_many_biases_beside_a_history(lib, biases, window, types):  # noqa: F811
+    """An entry and a count share a word up to 4095 entries; tokens of both lists, of one, and entries given twice."""
+    x = make(3, 9001, types[0], 700, biases, 1, seed=biases)
+    x["bias_ids"][:, ::3] = x["bias_ids"][:, 1::3][:, :x["bias_ids"][:, ::3].shape[1]] if biases % 3 == 0 else x["bias_ids"][:, ::3]
+    x["history"][:, ::5] = 17                                  # counted, and biased by the entries set here
+    x["bias_ids"][:, 5], x["bias_ids"][:, 9] = 17, 17
+    run(lib, x, types[1], window)
+
+
+def test_counts_that_fill_their_bits(lib):  # noqa: F811
+    """More than 2^20 tokens counted, with biases."""
+    n = (1 << 20) + 5
+    x = make(1, 5000, F32, 8, 30)
+    x["history"] = torch.full((1, n), 4, dtype=torch.int32, device="cuda")
+    x["history"][0, :100] = torch.arange(100, dtype=torch.int32, device="cuda")
+    x["history_lens"] = torch.tensor([n], dtype=torch.int32, device="cuda")
+    x["bias_ids"][0, 3], x["bias_ids"][0, 4] = 4, 50
+    run(lib, x, F32)

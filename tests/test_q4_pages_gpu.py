@@ -445,3 +445,35 @@ def test_pool_behind_32_bits(lib):  # noqa: F811
     lib.KvRead(pages, ko, vo)()
     p, r = b.slot(0, 59)
     assert torch.equal(ko[0], b.k[p, r].float()) and torch.equal(vo[0], b.v[p, r].float())
+
+
+@pytest.mark.parametrize("prefix", [0, 70])
+def test_attend_most_sequences(lib, prefix):  # noqa: F811
+    run_attend(lib, (2, 1, 16), [1 + s % 21 for s in range(4096)], 1, prefix, 8, F16, F16)
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (4, 4, 128), (8, 8, 48), (20, 4, 96)])
+@pytest.mark.parametrize("n_new", [1, 3])
+def test_attend_units_behind_one_another(lib, heads, n_new):  # noqa: F811
+    """Many short sequences: warps walk through several units, whole ones and parts."""
+    lens = [max(n_new, 1 + (53 * s) % 67) for s in range(300)]
+    run_attend(lib, heads, lens, n_new, 0, 32, F16, F32, seed=n_new)
+
+
+def test_rows_behind_the_last_do_not_matter(lib):  # noqa: F811
+    """Other numbers in the rows behind each sequence's last one, and NaN pairs or others: the same bits."""
+    b = BatchQ4(lib, [5, 13, 30, 41, 100], 1, 0, 16, 2, 64)
+    q, out = rand(1, 5, 8, 64), torch.empty(5, 8, 64, device="cuda")
+    op = lib.AttendBatch(b.pages, q, out)
+    op()
+    first = out.clone()
+    for s, n in enumerate(b.lens):
+        for e in range(n, -(-n // 16) * 16):
+            for g in range(2):
+                for which in (0, 1):
+                    p, r = int(b.table[s, e // 16]), e % 16
+                    b.bytes[which][p, (g * 16 + r) * 32:(g * 16 + r) * 32 + 32] = 0x5A
+                    at = 16 * 2 * 32 + ((g * 16 + r) * 2) * 4
+                    b.bytes[which][p, at:at + 8] = torch.tensor([1e3, -7.0, math.inf, -math.inf], dtype=F16, device="cuda").view(torch.uint8)
+    op()
+    assert torch.equal(out, first) and out.isfinite().all()
