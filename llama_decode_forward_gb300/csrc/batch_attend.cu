@@ -938,11 +938,16 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
 // PACK: up to four query rows.  The eight columns of a product hold each of them twice;
 // the second four take the probabilities' second parts, so one product adds both.
 // FULL: head_dim is HDP, so that the distances of rows and pairs are constants.
-constexpr int kQ4Stages = 3;
-constexpr int kCtas64 = 4, kCtas128 = 4, kPieces64 = 2, kPieces128 = 1;
-__host__ __device__ constexpr int q4_pieces(int hdp) { return hdp == 64 ? kPieces64 : kPieces128; }
+// What bounds it: making the values.  A step of 32 rows of heads of 64 values takes a warp some 560
+// instructions, 230 of them for the 4096 values; the logical and the half-precision operations together keep their
+// two units busy 95 % of the time (one half each).  64 sequences of 1 to 8192 rows, 8 heads of 64 (194 MB): 58 us, 3.3 TB/s, 95 us
+// as first written; 32 of 1 to 4096, 32 heads of 128 (390 MB): 103 us, 3.8 TB/s, from 179 us.  F16 pages of the
+// same rows would be 3.2 times the bytes.  Steps of 16 rows take 5 to 20 % longer; of 64 rows, 3 % less on the
+// first, 20 % more where sequences are short.  Neither more blocks on an SM nor fewer (12 to 20 warps), nor an order of rows
+// without bank conflicts, changed these by more than 4 %.
+constexpr int kQ4Pieces = 2, kQ4Stages = 2;
 // Shared memory of a block's rings.
-__host__ __device__ constexpr int q4_rings(int hdp) { return kSuffixWarps * kQ4Stages * 2 * (2 * q4_pieces(hdp)) * 5 * hdp; }
+__host__ __device__ constexpr int q4_rings(int hdp) { return kSuffixWarps * kQ4Stages * 2 * (2 * kQ4Pieces) * 5 * hdp; }
 
 // A 16-byte asynchronous copy to shared memory, or zeros.
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool there) {
@@ -953,7 +958,7 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? kCtas64 : nt == 2 ? 3 : 2) : (nt == 1 ? kCtas128 : 2); }
+__host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? 4 : nt == 2 ? 3 : 2) : (nt == 1 ? 3 : 2); }
 
 // Query rows of a unit: more than 16 are taken at once (up to 24, where the registers allow) as
 // long as one unit then does, since every unit makes the values anew.
@@ -983,7 +988,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
     suffix_q4_kernel(const __grid_constant__ PagesDev p, const __grid_constant__ AttendDev a, int first) {
     static_assert(!PACK || NT == 1, "four query rows");
     constexpr int C = HDP / 64, KS = HDP / 16, RU = 8 * NT;  // chunks of 64 dims; MMA steps of a dot product, and MMA tiles of the sums
-    constexpr int H = q4_pieces(HDP), OCT = 2 * H;           // pieces and octets of a step
+    constexpr int H = kQ4Pieces, OCT = 2 * H;                // pieces and octets of a step
     constexpr int S = kQ4Stages, NUMBERS = OCT * 4 * HDP, PAIRS = OCT * HDP, STAGE = 2 * (NUMBERS + PAIRS);
     extern __shared__ __align__(16) int seqs[];
     if (first) griddep_wait();
