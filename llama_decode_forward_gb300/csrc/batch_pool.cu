@@ -111,16 +111,17 @@ __device__ __forceinline__ N block_scan(N x, N* tmp, N* all) {
     __syncthreads();
     if (lane == 31) tmp[warp] = s;
     __syncthreads();
-    N before = 0, sum = 0;
+    N t = tmp[lane];                         // (as many warps as lanes)
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; w++) {
-        const N v = tmp[w];
-        before += w < warp ? v : 0;
-        sum += v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const N v = __shfl_up_sync(0xffffffffu, t, o);
+        if (lane >= o) t += v;
     }
-    *all = sum;
-    return before + s - x;
+    *all = __shfl_sync(0xffffffffu, t, 31);
+    const N before = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+    return (warp > 0 ? before : 0) + s - x;
 }
+static_assert(kPlanWarps == 32, "a warp adds up the warps' sums");
 
 // The run of `n` things that block `rank` handles: whole warps' words of 32.
 __device__ __forceinline__ void share_of(int n, int rank, int blocks, int* lo, int* hi) {
@@ -217,10 +218,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         copy = tail > 0 && !stays;
         need = pages_of(now, shift) - full - stays;
     }
-    long long all_need;
-    int all_copy;
-    const long long need_before = block_scan((long long)need, tmp_wide, &all_need);
-    const int copy_before = block_scan(copy, tmp, &all_copy);
+    // both sums in one: copies in the lower bits (a thread has at most one)
+    long long both;
+    const long long both_before = block_scan((long long)need << 12 | copy, tmp_wide, &both);
+    const long long all_need = both >> 12, need_before = both_before >> 12;
+    const int all_copy = (int)(both & 4095), copy_before = (int)(both_before & 4095);
     // pages, in runs of 32: free ones are held by no sequence, in whole or in part
     int lo, hi;
     share_of(p.n_pages, rank, BLOCKS, &lo, &hi);
