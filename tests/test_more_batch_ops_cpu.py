@@ -121,7 +121,7 @@ def test_pool_calls_refuse_their_own_arguments():
     (dict(repetition=P + 2), BAD), (dict(frequency=P + 1), BAD), (dict(presence=P + 2), BAD), (dict(bias_ids=P + 2), BAD),
     (dict(bias=P + 3), BAD), (dict(masks=P + 2), BAD), (dict(mask_of=P + 2), BAD), (dict(stride=99), BAD), (dict(out_stride=-100), BAD),
     (dict(history_stride=49), BAD), (dict(mask_stride=3), BAD), (dict(out=P), BAD), (dict(out=P, out_dtype=L.LLM_F32, out_stride=104), BAD),
-    (dict(n_rows=1 << 28), UNSUP),
+    (dict(n_rows=1 << 28, vocab=1 << 17, stride=1 << 17, out_stride=1 << 17, mask_stride=1 << 12), UNSUP),
 ])
 def test_adjust_refused(kw, status):
     refused(B._lib.llm_logits_adjust(ref(adjust(**kw)), None), status)
