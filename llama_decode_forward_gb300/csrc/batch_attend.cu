@@ -864,11 +864,11 @@ Plan make_plan(const llm_pages* p, const llm_attend* a, int sms, bool q4) {
         pl.prefix_blocks = (int)std::max<long long>(1, std::min<long long>(sms, tiles / 2));
         pl.prefix_rows = (units + pl.prefix_blocks) * 256;
     }
+    pl.unit_rows = q4 ? unit_rows_q4((int)srows, p->head_dim) : unit_rows((int)srows);
     if (p->max_pages > 0) {
         // workers for as many blocks as an SM holds at once, but no more than the
         // longest sequences could keep busy
-        const int ru = q4 ? unit_rows_q4((int)srows, p->head_dim) : unit_rows((int)srows);
-        pl.unit_rows = ru;
+        const int ru = pl.unit_rows;
         const long long units = (long long)p->n_kv_heads * ((srows + ru - 1) / ru),
                         most = units * p->n_seqs * (((long long)p->max_pages * p->page_size + 15) / 16 + kUnit),
                         blocks = (most + kQuantum * kSuffixWarps - 1) / (kQuantum * kSuffixWarps);
