@@ -660,6 +660,14 @@ typedef struct {
 int64_t llm_batch_pages_bytes(const llm_handle *h, int32_t n_pages, int32_t page_size);
 int llm_decode_batch(llm_handle *h, const llm_batch *b);
 
+/* The same step on pages of 4-bit values (llm_kv_append_q4, llm_attend_batch_q4): pages
+ * holds llm_batch_q4_pages_bytes() bytes, [n_layers][K, V][n_pages] pages of
+ * llm_q4_page_bytes(); page_size is at least 8 and head_dim a multiple of 16 (UNSUPPORTED otherwise).  The
+ * prompt's rows stay FP16, in the handle's cache.  A handle may take steps of both kinds in
+ * turn, each on pages of its own. */
+int64_t llm_batch_q4_pages_bytes(const llm_handle *h, int32_t n_pages, int32_t page_size);
+int llm_decode_batch_q4(llm_handle *h, const llm_batch *b);
+
 /* ------------------------------------------------------------ GGUF files --
  * A model file in the GGUF version 3 layout of "Loading GGUF with the FFM API"
  * (codeloopback.dev, llm-gguf-loader-ffm): a 24-byte header (magic "GGUF",

@@ -452,11 +452,11 @@ class BatchDecoder:
     int32 [n_seqs, max_pages] are this object's tensors, to be written before each
     step; logits float32 [n_seqs, n_new, vocab] is the step's result.  ``pages``
     holds every layer's K and V pages; page_table starts with each sequence's own
-    pages in a row.  step() enqueues on the decoder's stream; where that is not the
+    pages in a row.  q4: pages of 4-bit values (llm_decode_batch_q4).  step() enqueues on the decoder's stream; where that is not the
     current one, it runs behind what the current stream has been given (the tensors'
     new values) and before what it is given next."""
 
-    def __init__(self, decoder, n_seqs: int, max_len: int, prefix_len: int, n_new: int = 1, page_size: int = 16):
+    def __init__(self, decoder, n_seqs: int, max_len: int, prefix_len: int, n_new: int = 1, page_size: int = 16, q4: bool = False):
         _int32(n_seqs=n_seqs, max_len=max_len, prefix_len=prefix_len, n_new=n_new, page_size=page_size)
         if page_size < 1:
             raise ValueError(f"page_size {page_size} is not positive")
@@ -465,13 +465,13 @@ class BatchDecoder:
         max_pages = -(-max_len // page_size)
         n_pages = n_seqs * max_pages
         _int32(n_pages=n_pages)
-        self.decoder = decoder
+        self.decoder, self.q4 = decoder, bool(q4)
         self._device, self._stream = dev, _torch_stream(decoder.stream, dev)
         # the tensors are the decoder's stream's: filled there, and their memory, when it is
         # given back, goes to later work of that stream only
         with torch.cuda.stream(self._stream):
-            self.pages = torch.zeros(max(1, _b.llm_batch_pages_bytes(decoder.h, n_pages, page_size)) // 2, dtype=torch.float16,
-                                     device=dev)
+            n_bytes = max(1, _b.llm_batch_pages_bytes(decoder.h, n_pages, page_size, q4))
+            self.pages = torch.zeros(n_bytes if q4 else n_bytes // 2, dtype=torch.uint8 if q4 else torch.float16, device=dev)
             self.page_table = torch.arange(n_pages, dtype=torch.int32, device=dev).view(n_seqs, max_pages)
             self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
             self.tokens = torch.zeros(n_seqs, n_new, dtype=torch.int32, device=dev)
@@ -489,10 +489,11 @@ class BatchDecoder:
         sequences hold is then up to PagesUpdate, which page_table and lens are written by."""
         if refs.shape[0] != self.struct.n_pages:
             raise ValueError(f"{refs.shape[0]} counts of holders for {self.struct.n_pages} pages")
-        c = _b.llm_get_config(self.decoder.h)
-        kv = self.pages[:2 * c.n_layers * refs.shape[0] * self.struct.page_size * c.n_kv_heads * c.head_dim]
-        kv = kv.view(c.n_layers, 2, refs.shape[0], self.struct.page_size, c.n_kv_heads, c.head_dim)
-        return PagePool(kv[:, 0], kv[:, 1], self.page_table, self.lens, refs, err=err)
+        c, p = _b.llm_get_config(self.decoder.h), self.struct
+        page = (_q4_page_bytes(p.page_size, c.n_kv_heads, c.head_dim),) if self.q4 else (p.page_size, c.n_kv_heads, c.head_dim)
+        shape = torch.Size((c.n_layers, 2, p.n_pages, *page))
+        kv = self.pages[:shape.numel()].view(shape)
+        return PagePool(kv[:, 0], kv[:, 1], self.page_table, self.lens, refs, page_size=p.page_size, err=err)
 
     def _use_on(self, stream) -> None:
         """What `stream` is given from now on may use the tensors."""
@@ -504,12 +505,12 @@ class BatchDecoder:
 
     def step(self) -> None:
         if _current_stream(self._device.index) == self._stream.cuda_stream:
-            _b.llm_decode_batch(self.decoder.h, self.struct)
+            _b.llm_decode_batch(self.decoder.h, self.struct, self.q4)
             return
         current = torch.cuda.current_stream(self._device)
         self._stream.wait_stream(current)
         try:
-            _b.llm_decode_batch(self.decoder.h, self.struct)
+            _b.llm_decode_batch(self.decoder.h, self.struct, self.q4)
         finally:
             self._use_on(current)
 

@@ -171,6 +171,8 @@ _SIGS = {
     "llm_logprobs": ([_vp, _vp], _int),
     "llm_batch_pages_bytes": ([_vp, _i32, _i32], ctypes.c_int64),
     "llm_decode_batch": ([_vp, _vp], _int),
+    "llm_batch_q4_pages_bytes": ([_vp, _i32, _i32], ctypes.c_int64),
+    "llm_decode_batch_q4": ([_vp, _vp], _int),
 }
 
 
@@ -286,19 +288,20 @@ def llm_prefill_f16_copy(h, enable: bool = True) -> None:
     _check(_lib.llm_prefill_f16_copy(h, 1 if enable else 0), h)
 
 
-def llm_batch_pages_bytes(h, n_pages: int, page_size: int) -> int:
+def llm_batch_pages_bytes(h, n_pages: int, page_size: int, q4: bool = False) -> int:
     for name, v in (("n_pages", n_pages), ("page_size", page_size)):
         if not -2 ** 31 <= int(v) < 2 ** 31:           # (ctypes would cut it off)
             raise ValueError(f"{name} {v} is not a 32-bit integer")
-    n = int(_lib.llm_batch_pages_bytes(h, int(n_pages), int(page_size)))
+    n = int((_lib.llm_batch_q4_pages_bytes if q4 else _lib.llm_batch_pages_bytes)(h, int(n_pages), int(page_size)))
     if n < 0:
         raise LlmError(n, "n_pages or page_size")
     return n
 
 
-def llm_decode_batch(h, batch: llm_batch) -> None:
-    """One step of a batch of sequences, enqueued on the handle's stream."""
-    _check(_lib.llm_decode_batch(h, ctypes.addressof(batch)), h)
+def llm_decode_batch(h, batch: llm_batch, q4: bool = False) -> None:
+    """One step of a batch of sequences, enqueued on the handle's stream; q4: on pages
+    of 4-bit values (llm_decode_batch_q4)."""
+    _check((_lib.llm_decode_batch_q4 if q4 else _lib.llm_decode_batch)(h, ctypes.addressof(batch)), h)
 
 
 def llm_sync(h):

@@ -985,10 +985,7 @@ int check_attend(const llm_pages* p, const llm_attend* a) {
 
 }  // namespace
 
-namespace {
-
-// llm_attend_batch; q4: over pages of 4-bit values.
-int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit, bool q4) {
+int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit, bool q4) {
     Q4Dev f{};
     int rc = q4 ? check_pages_q4(pages, true, &f) : check_pages(pages, true);
     if (rc || (rc = check_attend(pages, a))) return rc;
@@ -1062,6 +1059,8 @@ int attend(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int
                     "llm_attend_batch (join)");
 }
 
+namespace {
+
 int64_t attend_workspace(const llm_pages* pages, const llm_attend* a, bool q4) {
     Q4Dev f{};
     int rc = q4 ? check_pages_q4(pages, false, &f) : check_pages(pages, false);
@@ -1071,10 +1070,6 @@ int64_t attend_workspace(const llm_pages* pages, const llm_attend* a, bool q4) {
 
 }  // namespace
 
-int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit) {
-    return attend(pages, a, stream, timeout, wait_limit, false);
-}
-
 }  // namespace llm
 
 using namespace llm;
@@ -1083,8 +1078,8 @@ extern "C" int64_t llm_attend_batch_workspace(const llm_pages* pages, const llm_
 extern "C" int64_t llm_attend_batch_q4_workspace(const llm_pages* pages, const llm_attend* a) { return attend_workspace(pages, a, true); }
 
 extern "C" int llm_attend_batch(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
-    return attend_batch(pages, a, stream, nullptr, 0);
+    return attend_batch(pages, a, stream, nullptr, 0, false);
 }
 extern "C" int llm_attend_batch_q4(const llm_pages* pages, const llm_attend* a, llm_stream_t stream) {
-    return attend(pages, a, stream, nullptr, 0, true);
+    return attend_batch(pages, a, stream, nullptr, 0, true);
 }

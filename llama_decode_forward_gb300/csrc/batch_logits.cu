@@ -84,9 +84,10 @@ __device__ __forceinline__ void store4(float* p, bool vec, uint32_t in, const fl
 }
 __device__ __forceinline__ void store4(__half* p, bool vec, uint32_t in, const float (&x)[4]) {
     if (vec) {
-        if (in)
-            __stcs(reinterpret_cast<uint2*>(p), make_uint2(h2_bits(__float2half_rn(x[0]), __float2half_rn(x[1])),
-                                                           h2_bits(__float2half_rn(x[2]), __float2half_rn(x[3]))));
+        if (in) {
+            const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
+            __stcs(reinterpret_cast<uint2*>(p), make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < 4; k++)

@@ -892,7 +892,16 @@ extern "C" int64_t llm_batch_pages_bytes(const llm_handle* h, int32_t n_pages, i
     return rows > LLONG_MAX / row ? LLM_ERR_INVALID_ARG : rows * row;
 }
 
-extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
+extern "C" int64_t llm_batch_q4_pages_bytes(const llm_handle* h, int32_t n_pages, int32_t page_size) {
+    if (!alive(h) || n_pages < 0) return LLM_ERR_INVALID_ARG;
+    const int64_t page = llm_q4_page_bytes(page_size, h->cfg.n_kv_heads, h->cfg.head_dim);
+    if (page < 0) return page;
+    const long long all = 2LL * h->cfg.n_layers * n_pages;
+    return all > LLONG_MAX / page ? LLM_ERR_INVALID_ARG : all * page;
+}
+
+// llm_decode_batch; q4: on pages of 4-bit values.
+static int decode_batch(llm_handle* h, const llm_batch* b, bool q4) {
     LIVE_OR_RETURN(h);
     if (!b) return fail(h, LLM_ERR_INVALID_ARG, "the batch is NULL");
     if (h->broken) return fail(h, LLM_ERR_STATE, "handle has a device error; call llm_reset");
@@ -914,8 +923,9 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
         ((reinterpret_cast<uintptr_t>(b->tokens) | reinterpret_cast<uintptr_t>(b->lens) | reinterpret_cast<uintptr_t>(b->page_table) |
           reinterpret_cast<uintptr_t>(b->err)) & 3))
         return fail(h, LLM_ERR_INVALID_ARG, "a pointer of the batch is not aligned");
-    if (llm_batch_pages_bytes(h, b->n_pages, b->page_size) < 0)
-        return fail(h, LLM_ERR_INVALID_ARG, "n_pages %d of %d rows: negative, not a power of two, or too large", b->n_pages, b->page_size);
+    const int64_t all = q4 ? llm_batch_q4_pages_bytes(h, b->n_pages, b->page_size) : llm_batch_pages_bytes(h, b->n_pages, b->page_size);
+    if (all == LLM_ERR_UNSUPPORTED) return fail(h, LLM_ERR_UNSUPPORTED, "%s", llm_last_error(nullptr));
+    if (all < 0) return fail(h, LLM_ERR_INVALID_ARG, "n_pages %d of %d rows: negative, not a power of two, or too large", b->n_pages, b->page_size);
     // what the operators refuse, before anything is enqueued
     const llm_pages pages{b->n_seqs, b->n_new, b->prefix_len, b->page_size, b->n_pages, b->max_pages, h->cfg.n_kv_heads, h->cfg.head_dim,
                           static_cast<uint16_t*>(b->pages), static_cast<uint16_t*>(b->pages), b->page_table, b->lens, b->err};
@@ -923,7 +933,7 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     at.n_heads = h->cfg.n_heads;
     at.q_dtype = LLM_F32;
     at.out_dtype = LLM_F16;
-    const int64_t need = llm_attend_batch_workspace(&pages, &at);
+    const int64_t need = q4 ? llm_attend_batch_q4_workspace(&pages, &at) : llm_attend_batch_workspace(&pages, &at);
     if (need < 0) return fail(h, (int)need, "%s", llm_last_error(nullptr));
     if (b->n_seqs == 0) return LLM_OK;
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
@@ -969,7 +979,7 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     int launches = 0;
     try {
         rc = decode_batch_rows(pc, *b, h->prefill_ws, reinterpret_cast<float*>(h->batch_tab.ptr()), h->batch_tab_rows, h->batch_ws.ptr(),
-                               (int64_t)h->batch_ws.bytes, &why, &launches);
+                               (int64_t)h->batch_ws.bytes, q4, &why, &launches);
     } catch (const std::bad_alloc&) {
         rc = LLM_ERR_NO_MEMORY;
         why = "allocating the tensor maps";
@@ -977,6 +987,9 @@ extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) {
     h->launches += launches;
     return rc ? fail(h, rc, "batch step: %s", why ? why : llm_last_error(nullptr)) : LLM_OK;
 }
+
+extern "C" int llm_decode_batch(llm_handle* h, const llm_batch* b) { return decode_batch(h, b, false); }
+extern "C" int llm_decode_batch_q4(llm_handle* h, const llm_batch* b) { return decode_batch(h, b, true); }
 
 extern "C" int llm_prefill(llm_handle* h, const int32_t* tokens_host, int32_t n, int32_t pos0, float* logits_host,
                            int32_t* argmax_host) {

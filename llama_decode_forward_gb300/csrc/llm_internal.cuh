@@ -224,13 +224,14 @@ void check_host_memory();
 int fail_op(int status, const char* fmt, ...);
 // llm_attend_batch, with a word that waits which gave up set to kErrTimeout (or nullptr) and
 // a test's limit of the waits' probes (0: the usual one).
-int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit);
+// q4: over pages of 4-bit values.
+int attend_batch(const llm_pages* pages, const llm_attend* a, cudaStream_t stream, int* timeout, int wait_limit, bool q4);
 // A step of a batch (llm_decode_batch): `ws` holds prefill_workspace_bytes(c), tab the
 // angles of positions 0 .. tab_rows-1, attend_ws the attention's workspace.  Returns a
 // status; a CUDA error's text and the failing step are in *why (otherwise the reason is
-// llm_last_error(NULL)'s).  *launches counts kernels.
+// llm_last_error(NULL)'s).  *launches counts kernels.  q4: b.pages are pages of 4-bit values.
 int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* tab, int tab_rows, void* attend_ws,
-                      int64_t attend_ws_bytes, const char** why, int* launches);
+                      int64_t attend_ws_bytes, bool q4, const char** why, int* launches);
 cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_host, int n, int pos0, const char** msg);
 
 __host__ __device__ inline int dtype_bytes_x16(int wtype) {   // bytes per element, times 16

@@ -1300,7 +1300,7 @@ cudaError_t prefill_f16(const PrefillCtx& c, void* ws, const int32_t* tokens_hos
 }
 
 int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* tab, int tab_rows, void* attend_ws,
-                      int64_t attend_ws_bytes, const char** why, int* launches) {
+                      int64_t attend_ws_bytes, bool q4, const char** why, int* launches) {
     BatchBuffers bb;
     *launches = 0;
     *why = nullptr;
@@ -1338,7 +1338,8 @@ int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* 
     auto norm = [&](const float* gain) { return launch_dep(rmsnorm_rows_f16_kernel, norm_grid, norm_block, 0, c.st, bb.X, n, c.dim, gain, c.eps, bb.Xh); };
     BT_CK(launch_dep(embed_batch_kernel, dim3(n), dim3(256), 0, c.st, b.tokens, b.lens, b.n_new, c.vocab, c.embd, c.wtype, c.dim, bb.X, c.err),
           "embedding");
-    const size_t side = (size_t)b.n_pages * b.page_size * c.kv_dim;      // one layer's K or V pages
+    // 16-bit words of one layer's K or V pages
+    const size_t side = (size_t)b.n_pages * (q4 ? (size_t)llm_q4_page_bytes(b.page_size, c.n_kv, c.hd) / 2 : (size_t)b.page_size * c.kv_dim);
     for (int l = 0; l < c.n_layers; l++) {
         const LayerDev& L = c.layers[l];
         uint16_t* kp = static_cast<uint16_t*>(b.pages) + (size_t)(2 * l) * side;
@@ -1350,12 +1351,12 @@ int decode_batch_rows(const PrefillCtx& c, const llm_batch& b, void* ws, float* 
         // q is rotated in place and stays F32, as in the decode step
         llm_append ap{c.n_heads, c.rope_dims, c.neox, tab_rows, LLM_F32, LLM_F32, bb.QKV, bb.QKV + c.q_dim, bb.QKV + c.q_dim + c.kv_dim,
                       qkv_w, qkv_w, qkv_w, bb.QKV, qkv_w, tab};
-        int rc = llm_kv_append(&pages, &ap, c.st);
+        int rc = q4 ? llm_kv_append_q4(&pages, &ap, c.st) : llm_kv_append(&pages, &ap, c.st);
         if (rc) return rc;
         // the prompt's rows are the handle's cache; the output is the O projection's operand
         llm_attend at{c.n_heads, LLM_F32, LLM_F16, 1.0f / c.attn_div, bb.QKV, qkv_w, bb.Ah, c.q_dim,
                       reinterpret_cast<const uint16_t*>(L.kc), reinterpret_cast<const uint16_t*>(L.vc), c.kv_dim, attend_ws, attend_ws_bytes};
-        rc = attend_batch(&pages, &at, c.st, c.batch_err, c.batch_wait_limit);
+        rc = attend_batch(&pages, &at, c.st, c.batch_err, c.batch_wait_limit, q4);
         if (rc) return rc;
         *launches += 2 + (b.prefix_len > 0) + (b.max_pages > 0);
         GemmOut oo{nullptr, nullptr, bb.X, nullptr};

@@ -178,3 +178,10 @@ def test_binding_refuses_sizes_that_32_bits_do_not_hold():
             L.q4_pages(1, *args)
     with pytest.raises(ValueError, match="32-bit"):
         L.AdjustLogits(torch.zeros(2, 10), window=big)
+
+
+def test_decode_batch_of_4_bits_refuses_a_dead_handle():
+    b = B.llm_batch(n_seqs=1, n_new=1)
+    for h in (None, 0x1000):
+        assert B._lib.llm_decode_batch_q4(h, ctypes.addressof(b)) == BAD
+        assert B._lib.llm_batch_q4_pages_bytes(h, 1, 16) == BAD
