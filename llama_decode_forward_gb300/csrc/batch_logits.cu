@@ -160,26 +160,27 @@ __global__ void __launch_bounds__(kAdjThreads, 3) adjust_kernel(const __grid_con
         for (int i = threadIdx.x * 4; i < n_words + 4; i += 4 * kAdjThreads) *reinterpret_cast<uint4*>(words + i) = make_uint4(0, 0, 0, 0);
         __syncthreads();
         // take(i, place) for the entries i of a list that name a token of this block, four of them requested at a time
-        auto walk = [&](const int* ids, int n, auto take) {
-            for (int i = threadIdx.x; i < n; i += 4 * kAdjThreads) {
-                int at[4];
+        // (unsigned: a list has up to 2^31 - 1 entries, and the step behind the last one passes that)
+        auto walk = [&](const int* ids, uint32_t n, auto take) {
+            for (uint32_t i = threadIdx.x; i < n; i += 4 * kAdjThreads) {
+                uint32_t at[4];
 #pragma unroll
-                for (int k = 0; k < 4; k++) at[k] = i + k * kAdjThreads < n ? ids[i + k * kAdjThreads] - first : -1;
+                for (int k = 0; k < 4; k++) at[k] = i + k * kAdjThreads < n ? (uint32_t)ids[i + k * kAdjThreads] - (uint32_t)first : UINT_MAX;
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    if ((uint32_t)at[k] < (uint32_t)n_here) take(i + k * kAdjThreads, at[k]);
+                    if (at[k] < (uint32_t)n_here) take(i + k * kAdjThreads, (int)at[k]);
             }
         };
         if (counted) {
             const int h1 = max(0, min(a.history_lens[r], a.max_history)), h0 = a.window > 0 ? max(0, h1 - a.window) : 0;
-            walk(a.history + r * a.history_stride + h0, h1 - h0, [&](int, int at) {
+            walk(a.history + r * a.history_stride + h0, (uint32_t)(h1 - h0), [&](uint32_t, int at) {
                 if (atomicAdd(words + at, 1u) == 0) list[atomicAdd(listed, 1u)] = (uint16_t)at;
             });
         }
         // the larger entry takes the place above the count
         const uint32_t low = counted && !a.two ? (1u << kAdjCountBits) - 1 : 0u;
-        walk(a.bias_ids + r * a.n_bias, a.n_bias, [&](int i, int at) {
-            const uint32_t e = (uint32_t)(i + 1) << (low ? kAdjCountBits : 0);
+        walk(a.bias_ids + r * a.n_bias, (uint32_t)a.n_bias, [&](uint32_t i, int at) {
+            const uint32_t e = (i + 1) << (low ? kAdjCountBits : 0);
             uint32_t old = 0, seen;
             for (;; old = seen) {
                 seen = atomicCAS((a.two ? second : words) + at, old, e | (old & low));

@@ -241,3 +241,33 @@ def test_counts_that_fill_their_bits(lib):  # noqa: F811
     x["history_lens"] = torch.tensor([n], dtype=torch.int32, device="cuda")
     x["bias_ids"][0, 3], x["bias_ids"][0, 4] = 4, 50
     run(lib, x, F32)
+
+
+def test_lists_of_as_many_entries_as_31_bits_count(lib):  # noqa: F811
+    """Entries up to the last places that an int32 names, among others that are no tokens: what the same tokens give in
+    short lists."""
+    n = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("not enough memory for lists of 2^31 entries")
+    places = [0, 1, 511, 512, 2047, 2048, n - 4096, n - 2049, n - 2048, n - 513, n - 512, n - 2, n - 1]
+    tokens = torch.tensor([[17, 4, 17, 4999, 0, 17, 4, 250, 17, 9, 4, 250, 17]], dtype=torch.int32, device="cuda")
+    x = make(1, 5000, F32, 1)
+    x["history"], x["history_lens"] = tokens, torch.tensor([len(places)], dtype=torch.int32, device="cuda")
+    many = torch.full((1, n), -1, dtype=torch.int32, device="cuda")
+    many[0, places] = tokens[0]
+    y = {**x, "history": many, "history_lens": torch.tensor([n], dtype=torch.int32, device="cuda")}
+    out = torch.empty(1, 5000, device="cuda")
+    lib.AdjustLogits(**{**y, "out": out})()
+    check(out, *exact(x, 0))
+    lib.AdjustLogits(**{**y, "out": out}, window=n - 2)()                           # without the first two
+    x["history"], x["history_lens"] = tokens[:, 2:], x["history_lens"] - 2
+    check(out, *exact(x, 0))
+    # biases (the last entry of a token counts), alone and beside that history
+    values = torch.zeros(1, n, device="cuda")
+    b = rand(5, 1, len(places))
+    values[0, places] = b[0]
+    short, long = {"bias_ids": tokens, "bias": b}, {"bias_ids": many, "bias": values}
+    lib.AdjustLogits(x["logits"], out, **long)()
+    check(out, *exact({"logits": x["logits"], **short}, 0))
+    lib.AdjustLogits(**{**y, **long, "out": out}, window=n - 2)()
+    check(out, *exact({**x, **short}, 0))
