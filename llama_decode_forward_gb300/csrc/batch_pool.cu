@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         todo[threadIdx.x] = make_int4(full, held, wrong ? -2 : parent, 0);
         if (tail > 0) part = p.table[(long long)parent * p.max_pages + full];
     }
-    for (int j = gtid; j < p.n_pages; j += BLOCKS * kPlanThreads) {
+    // (unsigned: the step behind the last of up to 2^31 - 65 pages passes 2^31)
+    for (uint32_t j = gtid; j < (uint32_t)p.n_pages; j += BLOCKS * kPlanThreads) {
         write<ONE>(refs + j, p.refs[j]);
         write<ONE>(first + j, INT_MAX);
     }

@@ -316,3 +316,33 @@ def test_pools_behind_32_bits(lib):  # noqa: F811
     c()
     assert int(c.n_live) == n_pages - 1 and table.tolist() == [[7, far[1]], [7, n_pages - 2]]
     assert int(k[1, 7].float().mean()) == 9 and int(v[0, 7].float().mean()) == 11 and pool.errors() == 0
+
+
+def test_pools_of_as_many_pages_as_31_bits_count(lib):  # noqa: F811
+    """Tables alone over the largest pool: its last pages are counted, given out and moved as the others."""
+    n = 2 ** 31 - 65
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough memory for the counts of 2^31 pages")
+    z = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    refs, table, lens = torch.ones(n, dtype=torch.int32, device="cuda"), z(2, 4) - 1, z(2)
+    refs[[5, 2 ** 30, n - 3, n - 1]] = 0
+    pool = lib.PagePool(None, None, table, lens, refs, page_size=1)
+    rows = dev([3, 1])
+    op = lib.PagesUpdate(pool, None, rows)
+    op()
+    assert pool.errors() == 0 and table.tolist() == [[5, 2 ** 30, n - 3, -1], [n - 1, -1, -1, -1]] and lens.tolist() == [3, 1]
+    assert int(refs.min()) == 1 and int(refs.max()) == 1
+    rows[1] = 2
+    op()                                                           # nothing is free
+    assert pool.errors() == lib.LLM_PAGES_FULL and lens.tolist() == [3, 1] and int(refs.min()) == 1
+    pool.err.zero_()
+    rows[:] = dev([0, 1])
+    op()
+    assert pool.errors() == 0 and lens.tolist() == [0, 1] and (refs == 0).nonzero().flatten().tolist() == [5, 2 ** 30, n - 3]
+    del op
+    refs[n - 2], refs[n - 1] = 7, 9
+    c = lib.PagesCompact(pool)
+    c()
+    assert pool.errors() == 0 and int(c.n_live) == n - 3 and table[1].tolist() == [2 ** 30, -1, -1, -1]
+    assert [int(refs[j]) for j in (5, 2 ** 30, n - 4, n - 3, n - 2, n - 1)] == [7, 9, 1, 0, 0, 0]
+    assert [int(c.moved[j]) for j in (0, 5, 2 ** 30, n - 4, n - 3, n - 2, n - 1)] == [0, -1, -1, n - 4, -1, 5, 2 ** 30]
