@@ -186,14 +186,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         if (q.z == -2) continue;
         const int* mine = p.table + (long long)(s0 + i0) * p.max_pages;
         // (a sequence that goes on from itself keeps its whole pages: only the others change hands)
-        for (int i = (q.z == s0 + i0 ? q.x : 0) + lane; i < q.y; i += 32) {
+        // (entries are unsigned in every loop: with pages of one row a sequence has up to 2^31 - 2, and the step behind
+        // them passes 2^31)
+        for (uint32_t i = (uint32_t)(q.z == s0 + i0 ? q.x : 0) + lane; i < (uint32_t)q.y; i += 32) {
             const int j = mine[i];
             if (j < 0 || j >= p.n_pages) wrong |= LLM_PAGES_BAD_PAGE;
             else atomicSub(refs + j, 1);
         }
         if (q.z == s0 + i0) continue;
         const int* theirs = p.table + (long long)max(q.z, 0) * p.max_pages;
-        for (int i = lane; i < q.x; i += 32) {
+        for (uint32_t i = lane; i < (uint32_t)q.x; i += 32) {
             const int j = theirs[i];
             w.source[(long long)(s0 + i0) * p.max_pages + i] = j;
             if (j < 0 || j >= p.n_pages) wrong |= LLM_PAGES_BAD_PAGE;
@@ -331,8 +333,9 @@ __global__ void __launch_bounds__(kMoveThreads) update_move_kernel(const __grid_
         const int total = pages_of(r.w, shift), given = r.x + q.z;                 // the first entry with a fresh page
         int* mine = p.table + (long long)s * p.max_pages;
         if (q.y != s)
-            for (int i = lane; i < r.x; i += 32) mine[i] = w.source[(long long)s * p.max_pages + i];
-        for (int i = r.x + lane; i < max(total, q.x); i += 32) mine[i] = i < given ? r.z : i < total ? w.fresh[q.w + i - given] : -1;
+            for (uint32_t i = lane; i < (uint32_t)r.x; i += 32) mine[i] = w.source[(long long)s * p.max_pages + i];
+        for (uint32_t i = (uint32_t)r.x + lane; i < (uint32_t)max(total, q.x); i += 32)
+            mine[i] = i < (uint32_t)given ? r.z : i < (uint32_t)total ? w.fresh[(uint32_t)q.w + (i - given)] : -1;
         if (lane == 0) p.lens[s] = r.w;
     }
     if (p.n_layers == 0) return;
@@ -430,7 +433,7 @@ __global__ void __launch_bounds__(kMoveThreads)
         const long long room = (long long)p.max_pages << p.page_shift;
         if (lane == 0 && len > room) flag(p.err, LLM_PAGES_BAD_LEN);
         const int held = pages_of(max(0ll, min((long long)len, room)), p.page_shift);
-        for (int i = lane; i < held; i += 32) {
+        for (uint32_t i = lane; i < (uint32_t)held; i += 32) {
             const long long x = (long long)s * p.max_pages + i;
             const int j = p.table[x], to = j >= 0 && j < p.n_pages ? moved[j] : -1;
             if (to < 0) flag(p.err, LLM_PAGES_BAD_PAGE);

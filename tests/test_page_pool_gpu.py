@@ -346,3 +346,22 @@ def test_pools_of_as_many_pages_as_31_bits_count(lib):  # noqa: F811
     assert pool.errors() == 0 and int(c.n_live) == n - 3 and table[1].tolist() == [2 ** 30, -1, -1, -1]
     assert [int(refs[j]) for j in (5, 2 ** 30, n - 4, n - 3, n - 2, n - 1)] == [7, 9, 1, 0, 0, 0]
     assert [int(c.moved[j]) for j in (0, 5, 2 ** 30, n - 4, n - 3, n - 2, n - 1)] == [0, -1, -1, n - 4, -1, 5, 2 ** 30]
+
+
+def test_sequences_of_as_many_pages_as_31_bits_count(lib):  # noqa: F811
+    """The last entries of a table of 2^31 - 2 pages of one row are given up and taken again (the others all name
+    page 0)."""
+    n = 2 ** 31 - 2
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("not enough memory for a table of 2^31 entries")
+    table, refs = torch.zeros(1, n, dtype=torch.int32, device="cuda"), torch.zeros(20, dtype=torch.int32, device="cuda")
+    refs[0], lens, rows = n, dev([n]), dev([n - 8])
+    pool = lib.PagePool(None, None, table, lens, refs, page_size=1)
+    op = lib.PagesUpdate(pool, None, rows)
+    op()
+    assert pool.errors() == 0 and lens.tolist() == [n - 8] and refs.tolist() == [n - 8] + [0] * 19
+    assert table[0, -12:].tolist() == [0] * 4 + [-1] * 8 and not table[0, :-8].any()
+    rows[0] = n - 1
+    op()
+    assert pool.errors() == 0 and lens.tolist() == [n - 1] and refs.tolist() == [n - 8] + [1] * 7 + [0] * 12
+    assert table[0, -12:].tolist() == [0] * 4 + [1, 2, 3, 4, 5, 6, 7, -1] and not table[0, :-8].any()
