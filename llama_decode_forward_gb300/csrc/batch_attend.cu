@@ -486,9 +486,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_ctas(HDP, NT))
             j = 0;
             do s++;
             while (lens[s] == 0);
-            np = (lens[s] + 15) / 16;
+            np = pieces_of(lens[s]);
         };
-        int np = (lens[s] + 15) / 16;
+        int np = pieces_of(lens[s]);
         const long long in_seq = x0 - (long long)starts[s] * units;
         int j = (int)(in_seq / (np + kUnit)), pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
         if (pc >= np) {                      // it starts with empty pieces

@@ -149,9 +149,12 @@ __device__ __forceinline__ int clipped_len(const PagesDev& p, int s) {
     return (int)max(0ll, min((long long)p.lens[s], (long long)p.max_pages << p.page_shift));
 }
 
+// Pieces of `len` rows (unsigned: len may be 2^31 - 1).
+__device__ __forceinline__ int pieces_of(int len) { return (int)(((uint32_t)len + 15) / 16); }
+
 // What a unit of a sequence of `len` rows counts in the deal: its pieces, then kUnit
 // empty ones.
-__device__ __forceinline__ int weight(int len) { return len > 0 ? (len + 15) / 16 + kUnit : 0; }
+__device__ __forceinline__ int weight(int len) { return len > 0 ? pieces_of(len) + kUnit : 0; }
 
 // The sequences' row counts, and the sums of their weights before each.
 __device__ __forceinline__ void count_pieces(const PagesDev& p, const AttendDev& a, int* starts, int* lens) {

@@ -99,9 +99,9 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             g = 0;
             do s++;
             while (lens[s] == 0);
-            np = (lens[s] + 15) / 16;
+            np = pieces_of(lens[s]);
         };
-        int np = (lens[s] + 15) / 16;
+        int np = pieces_of(lens[s]);
         const long long in_seq = x0 - (long long)starts[s] * units;
         const int j0 = (int)(in_seq / (np + kUnit));
         int g = j0 / rt, tile = j0 % rt, pc = (int)(in_seq % (np + kUnit)), left = (int)(x1 - x0);
@@ -129,13 +129,13 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
         asm volatile("mov.u32 %0, 0x64006400;" : "=r"(k1024));
 
         // the step that is loaded next: octet lane % OCT's page (-1: nothing to read there), looked up ahead
-        int ls = s, lg = g, ltile = tile, lpc = pc, lnp = np, lleft = left, page = -1, lend = 0;
+        int ls = s, lg = g, ltile = tile, lpc = pc, lnp = np, lleft = left, page = -1;
+        // (rows of a step are counted from its first one: a row behind the last of 2^31 - 1 has no number)
         auto look = [&]() {
-            const int e = lpc * 16 + 8 * (lane % OCT);
-            lend = min(lens[ls], 16 * (lpc + min(lleft, H)));
+            const int in = 8 * (lane % OCT);
             page = -1;
-            if (e < lend) {
-                page = p.table[(long long)ls * p.max_pages + (e >> p.page_shift)];
+            if (in < min(lens[ls] - lpc * 16, 16 * min(lleft, H))) {
+                page = p.table[(long long)ls * p.max_pages + ((lpc * 16 + in) >> p.page_shift)];
                 if (page < 0 || page >= p.n_pages) {
                     flag(p.err, LLM_PAGES_BAD_PAGE);
                     page = -1;
@@ -146,13 +146,13 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
         // requests the step into a place of the ring, moves on and looks the next one up.  An octet without a page is zero;
         // rows of its page that are not the sequence's come along
         auto load = [&](int to) {
-            const int e0 = lpc * 16, first_row = lg << p.page_shift;
+            const uint32_t e0 = (uint32_t)lpc * 16, first_row = (uint32_t)lg << p.page_shift;
             pages_ok |= (__ballot_sync(0xffffffffu, page >= 0) & ((1u << OCT) - 1)) << (4 * to);
 #pragma unroll
             for (int i = 0; i < OCT; i += NO) {
                 const int pg = __shfl_sync(0xffffffffu, page, i + n_oct);
                 const unsigned long long off = (unsigned long long)(uint32_t)max(pg, 0) * page_bytes +
-                                               (unsigned long long)(uint32_t)(first_row + ((e0 + 8 * (i + n_oct)) & (int)mask)) * pitch;
+                                               (unsigned long long)(first_row + ((e0 + 8 * (i + n_oct)) & mask)) * pitch;
                 if (n_in) {
                     cp_async16_or_zero(n_to + to * STAGE + i * (8 * pitch), kp + off, pg >= 0);
                     cp_async16_or_zero(n_to + to * STAGE + NUMBERS + i * (8 * pitch), vp + off, pg >= 0);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             for (int i = 0; i < OCT; i += PO) {
                 const int oc = i + p_oct, pg = __shfl_sync(0xffffffffu, page, oc % OCT);
                 const unsigned long long off = (unsigned long long)(uint32_t)max(pg, 0) * page_bytes +
-                                               (unsigned long long)(uint32_t)(first_row + ((e0 + 8 * oc) & (int)mask)) * pairs;
+                                               (unsigned long long)(first_row + ((e0 + 8 * oc) & mask)) * pairs;
                 if (p_in && oc < OCT) cp_async16_or_zero(p_to + to * STAGE + i * (8 * pairs), dp + off, pg >= 0);
             }
             const int n = min(min(lleft, H), lnp - lpc);
@@ -291,18 +291,18 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                         }
                     }
                 }
-                const int e0 = (pc + i0) * 16, end = min(lens[s], e0 + 16 * min(H, count - i0));
-                const bool whole = e0 + 16 * H <= end && has_page == (1u << OCT) - 1;
+                const int e0 = (pc + i0) * 16, rest = min(lens[s] - e0, 16 * min(H, count - i0));
+                const bool whole = rest >= 16 * H && has_page == (1u << OCT) - 1;
                 // rows that are not there, and those that some query rows do not see
-                if (!whole || e0 + 16 * H - 1 > e_min) {
+                if (!whole || 16 * H - 1 > e_min - e0) {
 #pragma unroll
                     for (int h = 0; h < H; h++)
 #pragma unroll
                         for (int q = 0; q < NT; q++)
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
-                                const int at = e0 + 16 * h + r + (k >> 1) * 8;
-                                if (!((has_page >> (2 * h + (k >> 1))) & 1u) || at >= end || at > e[q][k & 1]) sc[h][q][k] = -INFINITY;
+                                const int at = 16 * h + r + (k >> 1) * 8;
+                                if (!((has_page >> (2 * h + (k >> 1))) & 1u) || at >= rest || at > e[q][k & 1] - e0) sc[h][q][k] = -INFINITY;
                             }
                 }
                 uint32_t ph[H][NT][2], pl[H][NT][2];
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                     if (!whole)              // rows behind the last: whatever is there, their values are 0
 #pragma unroll
                         for (int k = 0; k < 4; k++)
-                            if (e0 + 16 * h + 8 * (k / 2) + 2 * t + k % 2 >= end) vd[k] = 0;
+                            if (16 * h + 8 * (k / 2) + 2 * t + k % 2 >= rest) vd[k] = 0;
 #pragma unroll
                     for (int x = 0; x < 2; x++) {
                         const __half2 d = half2_of(__byte_perm(vd[2 * x], vd[2 * x + 1], 0x5410)), m = half2_of(__byte_perm(vd[2 * x], vd[2 * x + 1], 0x7632));
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
                     // a row that some new tokens see and others do not: where its V is not
                     // finite, 0 * V would reach those that do not, so it is added to the
                     // others alone and taken out of the product
-                    if (p.n_new > 1 && e0 + 16 * h + 15 > e_min) {
+                    if (p.n_new > 1 && 16 * h + 15 > e_min - e0) {
 #pragma unroll
                         for (int x = 0; x < 2; x++)
 #pragma unroll

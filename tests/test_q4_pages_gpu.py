@@ -477,3 +477,45 @@ def test_rows_behind_the_last_do_not_matter(lib):  # noqa: F811
                     b.bytes[which][p, at:at + 8] = torch.tensor([1e3, -7.0, math.inf, -math.inf], dtype=F16, device="cuda").view(torch.uint8)
     op()
     assert torch.equal(out, first) and out.isfinite().all()
+
+
+@pytest.mark.parametrize("kind", ["q4", "f16"])
+@pytest.mark.parametrize("n_new", [1, 5])
+@pytest.mark.parametrize("types", [(F32, F32), (F16, F16)])
+def test_attend_rows_up_to_the_last_that_31_bits_count(lib, kind, n_new, types):  # noqa: F811
+    """Sequences of up to 2^31 - 8 rows whose table names one page again and again, with keys so far below the last four
+    pages' that they count for nothing (scores differ by more than 80: 2^31 e^-80 is 4e-26): what those four alone give."""
+    from test_batch_ops_gpu import Batch
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("not enough memory for a table of 2^28 entries")
+    low, far = 6, [1, 4, 0, 3]                                      # pages
+    b = BatchQ4(lib, [32], n_new, 0, 8, 1, 16) if kind == "q4" else Batch(lib, [32], n_new, 0, 8, 1, 16, poison=False)
+    if kind == "q4":
+        for t, x in zip(b.bytes, (-60.0, 5.0)):
+            pairs = t[:, 64:].view(F16).view(b.n_pages, 8, 2)
+            pairs[:] = torch.where(pairs.isnan(), torch.tensor([0.1, -0.75], dtype=F16, device="cuda"), pairs)
+            pairs[low, :, 0], pairs[low, :, 1] = 0.0, x
+        b.read()
+    else:
+        b.k[low], b.v[low] = -60.0, 5.0
+    table = torch.full((1, (1 << 28) - 1), low, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pages = (lib.PagedBatchQ4(*b.bytes, table, lens, 8, 1, 16, n_new=n_new) if kind == "q4"
+             else lib.PagedBatch(b.k, b.v, table, lens, n_new=n_new))
+    q, out = rand(3, n_new, 4, 16).abs().add_(0.3).to(types[0]), torch.empty(n_new, 4, 16, dtype=types[1], device="cuda")
+    op = lib.AttendBatch(pages, q, out)
+    ko, vo = (torch.empty(n_new, 1, 16, device="cuda") for _ in range(2))
+    read = lib.KvRead(pages, ko, vo)
+    b.table = torch.tensor([far], dtype=torch.int32, device="cuda")
+    for n in (2 ** 31 - 8, 2 ** 31 - 9, 2 ** 31 - 15, 2 ** 31 - 16, 2 ** 31 - 17, 2 ** 31 - 23, 2 ** 31 - 32, 2 ** 31 - 41, 2 ** 30 + 3):
+        last = (n - 1) // 8
+        table[0, last - 3:last + 1] = b.table[0]
+        lens[0], b.lens = n, [n - 8 * (last - 3)]
+        op()
+        read()
+        check_attend(b, q, out, None, None, what=f"{n} rows,")
+        for row, s, e in b.rows():
+            p, r = b.slot(s, e)
+            assert torch.equal(ko[row], b.k[p, r].float()) and torch.equal(vo[row], b.v[p, r].float())
+        assert pages.errors() == 0
+        table[0, last - 3:last + 1] = low
