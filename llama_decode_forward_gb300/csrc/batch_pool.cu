@@ -220,6 +220,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         stays = tail > 0 && read<ONE>(refs + part) == 0 && read<ONE>(first + part) == s;
         copy = tail > 0 && !stays;
         need = pages_of(now, shift) - full - stays;
+        // (more than there are: known here already, whatever the sum below says; tables and workspaces are not gone through)
+        if (need > p.n_pages) plan_or<ONE>(&bad[1], LLM_PAGES_FULL);
     }
     // both sums in one: copies in the lower bits (a thread has at most one)
     long long both;

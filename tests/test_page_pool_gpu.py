@@ -365,3 +365,31 @@ def test_sequences_of_as_many_pages_as_31_bits_count(lib):  # noqa: F811
     op()
     assert pool.errors() == 0 and lens.tolist() == [n - 1] and refs.tolist() == [n - 8] + [1] * 7 + [0] * 12
     assert table[0, -12:].tolist() == [0] * 4 + [1, 2, 3, 4, 5, 6, 7, -1] and not table[0, :-8].any()
+
+
+def test_update_wants_as_many_pages_as_32_bits_count(lib):  # noqa: F811
+    """4096 sequences of as many pages as the pool has, 2^32 together.  The table, the workspace and what a place of
+    32 bits could reach around the workspace are there: a sum cut to 32 bits would go on, within these."""
+    n = 1 << 20
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("not enough memory for a table of 2^32 entries")
+    refs, lens = (torch.zeros(k, dtype=torch.int32, device="cuda") for k in (n, 4096))
+    table = torch.full((4096, n), -1, dtype=torch.int32, device="cuda")
+    pool = lib.PagePool(None, None, table, lens, refs, page_size=1)
+    rows = torch.full((4096,), n, dtype=torch.int32, device="cuda")
+    need = lib.binding._lib.llm_pages_update_workspace(lib.binding.ctypes.byref(pool.struct))
+    before, behind = 9 << 30, 2 << 30
+    ws = torch.empty(before + need + behind, dtype=torch.uint8, device="cuda")
+    assert ws.data_ptr() % 256 == 0 and need > table.numel() * 4
+    torch.cuda.synchronize()
+    call = lambda: lib.binding._lib.llm_pages_update(lib.binding.ctypes.byref(pool.struct), None, rows.data_ptr(), ws.data_ptr() + before, need, None)  # noqa: E731
+    assert call() == 0
+    torch.cuda.synchronize()
+    assert pool.errors() == lib.LLM_PAGES_FULL and not lens.any() and not refs.any() and int(table.max()) == -1
+    pool.err.zero_()
+    rows[1:] = 0
+    torch.cuda.synchronize()
+    assert call() == 0                                              # all of them for the first
+    torch.cuda.synchronize()
+    assert pool.errors() == 0 and torch.equal(table[0], torch.arange(n, dtype=torch.int32, device="cuda")) and int(table[1:].max()) == -1
+    assert int(lens[0]) == n and not lens[1:].any() and int(refs.min()) == 1 and int(refs.max()) == 1
