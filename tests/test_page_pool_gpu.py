@@ -393,3 +393,79 @@ def test_update_wants_as_many_pages_as_32_bits_count(lib):  # noqa: F811
     torch.cuda.synchronize()
     assert pool.errors() == 0 and torch.equal(table[0], torch.arange(n, dtype=torch.int32, device="cuda")) and int(table[1:].max()) == -1
     assert int(lens[0]) == n and not lens[1:].any() and int(refs.min()) == 1 and int(refs.max()) == 1
+
+
+# A plan runs as a cluster of blocks where n_seqs > 1024, n_pages > 16384 or there are more than 65536 entries.
+@pytest.mark.parametrize("n_seqs,n_pages", [(4096, 70000), (40, 70000)])
+def test_update_refusals_of_large_pools_change_nothing(lib, n_seqs, n_pages):  # noqa: F811
+    """The refusals of test_update_refusals_change_nothing where another block than the first finds the reason."""
+    p = Pool(lib, np.random.RandomState(n_seqs).randint(9, 81, n_seqs), 8, n_pages, 12, layers=0)
+    last, mid, held = n_seqs - 1, n_seqs // 2, p.lens.copy()
+
+    def refused(want, parents=None, rows=None):
+        run(lib, p, parents, rows, want=want)                      # (compares the whole state with what it was)
+        p.pool.err.zero_()
+
+    def with_one(x, at, v):
+        y = np.array(x, np.int32)
+        y[at] = v
+        return y
+
+    order = np.arange(n_seqs)
+    for at in (last, mid):
+        refused(16, with_one(order, at, n_seqs))
+        refused(16, with_one(order, at, -2), held)
+        refused(2, None, with_one(held, at, 97))
+        refused(2, None, with_one(held, at, -1))
+        refused(18, with_one(order, 0, n_seqs), with_one(held, at, -1))
+    # more pages than the five that the caller has left free
+    kept = np.flatnonzero(p.refs == 0)[:-5]
+    p.refs[kept], p.dev["refs"][torch.from_numpy(kept).cuda()] = 1, 1
+    for at in (last, mid):
+        refused(8, None, with_one(held, np.arange(at - 2, at + 1), 96))
+    run(lib, p, None, with_one(held, last, held[last] // 8 * 8 + 9))
+    held = p.lens.copy()
+    p.refs[kept], p.dev["refs"][torch.from_numpy(kept).cuda()] = 0, 0
+    # entries that name no page: given up, taken over whole and in part
+    for at in (last, mid):
+        for bad in (n_pages, -5):
+            good = int(p.table[at, 0])
+            p.table[at, 0] = bad
+            p.dev["table"][at, 0] = bad
+            refused(1, None, with_one(held, at, 0))
+            refused(1, with_one(order, 0, at), None)
+            p.table[at, 0] = good
+            p.dev["table"][at, 0] = good
+        i = (int(held[at]) - 1) // 8
+        if held[at] % 8:
+            good = int(p.table[at, i])
+            p.table[at, i] = n_pages + 3
+            p.dev["table"][at, i] = n_pages + 3
+            refused(1, with_one(order, 0, at), None)
+            p.table[at, i] = good
+            p.dev["table"][at, i] = good
+    # fewer counted holders than there are, of the highest page that is given up
+    at = int(max(range(n_seqs), key=lambda s: p.table[s, 0]))
+    j = int(p.table[at, 0])
+    p.refs[j], p.dev["refs"][j] = 0, 0
+    refused(1, None, with_one(held, at, 0))
+    p.refs[j], p.dev["refs"][j] = 1, 1
+    run(lib, p, order[::-1].copy(), None)                          # and it goes on
+    run(lib, p, None, np.minimum(96, p.lens + 3))
+
+
+@pytest.mark.parametrize("n_seqs,n_pages,width", [(1024, 5000, 12), (1025, 5000, 12), (30, 16384, 12), (30, 16385, 12), (512, 4000, 128), (512, 4000, 129)])
+def test_updates_and_copies_around_the_largest_plan_of_one_block(lib, n_seqs, n_pages, width):  # noqa: F811
+    """Both plans, with pages: copies from and to every block's share."""
+    r = np.random.RandomState(n_pages + n_seqs + width)
+    p = Pool(lib, r.randint(0, min(25, n_pages * 4 // n_seqs), n_seqs), 8, n_pages, width, layers=1)
+    for parents in (r.randint(-1, n_seqs, n_seqs), r.randint(0, n_seqs, n_seqs), np.arange(n_seqs)):
+        had = np.where(parents < 0, 0, p.lens[parents])
+        run(lib, p, parents, np.clip(had + r.randint(-8, 4, n_seqs), 0, 24))
+    assert (p.refs > 1).any() or n_seqs < 100
+    c = lib.PagesCompact(p.pool)
+    table, refs, moved, n, p.k, p.v = compacted(p)
+    c()
+    p.table, p.refs = table, refs
+    p.check()
+    assert np.array_equal(c.moved.cpu().numpy(), moved) and int(c.n_live) == n
