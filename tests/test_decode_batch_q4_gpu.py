@@ -216,3 +216,23 @@ def test_forks(lib):  # noqa: F811
         if step >= 11:
             assert (y[0] - x[1]).abs().max() <= TOL[cfg.wtype] and (y[2] - x[1]).abs().max() <= TOL[cfg.wtype]
     dec.close()
+
+
+@pytest.mark.parametrize("kw,page", [(dict(dim=320, n_heads=8, n_kv_heads=2, head_dim=40, number=85), 16), (dict(), 4)])
+def test_refusals_with_tensors_of_a_step_on_f16_pages(lib, kw, page):  # noqa: F811
+    """Every pointer is a real one (pages in FP16 are larger than those of 4-bit values), and nothing is written."""
+    cfg = config(**kw)
+    dec = lib.Decoder(cfg, synth.make_weights(cfg))
+    bd = lib.BatchDecoder(dec, 2, 20, 0, page_size=page)
+    put(bd, cfg, [1, 1])
+    bd.logits.fill_(7.0)
+    bd.pages.fill_(3.0)
+    torch.cuda.synchronize()
+    assert lib.binding._lib.llm_decode_batch_q4(dec.h, ctypes.addressof(bd.struct)) == lib.LLM_ERR_UNSUPPORTED
+    assert lib.llm_last_error(dec.h)
+    torch.cuda.synchronize()
+    assert (bd.logits == 7.0).all() and (bd.pages == 3.0).all() and bd.errors() == 0
+    bd.step()                                                       # the handle goes on
+    lib.llm_sync(dec.h)
+    assert bd.logits.isfinite().all() and not (bd.logits == 7.0).any() and bd.errors() == 0
+    dec.close()

@@ -519,3 +519,58 @@ def test_attend_rows_up_to_the_last_that_31_bits_count(lib, kind, n_new, types):
             assert torch.equal(ko[row], b.k[p, r].float()) and torch.equal(vo[row], b.v[p, r].float())
         assert pages.errors() == 0
         table[0, last - 3:last + 1] = low
+
+
+@pytest.mark.parametrize("offset", [0.3, 1000.24, -1000.24, 60000.0, -60000.0, 65503.0])
+@pytest.mark.parametrize("spread", [1e-6, 1e-4, 1e-2, 0.7, 40.0])
+def test_append_small_spreads_about_large_values(lib, offset, spread):  # noqa: F811
+    """m is off by up to half an FP16 step of the values, many times d: quotients far beyond 15, or far below 0."""
+    b = BatchQ4(lib, [9], 8, 0, 16, 2, 64)
+    k, v = (offset + spread * torch.rand(8, 2, 64, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    k[3, 0, 5], v[4, 1, 40] = k[3, 0, 5] + 15 * spread, v[4, 1, 40] - 15 * spread
+    before = [t.clone() for t in b.bytes]
+    lib.KvAppend(b.pages, None, k, v, torch.zeros(16, 0, 2, device="cuda"))()
+    check_append(b, before, None, k, v, None, torch.zeros(16, 0, 2), False)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("heads,n_new", [((20, 1, 48), 1), ((24, 1, 32), 1), ((36, 2, 16), 1), ((8, 2, 32), 5), ((6, 2, 48), 7), ((4, 1, 16), 6)])
+def test_attend_24_query_rows_of_short_heads(lib, heads, n_new, types):  # noqa: F811
+    run_attend(lib, heads, [max(n_new, n) for n in (1, 16, 17, 33, 250)] + [2], n_new, 70, 16, *types)
+    run_attend(lib, heads, [max(n_new, n) for n in (8, 31, 32, 65)], n_new, 0, 8, *types)
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (F16, F16)])
+@pytest.mark.parametrize("heads,n_new", [((25, 1, 32), 1), ((40, 1, 48), 1), ((8, 2, 32), 10), ((4, 1, 16), 33)])
+def test_attend_many_query_rows_of_short_heads(lib, heads, n_new, types):  # noqa: F811
+    run_attend(lib, heads, [max(n_new, n) for n in (1, 17, 100, 250)] + [3], n_new, 70, 16, *types)
+
+
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("what", [(math.inf, 0.0), (math.nan, math.nan), (60000.0, 60000.0)])
+@pytest.mark.parametrize("heads,n_new", [((4, 1, 64), 6), ((8, 2, 64), 5), ((6, 2, 48), 7), ((8, 2, 32), 5)])
+def test_attend_wild_values_of_later_tokens_in_24_query_rows(lib, heads, n_new, types, what):  # noqa: F811
+    """As test_attend_wild_values_of_later_tokens: they reach their token and the ones behind it, none before it."""
+    n_heads, n_kv, hd = heads
+    h, group = n_heads // n_kv, min(1, -(-hd // 32) - 1)
+    b = BatchQ4(lib, [37, 100], n_new, 40, 16, n_kv, hd)
+    n = 2 * n_new
+    q, pk, pv = rand(1, n, n_heads, hd, dtype=types[0]), rand(2, 40, n_kv, hd, dtype=F16), rand(3, 40, n_kv, hd, dtype=F16)
+    poke(b, 1, 0, 35, 0, group, *what)                              # V of the last token but one
+    poke(b, 0, 1, 98, 0, 0, math.nan, math.nan)                     # K of the last but one
+    out = torch.empty(n, n_heads, hd, dtype=types[1], device="cuda")
+    op = lib.AttendBatch(b.pages, q, out, pk, pv)
+    op()
+    p, r = b.slot(0, 35)
+    bad = ~b.v[p, r, 0].isfinite()
+    assert bad.any()
+    first, second = out[:n_new], out[n_new:]
+    assert first[:-2].isfinite().all() and second[:-2].isfinite().all()
+    assert not first[-2:, :h, bad].isfinite().any() and first[-2:, :h, ~bad].isfinite().all() and first[-2:, h:].isfinite().all()
+    assert second[-2:, :h].isnan().all() and second[-2:, h:].isfinite().all()
+    wild = out.clone()
+    poke(b, 1, 0, 35, 0, group, 0.1, -0.5)
+    poke(b, 0, 1, 98, 0, 0, 0.1, -0.5)
+    op()
+    check_attend(b, q, out, pk, pv)
+    assert torch.equal(out[:n_new - 2], wild[:n_new - 2]) and torch.equal(out[n_new:n - 2], wild[n_new:n - 2])
