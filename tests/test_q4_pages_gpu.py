@@ -574,3 +574,49 @@ def test_attend_wild_values_of_later_tokens_in_24_query_rows(lib, heads, n_new, 
     op()
     check_attend(b, q, out, pk, pv)
     assert torch.equal(out[:n_new - 2], wild[:n_new - 2]) and torch.equal(out[n_new:n - 2], wild[n_new:n - 2])
+
+
+@pytest.mark.parametrize("q_dtype,std", [(F32, 0.05), (F16, 0.05), (F32, 0.0), (F16, 0.0)])
+@pytest.mark.parametrize("heads", [(1, 1, 64), (8, 1, 64), (20, 1, 64), (4, 1, 128), (12, 1, 128), (7, 1, 48)])
+def test_attend_sums_of_many_rows_do_not_fall_short(lib, heads, q_dtype, std):  # noqa: F811
+    """2^26 rows (of 4096 pages) that count much alike, with values of one sign.
+
+    A share's sum takes N additions, one for each of its pieces of 16 rows, and the join one for each of at most W
+    parts.  Each is rounded to nearest, by at most H32 of the sum so far; over pieces in no order these are
+    independent, of deviation at most H32 / sqrt(3): six deviations of an element's sum, and of the mean error over the hd
+    elements, are allowed.  What may lean to one side: a piece's own sum, whose products the matrix instruction cuts off
+    (four cuts of at most a step, 2 H32), a probability as two F16 parts (2^-22), and the scores (attend_bound's ds,
+    which moves the mean of the values by at most twice that of their mean distance from it).  A sum that is itself cut
+    off at every piece falls short by half a step of a sum half as large on the average: 2e-5 and more here.
+    With std 0 (every row counts alike) a thread's sum of probabilities takes N / 2 additions, one a step of 32 rows, of equal
+    numbers, whose roundings are not independent: H32 of the sum so far each, half the sum on the average, H32 N / 4."""
+    n_heads, n_kv, hd = heads
+    n, page, n_pages = 1 << 26, 16, 4096
+    b = BatchQ4(lib, [n_pages * page], 1, 0, page, n_kv, hd)
+    g = -(-hd // 32)
+    pairs = b.bytes[1][:, page * n_kv * hd // 2:][:, :page * n_kv * g * 4].view(F16).view(b.n_pages, -1, 2)
+    r = torch.Generator().manual_seed(3)
+    pairs[..., 0] = (0.02 + 0.2 * torch.rand(pairs.shape[:2], generator=r)).half().cuda()
+    pairs[..., 1] = (0.5 + torch.rand(pairs.shape[:2], generator=r)).half().cuda()
+    b.read()
+    which = torch.randint(0, n_pages, (n // page,), generator=r)
+    pages = lib.PagedBatchQ4(*b.bytes, b.table[0][which.cuda()][None].contiguous(), torch.tensor([n], dtype=torch.int32, device="cuda"), page, n_kv, hd)
+    q, out = rand(4, 1, n_heads, hd, dtype=q_dtype, std=std), torch.empty(1, n_heads, hd, device="cuda")
+    lib.AttendBatch(pages, q, out)()
+    k, v = (b.gather(t, 0, n_pages * page)[:, 0] for t in (b.k, b.v))                 # [rows, hd]
+    count = torch.bincount(which, minlength=n_pages).double().cuda().repeat_interleave(page)
+    s = q[0].double() @ k.T * hd ** -0.5
+    w = count * (s - s.amax(-1, keepdim=True)).exp()
+    w /= w.sum(-1, keepdim=True)
+    want = w @ v
+    mag = float((q[0].double().abs() @ k.abs().T).max()) * hd ** -0.5
+    ds = mag * ((hd + 4) * 2 * H32 + 2.0 ** -22) + 3 * (mag + 2 * float(s.abs().max())) * H32 + 2.0 ** -22
+    apart = max(float((w[h] @ (v - want[h]).abs() / want[h]).max()) for h in range(n_heads))
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    workers = 4 * 2 * sms                                           # at least: two blocks of four warps an SM (at most four)
+    deviation = H32 * math.sqrt((n / 16 / workers + 2 * workers) / 3)
+    lean = 4 * 2 * H32 + 2.0 ** -22 + 2 * ds * apart + (H32 * n / 16 / workers / 4 if std == 0 else 0)
+    e = out[0].double() / want - 1
+    assert e.abs().max() <= lean + 6 * deviation, (float(e.abs().max()), lean, deviation)
+    assert e.mean(-1).abs().max() <= lean + 6 * deviation / math.sqrt(hd), (e.mean(-1).tolist(), lean, deviation)
+    assert pages.errors() == 0
