@@ -19,7 +19,7 @@ struct AttendDev {
     int out_f16;
     float* prefix_o;                // [n_kv * row tiles + blocks][2 groups][128][hd]
     float2* prefix_ml;              // [n_kv * row tiles + blocks][2][128]: Y, l
-    float* suffix_o;                // [units of all sequences + workers][up to 16 rows][hd]
+    float* suffix_o;                // [units of all sequences + workers][up to 16 rows, of 4-bit pages 24][hd]
     float2* suffix_ml;
     int* starts;                    // [n_seqs + 1]: pieces of the sequences before each
     int prefix_blocks, suffix_workers;

@@ -8,8 +8,9 @@ namespace llm {
 namespace {
 
 // A value is made where it is used: numbers become F16 by their bits (0x6400 | n is
-// 1024 + n, 0x6400 | 16 n is 1024 + 16 n; one exact operation takes the 1024 away) and
-// one fused multiply-add rounds d n + m to the F16 that it stands for.
+// 1024 + n, 0x6400 | 16 n is 1024 + 16 n; one exact operation takes the 1024 away: Kim,
+// Henry, Fahim and Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into
+// Cloud Scale Production", 2022) and one fused multiply-add rounds d n + m to the F16 that it stands for.
 // - K is the products' first operand: lane (r, t) holds dims 64 c + 16 t + {0 .. 15} of
 //   cached rows r and r + 8, two words of numbers.  Their half-words pair dims 0 and 4, 1
 //   and 5, ... of a word, so q is loaded in that order.
@@ -21,18 +22,20 @@ namespace {
 // warp has a ring of steps in shared memory, filled by asynchronous 16-byte copies: an
 // octet's numbers lie in a row, and so do its pairs, so a step of 32 rows of heads of 64
 // values takes five copies of a warp where loads into registers took 24.
-// - A piece's product is a sum of its own, added to the unit's in F32.  The matrix instruction cuts what it adds to
-//   its accumulator off towards zero, so a sum that went through it all the way fell short by some 2^-25 of itself
-//   a piece: 32 sequences of 1 to 4096 rows, heads of 128, F32, came out 1.8e-6 of the answer away from the exact one,
-//   8e-7 this way (a plain form in F32: 5e-7); one sequence of 2^26 rows 2e-4 to 4e-4 away.  It costs 1 to 2 %.
+// A piece's product is a sum of its own, added to the unit's in F32.  The matrix instruction cuts what it adds to
+// its accumulator off towards zero, so a sum that went through it all the way fell short by some 2^-25 of itself
+// a piece: 32 sequences of 1 to 4096 rows, heads of 128, F32, came out 1.8e-6 of the answer away from the exact one,
+// 8e-7 this way (a plain form in F32: 5e-7); one sequence of 2^26 rows 2e-4 to 4e-4 away.  It costs 1 to 2 %.
 // PACK: up to four query rows.  The eight columns of a product hold each of them twice;
 // the second four take the probabilities' second parts, so one product adds both.
 // FULL: head_dim is HDP, so that the distances of rows and pairs are constants.
-// What bounds it: making the values.  A step of 32 rows of heads of 64 values takes a warp some 560
-// instructions, 230 of them for the 4096 values; the logical and the half-precision operations together keep their
-// two units busy 95 % of the time (one half each).  64 sequences of 1 to 8192 rows, 8 heads of 64 (194 MB): 58 us, 3.3 TB/s, 95 us
-// as first written; 32 of 1 to 4096, 32 heads of 128 (390 MB): 103 us, 3.8 TB/s, from 179 us.  F16 pages of the
-// same rows would be 3.2 times the bytes.  Steps of 16 rows take 5 to 20 % longer; of 64 rows, 3 % less on the
+// What bounds it: its instructions, no unit of them alone.  A step of 32 rows of heads of 64 values takes a warp 571
+// (smsp__inst_executed over the steps); making the 4096 values is 224 of them by this source (three for each of a lane's
+// 64 pairs, 8 shifts, 24 permutations).  64 sequences of 1 to 8192 rows, 8 heads of 64: issue 66 %, ALU 49 %, FMA (which
+// has the half-precision operations) 49 %, DRAM 40 %; a loop of independent logical and half-precision operations in
+// turn reaches 73 and 72 % of what each does alone, so the two units do not wait for one another.
+// That case (194 MB) takes 59 us, 3.3 TB/s, 95 us as first written; 32 sequences of 1 to 4096, 32 heads of 128 (390 MB)
+// 102 to 105 us, 3.7 TB/s, from 179 us.  F16 pages of the same rows would be 3.2 times the bytes.  Steps of 16 rows take 5 to 20 % longer; of 64 rows, 3 % less on the
 // first, 20 % more where sequences are short.  Neither more blocks on an SM nor fewer (12 to 20 warps), nor an order of rows
 // without bank conflicts, changed these by more than 4 %.
 constexpr int kQ4Pieces = 2, kQ4Stages = 2;
@@ -50,8 +53,8 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 __host__ __device__ constexpr int suffix_q4_ctas(int hdp, int nt) { return hdp == 64 ? (nt == 1 ? 4 : nt == 2 ? 3 : 2) : (nt == 1 ? 3 : 2); }
 
-// Pairs of numbers of a word, as F16 pairs.  (x & m | c in one instruction: left to itself the compiler takes
-// two, each with a constant of its own; a step of 32 rows then had 145 logical operations, of 777.)
+// Pairs of numbers of a word, as F16 pairs.  (x & m | c as one instruction: written as an expression, the 64
+// sequences above take 62.3 us for 59.1, the 32 with heads of 128 110.1 us for 101.8.)
 __device__ __forceinline__ __half2 half2_of(uint32_t x) { return *reinterpret_cast<const __half2*>(&x); }
 __device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t c) {
     uint32_t y;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(32 * kSuffixWarps, suffix_q4_ctas(HDP, NT))
             if (left > 0) next(s, g, tile, pc, np);
         }
     }
-    if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();   // (as the suffix kernel above)
+    if (!first && blockIdx.x + 1 == gridDim.x) griddep_wait();   // (as batch_attend.cu's suffix_kernel)
 }
 
 // (*e: whether it may have the shared memory that it needs)
@@ -510,7 +513,10 @@ int padded(int head_dim) { return head_dim <= 64 ? 64 : 128; }
 }  // namespace
 
 // More than 16 query rows are taken at once (up to 24, where the registers allow) as long as one unit then does,
-// since every unit makes the values anew.
+// since every unit makes the values anew.  64 sequences of up to 8192 rows: 20 rows of heads of 64 25.2 us, 28.9 us as two
+// units of 16; 24 rows of heads of 48 26.5 and 31.7 us; 12 sequences of 20 rows in F32 behind a prefix 42.1 and 43.1 us.
+// For 33 to 48 rows two units of 24 for three of 16 give nothing for sure: 40 rows in F16 128.4 us for 130.8 (64
+// sequences of 10 new tokens), 48 rows 137.3 us for 134.8, 40 rows in F32 53.3 us for 52.3 (12 sequences).
 int unit_rows_q4(int srows, int head_dim) { return srows <= 8 ? 8 : srows > 16 && srows <= 24 && head_dim <= 64 ? 24 : 16; }
 int suffix_ctas_q4(int unit_rows, int head_dim) { return suffix_q4_ctas(padded(head_dim), unit_rows / 8); }
 int suffix_smem_q4(int n_seqs, int head_dim) { return ((2 * n_seqs + 1) * 4 + 15) / 16 * 16 + q4_rings(padded(head_dim)); }

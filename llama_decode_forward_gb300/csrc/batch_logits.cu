@@ -19,7 +19,7 @@ namespace {
 // their logits once more.  Bound by the stream of logits, and by instructions where lists are long.
 // 256 rows of 151,936, F32: 46 us alone (6.8 TB/s), 66 us with 1024 tokens counted, 50 biases and
 // a mask (97 us when each word was looked at within the stream: most warps met a touched token in
-// most steps, one lane at a time), 79 us with 8000 tokens counted and 122 us with 30,000 (196 us and 400 us as
+// most steps, one lane at a time), 78 us with 8000 tokens counted and 120 us with 30,000 (196 us and 400 us as
 // clusters of blocks that share the reading of the lists and count in each other's shared memory).
 constexpr int kAdjThreads = 512, kAdjSteps = 4;                  // chunks of 128 tokens (four for each lane) of a warp
 constexpr int kAdjChunk = 128, kAdjSpan = kAdjThreads / 32 * kAdjSteps * kAdjChunk;      // tokens of a block

@@ -122,10 +122,12 @@ __device__ __forceinline__ uint32_t quantize8(const float (&u)[8], bool live, ui
     const float df = __half2float(d), mf = __half2float(m);
     uint32_t w = 0;
     if (!wild && df > 0.f) {
-        // n is the quotient's nearest integer.  A product with the reciprocal (1 / d and the product off by a rounding
-        // each, of a number below 24: 15 and what d's rounding adds, at most by half where d is the smallest F16) is within
-        // 2.9e-6 of it, and the quotient's own rounding 1.5e-6; so only one that lies near a half is divided.  1.5 2^23 + y
-        // holds y's nearest integer in its last bits.
+        // n is the nearest integer of the quotient x / d (rounded to F32), cut off at 0 and 15.  y = x (1 / d) is off by
+        // the rounding of 1 / d, the quotient by its own: where one of them is within [-0.5, 16], they lie within
+        // 2 * 2^-24 * 16 = 1.9e-6 of one another, so only a y that lies within 1e-5 of a half is divided.  (Elsewhere both
+        // are cut off alike, and that is common: m is rounded to F16, so a group with a small spread about a large
+        // value has quotients of any size and either sign.)  t = 1.5 2^23 + y holds y's nearest integer in its last bits
+        // where |y| < 2^22; beyond, t lies below kWhole or above kWhole + 15, as it should.
         constexpr float kWhole = 12582912.f;
         const float inv = __frcp_rn(df);
         float near = 0.f;
