@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
         stays = tail > 0 && read<ONE>(refs + part) == 0 && read<ONE>(first + part) == s;
         copy = tail > 0 && !stays;
         need = pages_of(now, shift) - full - stays;
-        // (more than there are: known here already, whatever the sum below says; tables and workspaces are not gone through)
+        // (a sequence that wants more pages than there are is refused without the sum below)
         if (need > p.n_pages) plan_or<ONE>(&bad[1], LLM_PAGES_FULL);
     }
     // both sums in one: copies in the lower bits (a thread has at most one)
